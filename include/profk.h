@@ -338,6 +338,111 @@ int profk_refine(const uint64_t* keys, int64_t R, int64_t k, const float* x, int
 int profk_exact(const float* x, int64_t n, int64_t k, float* out_vals, int64_t* out_idx,
                 cudaStream_t stream);
 
+/* ---- the selections of a language model --------------------------------- */
+
+/* Element type of the logits (and of their gradient). */
+typedef enum profk_type { PROFK_F32 = 0, PROFK_BF16 = 1, PROFK_F16 = 2 } profk_type;
+
+/* How profk_sample_tokens picks.  Each pointer is a device array of `rows`
+ * values, or NULL: every row then takes the `all_` value.
+ *   temperature  T >= 0; 0 takes the first token of the library order
+ *   top_k        keep the first top_k of the library order; <= 0 or >= n: off
+ *   top_p        of those, keep a token while the mass before it is below
+ *                top_p of theirs; >= 1: off, <= 0: one token
+ *   min_p        of those, keep the tokens of at least min_p times the largest
+ *                probability; <= 0: off, >= 1: only copies of the largest logit */
+typedef struct profk_sampling {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float all_temperature;
+  int32_t all_top_k;
+  float all_top_p;
+  float all_min_p;
+} profk_sampling;
+
+/* One token per row of logits, from given random numbers.  With m the
+ * largest allowed logit, x_i = (l_i - m) / T (0 where l_i = m) and
+ * w_i = exp(x_i), the kept tokens are a prefix of the library order (logits
+ * descending, equal ones by ascending index): top_k, then top_p over the mass
+ * of those, then min_p.  The token is the kept one with the largest
+ * x_i - log q_i (the lowest index of equal ones); for independent q_i ~ Exp(1)
+ * that is a draw with probability w_i / sum w over the kept.
+ *   logits       device, row r at r*ld elements, n values of `type`
+ *   n            1 <= n < 2^31
+ *   noise        device, row r at r*noise_ld; q_i > 0 (only the kept tokens'
+ *                are used, but any may be read); a NaN is never ahead.
+ *                noise_ld = 0 gives every row the same numbers
+ *   mask         device, or NULL: bit i % 32 of word i / 32 of the row (at
+ *                r*mask_ld words) is set where token i is allowed.  What the
+ *                others hold (NaN, inf) does not matter
+ *   out_tokens   device, rows int64
+ *   out_logprobs device, rows float: x_token - log(sum w over the kept); 0
+ *                when T = 0
+ * A logit of -inf is never kept.  A row in which nothing can be kept gives
+ * the token -1 and -inf; an allowed NaN, a negative or NaN temperature, or a
+ * NaN top_p or min_p gives -1 and NaN (the call does not wait for the device,
+ * so it cannot return PROFK_ERR_NAN).  Sums of w are exact 64-bit integer
+ * sums of rounded weights or float sums in a fixed order: the same call gives
+ * the same result.  The call only enqueues work on `stream`, allocates
+ * nothing, and may be captured in a graph.  rows = 0 is allowed. */
+int profk_sample_tokens(const void* logits, int type, int64_t rows, int64_t n, int64_t ld, const float* noise,
+                        int64_t noise_ld, const uint32_t* mask, int64_t mask_ld, const profk_sampling* how,
+                        int64_t* out_tokens, float* out_logprobs, cudaStream_t stream);
+
+/* How profk_route scores and gates. */
+#define PROFK_SCORE_SOFTMAX 0
+#define PROFK_SCORE_SIGMOID 1
+typedef struct profk_routing {
+  int score;           /* PROFK_SCORE_SOFTMAX or PROFK_SCORE_SIGMOID */
+  int normalize;       /* nonzero: the gates of a token sum to 1 */
+  const float* bias;   /* device, `experts` floats added to the logits for the choice only, or NULL */
+  const uint8_t* mask; /* device, `tokens` bytes, 0 for a token that is not routed (padding), or NULL */
+} profk_routing;
+
+/* Top-k experts of each token.  A token's choice is the first k experts in
+ * the library order of c = z + bias (float32), z its logits; c = -inf and NaN
+ * are never chosen, and slots left over (or all slots of a masked token) hold
+ * expert -1 and gate 0.  With y = z (softmax) or log sigmoid(z) (sigmoid) and
+ * p = softmax(y) over the experts, a chosen expert's gate is
+ *   normalize:  exp(y) / sum of exp(y) over the token's chosen experts
+ *   otherwise:  p (softmax) or sigmoid(z) (sigmoid).
+ * counts[e] is the number of slots that hold e.  The balance loss is
+ *   experts * sum_e (counts[e] / N) P_e,  P_e = sum_t n_t p_te / N,
+ * n_t the slots token t filled and N = sum n_t (0 when N = 0): 1 when every
+ * expert gets the same share, more when the favoured ones get more.
+ *   logits      device, token t at t*ld elements, `experts` values of `type`
+ *   experts     1 .. 1024 (else PROFK_ERR_UNSUPPORTED)
+ *   k           1 .. min(experts, 32) (above 32 PROFK_ERR_UNSUPPORTED)
+ *   out_gates   device, tokens*k floats, in the order of the choice
+ *   out_experts device, tokens*k int64
+ *   out_counts  device, `experts` int64
+ *   out_loss    device, one float, or NULL
+ * A NaN among the logits of a token that is not masked makes its gates and
+ * the loss NaN; its experts are still valid.  The call only enqueues work on
+ * `stream`, with a workspace from the library's pool; the same call gives the
+ * same bits.  tokens = 0 is allowed. */
+int profk_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t ld, int64_t k,
+                const profk_routing* how, float* out_gates, int64_t* out_experts, int64_t* out_counts, float* out_loss,
+                cudaStream_t stream);
+
+/* Gradient of profk_route with respect to the logits; the choice and the
+ * counts are constants.  `score` and `normalize` of `how` as in the call that
+ * gave `chosen`; its bias and mask are not looked at (a masked token has no
+ * chosen expert, and gets the gradient 0).
+ *   chosen      device, tokens*k int64 as out_experts; entries outside
+ *               [0, experts) are empty slots
+ *   counts      device, `experts` int64 (NULL when grad_loss is): out_counts,
+ *               or its sum over the devices that share the loss
+ *   grad_gates  device, tokens*k floats, or NULL: no gradient of the gates
+ *   grad_loss   device, one float, or NULL: no gradient of the loss
+ *   grad_logits device, token t at t*grad_ld elements, `experts` values of `type` */
+int profk_route_backward(const void* logits, int type, int64_t tokens, int64_t experts, int64_t ld, int64_t k,
+                         const profk_routing* how, const int64_t* chosen, const int64_t* counts,
+                         const float* grad_gates, const float* grad_loss, void* grad_logits, int64_t grad_ld,
+                         cudaStream_t stream);
+
 /* ---- calls that allocate nothing --------------------------------------- */
 
 /* Bytes of the fixed device scratch array behind profk_topk_noalloc.  Every

@@ -17,10 +17,11 @@ from ._abi import (OPT_FILTER_CTAS_PER_SM, OPT_FORCE_M, OPT_FORCE_S, OPT_FORCE_T
                    OPT_TIMING, OPT_WAIT_TEST, WAIT_TEST_OFF, WAIT_TEST_REFINE, WAIT_TEST_SAMPLER, WAIT_TEST_SORT, PARAMS_CORRECTED,
                    PARAMS_DEFAULT, PARAMS_EXACT, SAMPLER_AUTO, SAMPLER_GRID, SAMPLER_LISTS, SAMPLER_STEPS,
                    PARAMS_OLD, PATH_EXACT, PATH_FALLBACK, PATH_FILTER, PATH_TIE, ProfkError, ProfkStats)
+from ._lm import Routing, route, route_backward, sample_tokens
 
 __all__ = ["topk", "topk_batched", "topk_noalloc", "params", "workspace_size", "set_option", "get_option", "reset_options",
            "sample", "threshold", "filter_pass", "refine", "exact", "last_stage_ms", "ProfkError", "ProfkStats",
-           "lib"]
+           "lib", "sample_tokens", "route", "route_backward", "Routing"]
 
 
 def lib():

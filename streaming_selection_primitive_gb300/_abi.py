@@ -52,6 +52,21 @@ class ProfkStats(C.Structure):
         return dict(zip(_STATS_NAMES, _STATS_FMT.unpack(bytes(self))))
 
 
+F32, BF16, F16 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+
+
+class Sampling(C.Structure):
+    _fields_ = [
+        ("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p),
+        ("all_temperature", C.c_float), ("all_top_k", C.c_int32), ("all_top_p", C.c_float), ("all_min_p", C.c_float),
+    ]
+
+
+class Routing(C.Structure):
+    _fields_ = [("score", C.c_int), ("normalize", C.c_int), ("bias", C.c_void_p), ("mask", C.c_void_p)]
+
+
 _STATS_NAMES = tuple(name for name, _ in ProfkStats._fields_)
 _STATS_FMT = __import__("struct").Struct("=7q2f4iQfi")
 assert _STATS_FMT.size == C.sizeof(ProfkStats)
@@ -93,6 +108,14 @@ _SIGS = {
     "profk_last_stage_ms": (C.c_int, [C.POINTER(C.c_float), C.c_int]),
     "profk_topk_noalloc": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_double, C.c_uint64,
                                      C.c_void_p, C.c_void_p, C.c_void_p, C.POINTER(ProfkStats)]),
+    "profk_sample_tokens": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                                      C.c_void_p, C.c_int64, C.POINTER(Sampling), C.c_void_p, C.c_void_p,
+                                      C.c_void_p]),
+    "profk_route": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.POINTER(Routing),
+                              C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "profk_route_backward": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                       C.POINTER(Routing), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                       C.c_int64, C.c_void_p]),
 }
 
 

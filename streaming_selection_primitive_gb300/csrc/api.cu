@@ -20,6 +20,7 @@
 
 #include "../../include/profk.h"
 #include "kernels.h"
+#include "lm.h"
 #include "params.h"
 
 namespace profk {
@@ -1057,6 +1058,8 @@ done:
 }  // namespace
 
 bool pdl_enabled() { return g_opt[PROFK_OPT_PDL].load(std::memory_order_relaxed) != 0; }
+
+cudaError_t library_pool(cudaMemPool_t* out) { return pool_for_current_device(out); }
 
 }  // namespace profk
 

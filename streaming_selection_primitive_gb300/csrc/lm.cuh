@@ -1,0 +1,41 @@
+// Shared device pieces of the language-model selections (tokens.cu, route.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+
+namespace profk {
+
+__device__ __forceinline__ float lm_float(float v) { return v; }
+__device__ __forceinline__ float lm_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float lm_float(__half v) { return __half2float(v); }
+
+// One rounding, to the caller's type, at the end of a computation in float32.
+template <typename T>
+__device__ __forceinline__ T lm_cast(float v);
+template <>
+__device__ __forceinline__ float lm_cast<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 lm_cast<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half lm_cast<__half>(float v) { return __float2half_rn(v); }
+
+// Order key of a value that may be chosen: ord_key, whose smallest value (ord
+// of -inf) is above zero; 0 for what may not be chosen (-inf and NaN).
+__device__ __forceinline__ uint32_t choice_key(float v) { return v > -INFINITY ? ord_key(v) : 0u; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, d));
+  return v;
+}
+
+}  // namespace profk
