@@ -3,7 +3,9 @@
 Each translation unit is compiled by nvcc in parallel, then linked with
 ``nvcc -shared`` (CUDA runtime linked statically, so the library only needs the
 driver at run time).  Objects go to ``_build/``; the library to ``lib/``.
-A unit is recompiled when it or any header is newer than its object.
+A unit is recompiled when it or any header is newer than its object.  The
+language-model selections' Python half (csrc/binding.cpp) is compiled by g++
+against the installed torch and linked to the library.
 """
 from __future__ import annotations
 
@@ -19,6 +21,7 @@ INCLUDE = PKG.parent / "include"
 BUILD = PKG / "_build"
 LIBDIR = PKG / "lib"
 LIB = LIBDIR / "libprofk.so"
+BINDING_SOURCE = CSRC / "binding.cpp"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", str(INCLUDE)] + ARCH
@@ -49,20 +52,63 @@ def _compile(src: Path, obj: Path, verbose: bool) -> None:
         raise RuntimeError(f"nvcc failed for {src.name}:\n{r.stdout}\n{r.stderr}")
 
 
+def binding_path() -> Path:
+    """The native half of _lm.py, for the torch that is installed (its C++ interface differs by version)."""
+    import torch
+    return LIBDIR / f"profk_torch-{torch.__version__}.so"
+
+
+def _compile_binding(obj: Path, verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    home = Path(torch.__file__).resolve().parent
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for inc in (home / "include", home / "include" / "torch" / "csrc" / "api" / "include",
+                sysconfig.get_paths()["include"], Path(_nvcc()).resolve().parent.parent / "include"):
+        cmd += ["-isystem", str(inc)]
+    _run(cmd + ["-c", str(BINDING_SOURCE), "-o", str(obj)], BINDING_SOURCE.name, verbose)
+
+
+def _link_binding(obj: Path, out: Path, verbose: bool) -> None:
+    import torch
+    home = Path(torch.__file__).resolve().parent / "lib"
+    tmp = out.with_suffix(".so.tmp")
+    _run(["g++", "-shared", "-o", str(tmp), str(obj), f"-L{LIBDIR}", "-l:libprofk.so", "-Wl,-rpath,$ORIGIN", f"-L{home}",
+          f"-Wl,-rpath,{home}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"],
+         "the binding", verbose)
+    os.replace(tmp, out)
+
+
+def _run(cmd, what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {what} failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, force: bool = False) -> Path:
     """Compiles what is stale and links lib/libprofk.so; returns its path."""
     BUILD.mkdir(exist_ok=True)
     LIBDIR.mkdir(exist_ok=True)
     hdr = _headers_mtime()
+    binding = binding_path()
+    binding_obj = BUILD / (binding.stem + ".o")
+    binding_stale = force or not binding_obj.exists() or \
+        binding_obj.stat().st_mtime < max(BINDING_SOURCE.stat().st_mtime, hdr)
     jobs = []
     for name in SOURCES:
         src = CSRC / name
         obj = BUILD / (name + ".o")
         if force or not obj.exists() or obj.stat().st_mtime < max(src.stat().st_mtime, hdr):
             jobs.append((src, obj))
-    if jobs:
-        with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    if jobs or binding_stale:
+        with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+            extra = ex.submit(_compile_binding, binding_obj, verbose) if binding_stale else None
             list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
+            if extra is not None:
+                extra.result()
     objs = [BUILD / (n + ".o") for n in SOURCES]
     newest = max(o.stat().st_mtime for o in objs)
     if force or jobs or not LIB.exists() or LIB.stat().st_mtime < newest:
@@ -74,6 +120,8 @@ def build(verbose: bool = False, force: bool = False) -> Path:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force or not binding.exists() or binding.stat().st_mtime < binding_obj.stat().st_mtime:
+        _link_binding(binding_obj, binding, verbose)
     return LIB
 
 
