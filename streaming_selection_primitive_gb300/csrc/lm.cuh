@@ -26,6 +26,23 @@ __device__ __forceinline__ __half lm_cast<__half>(float v) { return __float2half
 // of -inf) is above zero; 0 for what may not be chosen (-inf and NaN).
 __device__ __forceinline__ uint32_t choice_key(float v) { return v > -INFINITY ? ord_key(v) : 0u; }
 
+constexpr float LOG2E = 1.44269504088896340736f;
+
+// 2^x by the hardware's approximation (two ulps; results below the normal
+// range are zero).
+__device__ __forceinline__ float lm_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / x by the hardware's approximation (one ulp), for x >= 1.
+__device__ __forceinline__ float lm_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);

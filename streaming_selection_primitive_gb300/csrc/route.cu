@@ -2,43 +2,127 @@
 //
 // A token t has one logit z_e per expert.  With y = z (softmax scores) or
 // y = log sigmoid(z) (sigmoid scores), p = softmax(y) over the experts.  The
-// choice is the first k experts in the library order of z + bias (descending,
-// ties by lower index, -inf and NaN never).  Gates: over the chosen,
-// softmax(y) when normalized, else p (softmax) or sigmoid(z).  Balance loss:
+// choice is the first k experts in the library order of c = z + bias
+// (descending, ties by lower index, -inf and NaN never).  Gates: over the
+// chosen, softmax(y) when normalized, else p (softmax) or sigmoid(z).  Balance
+// loss:
 //   loss = E sum_e (counts_e / N) P_e,  P_e = sum_t n_t p_te / N,
 // counts_e the slots given to expert e, n_t those token t filled, N = sum n_t.
+//
+// One warp takes a token: R = E / 32 logits a lane (rounded up to a power of
+// two), in registers, read once.  The choice runs on 32-bit keys that end in
+// the expert's index (sort_key), so that a round is one warp-wide maximum.
+#include <type_traits>
+
+#include <cooperative_groups.h>
+
+#include "../../include/profk.h"
 #include "lm.cuh"
 #include "lm.h"
-#include "../../include/profk.h"
+
+namespace cg = cooperative_groups;
 
 namespace profk {
 namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
+constexpr int CLUSTER = 8;  // CTAs of the one-launch form and of the join
+
+// ---------------------------------------------------------------------------
+// A lane's part of a token: R values, VEC consecutive ones at a time.
+template <typename T, int R>
+struct Part {
+  static constexpr int VEC = R < 16 / int(sizeof(T)) ? R : 16 / int(sizeof(T));
+  static __device__ __forceinline__ int expert(int r) { return ((r / VEC) * 32 + (threadIdx.x & 31)) * VEC + r % VEC; }
+};
+
+template <int BYTES>
+struct Bits;
+template <>
+struct Bits<2> { using type = unsigned short; };
+template <>
+struct Bits<4> { using type = unsigned; };
+template <>
+struct Bits<8> { using type = uint2; };
+template <>
+struct Bits<16> { using type = uint4; };
+
+// The lane's logits of one token, -inf beyond E.  vec: the row starts on a
+// boundary of VEC values, so a whole group is one load.
+template <typename T, int R>
+__device__ __forceinline__ void load_part(const T* row, int E, bool vec, float (&z)[R]) {
+  using P = Part<T, R>;
+#pragma unroll
+  for (int g = 0; g < R; g += P::VEC) {
+    const int e = P::expert(g);
+    if (vec && e + P::VEC <= E) {
+      union {
+        typename Bits<P::VEC * sizeof(T)>::type bits;
+        T v[P::VEC];
+      } u;
+      u.bits = __ldg(reinterpret_cast<const decltype(u.bits)*>(row + e));
+#pragma unroll
+      for (int j = 0; j < P::VEC; ++j) z[g + j] = lm_float(u.v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < P::VEC; ++j) z[g + j] = e + j < E ? lm_float(row[e + j]) : -INFINITY;
+    }
+  }
+}
+
+template <typename T, int R>
+__device__ __forceinline__ void store_part(T* row, int E, bool vec, const float (&d)[R]) {
+  using P = Part<T, R>;
+#pragma unroll
+  for (int g = 0; g < R; g += P::VEC) {
+    const int e = P::expert(g);
+    if (vec && e + P::VEC <= E) {
+      union {
+        typename Bits<P::VEC * sizeof(T)>::type bits;
+        T v[P::VEC];
+      } u;
+#pragma unroll
+      for (int j = 0; j < P::VEC; ++j) u.v[j] = lm_cast<T>(d[g + j]);
+      *reinterpret_cast<decltype(u.bits)*>(row + e) = u.bits;
+    } else {
+#pragma unroll
+      for (int j = 0; j < P::VEC; ++j)
+        if (e + j < E) row[e + j] = lm_cast<T>(d[g + j]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Scores.
 
 // log sigmoid(z), exact for large |z|.
 __device__ __forceinline__ float log_sigmoid(float z) { return fminf(z, 0.f) - log1pf(expf(-fabsf(z))); }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) { return lm_rcp(1.f + lm_exp2(-LOG2E * z)); }
 
-// The token's p, unnormalized, into s, and its sum (over the warp).  Softmax:
-// s = exp(z - max).  Sigmoid: s = sigmoid(z) exp(-c), c = min(max z, 0), so
-// that a token whose scores all underflow keeps their ratios.
-template <int NPL>
-__device__ __forceinline__ float token_scores(const float (&z)[NPL], float (&s)[NPL], int E, bool sig) {
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY;
-#pragma unroll
-  for (int r = 0; r < NPL; ++r)
-    if (lane + 32 * r < E) m = fmaxf(m, z[r]);
-  m = warp_max(m);
-  const float c = fminf(m, 0.f), ec = expf(c);
+// The token's p, unnormalized, into s; returns the sum over the warp.  `ref`
+// is the largest logit for softmax, any logit of the token for sigmoid.
+// Softmax: s = exp(z - ref).  Sigmoid: s = sigmoid(z), or, where that could
+// underflow for every expert (ref below -60) or a value is not finite, the
+// careful form: s = sigmoid(z) exp(-c) with c = min(max z, 0).
+template <int R>
+__device__ __forceinline__ float token_scores(const float (&z)[R], float (&s)[R], bool sig, float ref) {
   float sum = 0.f;
+  if (sig && ref > -60.f) {
 #pragma unroll
-  for (int r = 0; r < NPL; ++r) {
-    s[r] = 0.f;
-    if (lane + 32 * r < E) {
+    for (int r = 0; r < R; ++r) s[r] = sigmoid(z[r]);
+  } else if (!sig && fabsf(ref) < INFINITY) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = lm_exp2((z[r] - ref) * LOG2E);
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < R; ++r) m = fmaxf(m, z[r]);
+    m = warp_max(m);
+    const float c = fminf(m, 0.f), ec = expf(c);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
       if (sig) {
         const bool pos = z[r] >= 0.f;
         const float u = z[r] == -INFINITY ? 0.f : expf(pos ? -z[r] : z[r] - c);
@@ -46,169 +130,388 @@ __device__ __forceinline__ float token_scores(const float (&z)[NPL], float (&s)[
       } else {
         s[r] = z[r] == m ? 1.f : expf(z[r] - m);
       }
-      sum += s[r];
     }
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r) sum += s[r];
   return warp_sum(sum);
 }
 
-// The gate of lane j's chosen expert (logit zc; ok: the slot is filled), given
-// the token's softmax maximum and sum for the form that needs them.
-__device__ __forceinline__ float slot_gate(float zc, bool ok, bool sig, bool normalize, float p) {
+// Sum over lanes 0 .. width - 1 (a power of two; the others hold 0), in each of them.
+__device__ __forceinline__ float slots_sum(float v, int width) {
+  for (int d = width >> 1; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+  return v;
+}
+
+// The gate of the lane's slot (logit zc; ok: the slot is filled); p: the
+// softmax probability, for the form that needs it.  width: the power of two
+// not below k.
+__device__ __forceinline__ float slot_gate(float zc, bool ok, int width, bool sig, bool normalize, float p) {
   if (!normalize) return !ok ? 0.f : sig ? sigmoid(zc) : p;
   const float y = ok ? (sig ? log_sigmoid(zc) : zc) : -INFINITY;
   const float top = warp_max(y);
   const float e = ok ? (y == top ? 1.f : expf(y - top)) : 0.f;
-  const float sum = warp_sum(e);
+  const float sum = slots_sum(e, width);
   return ok ? e / sum : 0.f;
 }
 
-// One warp per token; the lane holds the logits of experts lane, lane + 32,
-// ...  Per CTA: the counts in shared memory (integers), the probabilities in
-// registers, joined warp by warp in a fixed order and written to `part`.
-template <typename T, int NPL>
-__global__ void __launch_bounds__(THREADS) k_route(RouteArgs a, float* part_p, unsigned* part_c) {
+// ---------------------------------------------------------------------------
+// The choice.
+
+// Key of an expert that sorts like (c descending, index ascending): ord(c)
+// with its low bits (as many as index the 32 R experts) replaced by the
+// inverted index.  For bf16 and f16 logits without a bias those bits carry
+// nothing, so the order is exact; for float32 sums two experts whose c agree
+// in the remaining 22 to 27 bits may come in the wrong order, which the
+// caller checks.  Below AVAILABLE: -inf, a negative NaN, or no expert.
+constexpr uint32_t AVAILABLE = 0x00800000u;  // ord of the lowest finite value
+
+template <int R>
+__device__ __forceinline__ uint32_t sort_key(float c, int e) {
+  const int b = __float_as_int(c + 0.f);  // -0 becomes +0
+  const uint32_t ord = static_cast<uint32_t>(b ^ ((b >> 31) | int(0x80000000)));
+  return (ord | (32u * R - 1u)) ^ static_cast<uint32_t>(e);
+}
+
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b), lo = min(a, b);
+  a = hi;
+  b = lo;
+}
+
+// Descending sort of a lane's keys (odd-even merge networks).
+template <int R>
+__device__ __forceinline__ void sort_lane(uint32_t (&v)[R]) {
+  if constexpr (R == 2) order2(v[0], v[1]);
+  if constexpr (R >= 4) {
+#pragma unroll
+    for (int p = 1; p < R; p <<= 1)
+#pragma unroll
+      for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+        for (int j = q % p; j + q < R; j += 2 * q)
+#pragma unroll
+          for (int i = 0; i < q; ++i)
+            if (i + j + q < R && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order2(v[i + j], v[i + j + q]);
+  }
+}
+
+// Lane j < k gets the j-th largest key, lane k (k < 32) the next one.  The
+// lanes' keys are consumed.  Up to eight keys a lane are sorted first, so that
+// a round looks at one key a lane and the lane that gave it moves up; more
+// are scanned each round.
+template <int R>
+__device__ __forceinline__ uint32_t pick(uint32_t (&v)[R], int rounds) {
+  const int lane = threadIdx.x & 31;
+  uint32_t mine = 0u;
+  if constexpr (R <= 8) sort_lane<R>(v);
+  for (int j = 0; j < rounds; ++j) {
+    uint32_t head = v[0];
+    if constexpr (R > 8) {
+#pragma unroll
+      for (int r = 1; r < R; ++r) head = max(head, v[r]);
+    }
+    const uint32_t top = __reduce_max_sync(FULL_MASK, head);
+    if (lane == j) mine = top;
+    if constexpr (R <= 8) {
+      if (head == top) {
+#pragma unroll
+        for (int r = 0; r + 1 < R; ++r) v[r] = v[r + 1];
+        v[R - 1] = 0u;
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) v[r] = v[r] == top ? 0u : v[r];
+    }
+  }
+  return mine;
+}
+
+// The choice by full order keys, one round of two reductions per slot: for
+// tokens whose sort_keys cannot tell.  Lane j gets slot j's expert or -1.
+template <typename T, int R>
+__device__ __noinline__ int pick_exact(const float (&c)[R], int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) key[r] = choice_key(c[r]);
+  int mine = -1;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0u;
+    int at = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (key[r] > best) {
+        best = key[r];
+        at = Part<T, R>::expert(r);
+      }
+    const uint32_t top = __reduce_max_sync(FULL_MASK, best);
+    if (top == 0u) break;
+    const int e = static_cast<int>(__reduce_min_sync(FULL_MASK, best == top ? unsigned(at) : 0xFFFFFFFFu));
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (Part<T, R>::expert(r) == e) key[r] = 0u;
+    if (lane == j) mine = e;
+  }
+  return mine;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.
+
+// The tokens of this CTA.  Leaves the CTA's slots per expert in cnt and the
+// sums of n_t p_te in psum (both E entries of shared memory; psum through
+// `stage`, WARPS x E), complete after the block barrier that ends it.
+template <typename T, int R>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, unsigned* cnt, float* psum, float* stage) {
+  using P = Part<T, R>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, k = a.k;
+  const bool exact = sizeof(T) == 2 && !a.bias;
+  const bool need_p = a.loss || (!a.normalize && !a.sigmoid);
+  int width = 1;
+  while (width < k) width <<= 1;
+  const T* logits = static_cast<const T*>(a.logits);
+  const bool vec = reinterpret_cast<uintptr_t>(logits) % (P::VEC * sizeof(T)) == 0 && a.ld % P::VEC == 0;
+  float acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = 0.f;
+  for (int64_t t = int64_t(blockIdx.x) * WARPS + warp; t < a.tokens; t += int64_t(gridDim.x) * WARPS) {
+    int mine = -1;  // lane j: the expert of slot j
+    float gate = 0.f;
+    if (!a.mask || a.mask[t]) {
+      const T* row = logits + t * a.ld;
+      float z[R];
+      load_part<T, R>(row, E, vec, z);
+      uint32_t key[R];
+      bool nan = false;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int e = P::expert(r);
+        nan |= z[r] != z[r];
+        key[r] = e < E ? sort_key<R>(a.bias ? z[r] + __ldg(a.bias + e) : z[r], e) : 0u;
+      }
+      nan = __any_sync(FULL_MASK, nan);
+      uint32_t got = pick<R>(key, exact || k == E || k == 32 ? k : k + 1);
+      constexpr uint32_t INDEX = 32u * R - 1u;
+      if (lane < k && got >= AVAILABLE) mine = static_cast<int>(INDEX ^ (got & INDEX));
+      float zc = mine >= 0 ? lm_float(row[mine]) : -INFINITY;
+      // Unsure: a key above that of +inf (a NaN), keys of different c that
+      // share their leading bits, or no next key to compare the last with.
+      const uint32_t next = __shfl_down_sync(FULL_MASK, got, 1);
+      bool unsure = lane < k && got > (0xff800000u | INDEX);
+      if (!exact) unsure |= mine >= 0 && (lane + 1 < k || k < E) && (lane == 31 || (got ^ next) <= INDEX);
+      if (__any_sync(FULL_MASK, unsure)) {
+        float c[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int e = P::expert(r);
+          c[r] = e < E ? (a.bias ? z[r] + __ldg(a.bias + e) : z[r]) : -INFINITY;
+        }
+        mine = pick_exact<T, R>(c, k);
+        zc = mine >= 0 ? lm_float(row[mine]) : -INFINITY;
+      }
+      const bool ok = mine >= 0;
+      const int filled = __popc(__ballot_sync(FULL_MASK, ok));
+      float p = 0.f;
+      if (need_p && filled) {
+        float s[R], ref = __shfl_sync(FULL_MASK, zc, 0);
+        if (!a.sigmoid && a.bias) {
+          ref = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < R; ++r) ref = fmaxf(ref, z[r]);
+          ref = warp_max(ref);
+        }
+        const float sum = token_scores<R>(z, s, a.sigmoid, ref);
+        const float scale = static_cast<float>(filled) / sum;
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = fmaf(s[r], scale, acc[r]);
+        p = (zc == ref ? 1.f : expf(zc - ref)) / sum;
+      }
+      gate = slot_gate(zc, ok, width, a.sigmoid, a.normalize, p);
+      if (ok) {
+        if (nan) gate = __int_as_float(0x7fc00000);
+        atomicAdd(cnt + mine, 1u);
+      }
+    }
+    if (lane < k) {
+      a.gates[t * k + lane] = gate;
+      a.chosen[t * k + lane] = mine;
+    }
+  }
+  if (a.loss) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (P::expert(r) < E) stage[warp * E + P::expert(r)] = acc[r];
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += THREADS) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += stage[w * E + e];
+      psum[e] = sum;
+    }
+  }
+  __syncthreads();
+}
+
+// counts, and the terms of the loss, of the experts of one CTA of a cluster;
+// rank 0 joins them: loss = E / N^2 sum_e counts_e (N P_e).
+__device__ __forceinline__ void finish_loss(int E, unsigned long long c, float term, float* loss) {
+  __shared__ float sf[32];
+  __shared__ unsigned long long sn[32];
+  __shared__ float cf[CLUSTER];
+  __shared__ unsigned long long cn[CLUSTER];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  term = warp_sum(term);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) c += __shfl_xor_sync(FULL_MASK, c, d);
+  if (lane == 0) {
+    sf[warp] = term;
+    sn[warp] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < warps; ++w) {
+      term += sf[w];
+      c += sn[w];
+    }
+    *cluster.map_shared_rank(&cf[cluster.block_rank()], 0) = term;
+    *cluster.map_shared_rank(&cn[cluster.block_rank()], 0) = c;
+  }
+  cluster.sync();
+  if (cluster.block_rank() == 0 && threadIdx.x == 0) {
+    float sum = 0.f;
+    unsigned long long n = 0;
+    for (int i = 0; i < CLUSTER; ++i) {
+      sum += cf[i];
+      n += cn[i];
+    }
+    const float N = n ? static_cast<float>(n) : 1.f;
+    *loss = static_cast<float>(E) * (sum / N) / N;
+  }
+}
+
+// Few tokens: one cluster, the CTAs' sums joined through distributed shared
+// memory; one launch and no workspace.
+template <typename T, int R>
+__global__ void __launch_bounds__(THREADS) __cluster_dims__(CLUSTER, 1, 1) k_route_one(RouteArgs a) {
   extern __shared__ unsigned char smem[];
-  unsigned* cnt = reinterpret_cast<unsigned*>(smem);  // E
-  float* sp = reinterpret_cast<float*>(cnt + a.experts);  // WARPS x E
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
+  const int E = a.experts;
+  unsigned* cnt = reinterpret_cast<unsigned*>(smem);
+  float* psum = reinterpret_cast<float*>(cnt + E);
+  float* stage = psum + E;
   for (int e = threadIdx.x; e < E; e += THREADS) cnt[e] = 0u;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  float acc[NPL];
+  route_tokens<T, R>(a, cnt, psum, stage);
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  unsigned long long n = 0;
+  float term = 0.f;
+  for (int e = cluster.block_rank() * THREADS + threadIdx.x; e < E; e += CLUSTER * THREADS) {
+    unsigned long long c = 0;
+    float p = 0.f;
 #pragma unroll
-  for (int r = 0; r < NPL; ++r) acc[r] = 0.f;
-  const T* logits = static_cast<const T*>(a.logits);
-  for (int64_t t = int64_t(blockIdx.x) * WARPS + warp; t < a.tokens; t += int64_t(gridDim.x) * WARPS) {
-    const T* row = logits + t * a.ld;
-    int mine = -1;  // lane j: the expert of slot j
-    int filled = 0;
-    float gate = 0.f;
-    if (!a.mask || a.mask[t]) {
-      float z[NPL], s[NPL];
-      uint32_t key[NPL];
-#pragma unroll
-      for (int r = 0; r < NPL; ++r) {
-        const int e = lane + 32 * r;
-        z[r] = e < E ? lm_float(row[e]) : -INFINITY;
-        key[r] = e < E ? choice_key(a.bias ? z[r] + a.bias[e] : z[r]) : 0u;
-      }
-      for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0u;
-        int at = 0;
-#pragma unroll
-        for (int r = 0; r < NPL; ++r)
-          if (key[r] > best) {
-            best = key[r];
-            at = r;
-          }
-        const uint32_t top = __reduce_max_sync(FULL_MASK, best);
-        if (top == 0u) break;
-        const unsigned e = __reduce_min_sync(FULL_MASK, best == top ? unsigned(lane + 32 * at) : 0xFFFFFFFFu);
-#pragma unroll
-        for (int r = 0; r < NPL; ++r)
-          if (lane + 32 * r == int(e)) key[r] = 0u;
-        if (lane == j) mine = int(e);
-        ++filled;
-      }
-      const bool ok = mine >= 0;
-      const float zc = ok ? lm_float(row[mine]) : -INFINITY;
-      float sum = 0.f, m = 0.f;
-      if (a.loss || (!a.normalize && !a.sigmoid)) {
-        sum = token_scores<NPL>(z, s, E, a.sigmoid);
-        if (filled) {
-          const float scale = float(filled) / sum;
-#pragma unroll
-          for (int r = 0; r < NPL; ++r) acc[r] += s[r] * scale;
-        }
-        m = -INFINITY;
-#pragma unroll
-        for (int r = 0; r < NPL; ++r) m = fmaxf(m, z[r]);
-        m = warp_max(m);
-      }
-      gate = slot_gate(zc, ok, a.sigmoid, a.normalize, (zc == m ? 1.f : expf(zc - m)) / sum);
-      bool nan = false;
-#pragma unroll
-      for (int r = 0; r < NPL; ++r) nan |= isnan(z[r]);
-      if (__any_sync(FULL_MASK, nan) && ok) gate = __int_as_float(0x7fc00000);
-      if (ok) atomicAdd(cnt + mine, 1u);
+    for (int i = 0; i < CLUSTER; ++i) {
+      c += *cluster.map_shared_rank(cnt + e, i);
+      if (a.loss) p += *cluster.map_shared_rank(psum + e, i);
     }
-    if (lane < a.k) {
-      a.gates[t * a.k + lane] = gate;
-      a.chosen[t * a.k + lane] = mine;
-    }
+    a.counts[e] = static_cast<int64_t>(c);
+    n += c;
+    term += static_cast<float>(c) * p;
   }
-#pragma unroll
-  for (int r = 0; r < NPL; ++r)
-    if (lane + 32 * r < E) sp[warp * E + lane + 32 * r] = acc[r];
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += THREADS) {
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) sum += sp[w * E + e];
-    part_p[int64_t(blockIdx.x) * E + e] = sum;
-    part_c[int64_t(blockIdx.x) * E + e] = cnt[e];
-  }
+  if (a.loss)
+    finish_loss(E, n, term, a.loss);
+  cluster.sync();  // every CTA's shared memory has been read
 }
 
-// Joins the CTAs' counts and probabilities in CTA order; one CTA.
-__global__ void __launch_bounds__(1024) k_route_join(int parts, int E, const float* part_p, const unsigned* part_c,
-                                                     int64_t* counts, float* loss) {
-  __shared__ float sf[32];
-  __shared__ unsigned long long sn[32];
-  __shared__ unsigned long long total;
+// Many tokens: each CTA writes its sums, and k_route_join adds them up.
+template <typename T, int R>
+__global__ void __launch_bounds__(THREADS) k_route(RouteArgs a, float* part_p, unsigned* part_c) {
+  extern __shared__ unsigned char smem[];
+  const int E = a.experts;
+  unsigned* cnt = reinterpret_cast<unsigned*>(smem);
+  float* psum = reinterpret_cast<float*>(cnt + E);
+  float* stage = psum + E;
+  for (int e = threadIdx.x; e < E; e += THREADS) cnt[e] = 0u;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
-  unsigned long long c = 0;
-  float p = 0.f;
-  if (e < E)
-    for (int i = 0; i < parts; ++i) {
-      c += part_c[int64_t(i) * E + e];
-      p += part_p[int64_t(i) * E + e];
-    }
-  if (e < E) counts[e] = static_cast<int64_t>(c);
-  if (!loss) return;
-  unsigned long long n = c;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(FULL_MASK, n, d);
-  if (lane == 0) sn[warp] = n;
-  __syncthreads();
-  if (e == 0) {
-    n = 0;
-    for (int w = 0; w < 32; ++w) n += sn[w];
-    total = n;
-  }
-  __syncthreads();
-  const float N = total ? static_cast<float>(total) : 1.f;
-  const float v = warp_sum((static_cast<float>(c) / N) * (p / N));
-  if (lane == 0) sf[warp] = v;
-  __syncthreads();
-  if (e == 0) {
-    float sum = 0.f;
-    for (int w = 0; w < 32; ++w) sum += sf[w];
-    *loss = static_cast<float>(E) * sum;
+  route_tokens<T, R>(a, cnt, psum, stage);
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    part_c[int64_t(blockIdx.x) * E + e] = cnt[e];
+    if (a.loss) part_p[int64_t(blockIdx.x) * E + e] = psum[e];
   }
 }
 
-// Gradient of the gates and of the balance loss, one warp per token; the
-// choice and the counts are constants.  dy as in the header's formulas, then
-// dz = dy (softmax) or dy sigmoid(-z).
-template <typename T, int NPL>
+// Adds the CTAs' sums in a fixed order: one cluster, 32 experts at a time a
+// CTA, the parts shared out over its warps.
+constexpr int JOIN_THREADS = 1024;
+__global__ void __launch_bounds__(JOIN_THREADS) __cluster_dims__(CLUSTER, 1, 1)
+    k_route_join(int parts, int E, const float* part_p, const unsigned* part_c, int64_t* counts, float* loss) {
+  __shared__ float sp[32][33];
+  __shared__ unsigned sc[32][33];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cluster.sync();  // every CTA runs before finish_loss writes to rank 0
+  pdl_wait();
+  pdl_trigger();
+  unsigned long long n = 0;
+  float term = 0.f;
+  for (int base = cluster.block_rank() * 32; base < E; base += CLUSTER * 32) {
+    const int e = base + lane;
+    unsigned c = 0u;
+    float p = 0.f;
+    if (e < E)
+#pragma unroll 4
+      for (int i = warp; i < parts; i += 32) {
+        c += __ldg(part_c + int64_t(i) * E + e);
+        if (loss) p += __ldg(part_p + int64_t(i) * E + e);
+      }
+    __syncthreads();
+    sc[warp][lane] = c;
+    sp[warp][lane] = p;
+    __syncthreads();
+    // Warp w joins expert base + w over the 32 warps' sums.
+    unsigned long long cc = sc[lane][warp];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) cc += __shfl_xor_sync(FULL_MASK, cc, d);
+    const float pp = warp_sum(sp[lane][warp]);
+    if (lane == 0 && base + warp < E) {
+      counts[base + warp] = static_cast<int64_t>(cc);
+      n += cc;
+      term += static_cast<float>(cc) * pp;
+    }
+  }
+  if (loss) finish_loss(E, n, term, loss);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the gates and of the balance loss; the choice and the counts
+// are constants.  With a_e = dL E counts_e n_t / N^2:
+//   dy = p (a - sum_e p_e a_e), and for the chosen
+//   + g_j (dg_j - sum g dg)                          normalized
+//   + p_i ([i chosen] dg_i - sum_j p_j dg_j)         softmax
+//   + g_j dg_j                                       sigmoid
+// and dz = dy (softmax) or dy sigmoid(-z).
+template <typename T, int R>
 __global__ void __launch_bounds__(THREADS) k_route_backward(RouteBackwardArgs a) {
+  using P = Part<T, R>;
   extern __shared__ unsigned char smem[];
   __shared__ unsigned long long total;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
-  float* extra = reinterpret_cast<float*>(smem) + warp * E;  // the chosen experts' part of dy
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, k = a.k;
+  float* extra = reinterpret_cast<float*>(smem) + warp * 32 * R;  // the chosen experts' part of dy
   if (threadIdx.x == 0) total = 0;
-  for (int e = lane; e < E; e += 32) extra[e] = 0.f;
+  for (int e = lane; e < 32 * R; e += 32) extra[e] = 0.f;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  float share[NPL];  // dL E counts_e / N^2
+  int width = 1;
+  while (width < k) width <<= 1;
+  float share[R];  // dL E counts_e / N^2
 #pragma unroll
-  for (int r = 0; r < NPL; ++r) share[r] = 0.f;
+  for (int r = 0; r < R; ++r) share[r] = 0.f;
   if (a.grad_loss) {
     unsigned long long n = 0;
     for (int e = threadIdx.x; e < E; e += THREADS) n += static_cast<unsigned long long>(a.counts[e]);
@@ -217,62 +520,62 @@ __global__ void __launch_bounds__(THREADS) k_route_backward(RouteBackwardArgs a)
     const float N = total ? static_cast<float>(total) : 1.f;
     const float f = *a.grad_loss * static_cast<float>(E) / N;
 #pragma unroll
-    for (int r = 0; r < NPL; ++r)
-      if (lane + 32 * r < E) share[r] = f * (static_cast<float>(a.counts[lane + 32 * r]) / N);
+    for (int r = 0; r < R; ++r)
+      if (P::expert(r) < E) share[r] = f * (static_cast<float>(a.counts[P::expert(r)]) / N);
   }
   const T* logits = static_cast<const T*>(a.logits);
   T* grad = static_cast<T*>(a.grad_logits);
+  const bool vec = reinterpret_cast<uintptr_t>(logits) % (P::VEC * sizeof(T)) == 0 && a.ld % P::VEC == 0;
+  const bool out_vec = reinterpret_cast<uintptr_t>(grad) % (P::VEC * sizeof(T)) == 0 && a.grad_ld % P::VEC == 0;
   for (int64_t t = int64_t(blockIdx.x) * WARPS + warp; t < a.tokens; t += int64_t(gridDim.x) * WARPS) {
     const T* row = logits + t * a.ld;
-    T* out = grad + t * a.grad_ld;
-    int64_t mine = lane < a.k ? a.chosen[t * a.k + lane] : -1;
+    const int64_t mine = lane < k ? a.chosen[t * k + lane] : -1;
     const bool ok = mine >= 0 && mine < E;
     const int filled = __popc(__ballot_sync(FULL_MASK, ok));
+    float z[R], s[R];
     if (!filled) {  // masked, or nothing to choose: no gradient
-      for (int e = lane; e < E; e += 32) out[e] = lm_cast<T>(0.f);
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = 0.f;
+      store_part<T, R>(grad + t * a.grad_ld, E, out_vec, s);
       continue;
     }
-    float z[NPL], s[NPL];
+    load_part<T, R>(row, E, vec, z);
     float m = -INFINITY;
 #pragma unroll
-    for (int r = 0; r < NPL; ++r) {
-      const int e = lane + 32 * r;
-      z[r] = e < E ? lm_float(row[e]) : -INFINITY;
-      m = fmaxf(m, z[r]);
-    }
+    for (int r = 0; r < R; ++r) m = fmaxf(m, z[r]);
     m = warp_max(m);
-    const float inv = 1.f / token_scores<NPL>(z, s, E, a.sigmoid);
+    const float inv = 1.f / token_scores<R>(z, s, a.sigmoid, m);
+    const float n_t = static_cast<float>(filled);
     float dot = 0.f;
+    if (a.grad_loss) {
 #pragma unroll
-    for (int r = 0; r < NPL; ++r) {
-      s[r] *= inv;  // p
-      dot += s[r] * share[r];
+      for (int r = 0; r < R; ++r) dot = fmaf(s[r], share[r], dot);
+      dot = warp_sum(dot) * inv * n_t;
     }
-    dot = warp_sum(dot) * filled;
     if (a.grad_gates) {
       const float zc = ok ? lm_float(row[mine]) : -INFINITY;
-      const float g = slot_gate(zc, ok, a.sigmoid, a.normalize, (zc == m ? 1.f : expf(zc - m)) * inv);
-      const float dg = ok ? a.grad_gates[t * a.k + lane] : 0.f;
-      const float gd = warp_sum(g * dg);
+      const float g = slot_gate(zc, ok, width, a.sigmoid, a.normalize, (zc == m ? 1.f : expf(zc - m)) * inv);
+      const float dg = ok ? a.grad_gates[t * k + lane] : 0.f;
       float d = g * dg;
-      if (a.normalize)
-        d = g * (dg - gd);
-      else if (!a.sigmoid)
-        dot += gd;
-      if (ok) extra[mine] = d;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < NPL; ++r) {
-      const int e = lane + 32 * r;
-      if (e < E) {
-        float dy = s[r] * (share[r] * filled - dot) + extra[e];
-        if (a.sigmoid) dy *= sigmoid(-z[r]);
-        out[e] = lm_cast<T>(dy);
+      if (a.normalize || !a.sigmoid) {
+        const float gd = __shfl_sync(FULL_MASK, slots_sum(d, width), 0);
+        if (a.normalize)
+          d = g * (dg - gd);
+        else
+          dot += gd;
       }
+      if (ok) extra[mine] = d;
+      __syncwarp();
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float dy = fmaf(s[r] * inv, fmaf(share[r], n_t, -dot), extra[P::expert(r)]);
+      if (a.sigmoid) dy *= sigmoid(-z[r]);
+      s[r] = dy;
+    }
+    store_part<T, R>(grad + t * a.grad_ld, E, out_vec, s);
     __syncwarp();
-    if (ok) extra[mine] = 0.f;
+    if (a.grad_gates && ok) extra[mine] = 0.f;
     __syncwarp();
   }
 }
@@ -286,7 +589,7 @@ cudaError_t by_type(int type, F&& f) {
   }
 }
 
-// The smallest NPL with 32 NPL >= E.
+// The smallest R with 32 R >= E.
 template <typename F>
 cudaError_t by_width(int E, F&& f) {
   if (E <= 32) return f(std::integral_constant<int, 1>{});
@@ -297,37 +600,44 @@ cudaError_t by_width(int E, F&& f) {
   return f(std::integral_constant<int, 32>{});
 }
 
-int route_grid(int64_t tokens) {
+int route_grid(int64_t tokens, int per_sm) {
   const int64_t need = (tokens + WARPS - 1) / WARPS;
-  const int64_t most = 2 * static_cast<int64_t>(sms());
+  const int64_t most = per_sm * static_cast<int64_t>(sms());
   return static_cast<int>(need < most ? need : most);
 }
+
+// One launch up to this many tokens: each of the cluster's warps takes 16.
+constexpr int64_t ONE_TOKENS = 16 * CLUSTER * WARPS;
 
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
-  const int grid = route_grid(a.tokens);
-  if (grid == 0)  // no tokens: zero counts and loss
-    return launch_kernel(k_route_join, dim3(1), dim3(1024), 0, stream, 0, a.experts, static_cast<const float*>(nullptr),
-                         static_cast<const unsigned*>(nullptr), a.counts, a.loss);
+  const size_t smem = size_t(2 + WARPS) * a.experts * 4;
+  if (a.tokens <= ONE_TOKENS)
+    return by_type(a.type, [&](auto t) {
+      return by_width(a.experts, [&](auto w) {
+        return launch_kernel(k_route_one<decltype(t), decltype(w)::value>, dim3(CLUSTER), dim3(THREADS), smem, stream, a);
+      });
+    });
+  const int grid = route_grid(a.tokens, 4);
   cudaMemPool_t pool;
   cudaError_t err = library_pool(&pool);
   if (err != cudaSuccess) return err;
   void* part = nullptr;
   const size_t each = size_t(grid) * a.experts * 4;
-  err = cudaMallocFromPoolAsync(&part, 2 * each, pool, stream);
+  err = cudaMallocFromPoolAsync(&part, (a.loss ? 2 : 1) * each, pool, stream);
   if (err != cudaSuccess) return err;
-  float* part_p = static_cast<float*>(part);
-  unsigned* part_c = reinterpret_cast<unsigned*>(static_cast<char*>(part) + each);
+  unsigned* part_c = static_cast<unsigned*>(part);
+  float* part_p = reinterpret_cast<float*>(static_cast<char*>(part) + each);
   err = by_type(a.type, [&](auto t) {
     return by_width(a.experts, [&](auto w) {
-      const size_t smem = size_t(1 + WARPS) * a.experts * 4;
       return launch_kernel(k_route<decltype(t), decltype(w)::value>, dim3(grid), dim3(THREADS), smem, stream, a, part_p,
                            part_c);
     });
   });
   if (err == cudaSuccess)
-    err = launch_kernel(k_route_join, dim3(1), dim3(1024), 0, stream, grid, a.experts, part_p, part_c, a.counts, a.loss);
+    err = launch_kernel(k_route_join, dim3(CLUSTER), dim3(JOIN_THREADS), 0, stream, grid, a.experts, part_p, part_c,
+                        a.counts, a.loss);
   const cudaError_t freed = cudaFreeAsync(part, stream);
   return err != cudaSuccess ? err : freed;
 }
@@ -335,8 +645,9 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
   return by_type(a.type, [&](auto t) {
     return by_width(a.experts, [&](auto w) {
-      return launch_kernel(k_route_backward<decltype(t), decltype(w)::value>, dim3(route_grid(a.tokens)), dim3(THREADS),
-                           size_t(WARPS) * a.experts * 4, stream, a);
+      constexpr int R = decltype(w)::value;
+      return launch_kernel(k_route_backward<decltype(t), R>, dim3(route_grid(a.tokens, 4)), dim3(THREADS),
+                           size_t(WARPS) * 32 * R * 4, stream, a);
     });
   });
 }
