@@ -153,6 +153,19 @@ def test_infinite_and_nan_logits(pk, cuda_device):
         assert (d[3] == 0).all() and torch.isfinite(d[[0, 1, 4, 5]]).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_negative_nan_is_a_nan(pk, cuda_device, dtype):
+    z, _ = inputs(4, 40, dtype, 19, cuda_device)
+    bits = {torch.float32: (torch.int32, -0x400000), torch.bfloat16: (torch.int16, -0x40), torch.float16: (torch.int16, -0x200)}
+    kind, value = bits[dtype]
+    z.view(kind)[2, 11] = value
+    assert torch.isnan(z[2, 11])
+    for bias in (None, torch.zeros(40, device=cuda_device)):
+        r = pk.route(z, 5, bias=bias)
+        assert torch.isnan(r.gates[2]).all() and torch.isnan(r.loss) and 11 not in r.experts[2].tolist()
+        assert (r.experts >= 0).all() and torch.isfinite(r.gates[[0, 1, 3]]).all()
+
+
 def test_a_bias_chooses_only(pk, cuda_device):
     z, _ = inputs(64, 32, torch.float32, 10, cuda_device)
     bias = torch.zeros(32, device=cuda_device)
