@@ -27,6 +27,7 @@ __device__ __forceinline__ __half lm_cast<__half>(float v) { return __float2half
 __device__ __forceinline__ uint32_t choice_key(float v) { return v > -INFINITY ? ord_key(v) : 0u; }
 
 constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float LN2 = 0.69314718055994530942f;
 
 // 2^x by the hardware's approximation (two ulps; results below the normal
 // range are zero).
@@ -53,6 +54,32 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, d));
   return v;
+}
+
+// Launches a kernel whose CTAs form clusters of `cluster`, with any amount of
+// dynamic shared memory, as launch_kernel does.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, size_t smem,
+                                   cudaStream_t stream, Args... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  ++launch_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace profk
