@@ -9,19 +9,19 @@
 // rates w_i); its log-probability is x_i - log sum kept w.
 //
 // A cluster of CTAs takes a row.  Each CTA reads its slice once, into shared
-// memory where it fits, and makes its passes there:
-//   1. the maximum (joined over the cluster through distributed shared memory);
-//   2. for top-p the mass of the row, and for both cuts a histogram of one
-//      element in 16, from which a value is taken that should lie just below
-//      the last token to be kept: what follows touches only elements above it;
-//   3. a histogram of counts and masses over 1024 equal ranges of keys between
-//      that value and the maximum, repeated inside the range where the count or
-//      the mass crosses its target until that holds at most LIST keys, which
-//      every CTA ranks;
-//   4. the race among the kept, the only pass that reads noise.
-// Steps 2 and 3 are this library's method (sample, filter, check, refine): the
-// check is the crossing itself, and where the value of step 2 turns out too
-// high, step 3 runs over everything.
+// memory where it fits, and works there:
+//   1. its maximum, and for top-p its mass, both relative to its own maximum;
+//   2. the first keys of its slice, sorted: of the threads' maxima a value is
+//      taken that at least that many of them reach, and only what lies at or
+//      above it is ranked;
+//   3. the CTAs exchange these (one cluster barrier), and the row's first keys
+//      are known.  For top-k up to TOP, and for most rows under top-p and
+//      min-p, they are all that can be kept: one warp cuts them and runs the
+//      race, which reads the noise of the kept tokens only;
+//   4. otherwise the cuts are found by histograms of counts and masses over
+//      equal ranges of keys, repeated inside the range where the count or the
+//      mass crosses its target until that holds at most LIST keys; then every
+//      CTA races over its kept tokens.
 //
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
@@ -40,14 +40,14 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int BINS = 1024;     // of one histogram pass
+constexpr int TOP = 128;        // keys of a slice that step 2 can sort
+constexpr int TOP_P = 64;       // and those it sorts for top-p and min-p
+constexpr int CANDIDATES = 1024;
+constexpr int BINS = 1024;      // of one histogram pass
 constexpr int PER = BINS / THREADS;
-constexpr int LIST = 256;      // keys that are ranked directly
-constexpr int SAMPLE_BINS = 256;
-constexpr float SAMPLE_SCALE = 8.f;  // bins per unit of x
-constexpr int SAMPLE_EVERY = 16;
-constexpr int SLICE_BYTES = 64 << 10;   // of a row in one CTA's shared memory, where the cluster is not at its largest
-constexpr int SLICE_MOST = 190 << 10;   // and in any case; beyond it the passes read global memory
+constexpr int LIST = 256;       // keys of a bin that are ranked directly
+constexpr int SLICE_BYTES = 64 << 10;  // of a row in one CTA's shared memory, where the cluster is not at its largest
+constexpr int SLICE_MOST = 180 << 10;  // and in any case; beyond it the passes read global memory
 constexpr int SLICE_LEAST = 8 << 10;
 using u64 = unsigned long long;
 
@@ -62,24 +62,40 @@ __device__ __forceinline__ void better(Best& a, const Best& b) {
   if (b.index != NONE && (a.index == NONE || b.score > a.score || (b.score == a.score && b.index < a.index))) a = b;
 }
 
+// What a CTA tells the others after step 2.
+struct Part {
+  float top;     // the slice's maximum (NaN if it holds one)
+  float tau;     // as many of its keys as were asked for reach this value
+  float mass;    // sum of exp((l - top) / T), for top-p
+  int keys;      // sorted keys sent; -1: too many candidates to rank
+};
+
 struct Shared {
   // Written by other CTAs of the cluster.
-  unsigned merged_c[BINS];
-  u64 merged_m[BINS];
-  u64 list[2][LIST];
-  unsigned sample[SAMPLE_BINS];
-  float ex_max[MAX_CLUSTER];
-  u64 ex_z[MAX_CLUSTER];
-  u64 ex_kept[MAX_CLUSTER];
+  alignas(16) unsigned merged_c[BINS];
+  alignas(16) u64 merged_m[BINS];
+  union {
+    u64 tops[MAX_CLUSTER][TOP];  // step 3
+    u64 list[2][LIST];           // step 4
+  };
+  Part part[MAX_CLUSTER];
   Best ex_best[MAX_CLUSTER];
+  u64 ex_kept[MAX_CLUSTER];
   // This CTA's own.
-  unsigned count[BINS];
-  unsigned lo[BINS], hi[BINS];  // 64-bit masses in two words
+  union {
+    struct {
+      alignas(16) unsigned count[BINS];
+      alignas(16) unsigned lo[BINS];  // 64-bit masses in two words
+      alignas(16) unsigned hi[BINS];
+    };
+    alignas(16) u64 candidates[CANDIDATES + 2];
+  };
   u64 sorted[LIST];
   u64 wc[WARPS], wm[WARPS], red[WARPS];
-  float redf[WARPS];
+  float redf[WARPS], redt[WARPS];
   Best best[WARPS];
   unsigned slot;
+  int enough;
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
@@ -255,20 +271,31 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, u64 lo
       }
     }
     cluster.sync();
-    // This CTA joins every C-th bin and tells everybody.
-    const int C = cluster.num_blocks();
-    for (int b = threadIdx.x * C + cluster.block_rank(); b < BINS; b += THREADS * C) {
-      unsigned c = 0;
-      u64 m = 0;
+    // This CTA joins its share of the bins, four a thread, and tells everybody.
+    const int C = cluster.num_blocks(), share = BINS / C;
+    for (int b = cluster.block_rank() * share + 4 * threadIdx.x; b < (static_cast<int>(cluster.block_rank()) + 1) * share;
+         b += 4 * THREADS) {
+      uint4 c = make_uint4(0, 0, 0, 0);
+      u64 m[4] = {0, 0, 0, 0};
+#pragma unroll 4
       for (int i = 0; i < C; ++i) {
         const Shared* o = cluster.map_shared_rank(&s, i);
-        c += o->count[b];
-        m += (u64(o->hi[b]) << 32) + o->lo[b];
+        const uint4 oc = *reinterpret_cast<const uint4*>(o->count + b), ol = *reinterpret_cast<const uint4*>(o->lo + b),
+                    oh = *reinterpret_cast<const uint4*>(o->hi + b);
+        c.x += oc.x;
+        c.y += oc.y;
+        c.z += oc.z;
+        c.w += oc.w;
+        m[0] += (u64(oh.x) << 32) + ol.x;
+        m[1] += (u64(oh.y) << 32) + ol.y;
+        m[2] += (u64(oh.z) << 32) + ol.z;
+        m[3] += (u64(oh.w) << 32) + ol.w;
       }
       for (int i = 0; i < C; ++i) {
         Shared* o = cluster.map_shared_rank(&s, i);
-        o->merged_c[b] = c;
-        o->merged_m[b] = m;
+        *reinterpret_cast<uint4*>(o->merged_c + b) = c;
+        *reinterpret_cast<ulonglong2*>(o->merged_m + b) = make_ulonglong2(m[0], m[1]);
+        *reinterpret_cast<ulonglong2*>(o->merged_m + b + 2) = make_ulonglong2(m[2], m[3]);
       }
     }
     cluster.sync();
@@ -419,43 +446,54 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, u64 l
   }
 }
 
-// Where x should be cut (in bins of the sample's histogram) so that the tokens
-// above hold the first k of the row, or all but a share of the mass: whole
-// warp, every lane gets the answer.  SAMPLE_BINS: nowhere.
-__device__ __forceinline__ int sample_cut(const unsigned* hist, bool by_k, float k, float spare) {
-  constexpr int EACH = SAMPLE_BINS / 32;
+// ceil(p Z) in integers, at least 1 and at most Z: a token is kept while the
+// mass before it is below this.
+__device__ __forceinline__ u64 mass_target(float p, u64 Z) {
+  if (!(p > 0.f)) return 1;
+  const unsigned bits = __float_as_uint(p), ex = bits >> 23;  // p < 1
+  const u64 man = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  const int e = ex ? 150 - static_cast<int>(ex) : 149;  // p = man 2^-e, e >= 24
+  const u64 hi = __umul64hi(Z, man), lo = Z * man;
+  u64 q = 0;
+  bool rest;
+  if (e >= 128) {
+    rest = (hi | lo) != 0;
+  } else if (e >= 64) {
+    q = hi >> (e - 64);
+    rest = lo != 0 || (e > 64 && (hi << (128 - e)) != 0);
+  } else {
+    q = (hi << (64 - e)) | (lo >> e);
+    rest = (lo << (64 - e)) != 0;
+  }
+  q += rest ? 1 : 0;
+  return q < 1 ? 1 : q > Z ? Z : q;
+}
+
+// The want-th largest of the block's thread maxima, or less: of each warp the
+// ceil(want / WARPS)-th largest, of those the least.  At least `want` threads
+// reach it.  Called with the warp's own maxima; the block's value is in redt
+// after a barrier.
+__device__ __forceinline__ float warp_tau(float top, int want) {
+  uint32_t key = choice_key(top);
+  uint32_t got = 0u;
   const int lane = threadIdx.x & 31;
-  float v[EACH], sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < EACH; ++j) {
-    const int b = lane * EACH + j;
-    v[j] = static_cast<float>(hist[b]);
-    if (!by_k) v[j] *= SAMPLE_EVERY * __expf(-static_cast<float>(b) / SAMPLE_SCALE);
-    sum += v[j];
+  for (int j = 0; j < want; j += WARPS) {
+    got = __reduce_max_sync(FULL_MASK, key);
+    if (lane == __ffs(__ballot_sync(FULL_MASK, key == got)) - 1) key = 0u;
   }
-  float before = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const float o = __shfl_up_sync(FULL_MASK, before, d);
-    if (lane >= d) before += o;
+  return got ? key_to_float(got) : -INFINITY;
+}
+
+// Candidates larger than a key: its rank, as keys are distinct.  (An odd number
+// of them is followed by a 0.)
+__device__ __forceinline__ int larger_keys(const Shared& s, int keys, u64 key) {
+  int above = 0;
+#pragma unroll 4
+  for (int j = 0; j < keys; j += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s.candidates + j);
+    above += (o.x > key) + (o.y > key);
   }
-  const float total = __shfl_sync(FULL_MASK, before, 31);
-  before -= sum;
-  // k: four standard deviations of the sample's count above its mean, and a few.
-  const float expect = k / SAMPLE_EVERY, want = expect + 4.f * sqrtf(expect) + 8.f;
-  int cut = SAMPLE_BINS;
-#pragma unroll
-  for (int j = EACH - 1; j >= 0; --j) {
-    float above = before;  // with bins up to this one
-#pragma unroll
-    for (int i = 0; i <= j; ++i) above += v[i];
-    const int b = lane * EACH + j;
-    // Mass: what the bins below hold by the sample, two more of its elements
-    // at the edge, and a fifth of room.
-    const float tail = total - above + 2.f * SAMPLE_EVERY * __expf(-static_cast<float>(b + 1) / SAMPLE_SCALE);
-    if (by_k ? above >= want : tail <= 0.8f * spare) cut = b + 1;
-  }
-  return static_cast<int>(__reduce_min_sync(FULL_MASK, static_cast<unsigned>(cut)));
+  return above;
 }
 
 template <typename T, bool RESIDENT>
@@ -468,13 +506,20 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = blockIdx.x / C;
-  for (int b = threadIdx.x; b < SAMPLE_BINS; b += THREADS) s.sample[b] = s.count[b] = 0u;
+  auto started = cluster.barrier_arrive();  // waited for before the first write to another CTA
+  if (threadIdx.x == 0) s.slot = 0;
   pdl_wait();
   pdl_trigger();
   const float temperature = a.temperature ? a.temperature[r] : a.all_temperature;
   const int32_t k = a.top_k ? a.top_k[r] : a.all_top_k;
   const float p = a.top_p ? a.top_p[r] : a.all_top_p;
   const float min_p = a.min_p ? a.min_p[r] : a.all_min_p;
+  const bool greedy = temperature == 0.f;
+  const bool by_k = !greedy && k > 0 && k < a.n, by_p = !greedy && p < 1.f;
+  // Keys that step 2 sorts (0: it would not help).
+  const int want = greedy ? 1 : by_k ? (k <= TOP ? k : 0) : by_p || min_p > 0.f ? TOP_P : 0;
+  // Keys for which a value is looked for that as many reach.
+  const int reach = want ? want : by_k && k <= THREADS ? k : 0;
   S sl;
   sl.row = static_cast<const T*>(a.logits) + r * a.ld;
   sl.mask = a.mask ? a.mask + r * a.mask_ld : nullptr;
@@ -484,8 +529,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   const int64_t all = (a.n + sl.phase + VEC - 1) / VEC;
   sl.v0 = static_cast<int64_t>(rank) * per_cta;
   sl.nv = static_cast<int>(all <= sl.v0 ? 0 : all - sl.v0 < per_cta ? all - sl.v0 : per_cta);
+  // An infinite T: the smallest number, so that -inf stays -inf.
+  sl.inv = fmaxf(1.f / temperature, __int_as_float(1));
+  sl.inv2 = sl.inv * LOG2E;
+  sl.index_bits = 32 - __clz(static_cast<int>(a.n - 1));
+  const int e = min(62 - sl.index_bits, 44);
+  sl.scale = __int_as_float((127 + e) << 23);
 
-  // 1. The slice, and the largest logit (NaN if there is one).
+  // 1. The slice, and its largest logit (NaN if there is one).
   float top = -INFINITY;
   {
     constexpr int AHEAD = 4;  // loads under way a thread
@@ -520,18 +571,110 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
       }
     }
   }
+  float widest = top;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, d));
-  if (lane == 0) s.redf[warp] = top;
-  cluster.sync();  // every CTA runs, and has cleared what others add to
+  for (int d = 16; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
+  if (lane == 0) s.redf[warp] = widest;
+  if (reach) {
+    if (RESIDENT && sl.nv < THREADS) {
+      // Fewer vectors than threads: the threads' maxima of single elements instead.
+      __syncthreads();
+      const T* flat = reinterpret_cast<const T*>(sl.store);
+      top = -INFINITY;
+      for (int i = threadIdx.x; i < sl.nv * VEC; i += THREADS) top = fmaxf(top, lm_float(flat[i]));
+    }
+    const float least = warp_tau(top, reach);
+    if (lane == 0) s.redt[warp] = least;
+  }
+  __syncthreads();
+  widest = s.redf[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) widest = max_nan(widest, s.redf[w]);
+  float tau = -INFINITY;
+  if (reach) {
+    tau = s.redt[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) tau = fminf(tau, s.redt[w]);
+  }
+  sl.m = widest;
+
+  // 2. The slice's mass, and its first keys.
+  float mass = 0.f;
+  const bool need_mass = by_p && !by_k;
+  int keys = 0;
+  if (want || need_mass) {
+    for (int turn = 0;; ++turn) {
+      for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
+        float x[VEC];
+        sl.load(v, x);
+        const float most = max_of(x, VEC);
+        if (want && most >= tau && most > -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (x[j] >= tau && x[j] > -INFINITY) {
+              const unsigned at = atomicAdd(&s.slot, 1u);
+              if (at < CANDIDATES) s.candidates[at] = sl.key(x[j], sl.element(v) + j);
+            }
+        }
+        if (need_mass && turn == 0) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
+#pragma unroll
+          for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < d; ++j) x[j] += x[j + d];
+          mass += x[0];
+        }
+      }
+      __syncthreads();  // the candidates are complete; redf has been read
+      keys = static_cast<int>(s.slot);
+      if (keys <= CANDIDATES || turn == 2) break;
+      // Too many (neighbours are alike, so that some warps' maxima are low):
+      // again from the want-th largest of those that were stored.
+      for (int i = threadIdx.x; i < CANDIDATES; i += THREADS)
+        if (larger_keys(s, CANDIDATES, s.candidates[i]) == want - 1) s.thr = s.candidates[i];
+      __syncthreads();
+      tau = sl.logit_of(s.thr);
+      if (threadIdx.x == 0) s.slot = 0;
+      __syncthreads();
+    }
+    mass = warp_sum(mass);
+    if (lane == 0) s.redf[warp] = mass;
+  }
+  cluster.barrier_wait(std::move(started));
+  if (keys > CANDIDATES) {  // copies of one value
+    keys = -1;
+  } else if (want) {
+    // The first `want` go to every CTA that looks at them.
+    const int readers = by_k || greedy ? 1 : C;
+    if (threadIdx.x == 0) s.candidates[keys] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < keys; i += THREADS) {
+      const u64 mine = s.candidates[i];
+      const int above = larger_keys(s, keys, mine);
+      if (above < want)
+        for (int c = 0; c < readers; ++c) cluster.map_shared_rank(&s, c)->tops[rank][above] = mine;
+    }
+    keys = keys < want ? keys : want;
+  }
+  __syncthreads();
   if (threadIdx.x < C) {
-    top = s.redf[0];
-    for (int w = 1; w < WARPS; ++w) top = max_nan(top, s.redf[w]);
-    cluster.map_shared_rank(&s, threadIdx.x)->ex_max[rank] = top;
+    mass = 0.f;
+    if (need_mass)
+      for (int w = 0; w < WARPS; ++w) mass += s.redf[w];
+    cluster.map_shared_rank(&s, threadIdx.x)->part[rank] = Part{widest, tau, mass, keys};
   }
   cluster.sync();
-  top = s.ex_max[0];
-  for (int i = 1; i < C; ++i) top = max_nan(top, s.ex_max[i]);
+
+  // 3. The row's maximum, mass and first keys.
+  top = s.part[0].top;
+  tau = s.part[0].tau;
+  int found = 0;  // keys of all CTAs, or -1
+  for (int i = 0; i < C; ++i) {
+    top = max_nan(top, s.part[i].top);
+    tau = fmaxf(tau, s.part[i].tau);
+    found = found < 0 || s.part[i].keys < 0 ? -1 : found + s.part[i].keys;
+  }
   const bool bad = isnan(top) || !(temperature >= 0.f) || isnan(p) || isnan(min_p);
   if (bad || top == -INFINITY) {
     if (rank == 0 && threadIdx.x == 0) {
@@ -541,108 +684,129 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
     return;
   }
   sl.m = top;
-  // An infinite T: the smallest number, so that -inf stays -inf.
-  sl.inv = fmaxf(1.f / temperature, __int_as_float(1));
-  sl.inv2 = sl.inv * LOG2E;
-  int digits = 0;
-  while ((int64_t(1) << digits) < a.n) ++digits;
-  sl.index_bits = digits;
-  const int e = 62 - digits < 44 ? 62 - digits : 44;
-  sl.scale = __int_as_float((127 + e) << 23);
+  u64 Z = 0;
+  if (need_mass)
+    for (int i = 0; i < C; ++i) Z += sl.fixed(s.part[i].mass * sl.weight(s.part[i].top));
+  const float floor_w = fminf(min_p, 1.f);
+  const float* noise = a.noise + r * a.noise_ld;
+  if (want && found >= 0) {
+    const bool decide = !by_k && !greedy;  // whether these keys are enough is not known beforehand
+    if (rank != 0 && !decide) return;
+    // Merge: a key's place is the number of larger ones in each of the sorted lists.
+    const int got = found < want ? found : want;
+    for (int i = threadIdx.x; i < C * want; i += THREADS) {
+      const int c = i / want, j = i - c * want;
+      if (j >= s.part[c].keys) continue;
+      const u64 mine = s.tops[c][j];
+      int place = j;
+      for (int o = 0; o < C && place < want; ++o) {
+        if (o == c) continue;
+        int lo = 0, hi = s.part[o].keys;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (s.tops[o][mid] > mine)
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        place += lo;
+      }
+      if (place < want) s.sorted[place] = mine;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int EACH = TOP / 32;
+      float l[EACH], w[EACH];
+      u64 part[EACH], sum = 0;
+#pragma unroll
+      for (int j = 0; j < EACH; ++j) {
+        const int at = lane * EACH + j;
+        l[j] = at < got ? sl.logit_of(s.sorted[at]) : -INFINITY;
+        w[j] = at < got ? sl.weight(l[j]) : 0.f;
+        part[j] = sl.fixed(w[j]);
+        sum += part[j];
+      }
+      u64 before = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(FULL_MASK, before, d);
+        if (lane >= d) before += o;
+      }
+      const u64 total = __shfl_sync(FULL_MASK, before, 31);
+      before -= sum;
+      if (by_k) Z = total;
+      const u64 target = by_p ? mass_target(p, Z) : ~u64(0);
+      // Enough: the list holds everything, or reaches the mass, or falls below min-p.
+      const float last = got ? sl.weight(sl.logit_of(s.sorted[got - 1])) : 0.f;
+      const bool enough = !decide || found < want || (by_p && total >= target) || last < floor_w;
+      if (lane == 0) s.enough = enough;
+      if (enough && rank == 0) {
+        u64 kept = 0;
+        Best best{-INFINITY, 0.f, NONE};
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          const int at = lane * EACH + j;
+          if (at < got && (before < target || at == 0) && w[j] >= floor_w && sl.x(l[j]) > -INFINITY) {
+            const unsigned i =
+                static_cast<unsigned>(((u64(1) << sl.index_bits) - 1) - (s.sorted[at] & ((u64(1) << sl.index_bits) - 1)));
+            const float score = greedy ? 0.f : fmaxf(fmaf(lm_log2(noise[i]), -LN2, sl.x(l[j])), -INFINITY);
+            kept += part[j];
+            better(best, Best{score, l[j], i});
+          }
+          before += part[j];
+        }
+        kept = warp_sum64(kept);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+          Best o;
+          o.score = __shfl_xor_sync(FULL_MASK, best.score, d);
+          o.logit = __shfl_xor_sync(FULL_MASK, best.logit, d);
+          o.index = __shfl_xor_sync(FULL_MASK, best.index, d);
+          better(best, o);
+        }
+        if (lane == 0) {  // the largest logit is always kept, so there is one
+          a.out_tokens[r] = static_cast<int64_t>(best.index);
+          a.out_logprobs[r] = greedy ? 0.f : sl.x(best.logit) - logf(static_cast<float>(kept) / sl.scale);
+        }
+      }
+    }
+    __syncthreads();
+    if (s.enough) return;
+  }
 
-  const bool greedy = temperature == 0.f;
-  const bool by_k = !greedy && k > 0 && k < a.n, by_p = !greedy && p < 1.f;
+  // 4. The cuts, over everything above a value that surely is not kept: for
+  // top-k a value that k keys of one slice reach; for top-p the value at which
+  // n tokens together weigh less than what may be left out.
   u64 thr = greedy ? sl.value_key(top) : 0;  // copies of the maximum; the lowest index wins the race
   if (by_k || by_p) {
-    // 2. The row's mass, and the value below which nothing should be kept.
-    u64 Z = 0;
-    if (!by_k) {
-      for (int v = threadIdx.x; v < sl.nv;) {
-        float sum = 0.f;
-        for (int i = 0; i < 16 && v < sl.nv; ++i, v += THREADS) {
-          float x[VEC];
-          sl.load(v, x);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
-#pragma unroll
-          for (int d = VEC / 2; d; d >>= 1)
-#pragma unroll
-            for (int j = 0; j < d; ++j) x[j] += x[j + d];
-          sum += x[0];
-        }
-        Z += sl.fixed(sum);
-      }
-      Z = block_sum64(Z, s);
-      if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->ex_z[rank] = Z;
-    }
-    const bool sampled = a.n > 4096;
-    if (sampled) {
-      // One vector in SAMPLE_EVERY, at a place that moves along (and so spreads over the banks).
-      for (int q = threadIdx.x; q * SAMPLE_EVERY < sl.nv; q += THREADS) {
-        const int v = q * SAMPLE_EVERY + (q & (SAMPLE_EVERY - 1));
-        if (v >= sl.nv) continue;
-        float x[VEC];
-        sl.load(v, x);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (x[j] != -INFINITY) {
-            const float at = fminf(-sl.x(x[j]) * SAMPLE_SCALE, SAMPLE_BINS - 1.f);
-            atomicAdd(&s.count[static_cast<int>(at)], 1u);
-          }
-      }
-      __syncthreads();
-      for (int b = threadIdx.x; b < SAMPLE_BINS * C; b += THREADS) {
-        const unsigned c = s.count[b % SAMPLE_BINS];
-        if (c) atomicAdd(&cluster.map_shared_rank(&s, b / SAMPLE_BINS)->sample[b % SAMPLE_BINS], c);
-      }
-    }
-    if (sampled || !by_k) cluster.sync();
-    if (!by_k) {
-      Z = 0;
-      for (int i = 0; i < C; ++i) Z += s.ex_z[i];
-    }
-    // Without a sample, or without an answer: weights below the last bin's are
-    // nothing beside the maximum's.
-    const int cut = sampled ? sample_cut(s.sample, by_k, static_cast<float>(k),
-                                         (1.f - p) * (static_cast<float>(Z) / sl.scale))
-                            : SAMPLE_BINS;
-    const float at = top - temperature * (static_cast<float>(cut) / SAMPLE_SCALE);
+    float at = -INFINITY;
+    if (by_k)
+      at = tau;
+    else
+      at = top - temperature * __logf(static_cast<float>(a.n) / (0.99f * (1.f - fmaxf(p, 0.f)) * (static_cast<float>(Z) / sl.scale)));
     const u64 hi = sl.value_key(top) | ((u64(1) << sl.index_bits) - 1);
-    // (A maximum of +inf, or a cut that is no number: from the bottom.)
-    u64 lo = at < top && at > -INFINITY ? sl.value_key(at) : 0;
-
-    // 3. The cuts.
-    bool fresh = false, cut_k = by_k;
+    const u64 lo = at <= top && at > -INFINITY ? sl.value_key(at) : 0;
+    bool fresh = false, cut_k = false;
+    cluster.sync();  // the keys of step 3 have been read: list takes their place
     if (by_k) {
-      bool found = select(sl, s, cluster, lo, hi, false, static_cast<u64>(k), 0, fresh);
-      if (!found && lo) {
-        lo = 0;
-        fresh = false;
-        found = select(sl, s, cluster, lo, hi, false, static_cast<u64>(k), 0, fresh);
-      }
-      cut_k = found;
-      Z = found ? s.z : s.total_m;  // not found: there are no more than k
-      if (found) thr = s.thr;
+      cut_k = select(sl, s, cluster, lo, hi, false, static_cast<u64>(k), 0, fresh);
+      Z = cut_k ? s.z : s.total_m;  // not found: there are no more than k
+      if (cut_k) thr = s.thr;
     }
     if (by_p) {
-      // Kept while the mass before is below p Z: an integer comparison.
-      const double want = ceil(static_cast<double>(p) * static_cast<double>(Z));
-      u64 target = want >= 1.0 ? static_cast<u64>(want) : 1ull;
-      target = target < Z ? target : Z;
       __syncthreads();  // s.z, s.thr and s.total_m have been read
-      bool found = select(sl, s, cluster, lo, hi, true, target, 1, fresh);
-      if (!found && lo) {
+      const u64 target = mass_target(p, Z);
+      bool cut_p = select(sl, s, cluster, lo, hi, true, target, 1, fresh);
+      if (!cut_p && lo) {  // the masses' roundings used up what `lo` leaves out
         fresh = false;
-        found = select(sl, s, cluster, 0, hi, true, target, 1, fresh);
+        cut_p = select(sl, s, cluster, 0, hi, true, target, 1, fresh);
       }
-      // Not found: Z's rounding asks for more than there is, so everything stays.
-      if (found && (!cut_k || s.thr > thr)) thr = s.thr;
+      // Still not: Z's rounding asks for more than there is, so everything stays.
+      if (cut_p && s.thr > thr) thr = s.thr;
     }
   }
 
-  // 4. The race over the kept.
-  const float floor_w = fminf(min_p, 1.f);
-  const float* noise = a.noise + r * a.noise_ld;
+  // The race over the kept.
   Best best{-INFINITY, 0.f, NONE};
   u64 kept = 0;
   const float floor_l = sl.logit_of(thr);
