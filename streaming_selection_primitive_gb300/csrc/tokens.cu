@@ -26,6 +26,8 @@
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
 // the same whatever order the atomics take.
+#include <cfloat>
+
 #include <cooperative_groups.h>
 
 #include "../../include/profk.h"
@@ -40,13 +42,13 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int TOP = 128;        // keys of a slice that step 2 can sort
-constexpr int TOP_P = 64;       // and those it sorts for top-p and min-p
+constexpr int TOP = 128;        // keys of a slice that step 2 can sort (the merge searches lists of up to 2^8 - 1)
+constexpr int TOP_P = 128;      // and those it sorts for top-p and min-p
 constexpr int CANDIDATES = 1024;
 constexpr int BINS = 1024;      // of one histogram pass
 constexpr int PER = BINS / THREADS;
 constexpr int LIST = 256;       // keys of a bin that are ranked directly
-constexpr int SLICE_BYTES = 64 << 10;  // of a row in one CTA's shared memory, where the cluster is not at its largest
+constexpr int SLICE_BYTES = 66 << 10;  // of a row in one CTA's shared memory, where the cluster is not at its largest
 constexpr int SLICE_MOST = 180 << 10;  // and in any case; beyond it the passes read global memory
 constexpr int SLICE_LEAST = 8 << 10;
 using u64 = unsigned long long;
@@ -70,14 +72,24 @@ struct Part {
   int keys;      // sorted keys sent; -1: too many candidates to rank
 };
 
+// What late_row gets.
+struct Late {
+  const float* noise;
+  int64_t* token;
+  float* logprob;
+  u64 Z;
+  int32_t k;
+  float p, temperature, floor_w, tau;
+  bool by_k, by_p;
+};
+
 struct Shared {
   // Written by other CTAs of the cluster.
   alignas(16) unsigned merged_c[BINS];
   alignas(16) u64 merged_m[BINS];
-  union {
-    u64 tops[MAX_CLUSTER][TOP];  // step 3
-    u64 list[2][LIST];           // step 4
-  };
+  u64 tops[MAX_CLUSTER][TOP];     // step 3: first keys, and their noise
+  float tops_q[MAX_CLUSTER][TOP];
+  u64 list[2][LIST];              // step 4
   Part part[MAX_CLUSTER];
   Best ex_best[MAX_CLUSTER];
   u64 ex_kept[MAX_CLUSTER];
@@ -91,14 +103,18 @@ struct Shared {
     alignas(16) u64 candidates[CANDIDATES + 2];
   };
   u64 sorted[LIST];
+  float sorted_q[TOP];
   u64 wc[WARPS], wm[WARPS], red[WARPS];
-  float redf[WARPS], redt[WARPS];
+  float redf[WARPS];
+  uint32_t redk[WARPS];
   Best best[WARPS];
   unsigned slot;
   int enough;
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
+  Late late;
+  alignas(8) unsigned char slice[96];  // the row's Slice
 };
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -113,18 +129,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float max_of(const float* x, int n) {
-  float top = x[0];
-#pragma unroll
-  for (int j = 1; j < n; ++j) top = fmaxf(top, x[j]);
-  return top;
-}
-
 // log2 of a positive number by the hardware's approximation; zero gives -inf.
 __device__ __forceinline__ float lm_log2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max_of(const float* x, int n) {
+  float top = x[0];
+#pragma unroll
+  for (int j = 1; j < n; ++j) top = fmaxf(top, x[j]);
+  return top;
 }
 
 // One row as a CTA of its cluster sees it.  Positions are counted from the
@@ -199,6 +215,41 @@ struct Slice {
       fetch(v, x);
   }
 
+  // Element j of a vector (inside the row, allowed).
+  __device__ __forceinline__ float one(int v, int j) const {
+    if constexpr (RESIDENT)
+      return lm_float(reinterpret_cast<const T*>(store + v)[j]);
+    else
+      return lm_float(row[element(v) + j]);
+  }
+
+  // body(l, i) for every element of the slice at or above floor (finite or
+  // +inf).  A thread first marks those of several vectors and then takes them
+  // one by one, so that the lanes' hits meet in the same turns.
+  template <typename F>
+  __device__ __forceinline__ void above(float floor, F&& body) const {
+    constexpr int GROUP = 32 / VEC;
+    for (int v = threadIdx.x; v < nv; v += GROUP * THREADS) {
+      unsigned hits = 0;
+#pragma unroll
+      for (int g = 0; g < GROUP; ++g) {
+        const int u = v + g * THREADS;
+        if (u >= nv) break;
+        float x[VEC];
+        load(u, x);
+        if (max_of(x, VEC) < floor) continue;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) hits |= x[j] >= floor ? 1u << (g * VEC + j) : 0u;
+      }
+      while (hits) {
+        const int b = __ffs(hits) - 1;
+        hits &= hits - 1;
+        const int u = v + b / VEC * THREADS, j = b % VEC;
+        body(one(u, j), element(u) + j);
+      }
+    }
+  }
+
   __device__ __forceinline__ void keep(int v, const float (&x)[VEC]) const {
     union {
       uint4 bits;
@@ -222,6 +273,10 @@ struct Slice {
   __device__ __forceinline__ u64 key(float l, int64_t i) const {
     return value_key(l) | ((u64(1) << index_bits) - 1 - static_cast<u64>(i));
   }
+  __device__ __forceinline__ int64_t index_of(u64 key) const {
+    const u64 ones = (u64(1) << index_bits) - 1;
+    return static_cast<int64_t>(ones - (key & ones));
+  }
   __device__ __forceinline__ float logit_of(u64 key) const {
     const uint32_t ord = static_cast<uint32_t>(key >> index_bits) << DROP;
     // The dropped bits of a negative value's order key are ones.
@@ -240,36 +295,49 @@ __device__ __forceinline__ u64 block_sum64(u64 v, Shared& s) {
   return r;
 }
 
-// Histogram of the slice's keys in [lo, hi], joined over the cluster, and the
-// bin where the running count (or mass) from the top first reaches `target`:
-// s.bin, s.above_*, s.in_c; s.bin = BINS where it does not.  fresh: the joined
-// histogram of the same range is still in place.
+// What a histogram is made of: first, all elements at or above `floor` in equal
+// ranges of x from the maximum down (the last takes what is beyond); then
+// those of the first one's bin `bin0` with keys in [lo, hi], in equal ranges of
+// keys from hi down.
+struct Level {
+  float floor;
+  float per_x;  // bins per unit of x of the first
+  int bin0;     // -1: the first
+  u64 lo, hi;
+  int shift;
+
+  template <typename S>
+  __device__ __forceinline__ int bin_of(const S& sl, float l, int64_t i) const {
+    const int b = static_cast<int>(fminf(-sl.x(l) * per_x, BINS - 1.f));
+    if (bin0 < 0) return b;
+    const u64 key = sl.key(l, i);
+    return b != bin0 || key < lo || key > hi ? -1 : static_cast<int>((hi - key) >> shift);
+  }
+  __device__ __forceinline__ void fit() {
+    shift = 0;
+    while (((hi - lo) >> shift) >= BINS) ++shift;
+  }
+};
+
+// The histogram, joined over the cluster, and the bin where the running count
+// (or mass) from the top first reaches `target`: s.bin, s.above_*, s.in_c;
+// s.bin = BINS where it does not.  fresh: the joined histogram is in place.
 template <typename S>
-__device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, u64 lo, u64 hi, int shift, bool by_mass,
-                      u64 target, bool fresh) {
+__device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const Level& lv, bool by_mass, u64 target,
+                      bool fresh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!fresh) {
     for (int b = threadIdx.x; b < BINS; b += THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0u;
     __syncthreads();
-    const float floor_l = sl.logit_of(lo);
-    for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
-      float x[S::VEC];
-      sl.load(v, x);
-      const float top = max_of(x, S::VEC);
-      if (top == -INFINITY || top < floor_l) continue;
-#pragma unroll
-      for (int j = 0; j < S::VEC; ++j) {
-        if (x[j] == -INFINITY) continue;
-        const u64 key = sl.key(x[j], sl.element(v) + j);
-        if (key < lo || key > hi) continue;
-        const unsigned b = static_cast<unsigned>((key - lo) >> shift);
-        const u64 mass = sl.fixed(sl.weight(x[j]));
-        atomicAdd(&s.count[b], 1u);
-        const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
-        const unsigned mh = static_cast<unsigned>(mass >> 32) + (old + ml < old ? 1u : 0u);
-        if (mh) atomicAdd(&s.hi[b], mh);
-      }
-    }
+    sl.above(lv.floor, [&](float l, int64_t i) {
+      const int b = lv.bin_of(sl, l, i);
+      if (b < 0) return;
+      const u64 mass = sl.fixed(sl.weight(l));
+      atomicAdd(&s.count[b], 1u);
+      const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
+      const unsigned mh = static_cast<unsigned>(mass >> 32) + (old + ml < old ? 1u : 0u);
+      if (mh) atomicAdd(&s.hi[b], mh);
+    });
     cluster.sync();
     // This CTA joins its share of the bins, four a thread, and tells everybody.
     const int C = cluster.num_blocks(), share = BINS / C;
@@ -300,13 +368,13 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, u64 lo
     }
     cluster.sync();
   }
-  // Thread t takes bins BINS - 1 - PER t .. downwards.
-  const int top = BINS - 1 - PER * threadIdx.x;
+  // Thread t takes bins PER t and on.
+  const int first = PER * threadIdx.x;
   u64 tc = 0, tm = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    tc += s.merged_c[top - j];
-    tm += s.merged_m[top - j];
+    tc += s.merged_c[first + j];
+    tm += s.merged_m[first + j];
   }
   u64 ic = tc, im = tm;
 #pragma unroll
@@ -331,10 +399,10 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, u64 lo
   if (threadIdx.x == THREADS - 1) s.total_m = bm + tm;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const u64 nc = s.merged_c[top - j], nm = s.merged_m[top - j];
+    const u64 nc = s.merged_c[first + j], nm = s.merged_m[first + j];
     const u64 before = by_mass ? bm : bc, with = before + (by_mass ? nm : nc);
     if (before < target && target <= with) {
-      s.bin = static_cast<unsigned>(top - j);
+      s.bin = static_cast<unsigned>(first + j);
       s.above_c = bc;
       s.above_m = bm;
       s.in_c = nc;
@@ -345,37 +413,38 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, u64 lo
   __syncthreads();
 }
 
-__device__ __forceinline__ int shift_for(u64 lo, u64 hi) {
-  int shift = 0;
-  while (((hi - lo) >> shift) >= BINS) ++shift;
-  return shift;
-}
-
 // The key down to which tokens are kept, s.thr (every kept key >= it), and the
-// mass of those, s.z: the first `target` keys of [lo, hi] from the top, or as
-// many as it takes for their mass to reach it.  False: all of [lo, hi] does
-// not reach it (then s.total_m is its mass).
+// mass of those, s.z: the first `target` keys from the top, or as many as it
+// takes for their mass to reach it.  False: all that `lv` counts does not reach
+// it (then s.total_m is its mass).
 template <typename S>
-__device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, u64 lo, u64 hi, bool by_mass, u64 target,
-                       int which, bool& fresh) {
+__device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level lv, bool by_mass, u64 target, int which,
+                       bool& fresh) {
   const int lane = threadIdx.x & 31;
   u64 above_c = 0, above_m = 0;
   for (int level = 0;; ++level) {
-    const int shift = shift_for(lo, hi);
-    cross(sl, s, cluster, lo, hi, shift, by_mass, target - (by_mass ? above_m : above_c), fresh && level == 0);
-    if (s.bin == BINS) {
-      fresh = level == 0;
-      return false;
-    }
+    cross(sl, s, cluster, lv, by_mass, target - (by_mass ? above_m : above_c), fresh && level == 0);
+    fresh = level == 0;
+    if (s.bin == BINS) return false;
     above_c += s.above_c;
     above_m += s.above_m;
     const u64 in_c = s.in_c;
-    const unsigned bin = s.bin;
-    lo += u64(bin) << shift;
-    const u64 last = lo + ((u64(1) << shift) - 1);
-    hi = last < hi ? last : hi;
-    fresh = level == 0;
+    const int bin = static_cast<int>(s.bin);
+    // A value below the bin's (x's roundings blur it by far less than half a bin).
+    const float T = 1.f / sl.inv, low = sl.m - T * ((bin + 1.5f) / lv.per_x);
     if (in_c > LIST) {
+      if (lv.bin0 < 0) {
+        const float top = sl.m - T * ((bin - 0.5f) / lv.per_x);
+        lv.bin0 = bin;
+        lv.hi = sl.value_key(bin > 0 && top <= sl.m && top > -INFINITY ? top : sl.m) | ((u64(1) << sl.index_bits) - 1);
+        lv.lo = bin + 1 < BINS && low <= sl.m && low > -INFINITY ? sl.value_key(low) : 0;
+      } else {
+        lv.hi -= u64(bin) << lv.shift;
+        const u64 width = (u64(1) << lv.shift) - 1;
+        if (lv.hi - lv.lo > width) lv.lo = lv.hi - width;
+      }
+      if (lv.lo) lv.floor = fmaxf(lv.floor, sl.logit_of(lv.lo));
+      lv.fit();
       __syncthreads();  // s.bin and the rest have been read
       continue;
     }
@@ -386,24 +455,14 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, u64 l
     for (int i = 0; i < rank; ++i) base += cluster.map_shared_rank(&s, i)->count[bin];
     if (threadIdx.x == 0) s.slot = base;
     __syncthreads();
-    if (s.count[bin] != 0u) {
-      const float floor_l = sl.logit_of(lo);
-      for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
-        float x[S::VEC];
-        sl.load(v, x);
-        const float top = max_of(x, S::VEC);
-        if (top == -INFINITY || top < floor_l) continue;
-#pragma unroll
-        for (int j = 0; j < S::VEC; ++j) {
-          if (x[j] == -INFINITY) continue;
-          const u64 key = sl.key(x[j], sl.element(v) + j);
-          if (key < lo || key > hi) continue;
-          const unsigned at = atomicAdd(&s.slot, 1u);
-          if (at < LIST)
-            for (int i = 0; i < C; ++i) cluster.map_shared_rank(&s, i)->list[which][at] = key;
-        }
-      }
-    }
+    const float floor = lv.bin0 < 0 && bin + 1 < BINS && low <= sl.m ? fmaxf(lv.floor, low) : lv.floor;
+    if (s.count[bin] != 0u)
+      sl.above(floor, [&](float l, int64_t i) {
+        if (lv.bin_of(sl, l, i) != bin) return;
+        const unsigned at = atomicAdd(&s.slot, 1u);
+        if (at < LIST)
+          for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->list[which][at] = sl.key(l, i);
+      });
     cluster.sync();
     // Rank of each key: two threads count the larger ones of half the list each.
     const int m = static_cast<int>(in_c), item = threadIdx.x >> 1;
@@ -469,31 +528,160 @@ __device__ __forceinline__ u64 mass_target(float p, u64 Z) {
   return q < 1 ? 1 : q > Z ? Z : q;
 }
 
-// The want-th largest of the block's thread maxima, or less: of each warp the
-// ceil(want / WARPS)-th largest, of those the least.  At least `want` threads
-// reach it.  Called with the warp's own maxima; the block's value is in redt
-// after a barrier.
-__device__ __forceinline__ float warp_tau(float top, int want) {
-  uint32_t key = choice_key(top);
-  uint32_t got = 0u;
-  const int lane = threadIdx.x & 31;
-  for (int j = 0; j < want; j += WARPS) {
-    got = __reduce_max_sync(FULL_MASK, key);
-    if (lane == __ffs(__ballot_sync(FULL_MASK, key == got)) - 1) key = 0u;
+// A value that at least `want` of the block's thread maxima reach, and not many
+// more: bisection over the keys between the least maximum and the largest
+// (each under a count over the block).  -inf if there are no more than `want`.
+__device__ __forceinline__ float block_tau(float top, float widest, int want, Shared& s) {
+  const uint32_t key = choice_key(top);
+  const uint32_t least = __reduce_min_sync(FULL_MASK, key ? key : ~0u);
+  if ((threadIdx.x & 31) == 0) s.redk[threadIdx.x >> 5] = least;
+  int count = __syncthreads_count(key != 0u);
+  if (count <= want) return -INFINITY;
+  uint32_t lo = s.redk[0], hi = choice_key(widest) + 1u;
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) lo = min(lo, s.redk[w]);
+  while (hi - lo > 1u && count > want + want / 8 + 4) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int c = __syncthreads_count(key >= mid);
+    if (c >= want) {
+      lo = mid;
+      count = c;
+    } else {
+      hi = mid;
+    }
   }
-  return got ? key_to_float(got) : -INFINITY;
+  return key_to_float(lo);
 }
 
-// Candidates larger than a key: its rank, as keys are distinct.  (An odd number
-// of them is followed by a 0.)
-__device__ __forceinline__ int larger_keys(const Shared& s, int keys, u64 key) {
-  int above = 0;
+// body(i, rank) for every candidate, rank being the number of larger ones (they
+// are distinct); each is ranked by as many neighbouring threads as there are
+// to spare, up to 8, and the first of them calls body.  begin(i) runs before
+// the ranking and returns what body gets as well.  Called by the whole block;
+// an odd number of candidates is followed by a 0.
+template <typename B, typename F>
+__device__ __forceinline__ void rank_candidates(const Shared& s, int keys, B&& begin, F&& body) {
+  int split = 1;
+  while (split < 8 && keys * split * 2 <= THREADS) split *= 2;
+  const int sub = threadIdx.x & (split - 1);
+  for (int base = 0; base < keys; base += THREADS / split) {
+    const int i = base + threadIdx.x / split;
+    const u64 mine = i < keys ? s.candidates[i] : ~u64(0);
+    const auto what = begin(i < keys && sub == 0, mine);
+    int above = 0;
 #pragma unroll 4
-  for (int j = 0; j < keys; j += 2) {
-    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s.candidates + j);
-    above += (o.x > key) + (o.y > key);
+    for (int j = 2 * sub; j < keys; j += 2 * split) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s.candidates + j);
+      above += (o.x > mine) + (o.y > mine);
+    }
+    for (int d = split >> 1; d; d >>= 1) above += __shfl_xor_sync(FULL_MASK, above, d);
+    if (i < keys && sub == 0) body(mine, above, what);
   }
-  return above;
+}
+
+// x - log q; NaN noise is never ahead.
+__device__ __forceinline__ float race(float x, float q) { return fmaxf(fmaf(lm_log2(q), -LN2, x), -INFINITY); }
+
+// The best of the lanes' bests, in every lane.
+__device__ __forceinline__ void warp_best(Best& best) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    Best o;
+    o.score = __shfl_xor_sync(FULL_MASK, best.score, d);
+    o.logit = __shfl_xor_sync(FULL_MASK, best.logit, d);
+    o.index = __shfl_xor_sync(FULL_MASK, best.index, d);
+    better(best, o);
+  }
+}
+
+template <typename S>
+__device__ __forceinline__ void write_row(const S& sl, const Best& best, u64 kept, bool greedy, int64_t* token,
+                                          float* logprob) {
+  // The largest logit is always kept, so an index has been found.
+  *token = static_cast<int64_t>(best.index);
+  *logprob = greedy ? 0.f : sl.x(best.logit) - logf(static_cast<float>(kept) / sl.scale);
+}
+
+// Joins the race over the threads and CTAs and writes the row's answer.
+template <typename S>
+__device__ __forceinline__ void finish(const S& sl, Shared& s, cg::cluster_group& cluster, Best best, u64 kept, bool greedy,
+                                       int64_t* token, float* logprob) {
+  const int rank = cluster.block_rank();
+  kept = block_sum64(kept, s);
+  warp_best(best);
+  if ((threadIdx.x & 31) == 0) s.best[threadIdx.x >> 5] = best;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < WARPS; ++w) better(best, s.best[w]);
+    Shared* leader = cluster.map_shared_rank(&s, 0);
+    leader->ex_best[rank] = best;
+    leader->ex_kept[rank] = kept;
+  }
+  cluster.sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    for (int i = 1; i < static_cast<int>(cluster.num_blocks()); ++i) {
+      better(best, s.ex_best[i]);
+      kept += s.ex_kept[i];
+    }
+    write_row(sl, best, kept, greedy, token, logprob);
+  }
+}
+
+// 4. The cuts, over everything above a value that surely is not kept: for
+// top-k a value that k keys of one slice reach; for top-p the value at which n
+// tokens together weigh less than what may be left out.  Then the race.  (A
+// function of its own: the registers that it needs would be spilled by rows
+// that never come here, at a microsecond a row.)
+template <typename S>
+__device__ __noinline__ void late_row(Shared& s) {
+  static_assert(sizeof(S) <= sizeof(s.slice), "room for the slice");
+  const S sl = *reinterpret_cast<const S*>(s.slice);
+  const Late& late = s.late;
+  cg::cluster_group cluster = cg::this_cluster();
+  const float temperature = late.temperature, top = sl.m;
+  const bool greedy = temperature == 0.f;
+  u64 Z = late.Z;
+  u64 thr = greedy ? sl.value_key(top) : 0;  // copies of the maximum; the lowest index wins the race
+  if (late.by_k || late.by_p) {
+    const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) / sl.scale);
+    const float floor = late.by_k ? late.tau : top - temperature * __logf(static_cast<float>(sl.n) / (0.99f * left));
+    const bool bounded = floor <= top && floor > -INFINITY;
+    Level lv{};
+    lv.bin0 = -1;
+    lv.floor = bounded ? floor : -FLT_MAX;
+    // The bins end at the floor, and where weights are nothing beside the maximum's.
+    const float reach_x = bounded ? fminf(-sl.x(floor), 64.f) : 64.f;
+    lv.per_x = BINS / fmaxf(reach_x, 1e-3f);
+    bool fresh = false;
+    for (int turn = late.by_k ? 0 : 1; turn < (late.by_p ? 2 : 1); ++turn) {  // the first k, then their share p
+      const u64 target = turn ? mass_target(late.p, Z) : static_cast<u64>(late.k);
+      bool cut;
+      for (;;) {
+        __syncthreads();  // what the turn before left in s has been read
+        cut = select(sl, s, cluster, lv, turn == 1, target, turn, fresh);
+        if (cut || turn == 0 || lv.floor == -FLT_MAX) break;
+        lv.floor = -FLT_MAX;  // the masses' roundings used up what the floor leaves out
+        fresh = false;
+      }
+      // Without a cut: there are no more than k, or Z's rounding asks for more
+      // mass than there is, so that everything stays.
+      if (turn == 0) Z = cut ? s.z : s.total_m;
+      if (cut && s.thr > thr) thr = s.thr;
+    }
+  }
+  // (ln min_p: with room for its and the weights' roundings.)
+  const float floor_w = late.floor_w;
+  float floor = thr ? sl.logit_of(thr) : -FLT_MAX;
+  if (floor_w > 0.f) floor = fmaxf(floor, fminf(top, top + temperature * (1.001f * __logf(floor_w) - 1e-3f)));
+  Best best{-INFINITY, 0.f, NONE};
+  u64 kept = 0;
+  const float* noise = late.noise;
+  sl.above(floor, [&](float l, int64_t i) {
+    const float w = sl.weight(l), x = sl.x(l);
+    if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
+    kept += sl.fixed(w);
+    better(best, Best{greedy ? 0.f : race(x, noise[i]), l, static_cast<unsigned>(i)});
+  });
+  finish(sl, s, cluster, best, kept, greedy, late.token, late.logprob);
 }
 
 template <typename T, bool RESIDENT>
@@ -575,86 +763,83 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
 #pragma unroll
   for (int d = 16; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
   if (lane == 0) s.redf[warp] = widest;
-  if (reach) {
-    if (RESIDENT && sl.nv < THREADS) {
-      // Fewer vectors than threads: the threads' maxima of single elements instead.
-      __syncthreads();
-      const T* flat = reinterpret_cast<const T*>(sl.store);
-      top = -INFINITY;
-      for (int i = threadIdx.x; i < sl.nv * VEC; i += THREADS) top = fmaxf(top, lm_float(flat[i]));
-    }
-    const float least = warp_tau(top, reach);
-    if (lane == 0) s.redt[warp] = least;
-  }
   __syncthreads();
   widest = s.redf[0];
 #pragma unroll
   for (int w = 1; w < WARPS; ++w) widest = max_nan(widest, s.redf[w]);
   float tau = -INFINITY;
-  if (reach) {
-    tau = s.redt[0];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) tau = fminf(tau, s.redt[w]);
+  if (reach > 1 && !isnan(widest)) {
+    if (RESIDENT && sl.nv < THREADS) {
+      // Fewer vectors than threads: the threads' maxima of single elements instead.
+      const T* flat = reinterpret_cast<const T*>(sl.store);
+      top = -INFINITY;
+      for (int i = threadIdx.x; i < sl.nv * VEC; i += THREADS) top = fmaxf(top, lm_float(flat[i]));
+    }
+    tau = block_tau(top, widest, reach, s);
   }
+  if (reach == 1) tau = widest;
   sl.m = widest;
 
   // 2. The slice's mass, and its first keys.
   float mass = 0.f;
   const bool need_mass = by_p && !by_k;
+  const float* noise = a.noise + r * a.noise_ld;
+  if (need_mass) {
+    for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
+      float x[VEC];
+      sl.load(v, x);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
+#pragma unroll
+      for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < d; ++j) x[j] += x[j + d];
+      mass += x[0];
+    }
+    mass = warp_sum(mass);
+  }
   int keys = 0;
-  if (want || need_mass) {
+  if (want && !isnan(widest)) {
     for (int turn = 0;; ++turn) {
-      for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
-        float x[VEC];
-        sl.load(v, x);
-        const float most = max_of(x, VEC);
-        if (want && most >= tau && most > -INFINITY) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            if (x[j] >= tau && x[j] > -INFINITY) {
-              const unsigned at = atomicAdd(&s.slot, 1u);
-              if (at < CANDIDATES) s.candidates[at] = sl.key(x[j], sl.element(v) + j);
-            }
-        }
-        if (need_mass && turn == 0) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
-#pragma unroll
-          for (int d = VEC / 2; d; d >>= 1)
-#pragma unroll
-            for (int j = 0; j < d; ++j) x[j] += x[j + d];
-          mass += x[0];
-        }
-      }
-      __syncthreads();  // the candidates are complete; redf has been read
+      sl.above(fmaxf(tau, -FLT_MAX), [&](float l, int64_t i) {
+        const unsigned at = atomicAdd(&s.slot, 1u);
+        if (at < CANDIDATES) s.candidates[at] = sl.key(l, i);
+      });
+      __syncthreads();
       keys = static_cast<int>(s.slot);
       if (keys <= CANDIDATES || turn == 2) break;
-      // Too many (neighbours are alike, so that some warps' maxima are low):
+      // Too many (neighbours are alike, so that a thread holds several):
       // again from the want-th largest of those that were stored.
-      for (int i = threadIdx.x; i < CANDIDATES; i += THREADS)
-        if (larger_keys(s, CANDIDATES, s.candidates[i]) == want - 1) s.thr = s.candidates[i];
+      rank_candidates(
+          s, CANDIDATES, [](bool, u64) { return 0; },
+          [&](u64 key, int rank, int) {
+            if (rank == want - 1) s.thr = key;
+          });
       __syncthreads();
       tau = sl.logit_of(s.thr);
       if (threadIdx.x == 0) s.slot = 0;
       __syncthreads();
     }
-    mass = warp_sum(mass);
-    if (lane == 0) s.redf[warp] = mass;
+    if (threadIdx.x == 0 && keys <= CANDIDATES) s.candidates[keys] = 0;
   }
+  __syncthreads();  // redf has been read
+  if (lane == 0) s.redf[warp] = mass;
   cluster.barrier_wait(std::move(started));
   if (keys > CANDIDATES) {  // copies of one value
     keys = -1;
-  } else if (want) {
-    // The first `want` go to every CTA that looks at them.
+  } else if (keys > 0) {
+    // The first `want`, with their noise, go to every CTA that looks at them.
     const int readers = by_k || greedy ? 1 : C;
-    if (threadIdx.x == 0) s.candidates[keys] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < keys; i += THREADS) {
-      const u64 mine = s.candidates[i];
-      const int above = larger_keys(s, keys, mine);
-      if (above < want)
-        for (int c = 0; c < readers; ++c) cluster.map_shared_rank(&s, c)->tops[rank][above] = mine;
-    }
+    rank_candidates(
+        s, keys, [&](bool some, u64 key) { return some && !greedy ? noise[sl.index_of(key)] : 1.f; },
+        [&](u64 key, int place, float q) {
+          if (place < want)
+            for (int c = 0; c < readers; ++c) {
+              Shared* o = cluster.map_shared_rank(&s, c);
+              o->tops[rank][place] = key;
+              o->tops_q[rank][place] = q;
+            }
+        });
     keys = keys < want ? keys : want;
   }
   __syncthreads();
@@ -688,30 +873,42 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   if (need_mass)
     for (int i = 0; i < C; ++i) Z += sl.fixed(s.part[i].mass * sl.weight(s.part[i].top));
   const float floor_w = fminf(min_p, 1.f);
-  const float* noise = a.noise + r * a.noise_ld;
   if (want && found >= 0) {
     const bool decide = !by_k && !greedy;  // whether these keys are enough is not known beforehand
     if (rank != 0 && !decide) return;
     // Merge: a key's place is the number of larger ones in each of the sorted lists.
     const int got = found < want ? found : want;
-    for (int i = threadIdx.x; i < C * want; i += THREADS) {
-      const int c = i / want, j = i - c * want;
-      if (j >= s.part[c].keys) continue;
+    // (The lists' shares of `want` reach the least of them, so no key below it counts.)
+    u64 least = ~u64(0);
+    const int each = (want + C - 1) / C;
+    for (int c = 0; c < C; ++c) {
+      const u64 key = s.part[c].keys >= each ? s.tops[c][each - 1] : 0;
+      least = key < least ? key : least;
+    }
+    for (int i = threadIdx.x; i < C * TOP; i += THREADS) {
+      const int c = i / TOP, j = i % TOP;
+      if (j >= s.part[c].keys || s.tops[c][j] < least) continue;
       const u64 mine = s.tops[c][j];
       int place = j;
-      for (int o = 0; o < C && place < want; ++o) {
-        if (o == c) continue;
-        int lo = 0, hi = s.part[o].keys;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (s.tops[o][mid] > mine)
-            lo = mid + 1;
-          else
-            hi = mid;
-        }
-        place += lo;
+      for (int first = 0; first < C; first += 4) {
+        // Four lists at a time, so that their searches overlap.
+        int at[4] = {0, 0, 0, 0}, len[4];
+#pragma unroll
+        for (int o = 0; o < 4; ++o) len[o] = first + o < C && first + o != c ? s.part[first + o].keys : 0;
+#pragma unroll
+        for (int bit = 7; bit >= 0; --bit)
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {
+            const int to = at[o] + (1 << bit);
+            const u64 key = s.tops[(first + o) & (MAX_CLUSTER - 1)][to <= len[o] ? to - 1 : 0];
+            at[o] = to <= len[o] && key > mine ? to : at[o];
+          }
+        place += at[0] + at[1] + at[2] + at[3];
       }
-      if (place < want) s.sorted[place] = mine;
+      if (place < want) {
+        s.sorted[place] = mine;
+        s.sorted_q[place] = s.tops_q[c][j];
+      }
     }
     __syncthreads();
     if (warp == 0) {
@@ -747,120 +944,53 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
         for (int j = 0; j < EACH; ++j) {
           const int at = lane * EACH + j;
           if (at < got && (before < target || at == 0) && w[j] >= floor_w && sl.x(l[j]) > -INFINITY) {
-            const unsigned i =
-                static_cast<unsigned>(((u64(1) << sl.index_bits) - 1) - (s.sorted[at] & ((u64(1) << sl.index_bits) - 1)));
-            const float score = greedy ? 0.f : fmaxf(fmaf(lm_log2(noise[i]), -LN2, sl.x(l[j])), -INFINITY);
             kept += part[j];
-            better(best, Best{score, l[j], i});
+            better(best, Best{greedy ? 0.f : race(sl.x(l[j]), s.sorted_q[at]), l[j],
+                              static_cast<unsigned>(sl.index_of(s.sorted[at]))});
           }
           before += part[j];
         }
         kept = warp_sum64(kept);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-          Best o;
-          o.score = __shfl_xor_sync(FULL_MASK, best.score, d);
-          o.logit = __shfl_xor_sync(FULL_MASK, best.logit, d);
-          o.index = __shfl_xor_sync(FULL_MASK, best.index, d);
-          better(best, o);
-        }
-        if (lane == 0) {  // the largest logit is always kept, so there is one
-          a.out_tokens[r] = static_cast<int64_t>(best.index);
-          a.out_logprobs[r] = greedy ? 0.f : sl.x(best.logit) - logf(static_cast<float>(kept) / sl.scale);
-        }
+        warp_best(best);
+        if (lane == 0) write_row(sl, best, kept, greedy, a.out_tokens + r, a.out_logprobs + r);
       }
     }
     __syncthreads();
     if (s.enough) return;
   }
 
-  // 4. The cuts, over everything above a value that surely is not kept: for
-  // top-k a value that k keys of one slice reach; for top-p the value at which
-  // n tokens together weigh less than what may be left out.
-  u64 thr = greedy ? sl.value_key(top) : 0;  // copies of the maximum; the lowest index wins the race
-  if (by_k || by_p) {
-    float at = -INFINITY;
-    if (by_k)
-      at = tau;
-    else
-      at = top - temperature * __logf(static_cast<float>(a.n) / (0.99f * (1.f - fmaxf(p, 0.f)) * (static_cast<float>(Z) / sl.scale)));
-    const u64 hi = sl.value_key(top) | ((u64(1) << sl.index_bits) - 1);
-    const u64 lo = at <= top && at > -INFINITY ? sl.value_key(at) : 0;
-    bool fresh = false, cut_k = false;
-    cluster.sync();  // the keys of step 3 have been read: list takes their place
-    if (by_k) {
-      cut_k = select(sl, s, cluster, lo, hi, false, static_cast<u64>(k), 0, fresh);
-      Z = cut_k ? s.z : s.total_m;  // not found: there are no more than k
-      if (cut_k) thr = s.thr;
+  if (want || by_k || by_p) {
+    if (threadIdx.x == 0) {
+      *reinterpret_cast<S*>(s.slice) = sl;
+      s.late = Late{noise, a.out_tokens + r, a.out_logprobs + r, Z, k, p, temperature, floor_w, tau, by_k, by_p};
     }
-    if (by_p) {
-      __syncthreads();  // s.z, s.thr and s.total_m have been read
-      const u64 target = mass_target(p, Z);
-      bool cut_p = select(sl, s, cluster, lo, hi, true, target, 1, fresh);
-      if (!cut_p && lo) {  // the masses' roundings used up what `lo` leaves out
-        fresh = false;
-        cut_p = select(sl, s, cluster, 0, hi, true, target, 1, fresh);
-      }
-      // Still not: Z's rounding asks for more than there is, so everything stays.
-      if (cut_p && s.thr > thr) thr = s.thr;
-    }
+    __syncthreads();
+    late_row<S>(s);
+    return;
   }
 
-  // The race over the kept.
+  // No filter: a race among all.
   Best best{-INFINITY, 0.f, NONE};
   u64 kept = 0;
-  const float floor_l = sl.logit_of(thr);
   for (int v = threadIdx.x; v < sl.nv;) {
     float sum = 0.f;
     for (int i = 0; i < 16 && v < sl.nv; ++i, v += THREADS) {
       float x[VEC];
       sl.load(v, x);
-      const float most = max_of(x, VEC);
-      if (most == -INFINITY || most < floor_l) continue;
+      if (max_of(x, VEC) == -INFINITY) continue;
       const int64_t first = sl.element(v);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        if (x[j] == -INFINITY || (thr && sl.key(x[j], first + j) < thr)) continue;
-        const float w = sl.weight(x[j]), xt = sl.x(x[j]);
-        if (w < floor_w || xt == -INFINITY) continue;
-        if (thr)
-          kept += sl.fixed(w);
-        else
-          sum += w;
-        // NaN noise is never ahead.
-        const float score = greedy ? 0.f : fmaxf(fmaf(lm_log2(noise[first + j]), -LN2, xt), -INFINITY);
+        const float xt = sl.x(x[j]);
+        if (xt == -INFINITY) continue;
+        sum += sl.weight(x[j]);
+        const float score = race(xt, noise[first + j]);
         if (best.index == NONE || score > best.score) best = Best{score, x[j], static_cast<unsigned>(first + j)};
       }
     }
     kept += sl.fixed(sum);
   }
-  kept = block_sum64(kept, s);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    Best o;
-    o.score = __shfl_xor_sync(FULL_MASK, best.score, d);
-    o.logit = __shfl_xor_sync(FULL_MASK, best.logit, d);
-    o.index = __shfl_xor_sync(FULL_MASK, best.index, d);
-    better(best, o);
-  }
-  if (lane == 0) s.best[warp] = best;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < WARPS; ++w) better(best, s.best[w]);
-    Shared* leader = cluster.map_shared_rank(&s, 0);
-    leader->ex_best[rank] = best;
-    leader->ex_kept[rank] = kept;
-  }
-  cluster.sync();
-  if (rank == 0 && threadIdx.x == 0) {
-    for (int i = 1; i < C; ++i) {
-      better(best, s.ex_best[i]);
-      kept += s.ex_kept[i];
-    }
-    // The largest logit is always kept, so an index has been found.
-    a.out_tokens[r] = static_cast<int64_t>(best.index);
-    a.out_logprobs[r] = greedy ? 0.f : sl.x(best.logit) - logf(static_cast<float>(kept) / sl.scale);
-  }
+  finish(sl, s, cluster, best, kept, false, a.out_tokens + r, a.out_logprobs + r);
 }
 
 // CTAs of a row's cluster.  As few as hold its slices in shared memory at two
