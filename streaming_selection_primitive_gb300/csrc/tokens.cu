@@ -19,9 +19,12 @@
 //      min-p, they are all that can be kept: one warp cuts them and runs the
 //      race, which reads the noise of the kept tokens only;
 //   4. otherwise the cuts are found by histograms of counts and masses over
-//      equal ranges of keys, repeated inside the range where the count or the
-//      mass crosses its target until that holds at most LIST keys; then every
-//      CTA races over its kept tokens.
+//      equal ranges of x, then of keys, repeated inside the range where the
+//      count or the mass crosses its target until that holds at most LIST
+//      keys; then every CTA races over its kept tokens.  For top-p a sample of
+//      the row tells above which value the crossing should lie, so that the
+//      histogram touches little else; where it does not, it is made again from
+//      a value that surely is below.
 //
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
@@ -46,6 +49,8 @@ constexpr int TOP = 128;        // keys of a slice that step 2 can sort (the mer
 constexpr int TOP_P = 128;      // and those it sorts for top-p and min-p
 constexpr int CANDIDATES = 1024;
 constexpr int BINS = 1024;      // of one histogram pass
+constexpr int SAMPLE_BINS = 64; // of the sample of a slice: a quarter of a unit of x each
+constexpr int SAMPLE_EVERY = 16;
 constexpr int PER = BINS / THREADS;
 constexpr int LIST = 256;       // keys of a bin that are ranked directly
 constexpr int SLICE_BYTES = 66 << 10;  // of a row in one CTA's shared memory, where the cluster is not at its largest
@@ -90,6 +95,7 @@ struct Shared {
   u64 tops[MAX_CLUSTER][TOP];     // step 3: first keys, and their noise
   float tops_q[MAX_CLUSTER][TOP];
   u64 list[2][LIST];              // step 4
+  unsigned sample[MAX_CLUSTER][SAMPLE_BINS];
   Part part[MAX_CLUSTER];
   Best ex_best[MAX_CLUSTER];
   u64 ex_kept[MAX_CLUSTER];
@@ -102,10 +108,11 @@ struct Shared {
     };
     alignas(16) u64 candidates[CANDIDATES + 2];
   };
+  unsigned own_sample[SAMPLE_BINS];
   u64 sorted[LIST];
   float sorted_q[TOP];
   u64 wc[WARPS], wm[WARPS], red[WARPS];
-  float redf[WARPS];
+  float redf[WARPS], mass[WARPS];
   uint32_t redk[WARPS];
   Best best[WARPS];
   unsigned slot;
@@ -339,31 +346,33 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const 
       if (mh) atomicAdd(&s.hi[b], mh);
     });
     cluster.sync();
-    // This CTA joins its share of the bins, four a thread, and tells everybody.
-    const int C = cluster.num_blocks(), share = BINS / C;
-    for (int b = cluster.block_rank() * share + 4 * threadIdx.x; b < (static_cast<int>(cluster.block_rank()) + 1) * share;
-         b += 4 * THREADS) {
-      uint4 c = make_uint4(0, 0, 0, 0);
-      u64 m[4] = {0, 0, 0, 0};
-#pragma unroll 4
-      for (int i = 0; i < C; ++i) {
-        const Shared* o = cluster.map_shared_rank(&s, i);
-        const uint4 oc = *reinterpret_cast<const uint4*>(o->count + b), ol = *reinterpret_cast<const uint4*>(o->lo + b),
-                    oh = *reinterpret_cast<const uint4*>(o->hi + b);
-        c.x += oc.x;
-        c.y += oc.y;
-        c.z += oc.z;
-        c.w += oc.w;
-        m[0] += (u64(oh.x) << 32) + ol.x;
-        m[1] += (u64(oh.y) << 32) + ol.y;
-        m[2] += (u64(oh.z) << 32) + ol.z;
-        m[3] += (u64(oh.w) << 32) + ol.w;
+    // This CTA joins its share of the bins: of C neighbouring threads each reads
+    // four bins of one CTA, and, when they have added them up, tells one.
+    const int C = cluster.num_blocks(), share = BINS / C, with = threadIdx.x % C;
+    const Shared* from = cluster.map_shared_rank(&s, with);
+    Shared* to = cluster.map_shared_rank(&s, with);
+    for (int base = 0; base < share * C / 4; base += THREADS) {
+      const int b = cluster.block_rank() * share + (base + static_cast<int>(threadIdx.x)) / C * 4;
+      const bool some = base + static_cast<int>(threadIdx.x) < share * C / 4;
+      uint4 c = make_uint4(0, 0, 0, 0), ml = c, mh = c;
+      if (some) {
+        c = *reinterpret_cast<const uint4*>(from->count + b);
+        ml = *reinterpret_cast<const uint4*>(from->lo + b);
+        mh = *reinterpret_cast<const uint4*>(from->hi + b);
       }
-      for (int i = 0; i < C; ++i) {
-        Shared* o = cluster.map_shared_rank(&s, i);
-        *reinterpret_cast<uint4*>(o->merged_c + b) = c;
-        *reinterpret_cast<ulonglong2*>(o->merged_m + b) = make_ulonglong2(m[0], m[1]);
-        *reinterpret_cast<ulonglong2*>(o->merged_m + b + 2) = make_ulonglong2(m[2], m[3]);
+      u64 m[4] = {(u64(mh.x) << 32) + ml.x, (u64(mh.y) << 32) + ml.y, (u64(mh.z) << 32) + ml.z, (u64(mh.w) << 32) + ml.w};
+      for (int d = C >> 1; d; d >>= 1) {
+        c.x += __shfl_xor_sync(FULL_MASK, c.x, d);
+        c.y += __shfl_xor_sync(FULL_MASK, c.y, d);
+        c.z += __shfl_xor_sync(FULL_MASK, c.z, d);
+        c.w += __shfl_xor_sync(FULL_MASK, c.w, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] += __shfl_xor_sync(FULL_MASK, m[j], d);
+      }
+      if (some) {
+        *reinterpret_cast<uint4*>(to->merged_c + b) = c;
+        *reinterpret_cast<ulonglong2*>(to->merged_m + b) = make_ulonglong2(m[0], m[1]);
+        *reinterpret_cast<ulonglong2*>(to->merged_m + b + 2) = make_ulonglong2(m[2], m[3]);
       }
     }
     cluster.sync();
@@ -626,8 +635,61 @@ __device__ __forceinline__ void finish(const S& sl, Shared& s, cg::cluster_group
   }
 }
 
-// 4. The cuts, over everything above a value that surely is not kept: for
-// top-k a value that k keys of one slice reach; for top-p the value at which n
+// The first level of a selection among the logits at or above `floor` (not a
+// number of the row's: from the bottom).
+template <typename S>
+__device__ __forceinline__ Level level_above(const S& sl, float floor) {
+  const bool bounded = floor <= sl.m && floor > -INFINITY;
+  Level lv{};
+  lv.bin0 = -1;
+  lv.floor = bounded ? floor : -FLT_MAX;
+  // The bins end at the floor, and where weights are nothing beside the maximum's.
+  const float reach = bounded ? fminf(-sl.x(floor), 64.f) : 64.f;
+  lv.per_x = BINS / fmaxf(reach, 1e-3f);
+  return lv;
+}
+
+// How far below the maximum (in x) the slices' samples put the point under
+// which `left` of mass lies, with a fifth of room and two elements more.
+template <typename S>
+__device__ __forceinline__ float sample_reach(const S& sl, Shared& s, float left) {
+  static_assert(SAMPLE_BINS == 64, "two bins a lane");
+  const int C = cg::this_cluster().num_blocks();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    float mass[2] = {0.f, 0.f};
+    for (int c = 0; c < C; ++c) {
+      // Bins of a slice count from its own maximum.
+      const int away = static_cast<int>(fminf(-4.f * sl.x(s.part[c].top), SAMPLE_BINS) + 0.5f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * lane + j - away;
+        if (b >= 0) mass[j] += static_cast<float>(s.sample[c][b]);
+      }
+    }
+    float edge[2], tail = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      edge[j] = SAMPLE_EVERY * __expf(-0.25f * (2 * lane + j));  // what one of the bin's elements stands for
+      tail += mass[j] *= edge[j];
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {  // of this lane's bins and those below
+      const float o = __shfl_down_sync(FULL_MASK, tail, d);
+      if (lane + d < 32) tail += o;
+    }
+    unsigned cut = SAMPLE_BINS;
+    if (tail - mass[0] + 2.f * edge[1] <= 0.8f * left) cut = 2 * lane + 1;
+    if (lane > 0 && tail + 2.f * edge[0] <= 0.8f * left) cut = 2 * lane;
+    cut = __reduce_min_sync(FULL_MASK, cut);
+    if (lane == 0) s.slot = cut;
+  }
+  __syncthreads();
+  return 0.25f * static_cast<float>(s.slot);
+}
+
+// 4. The cuts, over everything above a value that is not kept: for top-k one
+// that k keys of one slice reach; for top-p the sample's, or the one at which n
 // tokens together weigh less than what may be left out.  Then the race.  (A
 // function of its own: the registers that it needs would be spilled by rows
 // that never come here, at a microsecond a row.)
@@ -643,14 +705,10 @@ __device__ __noinline__ void late_row(Shared& s) {
   u64 thr = greedy ? sl.value_key(top) : 0;  // copies of the maximum; the lowest index wins the race
   if (late.by_k || late.by_p) {
     const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) / sl.scale);
-    const float floor = late.by_k ? late.tau : top - temperature * __logf(static_cast<float>(sl.n) / (0.99f * left));
-    const bool bounded = floor <= top && floor > -INFINITY;
-    Level lv{};
-    lv.bin0 = -1;
-    lv.floor = bounded ? floor : -FLT_MAX;
-    // The bins end at the floor, and where weights are nothing beside the maximum's.
-    const float reach_x = bounded ? fminf(-sl.x(floor), 64.f) : 64.f;
-    lv.per_x = BINS / fmaxf(reach_x, 1e-3f);
+    const float sure = late.by_k ? late.tau : top - temperature * __logf(static_cast<float>(sl.n) / (0.99f * left));
+    const float likely = late.by_k ? sure : top - temperature * sample_reach(sl, s, left);
+    // From the highest floor to the lowest: the values tried one after another.
+    Level lv = level_above(sl, likely <= top && likely > sure ? likely : sure);
     bool fresh = false;
     for (int turn = late.by_k ? 0 : 1; turn < (late.by_p ? 2 : 1); ++turn) {  // the first k, then their share p
       const u64 target = turn ? mass_target(late.p, Z) : static_cast<u64>(late.k);
@@ -659,7 +717,9 @@ __device__ __noinline__ void late_row(Shared& s) {
         __syncthreads();  // what the turn before left in s has been read
         cut = select(sl, s, cluster, lv, turn == 1, target, turn, fresh);
         if (cut || turn == 0 || lv.floor == -FLT_MAX) break;
-        lv.floor = -FLT_MAX;  // the masses' roundings used up what the floor leaves out
+        // The sample's answer was too high, or roundings used up what the sure
+        // floor leaves out.
+        lv = level_above(sl, lv.floor > sure ? sure : -INFINITY);
         fresh = false;
       }
       // Without a cut: there are no more than k, or Z's rounding asks for more
@@ -724,8 +784,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   const int e = min(62 - sl.index_bits, 44);
   sl.scale = __int_as_float((127 + e) << 23);
 
-  // 1. The slice, and its largest logit (NaN if there is one).
-  float top = -INFINITY;
+  // 1. The slice, its largest logit (NaN if there is one) and, for top-p, its
+  // mass: a thread's sum of exp((l - ref) / T), ref being the largest of its
+  // logits so far.
+  const bool need_mass = by_p && !by_k;
+  if (threadIdx.x < SAMPLE_BINS) s.own_sample[threadIdx.x] = 0u;
+  float top = -INFINITY, mass = 0.f;
   {
     constexpr int AHEAD = 4;  // loads under way a thread
     for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
@@ -754,11 +818,24 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
           else
             sl.keep(u, x);
         }
+        const float before = top;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) top = max_nan(top, x[j]);
+        if (need_mass && top > -INFINITY) {
+          sl.m = top;
+          mass *= sl.weight(before);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
+#pragma unroll
+          for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < d; ++j) x[j] += x[j + d];
+          mass += x[0];
+        }
       }
     }
   }
+  const float ref = top;
   float widest = top;
 #pragma unroll
   for (int d = 16; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
@@ -779,25 +856,22 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   }
   if (reach == 1) tau = widest;
   sl.m = widest;
-
-  // 2. The slice's mass, and its first keys.
-  float mass = 0.f;
-  const bool need_mass = by_p && !by_k;
-  const float* noise = a.noise + r * a.noise_ld;
   if (need_mass) {
-    for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
+    // (A thread without a logit has no mass; nor has a slice, and its maximum is -inf.)
+    mass = warp_sum(mass > 0.f ? mass * sl.weight(ref) : 0.f);
+    if (lane == 0) s.mass[warp] = mass;
+    // One vector in SAMPLE_EVERY, at a place that moves along (and so spreads over the banks).
+    for (int q = threadIdx.x; q < sl.nv / SAMPLE_EVERY; q += THREADS) {
       float x[VEC];
-      sl.load(v, x);
+      sl.load(q * SAMPLE_EVERY + (q & (SAMPLE_EVERY - 1)), x);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
-#pragma unroll
-      for (int d = VEC / 2; d; d >>= 1)
-#pragma unroll
-        for (int j = 0; j < d; ++j) x[j] += x[j + d];
-      mass += x[0];
+      for (int j = 0; j < VEC; ++j)
+        if (x[j] > -INFINITY) atomicAdd(&s.own_sample[static_cast<int>(fminf(-4.f * sl.x(x[j]), SAMPLE_BINS - 1.f))], 1u);
     }
-    mass = warp_sum(mass);
   }
+
+  // 2. The slice's first keys.
+  const float* noise = a.noise + r * a.noise_ld;
   int keys = 0;
   if (want && !isnan(widest)) {
     for (int turn = 0;; ++turn) {
@@ -822,8 +896,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
     }
     if (threadIdx.x == 0 && keys <= CANDIDATES) s.candidates[keys] = 0;
   }
-  __syncthreads();  // redf has been read
-  if (lane == 0) s.redf[warp] = mass;
+  __syncthreads();
   cluster.barrier_wait(std::move(started));
   if (keys > CANDIDATES) {  // copies of one value
     keys = -1;
@@ -842,11 +915,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
         });
     keys = keys < want ? keys : want;
   }
-  __syncthreads();
+  if (need_mass)
+    for (int i = threadIdx.x; i < SAMPLE_BINS * C; i += THREADS)
+      cluster.map_shared_rank(&s, i / SAMPLE_BINS)->sample[rank][i % SAMPLE_BINS] = s.own_sample[i % SAMPLE_BINS];
   if (threadIdx.x < C) {
     mass = 0.f;
     if (need_mass)
-      for (int w = 0; w < WARPS; ++w) mass += s.redf[w];
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) mass += s.mass[w];
     cluster.map_shared_rank(&s, threadIdx.x)->part[rank] = Part{widest, tau, mass, keys};
   }
   cluster.sync();
