@@ -48,10 +48,10 @@ constexpr int MAX_CLUSTER = 8;
 constexpr int TOP = 128;        // keys of a slice that step 2 can sort (the merge searches lists of up to 2^8 - 1)
 constexpr int TOP_P = 128;      // and those it sorts for top-p and min-p
 constexpr int CANDIDATES = 1024;
-constexpr int BINS = 1024;      // of one histogram pass
-constexpr int SAMPLE_BINS = 64; // of the sample of a slice: a quarter of a unit of x each
+constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
+constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
+constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
 constexpr int SAMPLE_EVERY = 16;
-constexpr int PER = BINS / THREADS;
 constexpr int LIST = 256;       // keys of a bin that are ranked directly
 constexpr int SLICE_BYTES = 66 << 10;  // of a row in one CTA's shared memory, where the cluster is not at its largest
 constexpr int SLICE_MOST = 180 << 10;  // and in any case; beyond it the passes read global memory
@@ -99,6 +99,7 @@ struct Shared {
   Part part[MAX_CLUSTER];
   Best ex_best[MAX_CLUSTER];
   u64 ex_kept[MAX_CLUSTER];
+  u64 beyond[MAX_CLUSTER];
   // This CTA's own.
   union {
     struct {
@@ -120,6 +121,7 @@ struct Shared {
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
+  float likely[2];
   Late late;
   alignas(8) unsigned char slice[96];  // the row's Slice
 };
@@ -230,12 +232,14 @@ struct Slice {
       return lm_float(row[element(v) + j]);
   }
 
-  // body(l, i) for every element of the slice at or above floor (finite or
-  // +inf).  A thread first marks those of several vectors and then takes them
-  // one by one, so that the lanes' hits meet in the same turns.
-  template <typename F>
-  __device__ __forceinline__ void above(float floor, F&& body) const {
-    constexpr int GROUP = 32 / VEC;
+  // body(l, i, given(i)) for every element of the slice in [floor, ceil] (floor
+  // finite or +inf).  A thread first marks those of several vectors and then
+  // takes them four by four, so that the lanes' hits meet in the same turns and
+  // what `given` reads for them is under way together.  each(x) sees every
+  // vector that is looked at.
+  template <typename E, typename G, typename F>
+  __device__ __forceinline__ void among(float floor, float ceil, E&& each, G&& given, F&& body) const {
+    constexpr int GROUP = 32 / VEC, BATCH = 4;
     for (int v = threadIdx.x; v < nv; v += GROUP * THREADS) {
       unsigned hits = 0;
 #pragma unroll
@@ -244,17 +248,36 @@ struct Slice {
         if (u >= nv) break;
         float x[VEC];
         load(u, x);
+        each(x);
         if (max_of(x, VEC) < floor) continue;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) hits |= x[j] >= floor ? 1u << (g * VEC + j) : 0u;
+        for (int j = 0; j < VEC; ++j) hits |= x[j] >= floor && x[j] <= ceil ? 1u << (g * VEC + j) : 0u;
       }
       while (hits) {
-        const int b = __ffs(hits) - 1;
-        hits &= hits - 1;
-        const int u = v + b / VEC * THREADS, j = b % VEC;
-        body(one(u, j), element(u) + j);
+        float l[BATCH];
+        int64_t at[BATCH];
+        decltype(given(int64_t(0))) what[BATCH];
+        int some = 0;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          if (hits) {
+            const int b = __ffs(hits) - 1, u = v + b / VEC * THREADS;
+            hits &= hits - 1;
+            at[i] = element(u) + b % VEC;
+            l[i] = one(u, b % VEC);
+            what[i] = given(at[i]);
+            some = i + 1;
+          }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          if (i < some) body(l[i], at[i], what[i]);
       }
     }
+  }
+  template <typename F>
+  __device__ __forceinline__ void among(float floor, float ceil, F&& body) const {
+    among(floor, ceil, [](const float (&)[VEC]) {}, [](int64_t) { return 0; },
+          [&](float l, int64_t i, int) { body(l, i); });
   }
 
   __device__ __forceinline__ void keep(int v, const float (&x)[VEC]) const {
@@ -302,23 +325,35 @@ __device__ __forceinline__ u64 block_sum64(u64 v, Shared& s) {
   return r;
 }
 
-// What a histogram is made of: first, all elements at or above `floor` in equal
-// ranges of x from the maximum down (the last takes what is beyond); then
-// those of the first one's bin `bin0` with keys in [lo, hi], in equal ranges of
-// keys from hi down.
+// What a histogram is made of: first, the elements with logits in [floor,
+// ceil], in equal ranges of x from ceil down (the last takes what is beyond);
+// then those of the first one's bin `bin0` with keys in [lo, hi], in equal
+// ranges of keys from hi down.
 struct Level {
-  float floor;
-  float per_x;  // bins per unit of x of the first
-  int bin0;     // -1: the first
+  float floor, ceil;
+  float x0, per_x;  // -x of ceil; bins per unit of x of the first
+  int bin0;         // -1: the first
   u64 lo, hi;
   int shift;
 
   template <typename S>
   __device__ __forceinline__ int bin_of(const S& sl, float l, int64_t i) const {
-    const int b = static_cast<int>(fminf(-sl.x(l) * per_x, BINS - 1.f));
+    const int b = static_cast<int>(fmaxf(fminf((-sl.x(l) - x0) * per_x, BINS - 1.f), 0.f));
     if (bin0 < 0) return b;
     const u64 key = sl.key(l, i);
     return b != bin0 || key < lo || key > hi ? -1 : static_cast<int>((hi - key) >> shift);
+  }
+  // A value at or above all of a bin of the first, and one at or below (x's
+  // roundings blur its edges by far less than half a bin).
+  template <typename S>
+  __device__ __forceinline__ float high(const S& sl, int bin) const {
+    const float v = sl.m - (x0 + (bin - 0.5f) / per_x) / sl.inv;
+    return bin > 0 && v <= ceil ? v : ceil;
+  }
+  template <typename S>
+  __device__ __forceinline__ float low(const S& sl, int bin) const {
+    const float v = sl.m - (x0 + (bin + 1.5f) / per_x) / sl.inv;
+    return bin + 1 < BINS && v >= floor ? v : floor;
   }
   __device__ __forceinline__ void fit() {
     shift = 0;
@@ -328,23 +363,40 @@ struct Level {
 
 // The histogram, joined over the cluster, and the bin where the running count
 // (or mass) from the top first reaches `target`: s.bin, s.above_*, s.in_c;
-// s.bin = BINS where it does not.  fresh: the joined histogram is in place.
+// s.bin = BINS where it does not.  What lies above the first level's ceil
+// counts as above (its mass only).  fresh: the joined histogram is in place.
 template <typename S>
-__device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const Level& lv, bool by_mass, u64 target,
-                      bool fresh) {
+__device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const Level& lv, bool by_mass,
+                                      u64 target, bool fresh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool over = lv.bin0 < 0 && lv.ceil < sl.m;
   if (!fresh) {
     for (int b = threadIdx.x; b < BINS; b += THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0u;
     __syncthreads();
-    sl.above(lv.floor, [&](float l, int64_t i) {
-      const int b = lv.bin_of(sl, l, i);
-      if (b < 0) return;
-      const u64 mass = sl.fixed(sl.weight(l));
-      atomicAdd(&s.count[b], 1u);
-      const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
-      const unsigned mh = static_cast<unsigned>(mass >> 32) + (old + ml < old ? 1u : 0u);
-      if (mh) atomicAdd(&s.hi[b], mh);
-    });
+    u64 beyond = 0;
+    sl.among(
+        lv.floor, lv.ceil,
+        [&](const float (&x)[S::VEC]) {
+          if (!over) return;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < S::VEC; ++j) sum += x[j] > lv.ceil ? sl.weight(x[j]) : 0.f;
+          beyond += sl.fixed(sum);
+        },
+        [](int64_t) { return 0; },
+        [&](float l, int64_t i, int) {
+          const int b = lv.bin_of(sl, l, i);
+          if (b < 0) return;
+          const u64 mass = sl.fixed(sl.weight(l));
+          atomicAdd(&s.count[b], 1u);
+          const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
+          const unsigned mh = static_cast<unsigned>(mass >> 32) + (old + ml < old ? 1u : 0u);
+          if (mh) atomicAdd(&s.hi[b], mh);
+        });
+    if (over) {
+      beyond = block_sum64(beyond, s);
+      if (threadIdx.x < cluster.num_blocks()) cluster.map_shared_rank(&s, threadIdx.x)->beyond[cluster.block_rank()] = beyond;
+    }
     cluster.sync();
     // This CTA joins its share of the bins: of C neighbouring threads each reads
     // four bins of one CTA, and, when they have added them up, tells one.
@@ -377,15 +429,13 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const 
     }
     cluster.sync();
   }
-  // Thread t takes bins PER t and on.
-  const int first = PER * threadIdx.x;
-  u64 tc = 0, tm = 0;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    tc += s.merged_c[first + j];
-    tm += s.merged_m[first + j];
-  }
-  u64 ic = tc, im = tm;
+  u64 base = 0;
+  if (over)
+    for (int i = 0; i < static_cast<int>(cluster.num_blocks()); ++i) base += s.beyond[i];
+  // Thread t takes bin t.
+  const bool mine = threadIdx.x < BINS;
+  const u64 nc = mine ? s.merged_c[threadIdx.x] : 0, nm = mine ? s.merged_m[threadIdx.x] : 0;
+  u64 ic = nc, im = nm;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const u64 oc = __shfl_up_sync(FULL_MASK, ic, d), om = __shfl_up_sync(FULL_MASK, im, d);
@@ -400,24 +450,18 @@ __device__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const 
   }
   if (threadIdx.x == 0) s.bin = BINS;
   __syncthreads();
-  u64 bc = ic - tc, bm = im - tm;
+  u64 bc = ic - nc, bm = base + im - nm;
   for (int w = 0; w < warp; ++w) {
     bc += s.wc[w];
     bm += s.wm[w];
   }
-  if (threadIdx.x == THREADS - 1) s.total_m = bm + tm;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const u64 nc = s.merged_c[first + j], nm = s.merged_m[first + j];
-    const u64 before = by_mass ? bm : bc, with = before + (by_mass ? nm : nc);
-    if (before < target && target <= with) {
-      s.bin = static_cast<unsigned>(first + j);
-      s.above_c = bc;
-      s.above_m = bm;
-      s.in_c = nc;
-    }
-    bc += nc;
-    bm += nm;
+  if (threadIdx.x == BINS - 1) s.total_m = bm + nm;
+  const u64 before = by_mass ? bm : bc, with = before + (by_mass ? nm : nc);
+  if (before < target && target <= with) {
+    s.bin = threadIdx.x;
+    s.above_c = bc;
+    s.above_m = bm;
+    s.in_c = nc;
   }
   __syncthreads();
 }
@@ -439,20 +483,19 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
     above_m += s.above_m;
     const u64 in_c = s.in_c;
     const int bin = static_cast<int>(s.bin);
-    // A value below the bin's (x's roundings blur it by far less than half a bin).
-    const float T = 1.f / sl.inv, low = sl.m - T * ((bin + 1.5f) / lv.per_x);
     if (in_c > LIST) {
       if (lv.bin0 < 0) {
-        const float top = sl.m - T * ((bin - 0.5f) / lv.per_x);
+        const float high = lv.high(sl, bin), low = lv.low(sl, bin);
         lv.bin0 = bin;
-        lv.hi = sl.value_key(bin > 0 && top <= sl.m && top > -INFINITY ? top : sl.m) | ((u64(1) << sl.index_bits) - 1);
-        lv.lo = bin + 1 < BINS && low <= sl.m && low > -INFINITY ? sl.value_key(low) : 0;
+        lv.hi = sl.value_key(high) | ((u64(1) << sl.index_bits) - 1);
+        lv.lo = sl.value_key(low);
+        lv.floor = low;
+        lv.ceil = high;
       } else {
         lv.hi -= u64(bin) << lv.shift;
         const u64 width = (u64(1) << lv.shift) - 1;
         if (lv.hi - lv.lo > width) lv.lo = lv.hi - width;
       }
-      if (lv.lo) lv.floor = fmaxf(lv.floor, sl.logit_of(lv.lo));
       lv.fit();
       __syncthreads();  // s.bin and the rest have been read
       continue;
@@ -464,9 +507,9 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
     for (int i = 0; i < rank; ++i) base += cluster.map_shared_rank(&s, i)->count[bin];
     if (threadIdx.x == 0) s.slot = base;
     __syncthreads();
-    const float floor = lv.bin0 < 0 && bin + 1 < BINS && low <= sl.m ? fmaxf(lv.floor, low) : lv.floor;
+    const float floor = lv.bin0 < 0 ? lv.low(sl, bin) : lv.floor, ceil = lv.bin0 < 0 ? lv.high(sl, bin) : lv.ceil;
     if (s.count[bin] != 0u)
-      sl.above(floor, [&](float l, int64_t i) {
+      sl.among(floor, ceil, [&](float l, int64_t i) {
         if (lv.bin_of(sl, l, i) != bin) return;
         const unsigned at = atomicAdd(&s.slot, 1u);
         if (at < LIST)
@@ -635,57 +678,90 @@ __device__ __forceinline__ void finish(const S& sl, Shared& s, cg::cluster_group
   }
 }
 
-// The first level of a selection among the logits at or above `floor` (not a
-// number of the row's: from the bottom).
+// The first level of a selection among the logits in [floor, ceil] (a floor
+// that is no number of the row's: from the bottom).
 template <typename S>
-__device__ __forceinline__ Level level_above(const S& sl, float floor) {
-  const bool bounded = floor <= sl.m && floor > -INFINITY;
+__device__ __forceinline__ Level level_between(const S& sl, float floor, float ceil) {
+  const bool bounded = floor <= ceil && floor > -INFINITY;
   Level lv{};
   lv.bin0 = -1;
   lv.floor = bounded ? floor : -FLT_MAX;
+  lv.ceil = ceil;
+  lv.x0 = -sl.x(ceil);
   // The bins end at the floor, and where weights are nothing beside the maximum's.
   const float reach = bounded ? fminf(-sl.x(floor), 64.f) : 64.f;
-  lv.per_x = BINS / fmaxf(reach, 1e-3f);
+  lv.per_x = BINS / fmaxf(reach - lv.x0, 1e-4f);
   return lv;
 }
 
-// How far below the maximum (in x) the slices' samples put the point under
-// which `left` of mass lies, with a fifth of room and two elements more.
+// Where (in x below the maximum) the slices' samples put the point under which
+// `left` of mass lies: s.likely[0] surely further than that, and, where the
+// tokens above are many, s.likely[1] surely nearer (else 0).  Surely: by four
+// standard deviations of the sample's sum below the point.
 template <typename S>
-__device__ __forceinline__ float sample_reach(const S& sl, Shared& s, float left) {
-  static_assert(SAMPLE_BINS == 64, "two bins a lane");
+__device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left) {
+  constexpr int EACH = SAMPLE_BINS / 32;
   const int C = cg::this_cluster().num_blocks();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    float mass[2] = {0.f, 0.f};
+    float count[EACH] = {};
     for (int c = 0; c < C; ++c) {
       // Bins of a slice count from its own maximum.
-      const int away = static_cast<int>(fminf(-4.f * sl.x(s.part[c].top), SAMPLE_BINS) + 0.5f);
+      const int away = static_cast<int>(fminf(-SAMPLE_SCALE * sl.x(s.part[c].top), SAMPLE_BINS) + 0.5f);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = 2 * lane + j - away;
-        if (b >= 0) mass[j] += static_cast<float>(s.sample[c][b]);
+      for (int j = 0; j < EACH; ++j) {
+        const int b = EACH * lane + j - away;
+        if (b >= 0) count[j] += static_cast<float>(s.sample[c][b]);
       }
     }
-    float edge[2], tail = 0.f;
+    // Mass and its variance, of a lane's bins and all below; tokens, of those above.
+    float weight[EACH], mass[EACH], tail = 0.f, var = 0.f, tokens = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      edge[j] = SAMPLE_EVERY * __expf(-0.25f * (2 * lane + j));  // what one of the bin's elements stands for
-      tail += mass[j] *= edge[j];
+    for (int j = 0; j < EACH; ++j) {
+      weight[j] = SAMPLE_EVERY * __expf(-(EACH * lane + j + 0.5f) / SAMPLE_SCALE);
+      mass[j] = count[j] * weight[j];
+      tail += mass[j];
+      var += mass[j] * weight[j];
+      tokens += count[j];
     }
+    const float own_tail = tail, own_var = var, own_tokens = tokens;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {  // of this lane's bins and those below
-      const float o = __shfl_down_sync(FULL_MASK, tail, d);
-      if (lane + d < 32) tail += o;
+    for (int d = 1; d < 32; d <<= 1) {
+      const float ot = __shfl_down_sync(FULL_MASK, tail, d), ov = __shfl_down_sync(FULL_MASK, var, d),
+                  on = __shfl_up_sync(FULL_MASK, tokens, d);
+      if (lane + d < 32) {
+        tail += ot;
+        var += ov;
+      }
+      if (lane >= d) tokens += on;
     }
-    unsigned cut = SAMPLE_BINS;
-    if (tail - mass[0] + 2.f * edge[1] <= 0.8f * left) cut = 2 * lane + 1;
-    if (lane > 0 && tail + 2.f * edge[0] <= 0.8f * left) cut = 2 * lane;
-    cut = __reduce_min_sync(FULL_MASK, cut);
-    if (lane == 0) s.slot = cut;
+    tail -= own_tail;  // below the lane's bins
+    var -= own_var;
+    tokens -= own_tokens;
+    // The bin inside which the tail reaches `left`: the lane's last first.
+    float far = -1.f, near = 0.f;
+#pragma unroll
+    for (int j = EACH - 1; j >= 0; --j) {
+      if (tail <= left && left < tail + mass[j]) {
+        const float point = (EACH * lane + j + 1 - (left - tail) / mass[j]) / SAMPLE_SCALE;
+        const float blur = 0.02f + 4.f * sqrtf(var + weight[j] * mass[j]) / (mass[j] * SAMPLE_SCALE);
+        far = point + blur;
+        float above = tokens;
+#pragma unroll
+        for (int i = 0; i < j; ++i) above += count[i];
+        near = above * SAMPLE_EVERY > 4096.f ? fmaxf(point - blur, 0.f) : 0.f;
+      }
+      tail += mass[j];
+      var += mass[j] * weight[j];
+    }
+    const unsigned which = __ballot_sync(FULL_MASK, far >= 0.f);
+    if (which == 0u) far = INFINITY;  // the sample has no answer
+    if (which == 0u ? lane == 0 : lane == __ffs(which) - 1) {
+      s.likely[0] = far;
+      s.likely[1] = near;
+    }
   }
   __syncthreads();
-  return 0.25f * static_cast<float>(s.slot);
 }
 
 // 4. The cuts, over everything above a value that is not kept: for top-k one
@@ -706,9 +782,11 @@ __device__ __noinline__ void late_row(Shared& s) {
   if (late.by_k || late.by_p) {
     const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) / sl.scale);
     const float sure = late.by_k ? late.tau : top - temperature * __logf(static_cast<float>(sl.n) / (0.99f * left));
-    const float likely = late.by_k ? sure : top - temperature * sample_reach(sl, s, left);
-    // From the highest floor to the lowest: the values tried one after another.
-    Level lv = level_above(sl, likely <= top && likely > sure ? likely : sure);
+    if (!late.by_k) sample_point(sl, s, left);
+    const float far = late.by_k ? sure : top - temperature * s.likely[0];
+    const float ceil = late.by_k || s.likely[1] <= 0.f ? top : top - temperature * s.likely[1];
+    // From the narrowest range to the widest, tried one after another.
+    Level lv = far <= top && far > sure ? level_between(sl, far, ceil) : level_between(sl, sure, top);
     bool fresh = false;
     for (int turn = late.by_k ? 0 : 1; turn < (late.by_p ? 2 : 1); ++turn) {  // the first k, then their share p
       const u64 target = turn ? mass_target(late.p, Z) : static_cast<u64>(late.k);
@@ -717,9 +795,9 @@ __device__ __noinline__ void late_row(Shared& s) {
         __syncthreads();  // what the turn before left in s has been read
         cut = select(sl, s, cluster, lv, turn == 1, target, turn, fresh);
         if (cut || turn == 0 || lv.floor == -FLT_MAX) break;
-        // The sample's answer was too high, or roundings used up what the sure
-        // floor leaves out.
-        lv = level_above(sl, lv.floor > sure ? sure : -INFINITY);
+        // The sample's answer was wrong, or roundings used up what the sure floor
+        // leaves out.
+        lv = level_between(sl, lv.floor > sure ? sure : -INFINITY, top);
         fresh = false;
       }
       // Without a cut: there are no more than k, or Z's rounding asks for more
@@ -735,12 +813,14 @@ __device__ __noinline__ void late_row(Shared& s) {
   Best best{-INFINITY, 0.f, NONE};
   u64 kept = 0;
   const float* noise = late.noise;
-  sl.above(floor, [&](float l, int64_t i) {
-    const float w = sl.weight(l), x = sl.x(l);
-    if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
-    kept += sl.fixed(w);
-    better(best, Best{greedy ? 0.f : race(x, noise[i]), l, static_cast<unsigned>(i)});
-  });
+  sl.among(
+      floor, INFINITY, [](const float (&)[S::VEC]) {}, [&](int64_t i) { return greedy ? 1.f : noise[i]; },
+      [&](float l, int64_t i, float q) {
+        const float w = sl.weight(l), x = sl.x(l);
+        if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
+        kept += sl.fixed(w);
+        better(best, Best{greedy ? 0.f : race(x, q), l, static_cast<unsigned>(i)});
+      });
   finish(sl, s, cluster, best, kept, greedy, late.token, late.logprob);
 }
 
@@ -783,6 +863,17 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   sl.index_bits = 32 - __clz(static_cast<int>(a.n - 1));
   const int e = min(62 - sl.index_bits, 44);
   sl.scale = __int_as_float((127 + e) << 23);
+
+  if (!want && !by_k && !by_p) {
+    // Every token's noise will be read: L2 fetches it meanwhile.
+    const int64_t first = max(sl.element(0), int64_t(0)), last = min(sl.element(sl.nv), a.n);
+    const uintptr_t from = (reinterpret_cast<uintptr_t>(a.noise + r * a.noise_ld + first) + 15) & ~uintptr_t(15),
+                    to = reinterpret_cast<uintptr_t>(a.noise + r * a.noise_ld + last) & ~uintptr_t(15);
+    constexpr unsigned PIECE = 4096;
+    for (uintptr_t at = from + threadIdx.x * PIECE; at < to; at += THREADS * PIECE)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at),
+                   "r"(static_cast<unsigned>(to - at < PIECE ? to - at : PIECE)) : "memory");
+  }
 
   // 1. The slice, its largest logit (NaN if there is one) and, for top-p, its
   // mass: a thread's sum of exp((l - ref) / T), ref being the largest of its
@@ -866,7 +957,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
       sl.load(q * SAMPLE_EVERY + (q & (SAMPLE_EVERY - 1)), x);
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (x[j] > -INFINITY) atomicAdd(&s.own_sample[static_cast<int>(fminf(-4.f * sl.x(x[j]), SAMPLE_BINS - 1.f))], 1u);
+        if (x[j] > -INFINITY)
+          atomicAdd(&s.own_sample[static_cast<int>(fminf(-SAMPLE_SCALE * sl.x(x[j]), SAMPLE_BINS - 1.f))], 1u);
     }
   }
 
@@ -875,7 +967,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   int keys = 0;
   if (want && !isnan(widest)) {
     for (int turn = 0;; ++turn) {
-      sl.above(fmaxf(tau, -FLT_MAX), [&](float l, int64_t i) {
+      sl.among(fmaxf(tau, -FLT_MAX), INFINITY, [&](float l, int64_t i) {
         const unsigned at = atomicAdd(&s.slot, 1u);
         if (at < CANDIDATES) s.candidates[at] = sl.key(l, i);
       });
@@ -1048,20 +1140,44 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   // No filter: a race among all.
   Best best{-INFINITY, 0.f, NONE};
   u64 kept = 0;
-  for (int v = threadIdx.x; v < sl.nv;) {
+  constexpr int AHEAD = 16 / VEC;
+  const bool vec = reinterpret_cast<uintptr_t>(noise + sl.element(0)) % 16 == 0;
+  for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
+    float q[AHEAD][VEC];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int u = v + i * THREADS;
+      if (u >= sl.nv) break;
+      const int64_t first = sl.element(u);
+      if (vec && sl.inside(u)) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+          const float4 f = __ldcs(reinterpret_cast<const float4*>(noise + first + j));
+          q[i][j] = f.x;
+          q[i][j + 1] = f.y;
+          q[i][j + 2] = f.z;
+          q[i][j + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) q[i][j] = first + j >= 0 && first + j < a.n ? noise[first + j] : 1.f;
+      }
+    }
     float sum = 0.f;
-    for (int i = 0; i < 16 && v < sl.nv; ++i, v += THREADS) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int u = v + i * THREADS;
+      if (u >= sl.nv) break;
       float x[VEC];
-      sl.load(v, x);
-      if (max_of(x, VEC) == -INFINITY) continue;
-      const int64_t first = sl.element(v);
+      sl.load(u, x);
+      const unsigned first = static_cast<unsigned>(sl.element(u));
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float xt = sl.x(x[j]);
-        if (xt == -INFINITY) continue;
-        sum += sl.weight(x[j]);
-        const float score = race(xt, noise[first + j]);
-        if (best.index == NONE || score > best.score) best = Best{score, x[j], static_cast<unsigned>(first + j)};
+        sum += lm_exp2(xt * LOG2E);
+        const float score = race(xt, q[i][j]);
+        // (-inf: a token that cannot be kept, or one that noise of +inf puts last.)
+        if (score > best.score || (best.index == NONE && xt > -INFINITY)) best = Best{score, x[j], first + j};
       }
     }
     kept += sl.fixed(sum);
