@@ -97,6 +97,7 @@ struct Shared {
   u64 list[2][LIST];              // step 4
   unsigned sample[MAX_CLUSTER][SAMPLE_BINS];
   Part part[MAX_CLUSTER];
+  int enough;
   Best ex_best[MAX_CLUSTER];
   u64 ex_kept[MAX_CLUSTER];
   u64 beyond[MAX_CLUSTER];
@@ -107,7 +108,10 @@ struct Shared {
       alignas(16) unsigned lo[BINS];  // 64-bit masses in two words
       alignas(16) unsigned hi[BINS];
     };
-    alignas(16) u64 candidates[CANDIDATES + 2];
+    struct {
+      alignas(16) u64 candidates[CANDIDATES + 2];
+      float candidates_q[CANDIDATES];
+    };
   };
   unsigned own_sample[SAMPLE_BINS];
   u64 sorted[LIST];
@@ -116,8 +120,7 @@ struct Shared {
   float redf[WARPS], mass[WARPS];
   uint32_t redk[WARPS];
   Best best[WARPS];
-  unsigned slot;
-  int enough;
+  unsigned slot, merged;
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
@@ -374,6 +377,8 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
     for (int b = threadIdx.x; b < BINS; b += THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0u;
     __syncthreads();
     u64 beyond = 0;
+    float partial = 0.f;
+    int vectors = 0;
     sl.among(
         lv.floor, lv.ceil,
         [&](const float (&x)[S::VEC]) {
@@ -381,7 +386,11 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
           float sum = 0.f;
 #pragma unroll
           for (int j = 0; j < S::VEC; ++j) sum += x[j] > lv.ceil ? sl.weight(x[j]) : 0.f;
-          beyond += sl.fixed(sum);
+          partial += sum;
+          if (++vectors % 16 == 0) {
+            beyond += sl.fixed(partial);
+            partial = 0.f;
+          }
         },
         [](int64_t) { return 0; },
         [&](float l, int64_t i, int) {
@@ -394,7 +403,7 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
           if (mh) atomicAdd(&s.hi[b], mh);
         });
     if (over) {
-      beyond = block_sum64(beyond, s);
+      beyond = block_sum64(beyond + sl.fixed(partial), s);
       if (threadIdx.x < cluster.num_blocks()) cluster.map_shared_rank(&s, threadIdx.x)->beyond[cluster.block_rank()] = beyond;
     }
     cluster.sync();
@@ -608,7 +617,7 @@ __device__ __forceinline__ float block_tau(float top, float widest, int want, Sh
 // body(i, rank) for every candidate, rank being the number of larger ones (they
 // are distinct); each is ranked by as many neighbouring threads as there are
 // to spare, up to 8, and the first of them calls body.  begin(i) runs before
-// the ranking and returns what body gets as well.  Called by the whole block;
+// the ranking (with whether there is an i) and returns what body gets as well.  Called by the whole block;
 // an odd number of candidates is followed by a 0.
 template <typename B, typename F>
 __device__ __forceinline__ void rank_candidates(const Shared& s, int keys, B&& begin, F&& body) {
@@ -618,7 +627,7 @@ __device__ __forceinline__ void rank_candidates(const Shared& s, int keys, B&& b
   for (int base = 0; base < keys; base += THREADS / split) {
     const int i = base + threadIdx.x / split;
     const u64 mine = i < keys ? s.candidates[i] : ~u64(0);
-    const auto what = begin(i < keys && sub == 0, mine);
+    const auto what = begin(i < keys && sub == 0, i, mine);
     int above = 0;
 #pragma unroll 4
     for (int j = 2 * sub; j < keys; j += 2 * split) {
@@ -835,7 +844,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = blockIdx.x / C;
   auto started = cluster.barrier_arrive();  // waited for before the first write to another CTA
-  if (threadIdx.x == 0) s.slot = 0;
+  if (threadIdx.x == 0) s.slot = s.merged = 0;
   pdl_wait();
   pdl_trigger();
   const float temperature = a.temperature ? a.temperature[r] : a.all_temperature;
@@ -881,49 +890,62 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   const bool need_mass = by_p && !by_k;
   if (threadIdx.x < SAMPLE_BINS) s.own_sample[threadIdx.x] = 0u;
   float top = -INFINITY, mass = 0.f;
-  {
-    constexpr int AHEAD = 4;  // loads under way a thread
-    for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
-      uint4 bits[AHEAD];
-      bool in[AHEAD];
+  auto take = [&](float (&x)[VEC]) {
+    const float before = top;
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const int u = v + i * THREADS;
-        in[i] = u < sl.nv && sl.inside(u);
-        if (in[i]) bits[i] = sl.raw(u);
-      }
+    for (int j = 0; j < VEC; ++j) top = max_nan(top, x[j]);
+    if (need_mass && top > -INFINITY) {
+      sl.m = top;
+      mass *= sl.weight(before);
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const int u = v + i * THREADS;
-        if (u >= sl.nv) break;
-        float x[VEC];
-        if (in[i]) {
-          sl.unpack(bits[i], x);
-          if (sl.mask) sl.hide(sl.element(u), x);
+      for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
+#pragma unroll
+      for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < d; ++j) x[j] += x[j + d];
+      mass += x[0];
+    }
+  };
+  if constexpr (RESIDENT) {
+    // The whole slice is on its way at once, in four groups of copies; a thread
+    // reads what it copied itself.
+    const int group = ((sl.nv + THREADS - 1) / THREADS + 3) / 4 * THREADS;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      for (int v = g * group + threadIdx.x; v < min((g + 1) * group, sl.nv); v += THREADS) {
+        if (sl.inside(v)) {
+          const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(sl.store + v));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(sl.row + sl.element(v)) : "memory");
         } else {
-          sl.fetch(u, x);
-        }
-        if constexpr (RESIDENT) {
-          if (in[i] && !sl.mask)
-            sl.store[u] = bits[i];
-          else
-            sl.keep(u, x);
-        }
-        const float before = top;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) top = max_nan(top, x[j]);
-        if (need_mass && top > -INFINITY) {
-          sl.m = top;
-          mass *= sl.weight(before);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
-#pragma unroll
-          for (int d = VEC / 2; d; d >>= 1)
-#pragma unroll
-            for (int j = 0; j < d; ++j) x[j] += x[j + d];
-          mass += x[0];
+          float x[VEC];
+          sl.fetch(v, x);
+          sl.keep(v, x);
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+      if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      for (int v = g * group + threadIdx.x; v < min((g + 1) * group, sl.nv); v += THREADS) {
+        float x[VEC];
+        sl.load(v, x);
+        if (sl.mask && sl.inside(v)) {
+          sl.hide(sl.element(v), x);
+          sl.keep(v, x);
+        }
+        take(x);
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
+      float x[VEC];
+      sl.fetch(v, x);
+      take(x);
     }
   }
   const float ref = top;
@@ -977,7 +999,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
       // Too many (neighbours are alike, so that a thread holds several):
       // again from the want-th largest of those that were stored.
       rank_candidates(
-          s, CANDIDATES, [](bool, u64) { return 0; },
+          s, CANDIDATES, [](bool, int, u64) { return 0; },
           [&](u64 key, int rank, int) {
             if (rank == want - 1) s.thr = key;
           });
@@ -993,17 +1015,15 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   if (keys > CANDIDATES) {  // copies of one value
     keys = -1;
   } else if (keys > 0) {
-    // The first `want`, with their noise, go to every CTA that looks at them.
-    const int readers = by_k || greedy ? 1 : C;
+    // The first `want`, with their noise, go to the cluster's first CTA.
+    Shared* leader = cluster.map_shared_rank(&s, 0);
     rank_candidates(
-        s, keys, [&](bool some, u64 key) { return some && !greedy ? noise[sl.index_of(key)] : 1.f; },
+        s, keys, [&](bool some, int, u64 key) { return some && !greedy ? noise[sl.index_of(key)] : 1.f; },
         [&](u64 key, int place, float q) {
-          if (place < want)
-            for (int c = 0; c < readers; ++c) {
-              Shared* o = cluster.map_shared_rank(&s, c);
-              o->tops[rank][place] = key;
-              o->tops_q[rank][place] = q;
-            }
+          if (place < want) {
+            leader->tops[rank][place] = key;
+            leader->tops_q[rank][place] = q;
+          }
         });
     keys = keys < want ? keys : want;
   }
@@ -1043,12 +1063,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   const float floor_w = fminf(min_p, 1.f);
   if (want && found >= 0) {
     const bool decide = !by_k && !greedy;  // whether these keys are enough is not known beforehand
-    if (rank != 0 && !decide) return;
-    // Merge: a key's place is the number of larger ones in each of the sorted lists.
-    const int got = found < want ? found : want;
-    // (The lists' shares of `want` reach the least of them, so no key below it counts.)
+    if (rank != 0) {
+      if (!decide) return;
+      cluster.sync();  // the first CTA has written `enough`
+    } else {
+    // Merge.  (The lists' shares of `want` reach the least of them, so no key
+    // below it counts.)
+    const int got = found < want ? found : want, each = (want + C - 1) / C;
     u64 least = ~u64(0);
-    const int each = (want + C - 1) / C;
     for (int c = 0; c < C; ++c) {
       const u64 key = s.part[c].keys >= each ? s.tops[c][each - 1] : 0;
       least = key < least ? key : least;
@@ -1056,28 +1078,22 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
     for (int i = threadIdx.x; i < C * TOP; i += THREADS) {
       const int c = i / TOP, j = i % TOP;
       if (j >= s.part[c].keys || s.tops[c][j] < least) continue;
-      const u64 mine = s.tops[c][j];
-      int place = j;
-      for (int first = 0; first < C; first += 4) {
-        // Four lists at a time, so that their searches overlap.
-        int at[4] = {0, 0, 0, 0}, len[4];
-#pragma unroll
-        for (int o = 0; o < 4; ++o) len[o] = first + o < C && first + o != c ? s.part[first + o].keys : 0;
-#pragma unroll
-        for (int bit = 7; bit >= 0; --bit)
-#pragma unroll
-          for (int o = 0; o < 4; ++o) {
-            const int to = at[o] + (1 << bit);
-            const u64 key = s.tops[(first + o) & (MAX_CLUSTER - 1)][to <= len[o] ? to - 1 : 0];
-            at[o] = to <= len[o] && key > mine ? to : at[o];
-          }
-        place += at[0] + at[1] + at[2] + at[3];
-      }
-      if (place < want) {
-        s.sorted[place] = mine;
-        s.sorted_q[place] = s.tops_q[c][j];
-      }
+      const unsigned at = atomicAdd(&s.merged, 1u);
+      s.candidates[at] = s.tops[c][j];
+      s.candidates_q[at] = s.tops_q[c][j];
     }
+    __syncthreads();
+    const int merged = static_cast<int>(s.merged);
+    if (threadIdx.x == 0) s.candidates[merged] = 0;
+    __syncthreads();
+    rank_candidates(
+        s, merged, [&](bool some, int i, u64) { return some ? s.candidates_q[i] : 1.f; },
+        [&](u64 key, int place, float q) {
+          if (place < want) {
+            s.sorted[place] = key;
+            s.sorted_q[place] = q;
+          }
+        });
     __syncthreads();
     if (warp == 0) {
       constexpr int EACH = TOP / 32;
@@ -1104,8 +1120,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
       // Enough: the list holds everything, or reaches the mass, or falls below min-p.
       const float last = got ? sl.weight(sl.logit_of(s.sorted[got - 1])) : 0.f;
       const bool enough = !decide || found < want || (by_p && total >= target) || last < floor_w;
-      if (lane == 0) s.enough = enough;
-      if (enough && rank == 0) {
+      if (decide && lane < C) cluster.map_shared_rank(&s, lane)->enough = enough;
+      if (enough) {
         u64 kept = 0;
         Best best{-INFINITY, 0.f, NONE};
 #pragma unroll
@@ -1123,7 +1139,9 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
         if (lane == 0) write_row(sl, best, kept, greedy, a.out_tokens + r, a.out_logprobs + r);
       }
     }
-    __syncthreads();
+    if (!decide) return;
+    cluster.sync();
+    }
     if (s.enough) return;
   }
 
