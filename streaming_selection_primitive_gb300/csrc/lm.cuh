@@ -37,7 +37,14 @@ __device__ __forceinline__ float lm_exp2(float x) {
   return y;
 }
 
-// 1 / x by the hardware's approximation (one ulp), for x >= 1.
+__device__ __forceinline__ float lm_sqrt(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / x by the hardware's approximation (one ulp; x or results below the
+// normal range count as zero).  An exact division is 120 instructions.
 __device__ __forceinline__ float lm_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

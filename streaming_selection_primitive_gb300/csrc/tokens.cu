@@ -8,28 +8,32 @@
 // probability w_i / sum kept w (the least of independent exponential times of
 // rates w_i); its log-probability is x_i - log sum kept w.
 //
-// A cluster of CTAs takes a row.  Each CTA reads its slice once, into shared
-// memory where it fits, and works there:
-//   1. its maximum, and for top-p its mass, both relative to its own maximum;
-//   2. the first keys of its slice, sorted: of the threads' maxima a value is
-//      taken that at least that many of them reach, and only what lies at or
-//      above it is ranked;
-//   3. the CTAs exchange these (one cluster barrier), and the row's first keys
-//      are known.  For top-k up to TOP, and for most rows under top-p and
-//      min-p, they are all that can be kept: one warp cuts them and runs the
-//      race, which reads the noise of the kept tokens only;
+// One CTA takes a row, or a cluster of up to 8 where there are few rows (then
+// each takes a slice); rows that need step 4 are left to a second launch, with
+// clusters of 8, unless the first one has these:
+//   1. one read of the slice gives its maximum and, for top-p, its mass.
+//      What is needed of the slice again comes from the caches;
+//   2. its first keys, sorted: of the threads' maxima a value is taken that at
+//      least that many of them reach, and only what lies at or above it is
+//      ranked.  For top-p a sample of the row tells how many should do;
+//   3. a cluster's CTAs send theirs to the first, which merges them.  For top-k
+//      up to TOP, and for most rows under top-p and min-p, they are all that can
+//      be kept: one warp cuts them and runs the race, which reads the noise of
+//      these tokens only;
 //   4. otherwise the cuts are found by histograms of counts and masses over
 //      equal ranges of x, then of keys, repeated inside the range where the
 //      count or the mass crosses its target until that holds at most LIST
-//      keys; then every CTA races over its kept tokens.  For top-p a sample of
-//      the row tells above which value the crossing should lie, so that the
+//      keys; then every CTA races over its kept tokens.  For top-p the sample
+//      tells between which values the crossing should lie, so that the
 //      histogram touches little else; where it does not, it is made again from
 //      a value that surely is below.
 //
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
 // the same whatever order the atomics take.
+#include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -45,17 +49,16 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int TOP = 128;        // keys of a slice that step 2 can sort (the merge searches lists of up to 2^8 - 1)
-constexpr int TOP_P = 128;      // and those it sorts for top-p and min-p
+constexpr int TOP = 256;        // keys that step 2 can sort in a CTA that has the row to itself (half its threads),
+constexpr int TOP_SHARED = 128; // and in a cluster's
+constexpr int TOP_MIN_P = 64;   // and those that min-p seldom leaves more of
 constexpr int CANDIDATES = 1024;
 constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
-constexpr int SAMPLE_EVERY = 16;
-constexpr int LIST = 256;       // keys of a bin that are ranked directly
-constexpr int SLICE_BYTES = 66 << 10;  // of a row in one CTA's shared memory, where the cluster is not at its largest
-constexpr int SLICE_MOST = 180 << 10;  // and in any case; beyond it the passes read global memory
-constexpr int SLICE_LEAST = 8 << 10;
+constexpr int SECOND = 76, SECOND_CTAS = 4;  // clusters of the second launch (two CTAs an SM)
+constexpr int LIST = 128;       // keys of a bin that are ranked directly
+constexpr int SLICE_LEAST = 4 << 10;   // bytes of a row that are worth a CTA of a cluster
 using u64 = unsigned long long;
 
 // The race's state: the best score, its logit and index (NONE: none yet).
@@ -69,12 +72,16 @@ __device__ __forceinline__ void better(Best& a, const Best& b) {
   if (b.index != NONE && (a.index == NONE || b.score > a.score || (b.score == a.score && b.index < a.index))) a = b;
 }
 
-// What a CTA tells the others after step 2.
+// What a CTA tells the others after step 1 (for top-p),
 struct Part {
-  float top;     // the slice's maximum (NaN if it holds one)
-  float tau;     // as many of its keys as were asked for reach this value
-  float mass;    // sum of exp((l - top) / T), for top-p
-  int keys;      // sorted keys sent; -1: too many candidates to rank
+  float top;   // the slice's maximum (NaN if it holds one)
+  float mass;  // sum of exp((l - top) / T)
+};
+// and after step 2.
+struct Sent {
+  float top;
+  float tau;  // as many of its keys as were asked for reach this value
+  int keys;   // sorted keys sent; -1: too many candidates to rank
 };
 
 // What late_row gets.
@@ -90,41 +97,46 @@ struct Late {
 
 struct Shared {
   // Written by other CTAs of the cluster.
-  alignas(16) unsigned merged_c[BINS];
-  alignas(16) u64 merged_m[BINS];
-  u64 tops[MAX_CLUSTER][TOP];     // step 3: first keys, and their noise
-  float tops_q[MAX_CLUSTER][TOP];
-  u64 list[2][LIST];              // step 4
+  union {
+    struct {  // step 3: first keys, and their noise
+      u64 tops[MAX_CLUSTER][TOP_SHARED];
+      float tops_q[MAX_CLUSTER][TOP_SHARED];
+    };
+    struct {  // step 4
+      alignas(16) unsigned merged_c[BINS];
+      alignas(16) u64 merged_m[BINS];
+      alignas(16) u64 list[2][LIST + 2];
+    };
+  };
   unsigned sample[MAX_CLUSTER][SAMPLE_BINS];
   Part part[MAX_CLUSTER];
+  Sent sent[MAX_CLUSTER];
   int enough;
   Best ex_best[MAX_CLUSTER];
   u64 ex_kept[MAX_CLUSTER];
   u64 beyond[MAX_CLUSTER];
   // This CTA's own.
-  union {
-    struct {
-      alignas(16) unsigned count[BINS];
-      alignas(16) unsigned lo[BINS];  // 64-bit masses in two words
-      alignas(16) unsigned hi[BINS];
-    };
-    struct {
-      alignas(16) u64 candidates[CANDIDATES + 2];
-      float candidates_q[CANDIDATES];
-    };
-  };
+  alignas(16) unsigned count[BINS];
+  alignas(16) unsigned lo[BINS];  // 64-bit masses in two words
+  alignas(16) unsigned hi[BINS];
+  alignas(16) u64 candidates[CANDIDATES + 2];
+  float candidates_q[CANDIDATES];
   unsigned own_sample[SAMPLE_BINS];
-  u64 sorted[LIST];
+  alignas(16) float row_sample[SAMPLE_BINS];
+  u64 sorted[TOP];  // of step 3's list, or step 4's
   float sorted_q[TOP];
   u64 wc[WARPS], wm[WARPS], red[WARPS];
   float redf[WARPS], mass[WARPS];
   uint32_t redk[WARPS];
   Best best[WARPS];
-  unsigned slot, merged;
+  unsigned slot, merged, hits, marks[WARPS];
+  unsigned captured;  // keys that the first level found, in `candidates` unless there are more than fit
+  unsigned short hit[THREADS];
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
-  float likely[2];
+  float likely[3];
+  uint4 edge[2];
   Late late;
   alignas(8) unsigned char slice[96];  // the row's Slice
 };
@@ -141,6 +153,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Room for n entries of each lane of a list with the given length, which it
+// moves on: the lane's first place.  One atomic a warp (a thousand of them on
+// one word take microseconds); the whole warp calls it.
+__device__ __forceinline__ unsigned warp_reserve(unsigned* length, int n) {
+  const int lane = threadIdx.x & 31;
+  int with = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(FULL_MASK, with, d);
+    if (lane >= d) with += o;
+  }
+  unsigned base = 0;
+  if (lane == 31 && with) base = atomicAdd(length, static_cast<unsigned>(with));
+  return __shfl_sync(FULL_MASK, base, 31) + with - n;
+}
+
 // log2 of a positive number by the hardware's approximation; zero gives -inf.
 __device__ __forceinline__ float lm_log2(float x) {
   float y;
@@ -148,46 +176,67 @@ __device__ __forceinline__ float lm_log2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float max_of(const float* x, int n) {
-  float top = x[0];
-#pragma unroll
-  for (int j = 1; j < n; ++j) top = fmaxf(top, x[j]);
-  return top;
+// The same for numbers of the normal range (below it: -inf).
+__device__ __forceinline__ float lm_log2_normal(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // One row as a CTA of its cluster sees it.  Positions are counted from the
 // 16-byte boundary at or before the row (`phase` elements before it); a
-// vector is the VEC positions from a boundary.
-template <typename T, bool RESIDENT>
+// vector is the VEC positions from a boundary.  (Everything that reads a vector
+// goes through load, and what happens at a row's ends is kept out of it: these
+// kernels run most of their code once, so that its length is time.)
+template <typename T>
 struct Slice {
   static constexpr int VEC = 16 / int(sizeof(T));
   const T* row;
   const uint32_t* mask;
-  uint4* store;  // the slice's vectors in shared memory (RESIDENT)
+  const uint4* edge;  // shared memory: the row's first and last vector where they are not whole
   int64_t n;     // of the row
   int64_t v0;    // first vector
   int nv;        // vectors
   int phase;
-  float m, inv, inv2, scale;  // the maximum, 1 / T, log2(e) / T, the masses' unit
-  int index_bits;
+  float m, T_, inv, inv2;   // the maximum, T, 1 / T, log2(e) / T
+  float scale, unit;        // the masses' scale, and its inverse
+  int index_bits, sample_shift;  // one vector in 2^sample_shift is sampled
 
   // First element of a vector of the slice (may be outside the row).
   __device__ __forceinline__ int64_t element(int v) const { return (v0 + v) * VEC - phase; }
 
-  // Bit j: element i + j of the row is allowed (VEC bits; i + VEC <= n).
-  __device__ __forceinline__ unsigned allowed(int64_t i) const {
-    const int at = static_cast<int>(i & 31);
-    const uint32_t* w = mask + (i >> 5);
-    const uint32_t hi = at + VEC > 32 ? w[1] : 0u;
-    return __funnelshift_r(w[0], hi, at);
-  }
+  __device__ __forceinline__ bool is_allowed(int64_t i) const { return !mask || (mask[i >> 5] >> (i & 31) & 1u); }
 
   __device__ __forceinline__ bool inside(int v) const {
     const int64_t i = element(v);
     return i >= 0 && i + VEC <= n;
   }
 
-  __device__ __forceinline__ uint4 raw(int v) const { return __ldg(reinterpret_cast<const uint4*>(row + element(v))); }
+  // Elements that are not allowed become -inf, in the packed vector.
+  __device__ __forceinline__ uint4 hide(int64_t i, uint4 bits) const {
+    const int at = static_cast<int>(i & 31);
+    const uint32_t* w = mask + (i >> 5);
+    const uint32_t ok = __funnelshift_r(w[0], at + VEC > 32 ? w[1] : 0u, at);
+    unsigned* b = &bits.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        b[j] = ok >> j & 1u ? b[j] : 0xff800000u;
+      } else {
+        constexpr unsigned low = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+        const unsigned keep = (ok >> 2 * j & 1u) * 0xffffu | (ok >> (2 * j + 1) & 1u) * 0xffff0000u;
+        b[j] = (b[j] & keep) | (low * 0x10001u & ~keep);
+      }
+    }
+    return bits;
+  }
+
+  // A vector that lies inside the row.
+  __device__ __forceinline__ uint4 whole(int v) const {
+    const int64_t i = element(v);
+    const uint4 bits = __ldg(reinterpret_cast<const uint4*>(row + i));
+    return mask ? hide(i, bits) : bits;
+  }
 
   __device__ __forceinline__ void unpack(uint4 bits, float (&x)[VEC]) const {
     union {
@@ -199,104 +248,79 @@ struct Slice {
     for (int j = 0; j < VEC; ++j) x[j] = lm_float(u.t[j]);
   }
 
-  __device__ __forceinline__ void hide(int64_t i, float (&x)[VEC]) const {
-    const unsigned ok = allowed(i);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) x[j] = ok >> j & 1u ? x[j] : -INFINITY;
-  }
-
-  // A vector from global memory; elements outside the row or not allowed are -inf.
-  __device__ __forceinline__ void fetch(int v, float (&x)[VEC]) const {
-    const int64_t i = element(v);
-    if (inside(v)) {
-      unpack(raw(v), x);
-      if (mask) hide(i, x);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int64_t e = i + j;
-        x[j] = e >= 0 && e < n && (!mask || (mask[e >> 5] >> (e & 31) & 1u)) ? lm_float(row[e]) : -INFINITY;
-      }
-    }
-  }
-
+  // Any vector; elements outside the row or not allowed are -inf.
   __device__ __forceinline__ void load(int v, float (&x)[VEC]) const {
-    if constexpr (RESIDENT)
-      unpack(store[v], x);
-    else
-      fetch(v, x);
+    unpack(inside(v) ? whole(v) : edge[element(v) < 0 ? 0 : 1], x);
   }
 
   // Element j of a vector (inside the row, allowed).
-  __device__ __forceinline__ float one(int v, int j) const {
-    if constexpr (RESIDENT)
-      return lm_float(reinterpret_cast<const T*>(store + v)[j]);
-    else
-      return lm_float(row[element(v) + j]);
-  }
+  __device__ __forceinline__ float one(int v, int j) const { return lm_float(row[element(v) + j]); }
 
-  // body(l, i, given(i)) for every element of the slice in [floor, ceil] (floor
-  // finite or +inf).  A thread first marks those of several vectors and then
-  // takes them four by four, so that the lanes' hits meet in the same turns and
-  // what `given` reads for them is under way together.  each(x) sees every
-  // vector that is looked at.
-  template <typename E, typename G, typename F>
-  __device__ __forceinline__ void among(float floor, float ceil, E&& each, G&& given, F&& body) const {
-    constexpr int GROUP = 32 / VEC, BATCH = 4;
-    for (int v = threadIdx.x; v < nv; v += GROUP * THREADS) {
+  // body(l, i, given(i), place) for every element of the slice in [floor, ceil]
+  // (floor finite or +inf).  A lane first marks those of several vectors and
+  // then takes BATCH of them at a time, so that the lanes' hits meet in the same
+  // turns and what `given` reads for them is under way together.  each(x) sees every
+  // vector that is looked at.  place: the element's own in a list of the given
+  // length (null: none is kept).
+  template <int BATCH, typename E, typename G, typename F>
+  __device__ __forceinline__ void among(float floor, float ceil, unsigned* length, E&& each, G&& given, F&& body) const {
+    constexpr int GROUP = 32 / VEC;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int base = threadIdx.x - lane; base < nv; base += GROUP * THREADS) {
       unsigned hits = 0;
-#pragma unroll
+#pragma unroll 2
       for (int g = 0; g < GROUP; ++g) {
-        const int u = v + g * THREADS;
-        if (u >= nv) break;
-        float x[VEC];
-        load(u, x);
-        each(x);
-        if (max_of(x, VEC) < floor) continue;
+        const int u = base + lane + g * THREADS;
+        if (u < nv) {
+          float x[VEC];
+          load(u, x);
+          each(x);
+          unsigned some = 0;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) hits |= x[j] >= floor && x[j] <= ceil ? 1u << (g * VEC + j) : 0u;
+          for (int j = 0; j < VEC; ++j) some |= x[j] >= floor && x[j] <= ceil ? 1u << j : 0u;
+          hits |= some << (g * VEC);
+        }
       }
-      while (hits) {
+#pragma unroll 1
+      while (__any_sync(FULL_MASK, hits != 0u)) {
         float l[BATCH];
         int64_t at[BATCH];
         decltype(given(int64_t(0))) what[BATCH];
-        int some = 0;
+        const int some = min(__popc(hits), BATCH);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
-          if (hits) {
-            const int b = __ffs(hits) - 1, u = v + b / VEC * THREADS;
+          if (i < some) {
+            const int b = __ffs(hits) - 1, u = base + lane + b / VEC * THREADS;
             hits &= hits - 1;
             at[i] = element(u) + b % VEC;
             l[i] = one(u, b % VEC);
             what[i] = given(at[i]);
-            some = i + 1;
           }
+        const unsigned place = length ? warp_reserve(length, some) : 0u;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
-          if (i < some) body(l[i], at[i], what[i]);
+          if (i < some) body(l[i], at[i], what[i], place + i);
+        __syncwarp();
       }
     }
-  }
-  template <typename F>
-  __device__ __forceinline__ void among(float floor, float ceil, F&& body) const {
-    among(floor, ceil, [](const float (&)[VEC]) {}, [](int64_t) { return 0; },
-          [&](float l, int64_t i, int) { body(l, i); });
-  }
-
-  __device__ __forceinline__ void keep(int v, const float (&x)[VEC]) const {
-    union {
-      uint4 bits;
-      T t[VEC];
-    } u;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) u.t[j] = lm_cast<T>(x[j]);  // exact: they came from T
-    store[v] = u.bits;
   }
 
   // (l - m) / T: a NaN (an infinite maximum less itself, 0 times an infinite
   // 1 / T) is the maximum's own, 0.
   __device__ __forceinline__ float x(float l) const { return fminf((l - m) * inv, 0.f); }
   __device__ __forceinline__ float weight(float l) const { return lm_exp2(fminf((l - m) * inv2, 0.f)); }
+  // Sum of a vector's weights.
+  __device__ __forceinline__ float weights(const float (&x)[VEC]) const {
+    float w[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = weight(x[j]);
+#pragma unroll
+    for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < d; ++j) w[j] += w[j + d];
+    return w[0];
+  }
   __device__ __forceinline__ u64 fixed(float w) const { return __float2ull_rn(w * scale); }
 
   // Keys: the order key of the logit (16-bit types: its upper half) above the
@@ -328,13 +352,30 @@ __device__ __forceinline__ u64 block_sum64(u64 v, Shared& s) {
   return r;
 }
 
+// Sum of the values of the threads before this one.
+__device__ __forceinline__ u64 block_before64(u64 v, u64 (&sums)[WARPS]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 with = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 o = __shfl_up_sync(FULL_MASK, with, d);
+    if (lane >= d) with += o;
+  }
+  if (lane == 31) sums[warp] = with;
+  __syncthreads();
+  u64 before = with - v;
+#pragma unroll 1
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  return before;
+}
+
 // What a histogram is made of: first, the elements with logits in [floor,
 // ceil], in equal ranges of x from ceil down (the last takes what is beyond);
 // then those of the first one's bin `bin0` with keys in [lo, hi], in equal
 // ranges of keys from hi down.
 struct Level {
   float floor, ceil;
-  float x0, per_x;  // -x of ceil; bins per unit of x of the first
+  float x0, per_x, x_per;  // -x of ceil; bins of the first per unit of x, and the inverse
   int bin0;         // -1: the first
   u64 lo, hi;
   int shift;
@@ -350,16 +391,17 @@ struct Level {
   // roundings blur its edges by far less than half a bin).
   template <typename S>
   __device__ __forceinline__ float high(const S& sl, int bin) const {
-    const float v = sl.m - (x0 + (bin - 0.5f) / per_x) / sl.inv;
+    const float v = sl.m - (x0 + (bin - 0.5f) * x_per) * sl.T_;
     return bin > 0 && v <= ceil ? v : ceil;
   }
   template <typename S>
   __device__ __forceinline__ float low(const S& sl, int bin) const {
-    const float v = sl.m - (x0 + (bin + 1.5f) / per_x) / sl.inv;
+    const float v = sl.m - (x0 + (bin + 1.5f) * x_per) * sl.T_;
     return bin + 1 < BINS && v >= floor ? v : floor;
   }
   __device__ __forceinline__ void fit() {
     shift = 0;
+#pragma unroll 1
     while (((hi - lo) >> shift) >= BINS) ++shift;
   }
 };
@@ -371,16 +413,17 @@ struct Level {
 template <typename S>
 __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const Level& lv, bool by_mass,
                                       u64 target, bool fresh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool over = lv.bin0 < 0 && lv.ceil < sl.m;
+  const bool over = lv.bin0 < 0 && lv.ceil < sl.m, capture = lv.bin0 < 0;
   if (!fresh) {
+#pragma unroll 1
     for (int b = threadIdx.x; b < BINS; b += THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0u;
+    if (capture && threadIdx.x == 0) s.captured = 0;
     __syncthreads();
     u64 beyond = 0;
     float partial = 0.f;
     int vectors = 0;
-    sl.among(
-        lv.floor, lv.ceil,
+    sl.template among<1>(
+        lv.floor, lv.ceil, capture ? &s.captured : nullptr,
         [&](const float (&x)[S::VEC]) {
           if (!over) return;
           float sum = 0.f;
@@ -393,9 +436,10 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
           }
         },
         [](int64_t) { return 0; },
-        [&](float l, int64_t i, int) {
+        [&](float l, int64_t i, int, unsigned place) {
           const int b = lv.bin_of(sl, l, i);
           if (b < 0) return;
+          if (capture && place < CANDIDATES) s.candidates[place] = sl.key(l, i);
           const u64 mass = sl.fixed(sl.weight(l));
           atomicAdd(&s.count[b], 1u);
           const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
@@ -409,12 +453,13 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
     cluster.sync();
     // This CTA joins its share of the bins: of C neighbouring threads each reads
     // four bins of one CTA, and, when they have added them up, tells one.
-    const int C = cluster.num_blocks(), share = BINS / C, with = threadIdx.x % C;
+    const int C = cluster.num_blocks(), log_c = __ffs(C) - 1, share = BINS >> log_c, with = threadIdx.x & (C - 1);
     const Shared* from = cluster.map_shared_rank(&s, with);
     Shared* to = cluster.map_shared_rank(&s, with);
-    for (int base = 0; base < share * C / 4; base += THREADS) {
-      const int b = cluster.block_rank() * share + (base + static_cast<int>(threadIdx.x)) / C * 4;
-      const bool some = base + static_cast<int>(threadIdx.x) < share * C / 4;
+#pragma unroll 1
+    for (int base = 0; base < BINS / 4; base += THREADS) {
+      const int b = cluster.block_rank() * share + ((base + static_cast<int>(threadIdx.x)) >> log_c) * 4;
+      const bool some = base + static_cast<int>(threadIdx.x) < BINS / 4;
       uint4 c = make_uint4(0, 0, 0, 0), ml = c, mh = c;
       if (some) {
         c = *reinterpret_cast<const uint4*>(from->count + b);
@@ -422,6 +467,7 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
         mh = *reinterpret_cast<const uint4*>(from->hi + b);
       }
       u64 m[4] = {(u64(mh.x) << 32) + ml.x, (u64(mh.y) << 32) + ml.y, (u64(mh.z) << 32) + ml.z, (u64(mh.w) << 32) + ml.w};
+#pragma unroll 1
       for (int d = C >> 1; d; d >>= 1) {
         c.x += __shfl_xor_sync(FULL_MASK, c.x, d);
         c.y += __shfl_xor_sync(FULL_MASK, c.y, d);
@@ -440,30 +486,13 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
   }
   u64 base = 0;
   if (over)
+#pragma unroll 1
     for (int i = 0; i < static_cast<int>(cluster.num_blocks()); ++i) base += s.beyond[i];
   // Thread t takes bin t.
   const bool mine = threadIdx.x < BINS;
   const u64 nc = mine ? s.merged_c[threadIdx.x] : 0, nm = mine ? s.merged_m[threadIdx.x] : 0;
-  u64 ic = nc, im = nm;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const u64 oc = __shfl_up_sync(FULL_MASK, ic, d), om = __shfl_up_sync(FULL_MASK, im, d);
-    if (lane >= d) {
-      ic += oc;
-      im += om;
-    }
-  }
-  if (lane == 31) {
-    s.wc[warp] = ic;
-    s.wm[warp] = im;
-  }
   if (threadIdx.x == 0) s.bin = BINS;
-  __syncthreads();
-  u64 bc = ic - nc, bm = base + im - nm;
-  for (int w = 0; w < warp; ++w) {
-    bc += s.wc[w];
-    bm += s.wm[w];
-  }
+  const u64 bc = block_before64(nc, s.wc), bm = base + block_before64(nm, s.wm);
   if (threadIdx.x == BINS - 1) s.total_m = bm + nm;
   const u64 before = by_mass ? bm : bc, with = before + (by_mass ? nm : nc);
   if (before < target && target <= with) {
@@ -482,8 +511,8 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
 template <typename S>
 __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level lv, bool by_mass, u64 target, int which,
                        bool& fresh) {
-  const int lane = threadIdx.x & 31;
   u64 above_c = 0, above_m = 0;
+#pragma unroll 1
   for (int level = 0;; ++level) {
     cross(sl, s, cluster, lv, by_mass, target - (by_mass ? above_m : above_c), fresh && level == 0);
     fresh = level == 0;
@@ -513,53 +542,59 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
     // of the CTAs before it.
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
     unsigned base = 0;
+#pragma unroll 1
     for (int i = 0; i < rank; ++i) base += cluster.map_shared_rank(&s, i)->count[bin];
     if (threadIdx.x == 0) s.slot = base;
     __syncthreads();
     const float floor = lv.bin0 < 0 ? lv.low(sl, bin) : lv.floor, ceil = lv.bin0 < 0 ? lv.high(sl, bin) : lv.ceil;
-    if (s.count[bin] != 0u)
-      sl.among(floor, ceil, [&](float l, int64_t i) {
-        if (lv.bin_of(sl, l, i) != bin) return;
-        const unsigned at = atomicAdd(&s.slot, 1u);
-        if (at < LIST)
-          for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->list[which][at] = sl.key(l, i);
-      });
-    cluster.sync();
-    // Rank of each key: two threads count the larger ones of half the list each.
-    const int m = static_cast<int>(in_c), item = threadIdx.x >> 1;
-    const u64* list = s.list[which];
-    const u64 mine = item < m ? list[item] : 0;
-    int above = 0;
-    for (int i = threadIdx.x & 1; i < m; i += 2) above += list[i] > mine;
-    above += __shfl_xor_sync(FULL_MASK, above, 1);
-    if (item < m && !(threadIdx.x & 1)) s.sorted[above] = mine;
-    __syncthreads();
-    if (threadIdx.x < 32) {  // one warp adds the masses up in that order
-      constexpr int EACH = LIST / 32;
-      u64 mass[EACH], sum = 0;
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        const int at = lane * EACH + j;
-        mass[j] = at < m ? sl.fixed(sl.weight(sl.logit_of(s.sorted[at]))) : 0;
-        sum += mass[j];
-      }
-      u64 before = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const u64 o = __shfl_up_sync(FULL_MASK, before, d);
-        if (lane >= d) before += o;
-      }
-      before = above_m + before - sum;
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        const int at = lane * EACH + j;
-        const u64 b = by_mass ? before : above_c + at, w = b + (by_mass ? mass[j] : 1);
-        if (at < m && b < target && target <= w) {
-          s.thr = s.sorted[at];
-          s.z = before + mass[j];
+    auto send = [&](u64 key) {
+      const unsigned at = atomicAdd(&s.slot, 1u);
+      if (at < LIST)
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->list[which][at] = key;
+    };
+    if (s.count[bin] != 0u) {
+      if (s.captured <= CANDIDATES) {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < static_cast<int>(s.captured); i += THREADS) {
+          const u64 key = s.candidates[i];
+          if (lv.bin_of(sl, sl.logit_of(key), sl.index_of(key)) == bin) send(key);
         }
-        before += mass[j];
+      } else {
+        sl.template among<1>(
+            floor, ceil, nullptr, [](const float (&)[S::VEC]) {}, [](int64_t) { return 0; },
+            [&](float l, int64_t i, int, unsigned) {
+              if (lv.bin_of(sl, l, i) == bin) send(sl.key(l, i));
+            });
       }
+    }
+    cluster.sync();
+    // Rank of each key: the number of larger ones.  (Two at a time: an odd number
+    // is followed by a 0.)
+    const int m = static_cast<int>(in_c);
+    u64* list = s.list[which];
+    static_assert(LIST <= THREADS, "a key a thread");
+    if (threadIdx.x == 0) list[m] = 0;
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < m) {
+      const u64 mine = list[threadIdx.x];
+      int above = 0;
+#pragma unroll 2
+      for (int i = 0; i < m; i += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + i);
+        above += (o.x > mine) + (o.y > mine);
+      }
+      s.sorted[above] = mine;
+    }
+    __syncthreads();
+    // The masses before each, in that order.
+    const int at = threadIdx.x;
+    const u64 mass = at < m ? sl.fixed(sl.weight(sl.logit_of(s.sorted[at]))) : 0;
+    const u64 before = above_m + block_before64(mass, s.wm);
+    const u64 b = by_mass ? before : above_c + at, w = b + (by_mass ? mass : 1);
+    if (at < m && b < target && target <= w) {
+      s.thr = s.sorted[at];
+      s.z = before + mass;
     }
     __syncthreads();
     return true;
@@ -601,6 +636,7 @@ __device__ __forceinline__ float block_tau(float top, float widest, int want, Sh
   uint32_t lo = s.redk[0], hi = choice_key(widest) + 1u;
 #pragma unroll
   for (int w = 1; w < WARPS; ++w) lo = min(lo, s.redk[w]);
+#pragma unroll 1
   while (hi - lo > 1u && count > want + want / 8 + 4) {
     const uint32_t mid = lo + (hi - lo) / 2;
     const int c = __syncthreads_count(key >= mid);
@@ -621,19 +657,22 @@ __device__ __forceinline__ float block_tau(float top, float widest, int want, Sh
 // an odd number of candidates is followed by a 0.
 template <typename B, typename F>
 __device__ __forceinline__ void rank_candidates(const Shared& s, int keys, B&& begin, F&& body) {
-  int split = 1;
-  while (split < 8 && keys * split * 2 <= THREADS) split *= 2;
-  const int sub = threadIdx.x & (split - 1);
-  for (int base = 0; base < keys; base += THREADS / split) {
-    const int i = base + threadIdx.x / split;
+  int log_split = 0;
+#pragma unroll 1
+  while (log_split < 3 && keys << (log_split + 1) <= THREADS) ++log_split;
+  const int split = 1 << log_split, sub = threadIdx.x & (split - 1);
+#pragma unroll 1
+  for (int base = 0; base < keys; base += THREADS >> log_split) {
+    const int i = base + (threadIdx.x >> log_split);
     const u64 mine = i < keys ? s.candidates[i] : ~u64(0);
     const auto what = begin(i < keys && sub == 0, i, mine);
     int above = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int j = 2 * sub; j < keys; j += 2 * split) {
       const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s.candidates + j);
       above += (o.x > mine) + (o.y > mine);
     }
+#pragma unroll 1
     for (int d = split >> 1; d; d >>= 1) above += __shfl_xor_sync(FULL_MASK, above, d);
     if (i < keys && sub == 0) body(mine, above, what);
   }
@@ -659,7 +698,7 @@ __device__ __forceinline__ void write_row(const S& sl, const Best& best, u64 kep
                                           float* logprob) {
   // The largest logit is always kept, so an index has been found.
   *token = static_cast<int64_t>(best.index);
-  *logprob = greedy ? 0.f : sl.x(best.logit) - logf(static_cast<float>(kept) / sl.scale);
+  *logprob = greedy ? 0.f : sl.x(best.logit) - logf(static_cast<float>(kept) * sl.unit);
 }
 
 // Joins the race over the threads and CTAs and writes the row's answer.
@@ -672,6 +711,7 @@ __device__ __forceinline__ void finish(const S& sl, Shared& s, cg::cluster_group
   if ((threadIdx.x & 31) == 0) s.best[threadIdx.x >> 5] = best;
   __syncthreads();
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int w = 1; w < WARPS; ++w) better(best, s.best[w]);
     Shared* leader = cluster.map_shared_rank(&s, 0);
     leader->ex_best[rank] = best;
@@ -679,6 +719,7 @@ __device__ __forceinline__ void finish(const S& sl, Shared& s, cg::cluster_group
   }
   cluster.sync();
   if (rank == 0 && threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 1; i < static_cast<int>(cluster.num_blocks()); ++i) {
       better(best, s.ex_best[i]);
       kept += s.ex_kept[i];
@@ -699,35 +740,43 @@ __device__ __forceinline__ Level level_between(const S& sl, float floor, float c
   lv.x0 = -sl.x(ceil);
   // The bins end at the floor, and where weights are nothing beside the maximum's.
   const float reach = bounded ? fminf(-sl.x(floor), 64.f) : 64.f;
-  lv.per_x = BINS / fmaxf(reach - lv.x0, 1e-4f);
+  lv.x_per = fmaxf(reach - lv.x0, 1e-4f) * (1.f / BINS);
+  lv.per_x = lm_rcp(lv.x_per);
   return lv;
 }
 
 // Where (in x below the maximum) the slices' samples put the point under which
 // `left` of mass lies: s.likely[0] surely further than that, and, where the
-// tokens above are many, s.likely[1] surely nearer (else 0).  Surely: by four
-// standard deviations of the sample's sum below the point.
+// tokens above are many, s.likely[1] surely nearer (else 0); s.likely[2] the
+// number of tokens above.  Surely: by four standard deviations of the sample's
+// sum below the point.
 template <typename S>
 __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left) {
+  const float every = static_cast<float>(1 << sl.sample_shift);
   constexpr int EACH = SAMPLE_BINS / 32;
   const int C = cg::this_cluster().num_blocks();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    float count[EACH] = {};
+  if (threadIdx.x < SAMPLE_BINS) {
+    unsigned sum = 0;
+#pragma unroll 1
     for (int c = 0; c < C; ++c) {
       // Bins of a slice count from its own maximum.
-      const int away = static_cast<int>(fminf(-SAMPLE_SCALE * sl.x(s.part[c].top), SAMPLE_BINS) + 0.5f);
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        const int b = EACH * lane + j - away;
-        if (b >= 0) count[j] += static_cast<float>(s.sample[c][b]);
-      }
+      const int b = static_cast<int>(threadIdx.x) -
+                    static_cast<int>(fminf(-SAMPLE_SCALE * sl.x(s.part[c].top), SAMPLE_BINS) + 0.5f);
+      if (b >= 0) sum += s.sample[c][b];
     }
+    s.row_sample[threadIdx.x] = static_cast<float>(sum);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const float4 four = reinterpret_cast<const float4*>(s.row_sample)[lane];
+    static_assert(EACH == 4, "four bins a lane");
+    const float count[EACH] = {four.x, four.y, four.z, four.w};
     // Mass and its variance, of a lane's bins and all below; tokens, of those above.
     float weight[EACH], mass[EACH], tail = 0.f, var = 0.f, tokens = 0.f;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-      weight[j] = SAMPLE_EVERY * __expf(-(EACH * lane + j + 0.5f) / SAMPLE_SCALE);
+      weight[j] = every * __expf(-(EACH * lane + j + 0.5f) / SAMPLE_SCALE);
       mass[j] = count[j] * weight[j];
       tail += mass[j];
       var += mass[j] * weight[j];
@@ -748,17 +797,18 @@ __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left)
     var -= own_var;
     tokens -= own_tokens;
     // The bin inside which the tail reaches `left`: the lane's last first.
-    float far = -1.f, near = 0.f;
+    float far = -1.f, near = 0.f, above = 0.f;
 #pragma unroll
     for (int j = EACH - 1; j >= 0; --j) {
       if (tail <= left && left < tail + mass[j]) {
-        const float point = (EACH * lane + j + 1 - (left - tail) / mass[j]) / SAMPLE_SCALE;
-        const float blur = 0.02f + 4.f * sqrtf(var + weight[j] * mass[j]) / (mass[j] * SAMPLE_SCALE);
+        const float point = (EACH * lane + j + 1 - __fdividef(left - tail, mass[j])) / SAMPLE_SCALE;
+        const float blur = 0.02f + __fdividef(4.f * lm_sqrt(var + weight[j] * mass[j]), mass[j] * SAMPLE_SCALE);
         far = point + blur;
-        float above = tokens;
+        above = tokens;
 #pragma unroll
         for (int i = 0; i < j; ++i) above += count[i];
-        near = above * SAMPLE_EVERY > 4096.f ? fmaxf(point - blur, 0.f) : 0.f;
+        above *= every;
+        near = above > 4096.f ? fmaxf(point - blur, 0.f) : 0.f;
       }
       tail += mass[j];
       var += mass[j] * weight[j];
@@ -768,9 +818,107 @@ __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left)
     if (which == 0u ? lane == 0 : lane == __ffs(which) - 1) {
       s.likely[0] = far;
       s.likely[1] = near;
+      s.likely[2] = above;
     }
   }
   __syncthreads();
+}
+
+// The race where most tokens take part: every vector of the slice beside its
+// noise.  CUT: only keys from thr up and weights from floor_w up.  Scores are
+// in units of log 2; a vector's best is looked for where it beats the thread's.
+template <bool CUT, typename S>
+__device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 thr, float floor_w, Best& best, u64& kept) {
+  constexpr int VEC = S::VEC;
+  const bool vec = reinterpret_cast<uintptr_t>(noise + sl.element(0)) % 16 == 0;
+  // Kept: above the cut's logit, or its copies up to the cut's index.
+  const float cut = CUT && thr ? sl.logit_of(thr) : -FLT_MAX;
+  const int cut_index = static_cast<int>(CUT && thr ? sl.index_of(thr) : sl.n);
+  auto kept_here = [&](float x, int i, float w) {
+    return x > -INFINITY && (!CUT || ((x > cut || (x == cut && i <= cut_index)) && w >= floor_w));
+  };
+  float sum = 0.f;
+  int turn = 0;
+  constexpr int AHEAD = 16 / VEC;  // vectors under way a thread
+#pragma unroll 1
+  for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
+    float x[AHEAD][VEC], q[AHEAD][VEC];
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+      const int u = v + g * THREADS, first = static_cast<int>(sl.element(u));
+      const bool in = u < sl.nv && sl.inside(u);
+      if (in && vec) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+          const float4 f = __ldcs(reinterpret_cast<const float4*>(noise + first + j));
+          q[g][j] = f.x;
+          q[g][j + 1] = f.y;
+          q[g][j + 2] = f.z;
+          q[g][j + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          q[g][j] = in || (u < sl.nv && first + j >= 0 && first + j < sl.n) ? noise[first + j] : 1.f;
+      }
+      if (u < sl.nv) {
+        sl.load(u, x[g]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[g][j] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+      const int first = static_cast<int>(sl.element(v + g * THREADS));
+      float w[VEC], score[VEC], most = -INFINITY, least_q = FLT_MAX;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float x2 = fminf((x[g][j] - sl.m) * sl.inv2, 0.f);
+        w[j] = lm_exp2(x2);
+        score[j] = x2 - lm_log2_normal(q[g][j]);
+        if constexpr (CUT) {
+          const bool some = kept_here(x[g][j], first + j, w[j]);
+          w[j] = some ? w[j] : 0.f;
+          score[j] = some ? score[j] : -INFINITY;
+        }
+        most = fmaxf(most, score[j]);  // (NaN noise is never ahead)
+        least_q = fminf(least_q, q[g][j]);
+      }
+#pragma unroll
+      for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < d; ++j) w[j] += w[j + d];
+      sum += w[0];
+      if (least_q < FLT_MIN || (best.index == NONE && most == -INFINITY)) {
+        // Noise below the normal range, or a first token that is behind all others.
+#pragma unroll 1
+        for (int j = 0; j < VEC; ++j) {
+          const int i = first + j;
+          if (i < 0 || i >= sl.n || v + g * THREADS >= sl.nv || !sl.is_allowed(i)) continue;
+          const float l = lm_float(sl.row[i]), x2 = fminf((l - sl.m) * sl.inv2, 0.f);
+          const float exact = fmaxf(x2 - lm_log2(noise[i]), -INFINITY);
+          if (x2 > -INFINITY && kept_here(l, i, lm_exp2(x2)) && (exact > best.score || best.index == NONE))
+            best = Best{exact, l, static_cast<unsigned>(i)};
+        }
+      } else if (most > best.score) {
+        int at = VEC - 1;
+        float l = x[g][VEC - 1];
+#pragma unroll
+        for (int j = VEC - 2; j >= 0; --j)
+          if (score[j] == most) {
+            at = j;
+            l = x[g][j];
+          }
+        best = Best{most, l, static_cast<unsigned>(first + at)};
+      }
+    }
+    if (++turn % 16 == 0) {
+      kept += sl.fixed(sum);
+      sum = 0.f;
+    }
+  }
+  kept += sl.fixed(sum);
 }
 
 // 4. The cuts, over everything above a value that is not kept: for top-k one
@@ -788,18 +936,23 @@ __device__ __noinline__ void late_row(Shared& s) {
   const bool greedy = temperature == 0.f;
   u64 Z = late.Z;
   u64 thr = greedy ? sl.value_key(top) : 0;  // copies of the maximum; the lowest index wins the race
+  // Whether one token in 16 or more is kept, by the sample: then every sector of
+  // the noise is read anyway.
+  bool many = false, captured = false;
   if (late.by_k || late.by_p) {
-    const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) / sl.scale);
-    const float sure = late.by_k ? late.tau : top - temperature * __logf(static_cast<float>(sl.n) / (0.99f * left));
-    if (!late.by_k) sample_point(sl, s, left);
+    const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) * sl.unit);
+    const float sure = late.by_k ? late.tau : top - temperature * __logf(__fdividef(static_cast<float>(sl.n), 0.99f * left));
+    many = !late.by_k && s.likely[2] * 16.f >= static_cast<float>(sl.n);
     const float far = late.by_k ? sure : top - temperature * s.likely[0];
     const float ceil = late.by_k || s.likely[1] <= 0.f ? top : top - temperature * s.likely[1];
     // From the narrowest range to the widest, tried one after another.
     Level lv = far <= top && far > sure ? level_between(sl, far, ceil) : level_between(sl, sure, top);
     bool fresh = false;
+#pragma unroll 1
     for (int turn = late.by_k ? 0 : 1; turn < (late.by_p ? 2 : 1); ++turn) {  // the first k, then their share p
       const u64 target = turn ? mass_target(late.p, Z) : static_cast<u64>(late.k);
       bool cut;
+#pragma unroll 1
       for (;;) {
         __syncthreads();  // what the turn before left in s has been read
         cut = select(sl, s, cluster, lv, turn == 1, target, turn, fresh);
@@ -813,6 +966,7 @@ __device__ __noinline__ void late_row(Shared& s) {
       // mass than there is, so that everything stays.
       if (turn == 0) Z = cut ? s.z : s.total_m;
       if (cut && s.thr > thr) thr = s.thr;
+      captured = cut && lv.ceil >= top;  // the first level's keys hold all that are kept
     }
   }
   // (ln min_p: with room for its and the weights' roundings.)
@@ -822,130 +976,251 @@ __device__ __noinline__ void late_row(Shared& s) {
   Best best{-INFINITY, 0.f, NONE};
   u64 kept = 0;
   const float* noise = late.noise;
-  sl.among(
-      floor, INFINITY, [](const float (&)[S::VEC]) {}, [&](int64_t i) { return greedy ? 1.f : noise[i]; },
-      [&](float l, int64_t i, float q) {
-        const float w = sl.weight(l), x = sl.x(l);
-        if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
-        kept += sl.fixed(w);
-        better(best, Best{greedy ? 0.f : race(x, q), l, static_cast<unsigned>(i)});
-      });
+  auto run = [&](float l, int64_t i, float q, unsigned) {
+    const float w = sl.weight(l), x = sl.x(l);
+    if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
+    kept += sl.fixed(w);
+    better(best, Best{greedy ? 0.f : race(x, q), l, static_cast<unsigned>(i)});
+  };
+  if (many) {
+    race_all<true>(sl, noise, thr, floor_w, best, kept);
+  } else if (captured && s.captured <= CANDIDATES) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < static_cast<int>(s.captured); i += THREADS) {
+      const u64 key = s.candidates[i];
+      if (key >= thr) run(sl.logit_of(key), sl.index_of(key), noise[sl.index_of(key)], 0);
+    }
+  } else {
+    sl.template among<4>(
+        floor, INFINITY, nullptr, [](const float (&)[S::VEC]) {}, [&](int64_t i) { return greedy ? 1.f : noise[i]; }, run);
+  }
   finish(sl, s, cluster, best, kept, greedy, late.token, late.logprob);
 }
 
-template <typename T, bool RESIDENT>
-__global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int per_cta) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  using S = Slice<T, RESIDENT>;
+// The first `want` keys of the cluster's lists into s.sorted.  (The lists'
+// shares of `want` reach the least of them, so no key below it counts.)
+__device__ __forceinline__ void merge_keys(Shared& s, int C, int want) {
+  const int each = (want + C - 1) >> (__ffs(C) - 1);
+  u64 least = ~u64(0);
+#pragma unroll 1
+  for (int c = 0; c < C; ++c) {
+    const u64 key = s.sent[c].keys >= each ? s.tops[c][each - 1] : 0;
+    least = key < least ? key : least;
+  }
+#pragma unroll 1
+  for (int i = threadIdx.x; i < C * TOP_SHARED; i += THREADS) {
+    const int c = i / TOP_SHARED, j = i % TOP_SHARED;
+    if (j >= s.sent[c].keys || s.tops[c][j] < least) continue;
+    const unsigned at = atomicAdd(&s.merged, 1u);
+    s.candidates[at] = s.tops[c][j];
+    s.candidates_q[at] = s.tops_q[c][j];
+  }
+  __syncthreads();
+  const int merged = static_cast<int>(s.merged);
+  if (threadIdx.x == 0) s.candidates[merged] = 0;
+  __syncthreads();
+  rank_candidates(
+      s, merged, [&](bool some, int i, u64) { return some ? s.candidates_q[i] : 1.f; },
+      [&](u64 key, int place, float q) {
+        if (place < want) {
+          s.sorted[place] = key;
+          s.sorted_q[place] = q;
+        }
+      });
+  __syncthreads();
+}
+
+// Mass of the list s.sorted[0 .. got) (one warp).
+template <typename S>
+__device__ __forceinline__ u64 list_mass(const S& sl, const Shared& s, int got) {
+  u64 sum = 0;
+#pragma unroll 1
+  for (int at = threadIdx.x & 31; at < got; at += 32) sum += sl.fixed(sl.weight(sl.logit_of(s.sorted[at])));
+  return warp_sum64(sum);
+}
+
+// The race over a list that holds all that can be kept: the tokens before which
+// the mass is below `target` and whose weight is at least floor_w (one warp).
+template <typename S>
+__device__ __forceinline__ void race_list(const S& sl, const Shared& s, int got, u64 target, float floor_w, bool greedy,
+                                          int64_t* token, float* logprob) {
+  const int lane = threadIdx.x & 31;
+  u64 kept = 0, above = 0;
+  Best best{-INFINITY, 0.f, NONE};
+#pragma unroll 1
+  for (int base = 0; base < got && above < target; base += 32) {
+    const int at = base + lane;
+    const bool some = at < got;
+    const u64 key = some ? s.sorted[at] : 0;
+    const float l = some ? sl.logit_of(key) : -INFINITY, w = some ? sl.weight(l) : 0.f;
+    const u64 part = sl.fixed(w);
+    u64 with = part;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const u64 o = __shfl_up_sync(FULL_MASK, with, d);
+      if (lane >= d) with += o;
+    }
+    if (some && (above + with - part < target || at == 0) && w >= floor_w && sl.x(l) > -INFINITY) {
+      kept += part;
+      better(best, Best{greedy ? 0.f : race(sl.x(l), s.sorted_q[at]), l, static_cast<unsigned>(sl.index_of(key))});
+    }
+    above += __shfl_sync(FULL_MASK, with, 31);
+  }
+  kept = warp_sum64(kept);
+  warp_best(best);
+  if (lane == 0) write_row(sl, best, kept, greedy, token, logprob);
+}
+
+// Running maximum (NaN if there is one) over whole vectors of logits.
+template <typename T>
+struct VectorMax {
+  static_assert(sizeof(T) == 4);
+  float m = -INFINITY;
+  __device__ __forceinline__ void take(uint4 b) {
+    m = max_nan(max_nan(m, max_nan(__uint_as_float(b.x), __uint_as_float(b.y))),
+                max_nan(__uint_as_float(b.z), __uint_as_float(b.w)));
+  }
+  __device__ __forceinline__ float get() const { return m; }
+};
+__device__ __forceinline__ __nv_bfloat162 pair_max(__nv_bfloat162 a, unsigned b) {
+  return __hmax2_nan(a, *reinterpret_cast<__nv_bfloat162*>(&b));
+}
+__device__ __forceinline__ __half2 pair_max(__half2 a, unsigned b) { return __hmax2_nan(a, *reinterpret_cast<__half2*>(&b)); }
+template <typename P>
+struct PairMax {  // two 16-bit values at a time
+  P m;
+  __device__ __forceinline__ PairMax(P lowest) : m(lowest) {}
+  __device__ __forceinline__ void take(uint4 b) { m = pair_max(pair_max(pair_max(pair_max(m, b.x), b.y), b.z), b.w); }
+  __device__ __forceinline__ float get() const { return max_nan(lm_float(m.x), lm_float(m.y)); }
+};
+template <>
+struct VectorMax<__nv_bfloat16> : PairMax<__nv_bfloat162> {
+  __device__ __forceinline__ VectorMax() : PairMax(__float2bfloat162_rn(-INFINITY)) {}
+};
+template <>
+struct VectorMax<__half> : PairMax<__half2> {
+  __device__ __forceinline__ VectorMax() : PairMax(__float2half2_rn(-INFINITY)) {}
+};
+
+// Only: a launch that finishes every row.  First: one that finishes those that
+// step 3 can, and marks the others.  Second: the one that finishes those.
+enum class Phase : int { Only, First, Second };
+constexpr int64_t LEFT = -2;  // the mark, in out_tokens
+
+template <typename T, Phase phase>
+__device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int per_cta, Shared& s) {
+  using S = Slice<T>;
   constexpr int VEC = S::VEC;
-  Shared& s = *reinterpret_cast<Shared*>(smem);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r = blockIdx.x / C;
+  if (threadIdx.x == 0) s.slot = s.merged = s.hits = 0;
+  if (threadIdx.x < SAMPLE_BINS) s.own_sample[threadIdx.x] = 0u;
   auto started = cluster.barrier_arrive();  // waited for before the first write to another CTA
-  if (threadIdx.x == 0) s.slot = s.merged = 0;
-  pdl_wait();
-  pdl_trigger();
   const float temperature = a.temperature ? a.temperature[r] : a.all_temperature;
   const int32_t k = a.top_k ? a.top_k[r] : a.all_top_k;
   const float p = a.top_p ? a.top_p[r] : a.all_top_p;
   const float min_p = a.min_p ? a.min_p[r] : a.all_min_p;
   const bool greedy = temperature == 0.f;
   const bool by_k = !greedy && k > 0 && k < a.n, by_p = !greedy && p < 1.f;
-  // Keys that step 2 sorts (0: it would not help).
-  const int want = greedy ? 1 : by_k ? (k <= TOP ? k : 0) : by_p || min_p > 0.f ? TOP_P : 0;
-  // Keys for which a value is looked for that as many reach.
-  const int reach = want ? want : by_k && k <= THREADS ? k : 0;
+  const bool need_mass = by_p && !by_k, alone = C == 1;
+  // Keys that step 2 sorts (0: it would not help); for top-p in a CTA alone the sample may say otherwise.
+  int want = phase == Phase::Second ? 0 : greedy ? 1 : by_k ? (k <= (alone ? TOP : TOP_SHARED) ? k : 0) : min_p > 0.f ? TOP_MIN_P : by_p ? TOP_SHARED : 0;
   S sl;
   sl.row = static_cast<const T*>(a.logits) + r * a.ld;
   sl.mask = a.mask ? a.mask + r * a.mask_ld : nullptr;
-  sl.store = reinterpret_cast<uint4*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+  sl.edge = s.edge;
   sl.n = a.n;
   sl.phase = static_cast<int>(reinterpret_cast<uintptr_t>(sl.row) % 16 / sizeof(T));
   const int64_t all = (a.n + sl.phase + VEC - 1) / VEC;
   sl.v0 = static_cast<int64_t>(rank) * per_cta;
   sl.nv = static_cast<int>(all <= sl.v0 ? 0 : all - sl.v0 < per_cta ? all - sl.v0 : per_cta);
   // An infinite T: the smallest number, so that -inf stays -inf.
-  sl.inv = fmaxf(1.f / temperature, __int_as_float(1));
+  sl.T_ = temperature;
+  sl.inv = fmaxf(lm_rcp(temperature), __int_as_float(1));
   sl.inv2 = sl.inv * LOG2E;
   sl.index_bits = 32 - __clz(static_cast<int>(a.n - 1));
+  sl.sample_shift = min(max(sl.index_bits - 13, 0), 6);  // 4096 to 8192 elements of the row, where it has them
   const int e = min(62 - sl.index_bits, 44);
   sl.scale = __int_as_float((127 + e) << 23);
-
-  if (!want && !by_k && !by_p) {
+  sl.unit = __int_as_float((127 - e) << 23);
+  const float* noise = a.noise + r * a.noise_ld;
+  const bool free = !greedy && !by_k && !by_p && !(min_p > 0.f);  // no filter
+  if (free) {
     // Every token's noise will be read: L2 fetches it meanwhile.
     const int64_t first = max(sl.element(0), int64_t(0)), last = min(sl.element(sl.nv), a.n);
-    const uintptr_t from = (reinterpret_cast<uintptr_t>(a.noise + r * a.noise_ld + first) + 15) & ~uintptr_t(15),
-                    to = reinterpret_cast<uintptr_t>(a.noise + r * a.noise_ld + last) & ~uintptr_t(15);
+    const uintptr_t from = (reinterpret_cast<uintptr_t>(noise + first) + 15) & ~uintptr_t(15),
+                    to = reinterpret_cast<uintptr_t>(noise + last) & ~uintptr_t(15);
     constexpr unsigned PIECE = 4096;
+#pragma unroll 1
     for (uintptr_t at = from + threadIdx.x * PIECE; at < to; at += THREADS * PIECE)
       asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at),
                    "r"(static_cast<unsigned>(to - at < PIECE ? to - at : PIECE)) : "memory");
   }
 
-  // 1. The slice, its largest logit (NaN if there is one) and, for top-p, its
+  // 1. The slice's largest logit (NaN if it holds one) and, for top-p, its
   // mass: a thread's sum of exp((l - ref) / T), ref being the largest of its
   // logits so far.
-  const bool need_mass = by_p && !by_k;
-  if (threadIdx.x < SAMPLE_BINS) s.own_sample[threadIdx.x] = 0u;
-  float top = -INFINITY, mass = 0.f;
-  auto take = [&](float (&x)[VEC]) {
-    const float before = top;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) top = max_nan(top, x[j]);
-    if (need_mass && top > -INFINITY) {
+  float top = -INFINITY, mass = 0.f, own;  // own: of the thread's whole vectors
+  {
+    VectorMax<T> packed;
+    auto rescale = [&](float before) {
       sl.m = top;
       mass *= sl.weight(before);
+    };
+    constexpr int AHEAD = 4;  // loads under way a thread
+#pragma unroll 1
+    for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
+      uint4 bits[AHEAD];
+      bool in[AHEAD];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) x[j] = sl.weight(x[j]);
+      for (int i = 0; i < AHEAD; ++i) {
+        const int u = v + i * THREADS;
+        in[i] = u < sl.nv && sl.inside(u);
+        if (in[i]) bits[i] = sl.whole(u);
+      }
+      if (!need_mass) {
 #pragma unroll
-      for (int d = VEC / 2; d; d >>= 1)
+        for (int i = 0; i < AHEAD; ++i)
+          if (in[i]) packed.take(bits[i]);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < AHEAD; ++i) {
+          if (in[0]) {
+            float x[VEC];
+            sl.unpack(bits[0], x);
+            const float before = top;
 #pragma unroll
-        for (int j = 0; j < d; ++j) x[j] += x[j + d];
-      mass += x[0];
-    }
-  };
-  if constexpr (RESIDENT) {
-    // The whole slice is on its way at once, in four groups of copies; a thread
-    // reads what it copied itself.
-    const int group = ((sl.nv + THREADS - 1) / THREADS + 3) / 4 * THREADS;
+            for (int j = 0; j < VEC; ++j) top = max_nan(top, x[j]);
+            if (top > -INFINITY) {
+              rescale(before);
+              mass += sl.weights(x);
+            }
+          }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      for (int v = g * group + threadIdx.x; v < min((g + 1) * group, sl.nv); v += THREADS) {
-        if (sl.inside(v)) {
-          const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(sl.store + v));
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(sl.row + sl.element(v)) : "memory");
-        } else {
-          float x[VEC];
-          sl.fetch(v, x);
-          sl.keep(v, x);
+          for (int j = 0; j + 1 < AHEAD; ++j) {
+            bits[j] = bits[j + 1];
+            in[j] = in[j + 1];
+          }
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
-      if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
-      if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
-      for (int v = g * group + threadIdx.x; v < min((g + 1) * group, sl.nv); v += THREADS) {
-        float x[VEC];
-        sl.load(v, x);
-        if (sl.mask && sl.inside(v)) {
-          sl.hide(sl.element(v), x);
-          sl.keep(v, x);
+    own = top = max_nan(top, packed.get());
+    // The row's ends, an element a thread; whose vectors they are in will find them in shared memory.
+    if (threadIdx.x < 2 * VEC) {
+      const int which = threadIdx.x / VEC, v = which ? sl.nv - 1 : 0;
+      float x = -INFINITY;
+      if (sl.nv > 0 && !sl.inside(v) && (which == 0 ? sl.element(v) < 0 : sl.element(v) >= 0)) {
+        const int64_t i = sl.element(v) + threadIdx.x % VEC;
+        if (i >= 0 && i < a.n && sl.is_allowed(i)) x = lm_float(sl.row[i]);
+        const float before = top;
+        top = max_nan(top, x);
+        if (need_mass && top > -INFINITY) {
+          rescale(before);
+          mass += sl.weight(x);
         }
-        take(x);
       }
-    }
-  } else {
-#pragma unroll 4
-    for (int v = threadIdx.x; v < sl.nv; v += THREADS) {
-      float x[VEC];
-      sl.fetch(v, x);
-      take(x);
+      reinterpret_cast<T*>(s.edge)[threadIdx.x] = lm_cast<T>(x);
     }
   }
   const float ref = top;
@@ -954,45 +1229,115 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   for (int d = 16; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
   if (lane == 0) s.redf[warp] = widest;
   __syncthreads();
-  widest = s.redf[0];
+  widest = s.redf[lane & (WARPS - 1)];
 #pragma unroll
-  for (int w = 1; w < WARPS; ++w) widest = max_nan(widest, s.redf[w]);
-  float tau = -INFINITY;
-  if (reach > 1 && !isnan(widest)) {
-    if (RESIDENT && sl.nv < THREADS) {
-      // Fewer vectors than threads: the threads' maxima of single elements instead.
-      const T* flat = reinterpret_cast<const T*>(sl.store);
-      top = -INFINITY;
-      for (int i = threadIdx.x; i < sl.nv * VEC; i += THREADS) top = fmaxf(top, lm_float(flat[i]));
-    }
-    tau = block_tau(top, widest, reach, s);
-  }
-  if (reach == 1) tau = widest;
+  for (int d = WARPS / 2; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
   sl.m = widest;
+  cluster.barrier_wait(std::move(started));
+  u64 Z = 0;
   if (need_mass) {
     // (A thread without a logit has no mass; nor has a slice, and its maximum is -inf.)
     mass = warp_sum(mass > 0.f ? mass * sl.weight(ref) : 0.f);
     if (lane == 0) s.mass[warp] = mass;
-    // One vector in SAMPLE_EVERY, at a place that moves along (and so spreads over the banks).
-    for (int q = threadIdx.x; q < sl.nv / SAMPLE_EVERY; q += THREADS) {
+    // The sample: one vector in 2^sample_shift.  (What lies beyond the bins weighs nothing.)
+#pragma unroll 1
+    for (int q = threadIdx.x; q < sl.nv >> sl.sample_shift; q += THREADS) {
       float x[VEC];
-      sl.load(q * SAMPLE_EVERY + (q & (SAMPLE_EVERY - 1)), x);
+      sl.load(q << sl.sample_shift, x);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        if (x[j] > -INFINITY)
-          atomicAdd(&s.own_sample[static_cast<int>(fminf(-SAMPLE_SCALE * sl.x(x[j]), SAMPLE_BINS - 1.f))], 1u);
+      for (int j = 0; j < VEC; ++j) {
+        const float at = -SAMPLE_SCALE * sl.x(x[j]);
+        if (at < SAMPLE_BINS) atomicAdd(&s.own_sample[static_cast<int>(at)], 1u);
+      }
     }
+    __syncthreads();
+    mass = s.mass[lane & (WARPS - 1)];
+#pragma unroll
+    for (int d = WARPS / 2; d; d >>= 1) mass += __shfl_xor_sync(FULL_MASK, mass, d);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < SAMPLE_BINS * C; i += THREADS)
+      cluster.map_shared_rank(&s, i / SAMPLE_BINS)->sample[rank][i % SAMPLE_BINS] = s.own_sample[i % SAMPLE_BINS];
+    if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->part[rank] = Part{widest, mass};
+    cluster.sync();
+    float m = s.part[0].top;
+#pragma unroll 1
+    for (int i = 1; i < C; ++i) m = max_nan(m, s.part[i].top);
+    if (m > -INFINITY) {
+      sl.m = m;
+#pragma unroll 1
+      for (int i = 0; i < C; ++i) Z += sl.fixed(s.part[i].mass * sl.weight(s.part[i].top));
+      sample_point(sl, s, (1.f - fmaxf(p, 0.f)) * (static_cast<float>(Z) * sl.unit));
+      if (want) {
+        // How many keys should reach the mass: three standard deviations of a
+        // count of one in 2^sample_shift more, and a few.
+        const float tokens = s.likely[2];
+        const float most = 32.f + tokens + 3.f * lm_sqrt(static_cast<float>(1 << sl.sample_shift) * (tokens + 16.f));
+        const int limit = alone ? TOP : TOP_SHARED;
+        // (With min-p the tokens may end long before the mass.)
+        want = tokens > limit ? (min_p > 0.f ? TOP_MIN_P : 0) : static_cast<int>(fminf(most, static_cast<float>(limit)));
+      }
+    } else {
+      want = 0;  // a NaN, or nothing to choose
+    }
+  }
+  if (sl.nv > 0) {
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const int v = which ? sl.nv - 1 : 0;
+      if (sl.inside(v) || static_cast<int>(threadIdx.x) != v % THREADS) continue;
+      float x[VEC];
+      sl.load(v, x);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) own = fmaxf(own, x[j]);
+    }
+  }
+  // A value that as many keys reach as step 2 sorts, or as top-k keeps.
+  const int reach = want ? want : by_k && k <= THREADS ? k : 0;
+  const bool flat = sl.nv < THREADS;
+  float tau = reach == 1 ? widest : -INFINITY;
+  if (reach > 1 && !isnan(widest)) {
+    if (flat) {
+      // Fewer vectors than threads: the threads' maxima of single elements instead.
+      own = -INFINITY;
+#pragma unroll 1
+      for (int i = threadIdx.x; i < sl.nv * VEC; i += THREADS) {
+        const int64_t at = sl.element(0) + i;
+        if (at >= 0 && at < a.n && sl.is_allowed(at)) own = fmaxf(own, lm_float(sl.row[at]));
+      }
+    }
+    tau = block_tau(own, widest, reach, s);
   }
 
   // 2. The slice's first keys.
-  const float* noise = a.noise + r * a.noise_ld;
   int keys = 0;
-  if (want && !isnan(widest)) {
+  if (phase != Phase::Second && want && !isnan(widest)) {
+    // The threads whose maximum reaches tau; their vectors are shared out over all.
+    if (!flat && own >= fmaxf(tau, -FLT_MAX)) s.hit[atomicAdd(&s.hits, 1u)] = static_cast<unsigned short>(threadIdx.x);
+    __syncthreads();
+    const int per_thread = (sl.nv + THREADS - 1) / THREADS, shift = per_thread > 1 ? 32 - __clz(per_thread - 1) : 0;
+#pragma unroll 1
     for (int turn = 0;; ++turn) {
-      sl.among(fmaxf(tau, -FLT_MAX), INFINITY, [&](float l, int64_t i) {
-        const unsigned at = atomicAdd(&s.slot, 1u);
-        if (at < CANDIDATES) s.candidates[at] = sl.key(l, i);
-      });
+      const float least = fmaxf(tau, -FLT_MAX);
+      const int vectors = flat ? sl.nv : static_cast<int>(s.hits) << shift;
+#pragma unroll 1
+      for (int base = threadIdx.x - lane; base < vectors; base += THREADS) {
+        if (*reinterpret_cast<volatile unsigned*>(&s.slot) > CANDIDATES) break;  // (the count only says so)
+        const int i = base + lane, v = i >= vectors ? sl.nv : flat ? i : s.hit[i >> shift] + (i & ((1 << shift) - 1)) * THREADS;
+        unsigned some = 0;
+        if (v < sl.nv) {
+          float x[VEC];
+          sl.load(v, x);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) some |= x[j] >= least ? 1u << j : 0u;
+        }
+        if (__any_sync(FULL_MASK, some != 0u)) {
+          unsigned at = warp_reserve(&s.slot, __popc(some));
+#pragma unroll 1
+          for (; some; some &= some - 1, ++at)
+            if (at < CANDIDATES) s.candidates[at] = sl.key(sl.one(v, __ffs(some) - 1), sl.element(v) + __ffs(some) - 1);
+        }
+        __syncwarp();
+      }
       __syncthreads();
       keys = static_cast<int>(s.slot);
       if (keys <= CANDIDATES || turn == 2) break;
@@ -1009,44 +1354,37 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
       __syncthreads();
     }
     if (threadIdx.x == 0 && keys <= CANDIDATES) s.candidates[keys] = 0;
+    __syncthreads();
   }
-  __syncthreads();
-  cluster.barrier_wait(std::move(started));
   if (keys > CANDIDATES) {  // copies of one value
     keys = -1;
   } else if (keys > 0) {
-    // The first `want`, with their noise, go to the cluster's first CTA.
+    // The first `want`, with their noise: to the row's list, or to the cluster's first CTA.
     Shared* leader = cluster.map_shared_rank(&s, 0);
+    u64* to = alone ? s.sorted : leader->tops[rank];
+    float* to_q = alone ? s.sorted_q : leader->tops_q[rank];
     rank_candidates(
         s, keys, [&](bool some, int, u64 key) { return some && !greedy ? noise[sl.index_of(key)] : 1.f; },
         [&](u64 key, int place, float q) {
           if (place < want) {
-            leader->tops[rank][place] = key;
-            leader->tops_q[rank][place] = q;
+            to[place] = key;
+            to_q[place] = q;
           }
         });
     keys = keys < want ? keys : want;
   }
-  if (need_mass)
-    for (int i = threadIdx.x; i < SAMPLE_BINS * C; i += THREADS)
-      cluster.map_shared_rank(&s, i / SAMPLE_BINS)->sample[rank][i % SAMPLE_BINS] = s.own_sample[i % SAMPLE_BINS];
-  if (threadIdx.x < C) {
-    mass = 0.f;
-    if (need_mass)
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) mass += s.mass[w];
-    cluster.map_shared_rank(&s, threadIdx.x)->part[rank] = Part{widest, tau, mass, keys};
-  }
+  if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->sent[rank] = Sent{widest, tau, keys};
   cluster.sync();
 
-  // 3. The row's maximum, mass and first keys.
-  top = s.part[0].top;
-  tau = s.part[0].tau;
-  int found = 0;  // keys of all CTAs, or -1
-  for (int i = 0; i < C; ++i) {
-    top = max_nan(top, s.part[i].top);
-    tau = fmaxf(tau, s.part[i].tau);
-    found = found < 0 || s.part[i].keys < 0 ? -1 : found + s.part[i].keys;
+  // 3. The row's maximum and first keys.
+  top = s.sent[0].top;
+  tau = s.sent[0].tau;
+  int found = s.sent[0].keys;  // keys of all CTAs, or -1
+#pragma unroll 1
+  for (int i = 1; i < C; ++i) {
+    top = max_nan(top, s.sent[i].top);
+    tau = fmaxf(tau, s.sent[i].tau);
+    found = found < 0 || s.sent[i].keys < 0 ? -1 : found + s.sent[i].keys;
   }
   const bool bad = isnan(top) || !(temperature >= 0.f) || isnan(p) || isnan(min_p);
   if (bad || top == -INFINITY) {
@@ -1057,95 +1395,37 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
     return;
   }
   sl.m = top;
-  u64 Z = 0;
-  if (need_mass)
-    for (int i = 0; i < C; ++i) Z += sl.fixed(s.part[i].mass * sl.weight(s.part[i].top));
   const float floor_w = fminf(min_p, 1.f);
-  if (want && found >= 0) {
+  if constexpr (phase != Phase::Second) if (!free) {
     const bool decide = !by_k && !greedy;  // whether these keys are enough is not known beforehand
-    if (rank != 0) {
-      if (!decide) return;
-      cluster.sync();  // the first CTA has written `enough`
-    } else {
-    // Merge.  (The lists' shares of `want` reach the least of them, so no key
-    // below it counts.)
-    const int got = found < want ? found : want, each = (want + C - 1) / C;
-    u64 least = ~u64(0);
-    for (int c = 0; c < C; ++c) {
-      const u64 key = s.part[c].keys >= each ? s.tops[c][each - 1] : 0;
-      least = key < least ? key : least;
-    }
-    for (int i = threadIdx.x; i < C * TOP; i += THREADS) {
-      const int c = i / TOP, j = i % TOP;
-      if (j >= s.part[c].keys || s.tops[c][j] < least) continue;
-      const unsigned at = atomicAdd(&s.merged, 1u);
-      s.candidates[at] = s.tops[c][j];
-      s.candidates_q[at] = s.tops_q[c][j];
-    }
-    __syncthreads();
-    const int merged = static_cast<int>(s.merged);
-    if (threadIdx.x == 0) s.candidates[merged] = 0;
-    __syncthreads();
-    rank_candidates(
-        s, merged, [&](bool some, int i, u64) { return some ? s.candidates_q[i] : 1.f; },
-        [&](u64 key, int place, float q) {
-          if (place < want) {
-            s.sorted[place] = key;
-            s.sorted_q[place] = q;
-          }
-        });
-    __syncthreads();
-    if (warp == 0) {
-      constexpr int EACH = TOP / 32;
-      float l[EACH], w[EACH];
-      u64 part[EACH], sum = 0;
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        const int at = lane * EACH + j;
-        l[j] = at < got ? sl.logit_of(s.sorted[at]) : -INFINITY;
-        w[j] = at < got ? sl.weight(l[j]) : 0.f;
-        part[j] = sl.fixed(w[j]);
-        sum += part[j];
-      }
-      u64 before = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const u64 o = __shfl_up_sync(FULL_MASK, before, d);
-        if (lane >= d) before += o;
-      }
-      const u64 total = __shfl_sync(FULL_MASK, before, 31);
-      before -= sum;
-      if (by_k) Z = total;
-      const u64 target = by_p ? mass_target(p, Z) : ~u64(0);
-      // Enough: the list holds everything, or reaches the mass, or falls below min-p.
-      const float last = got ? sl.weight(sl.logit_of(s.sorted[got - 1])) : 0.f;
-      const bool enough = !decide || found < want || (by_p && total >= target) || last < floor_w;
-      if (decide && lane < C) cluster.map_shared_rank(&s, lane)->enough = enough;
-      if (enough) {
-        u64 kept = 0;
-        Best best{-INFINITY, 0.f, NONE};
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) {
-          const int at = lane * EACH + j;
-          if (at < got && (before < target || at == 0) && w[j] >= floor_w && sl.x(l[j]) > -INFINITY) {
-            kept += part[j];
-            better(best, Best{greedy ? 0.f : race(sl.x(l[j]), s.sorted_q[at]), l[j],
-                              static_cast<unsigned>(sl.index_of(s.sorted[at]))});
-          }
-          before += part[j];
+    bool enough = false;
+    if (want && found >= 0) {
+      if (rank == 0) {
+        const int got = found < want ? found : want;
+        if (!alone) merge_keys(s, C, want);
+        if (warp == 0) {
+          // Enough: the list holds everything, or reaches the mass, or falls below min-p.
+          const u64 total = list_mass(sl, s, got);
+          if (by_k) Z = total;
+          const u64 target = by_p ? mass_target(p, Z) : ~u64(0);
+          const float last = got ? sl.weight(sl.logit_of(s.sorted[got - 1])) : 0.f;
+          enough = !decide || found < want || (by_p && total >= target) || last < floor_w;
+          if (enough) race_list(sl, s, got, target, floor_w, greedy, a.out_tokens + r, a.out_logprobs + r);
+          if (phase == Phase::Only && decide && lane < C) cluster.map_shared_rank(&s, lane)->enough = enough;
         }
-        kept = warp_sum64(kept);
-        warp_best(best);
-        if (lane == 0) write_row(sl, best, kept, greedy, a.out_tokens + r, a.out_logprobs + r);
+      }
+      if (phase == Phase::Only) {
+        if (!decide) return;
+        cluster.sync();  // the first CTA has written `enough`
+        if (s.enough) return;
       }
     }
-    if (!decide) return;
-    cluster.sync();
+    if (phase == Phase::First) {
+      if (rank == 0 && threadIdx.x == 0 && !enough) a.out_tokens[r] = LEFT;
+      return;
     }
-    if (s.enough) return;
   }
-
-  if (want || by_k || by_p) {
+  if constexpr (phase != Phase::First) if (!free) {
     if (threadIdx.x == 0) {
       *reinterpret_cast<S*>(s.slice) = sl;
       s.late = Late{noise, a.out_tokens + r, a.out_logprobs + r, Z, k, p, temperature, floor_w, tau, by_k, by_p};
@@ -1155,60 +1435,48 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
     return;
   }
 
-  // No filter: a race among all.
-  Best best{-INFINITY, 0.f, NONE};
-  u64 kept = 0;
-  constexpr int AHEAD = 16 / VEC;
-  const bool vec = reinterpret_cast<uintptr_t>(noise + sl.element(0)) % 16 == 0;
-  for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
-    float q[AHEAD][VEC];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int u = v + i * THREADS;
-      if (u >= sl.nv) break;
-      const int64_t first = sl.element(u);
-      if (vec && sl.inside(u)) {
-#pragma unroll
-        for (int j = 0; j < VEC; j += 4) {
-          const float4 f = __ldcs(reinterpret_cast<const float4*>(noise + first + j));
-          q[i][j] = f.x;
-          q[i][j + 1] = f.y;
-          q[i][j + 2] = f.z;
-          q[i][j + 3] = f.w;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) q[i][j] = first + j >= 0 && first + j < a.n ? noise[first + j] : 1.f;
-      }
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int u = v + i * THREADS;
-      if (u >= sl.nv) break;
-      float x[VEC];
-      sl.load(u, x);
-      const unsigned first = static_cast<unsigned>(sl.element(u));
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float xt = sl.x(x[j]);
-        sum += lm_exp2(xt * LOG2E);
-        const float score = race(xt, q[i][j]);
-        // (-inf: a token that cannot be kept, or one that noise of +inf puts last.)
-        if (score > best.score || (best.index == NONE && xt > -INFINITY)) best = Best{score, x[j], first + j};
-      }
-    }
-    kept += sl.fixed(sum);
+  if constexpr (phase != Phase::Second) {  // no filter: a race among all
+    Best best{-INFINITY, 0.f, NONE};
+    u64 kept = 0;
+    race_all<false>(sl, noise, 0, 0.f, best, kept);
+    finish(sl, s, cluster, best, kept, false, a.out_tokens + r, a.out_logprobs + r);
   }
-  finish(sl, s, cluster, best, kept, false, a.out_tokens + r, a.out_logprobs + r);
 }
 
-// CTAs of a row's cluster.  As few as hold its slices in shared memory at two
-// CTAs an SM, and more while the rows leave SMs idle.
+template <typename T, Phase phase>
+__global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int per_cta) {
+  __shared__ Shared s;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int log_c = __ffs(cluster.num_blocks()) - 1;
+  const int64_t first = blockIdx.x >> log_c, clusters = gridDim.x >> log_c;
+  pdl_wait();
+  pdl_trigger();
+  if constexpr (phase != Phase::Second) {
+    sample_row<T, phase>(a, first, per_cta, s);
+  } else {
+    // This cluster's rows, THREADS at a time: which of them are marked.  (A row's
+    // mark goes only after every CTA of its cluster has taken it up.)
+#pragma unroll 1
+    for (int64_t base = first; base < a.rows; base += clusters * THREADS) {
+      const int64_t mine = base + clusters * threadIdx.x;
+      const unsigned marks = __ballot_sync(FULL_MASK, mine < a.rows && a.out_tokens[mine] == LEFT);
+      if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = marks;
+      __syncthreads();
+#pragma unroll 1
+      for (int w = 0; w < WARPS; ++w)
+#pragma unroll 1
+        for (unsigned left = s.marks[w]; left; left &= left - 1)
+          sample_row<T, phase>(a, base + clusters * (32 * w + __ffs(left) - 1), per_cta, s);
+      __syncthreads();
+    }
+  }
+}
+
+// CTAs of a row's cluster: as many as the SMs have room for at once, while
+// each still has a slice of some size.
 int cluster_of(int64_t rows, int64_t bytes) {
   int c = 1;
-  while (c < MAX_CLUSTER && bytes > c * SLICE_BYTES) c *= 2;
-  while (c < MAX_CLUSTER && rows * c * 2 <= sms() && bytes / (2 * c) >= SLICE_LEAST) c *= 2;
+  while (c < MAX_CLUSTER && rows * c * 2 <= 2 * sms() && bytes / (2 * c) >= SLICE_LEAST) c *= 2;
   return c;
 }
 
@@ -1216,14 +1484,14 @@ template <typename T>
 cudaError_t launch_typed(const TokenArgs& a, cudaStream_t stream) {
   constexpr int VEC = 16 / int(sizeof(T));
   const int64_t vectors = (a.n + 2 * VEC - 2) / VEC;  // at any alignment of the row
-  int c = cluster_of(a.rows, vectors * 16);
-  if (a.rows * c >= (int64_t(1) << 31)) c = 1;
-  const int64_t per_cta = (vectors + c - 1) / c;
-  const size_t base = (sizeof(Shared) + 15) / 16 * 16;
-  if (per_cta * 16 <= SLICE_MOST)
-    return launch_clusters(k_sample_tokens<T, true>, a.rows * c, THREADS, c, base + size_t(per_cta) * 16, stream, a,
-                           static_cast<int>(per_cta));
-  return launch_clusters(k_sample_tokens<T, false>, a.rows * c, THREADS, c, base, stream, a, static_cast<int>(per_cta));
+  auto launch = [&](auto kernel, int64_t rows, int c) {
+    return launch_clusters(kernel, rows * c, THREADS, c, 0, stream, a, static_cast<int>((vectors + c - 1) / c));
+  };
+  const int c = cluster_of(a.rows, vectors * 16), second = std::min(cluster_of(1, vectors * 16), SECOND_CTAS);
+  if (c > 1 || second == 1) return launch(k_sample_tokens<T, Phase::Only>, a.rows, c);
+  const cudaError_t e = launch(k_sample_tokens<T, Phase::First>, a.rows, c);
+  if (e != cudaSuccess) return e;
+  return launch(k_sample_tokens<T, Phase::Second>, a.rows < SECOND ? a.rows : SECOND, second);
 }
 
 }  // namespace
