@@ -370,7 +370,7 @@ typedef struct profk_sampling {
  * x_i - log q_i (the lowest index of equal ones); for independent q_i ~ Exp(1)
  * that is a draw with probability w_i / sum w over the kept.
  *   logits       device, row r at r*ld elements, n values of `type`
- *   n            1 <= n < 2^31
+ *   n            1 <= n < 2^30 (else PROFK_ERR_UNSUPPORTED)
  *   noise        device, row r at r*noise_ld; q_i > 0 (only the kept tokens'
  *                are used, but any may be read); a NaN is never ahead.
  *                noise_ld = 0 gives every row the same numbers

@@ -54,7 +54,7 @@ int profk_sample_tokens(const void* logits, int type, int64_t rows, int64_t n, i
   if (!how->temperature && !(how->all_temperature >= 0.f)) return PROFK_ERR_INVALID;
   if ((!how->top_p && std::isnan(how->all_top_p)) || (!how->min_p && std::isnan(how->all_min_p)))
     return PROFK_ERR_INVALID;
-  if (n >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31)) return PROFK_ERR_UNSUPPORTED;
+  if (n >= (int64_t(1) << 30) || rows >= (int64_t(1) << 28)) return PROFK_ERR_UNSUPPORTED;
   if (rows == 0) return PROFK_OK;
   if (!logits || !noise || !out_tokens || !out_logprobs) return PROFK_ERR_INVALID;
   if (!aligned(logits, type_size(type)) || !aligned(noise, 4) || !aligned(mask, 4) || !aligned(out_tokens, 8) ||

@@ -194,27 +194,25 @@ struct Slice {
   const T* row;
   const uint32_t* mask;
   const uint4* edge;  // shared memory: the row's first and last vector where they are not whole
-  int64_t n;     // of the row
-  int64_t v0;    // first vector
-  int nv;        // vectors
-  int phase;
+  const uint4* base;  // the slice's first vector
+  int n;              // of the row (an index has 32 bits: n < 2^30)
+  int first;          // element of the slice's first vector's first position (may be outside the row)
+  int nv;             // vectors
+  int in0, in1;       // those that lie inside the row
   float m, T_, inv, inv2;   // the maximum, T, 1 / T, log2(e) / T
   float scale, unit;        // the masses' scale, and its inverse
   int index_bits, sample_shift;  // one vector in 2^sample_shift is sampled
 
   // First element of a vector of the slice (may be outside the row).
-  __device__ __forceinline__ int64_t element(int v) const { return (v0 + v) * VEC - phase; }
+  __device__ __forceinline__ int element(int v) const { return first + v * VEC; }
 
-  __device__ __forceinline__ bool is_allowed(int64_t i) const { return !mask || (mask[i >> 5] >> (i & 31) & 1u); }
+  __device__ __forceinline__ bool is_allowed(int i) const { return !mask || (mask[i >> 5] >> (i & 31) & 1u); }
 
-  __device__ __forceinline__ bool inside(int v) const {
-    const int64_t i = element(v);
-    return i >= 0 && i + VEC <= n;
-  }
+  __device__ __forceinline__ bool inside(int v) const { return v >= in0 && v < in1; }
 
   // Elements that are not allowed become -inf, in the packed vector.
-  __device__ __forceinline__ uint4 hide(int64_t i, uint4 bits) const {
-    const int at = static_cast<int>(i & 31);
+  __device__ __forceinline__ uint4 hide(int i, uint4 bits) const {
+    const int at = i & 31;
     const uint32_t* w = mask + (i >> 5);
     const uint32_t ok = __funnelshift_r(w[0], at + VEC > 32 ? w[1] : 0u, at);
     unsigned* b = &bits.x;
@@ -233,9 +231,8 @@ struct Slice {
 
   // A vector that lies inside the row.
   __device__ __forceinline__ uint4 whole(int v) const {
-    const int64_t i = element(v);
-    const uint4 bits = __ldg(reinterpret_cast<const uint4*>(row + i));
-    return mask ? hide(i, bits) : bits;
+    const uint4 bits = __ldg(base + v);
+    return mask ? hide(element(v), bits) : bits;
   }
 
   __device__ __forceinline__ void unpack(uint4 bits, float (&x)[VEC]) const {
@@ -250,7 +247,7 @@ struct Slice {
 
   // Any vector; elements outside the row or not allowed are -inf.
   __device__ __forceinline__ void load(int v, float (&x)[VEC]) const {
-    unpack(inside(v) ? whole(v) : edge[element(v) < 0 ? 0 : 1], x);
+    unpack(inside(v) ? whole(v) : edge[v < in0 ? 0 : 1], x);
   }
 
   // Element j of a vector (inside the row, allowed).
@@ -285,8 +282,8 @@ struct Slice {
 #pragma unroll 1
       while (__any_sync(FULL_MASK, hits != 0u)) {
         float l[BATCH];
-        int64_t at[BATCH];
-        decltype(given(int64_t(0))) what[BATCH];
+        int at[BATCH];
+        decltype(given(0)) what[BATCH];
         const int some = min(__popc(hits), BATCH);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
@@ -327,12 +324,12 @@ struct Slice {
   // inverted index in index_bits bits.
   static constexpr int DROP = sizeof(T) == 2 ? 13 : 0;
   __device__ __forceinline__ u64 value_key(float l) const { return u64(ord_key(l) >> DROP) << index_bits; }
-  __device__ __forceinline__ u64 key(float l, int64_t i) const {
-    return value_key(l) | ((u64(1) << index_bits) - 1 - static_cast<u64>(i));
+  __device__ __forceinline__ u64 key(float l, int i) const {
+    return value_key(l) | (((1u << index_bits) - 1u) - static_cast<unsigned>(i));
   }
-  __device__ __forceinline__ int64_t index_of(u64 key) const {
-    const u64 ones = (u64(1) << index_bits) - 1;
-    return static_cast<int64_t>(ones - (key & ones));
+  __device__ __forceinline__ int index_of(u64 key) const {
+    const unsigned ones = (1u << index_bits) - 1u;
+    return static_cast<int>(ones - (static_cast<unsigned>(key) & ones));
   }
   __device__ __forceinline__ float logit_of(u64 key) const {
     const uint32_t ord = static_cast<uint32_t>(key >> index_bits) << DROP;
@@ -381,7 +378,7 @@ struct Level {
   int shift;
 
   template <typename S>
-  __device__ __forceinline__ int bin_of(const S& sl, float l, int64_t i) const {
+  __device__ __forceinline__ int bin_of(const S& sl, float l, int i) const {
     const int b = static_cast<int>(fmaxf(fminf((-sl.x(l) - x0) * per_x, BINS - 1.f), 0.f));
     if (bin0 < 0) return b;
     const u64 key = sl.key(l, i);
@@ -435,8 +432,8 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
             partial = 0.f;
           }
         },
-        [](int64_t) { return 0; },
-        [&](float l, int64_t i, int, unsigned place) {
+        [](int) { return 0; },
+        [&](float l, int i, int, unsigned place) {
           const int b = lv.bin_of(sl, l, i);
           if (b < 0) return;
           if (capture && place < CANDIDATES) s.candidates[place] = sl.key(l, i);
@@ -562,8 +559,8 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
         }
       } else {
         sl.template among<1>(
-            floor, ceil, nullptr, [](const float (&)[S::VEC]) {}, [](int64_t) { return 0; },
-            [&](float l, int64_t i, int, unsigned) {
+            floor, ceil, nullptr, [](const float (&)[S::VEC]) {}, [](int) { return 0; },
+            [&](float l, int i, int, unsigned) {
               if (lv.bin_of(sl, l, i) == bin) send(sl.key(l, i));
             });
       }
@@ -833,7 +830,7 @@ __device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 th
   const bool vec = reinterpret_cast<uintptr_t>(noise + sl.element(0)) % 16 == 0;
   // Kept: above the cut's logit, or its copies up to the cut's index.
   const float cut = CUT && thr ? sl.logit_of(thr) : -FLT_MAX;
-  const int cut_index = static_cast<int>(CUT && thr ? sl.index_of(thr) : sl.n);
+  const int cut_index = CUT && thr ? sl.index_of(thr) : sl.n;
   auto kept_here = [&](float x, int i, float w) {
     return x > -INFINITY && (!CUT || ((x > cut || (x == cut && i <= cut_index)) && w >= floor_w));
   };
@@ -845,7 +842,7 @@ __device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 th
     float x[AHEAD][VEC], q[AHEAD][VEC];
 #pragma unroll
     for (int g = 0; g < AHEAD; ++g) {
-      const int u = v + g * THREADS, first = static_cast<int>(sl.element(u));
+      const int u = v + g * THREADS, first = sl.element(u);
       const bool in = u < sl.nv && sl.inside(u);
       if (in && vec) {
 #pragma unroll
@@ -870,7 +867,7 @@ __device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 th
     }
 #pragma unroll
     for (int g = 0; g < AHEAD; ++g) {
-      const int first = static_cast<int>(sl.element(v + g * THREADS));
+      const int first = sl.element(v + g * THREADS);
       float w[VEC], score[VEC], most = -INFINITY, least_q = FLT_MAX;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
@@ -976,7 +973,7 @@ __device__ __noinline__ void late_row(Shared& s) {
   Best best{-INFINITY, 0.f, NONE};
   u64 kept = 0;
   const float* noise = late.noise;
-  auto run = [&](float l, int64_t i, float q, unsigned) {
+  auto run = [&](float l, int i, float q, unsigned) {
     const float w = sl.weight(l), x = sl.x(l);
     if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
     kept += sl.fixed(w);
@@ -992,7 +989,7 @@ __device__ __noinline__ void late_row(Shared& s) {
     }
   } else {
     sl.template among<4>(
-        floor, INFINITY, nullptr, [](const float (&)[S::VEC]) {}, [&](int64_t i) { return greedy ? 1.f : noise[i]; }, run);
+        floor, INFINITY, nullptr, [](const float (&)[S::VEC]) {}, [&](int i) { return greedy ? 1.f : noise[i]; }, run);
   }
   finish(sl, s, cluster, best, kept, greedy, late.token, late.logprob);
 }
@@ -1130,16 +1127,19 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   sl.row = static_cast<const T*>(a.logits) + r * a.ld;
   sl.mask = a.mask ? a.mask + r * a.mask_ld : nullptr;
   sl.edge = s.edge;
-  sl.n = a.n;
-  sl.phase = static_cast<int>(reinterpret_cast<uintptr_t>(sl.row) % 16 / sizeof(T));
-  const int64_t all = (a.n + sl.phase + VEC - 1) / VEC;
-  sl.v0 = static_cast<int64_t>(rank) * per_cta;
-  sl.nv = static_cast<int>(all <= sl.v0 ? 0 : all - sl.v0 < per_cta ? all - sl.v0 : per_cta);
+  sl.n = static_cast<int>(a.n);
+  const int phase_of_row = static_cast<int>(reinterpret_cast<uintptr_t>(sl.row) % 16 / sizeof(T));
+  const int all = (sl.n + phase_of_row + VEC - 1) / VEC, v0 = rank * per_cta;
+  sl.nv = max(min(all - v0, per_cta), 0);
+  sl.first = v0 * VEC - phase_of_row;
+  sl.base = reinterpret_cast<const uint4*>(sl.row - phase_of_row) + v0;
+  sl.in0 = sl.first < 0 ? 1 : 0;
+  sl.in1 = min(sl.nv, (sl.n - sl.first) / VEC);
   // An infinite T: the smallest number, so that -inf stays -inf.
   sl.T_ = temperature;
   sl.inv = fmaxf(lm_rcp(temperature), __int_as_float(1));
   sl.inv2 = sl.inv * LOG2E;
-  sl.index_bits = 32 - __clz(static_cast<int>(a.n - 1));
+  sl.index_bits = 32 - __clz(sl.n - 1);
   sl.sample_shift = min(max(sl.index_bits - 13, 0), 6);  // 4096 to 8192 elements of the row, where it has them
   const int e = min(62 - sl.index_bits, 44);
   sl.scale = __int_as_float((127 + e) << 23);
@@ -1148,7 +1148,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   const bool free = !greedy && !by_k && !by_p && !(min_p > 0.f);  // no filter
   if (free) {
     // Every token's noise will be read: L2 fetches it meanwhile.
-    const int64_t first = max(sl.element(0), int64_t(0)), last = min(sl.element(sl.nv), a.n);
+    const int first = max(sl.element(0), 0), last = max(min(sl.element(sl.nv), sl.n), first);
     const uintptr_t from = (reinterpret_cast<uintptr_t>(noise + first) + 15) & ~uintptr_t(15),
                     to = reinterpret_cast<uintptr_t>(noise + last) & ~uintptr_t(15);
     constexpr unsigned PIECE = 4096;
@@ -1211,8 +1211,8 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
       const int which = threadIdx.x / VEC, v = which ? sl.nv - 1 : 0;
       float x = -INFINITY;
       if (sl.nv > 0 && !sl.inside(v) && (which == 0 ? sl.element(v) < 0 : sl.element(v) >= 0)) {
-        const int64_t i = sl.element(v) + threadIdx.x % VEC;
-        if (i >= 0 && i < a.n && sl.is_allowed(i)) x = lm_float(sl.row[i]);
+        const int i = sl.element(v) + threadIdx.x % VEC;
+        if (i >= 0 && i < sl.n && sl.is_allowed(i)) x = lm_float(sl.row[i]);
         const float before = top;
         top = max_nan(top, x);
         if (need_mass && top > -INFINITY) {
@@ -1301,8 +1301,8 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
       own = -INFINITY;
 #pragma unroll 1
       for (int i = threadIdx.x; i < sl.nv * VEC; i += THREADS) {
-        const int64_t at = sl.element(0) + i;
-        if (at >= 0 && at < a.n && sl.is_allowed(at)) own = fmaxf(own, lm_float(sl.row[at]));
+        const int at = sl.element(0) + i;
+        if (at >= 0 && at < sl.n && sl.is_allowed(at)) own = fmaxf(own, lm_float(sl.row[at]));
       }
     }
     tau = block_tau(own, widest, reach, s);
