@@ -28,6 +28,9 @@
 //      histogram touches little else; where it does not, it is made again from
 //      a value that surely is below.
 //
+// A row without filters is one pass over its logits and noise together
+// (free_row).
+//
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
 // the same whatever order the atomics take.
@@ -151,6 +154,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = max_nan(v, __shfl_xor_sync(FULL_MASK, v, d));
+  return v;
 }
 
 // Room for n entries of each lane of a list with the given length, which it
@@ -821,18 +830,18 @@ __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left)
   __syncthreads();
 }
 
-// The race where most tokens take part: every vector of the slice beside its
-// noise.  CUT: only keys from thr up and weights from floor_w up.  Scores are
-// in units of log 2; a vector's best is looked for where it beats the thread's.
-template <bool CUT, typename S>
+// The race where many tokens take part: every vector of the slice beside its
+// noise; keys from thr up and weights from floor_w up.  Scores are in units of
+// log 2; a vector's best is looked for where it beats the thread's.
+template <typename S>
 __device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 thr, float floor_w, Best& best, u64& kept) {
   constexpr int VEC = S::VEC;
   const bool vec = reinterpret_cast<uintptr_t>(noise + sl.element(0)) % 16 == 0;
   // Kept: above the cut's logit, or its copies up to the cut's index.
-  const float cut = CUT && thr ? sl.logit_of(thr) : -FLT_MAX;
-  const int cut_index = CUT && thr ? sl.index_of(thr) : sl.n;
+  const float cut = thr ? sl.logit_of(thr) : -FLT_MAX;
+  const int cut_index = thr ? sl.index_of(thr) : sl.n;
   auto kept_here = [&](float x, int i, float w) {
-    return x > -INFINITY && (!CUT || ((x > cut || (x == cut && i <= cut_index)) && w >= floor_w));
+    return x > -INFINITY && (x > cut || (x == cut && i <= cut_index)) && w >= floor_w;
   };
   float sum = 0.f;
   int turn = 0;
@@ -874,11 +883,9 @@ __device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 th
         const float x2 = fminf((x[g][j] - sl.m) * sl.inv2, 0.f);
         w[j] = lm_exp2(x2);
         score[j] = x2 - lm_log2_normal(q[g][j]);
-        if constexpr (CUT) {
-          const bool some = kept_here(x[g][j], first + j, w[j]);
-          w[j] = some ? w[j] : 0.f;
-          score[j] = some ? score[j] : -INFINITY;
-        }
+        const bool some = kept_here(x[g][j], first + j, w[j]);
+        w[j] = some ? w[j] : 0.f;
+        score[j] = some ? score[j] : -INFINITY;
         most = fmaxf(most, score[j]);  // (NaN noise is never ahead)
         least_q = fminf(least_q, q[g][j]);
       }
@@ -980,7 +987,7 @@ __device__ __noinline__ void late_row(Shared& s) {
     better(best, Best{greedy ? 0.f : race(x, q), l, static_cast<unsigned>(i)});
   };
   if (many) {
-    race_all<true>(sl, noise, thr, floor_w, best, kept);
+    race_all(sl, noise, thr, floor_w, best, kept);
   } else if (captured && s.captured <= CANDIDATES) {
 #pragma unroll 1
     for (int i = threadIdx.x; i < static_cast<int>(s.captured); i += THREADS) {
@@ -1099,6 +1106,138 @@ struct VectorMax<__half> : PairMax<__half2> {
   __device__ __forceinline__ VectorMax() : PairMax(__float2half2_rn(-INFINITY)) {}
 };
 
+// A row without filters, in one pass: a thread's mass and best score stand
+// relative to the largest of its logits so far, `ref`; when that moves, the
+// mass is scaled, and the best's score is computed anew from its logit and
+// noise, so that all scores come from one formula and at last from the row's
+// maximum.
+template <typename S, typename Started>
+__device__ __forceinline__ void free_row(S& sl, Shared& s, cg::cluster_group& cluster, Started&& started,
+                                         const float* noise, float temperature, bool refused, int64_t* token,
+                                         float* logprob) {
+  constexpr int VEC = S::VEC, AHEAD = 16 / VEC;  // vectors under way a thread
+  const int C = cluster.num_blocks(), rank = cluster.block_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool vec = reinterpret_cast<uintptr_t>(noise + sl.first) % 16 == 0;
+  float ref = -INFINITY, top = -INFINITY, mass = 0.f, best_lq = 0.f;
+  Best best{-INFINITY, 0.f, NONE};
+  auto x2 = [&](float l) { return fminf((l - ref) * sl.inv2, 0.f); };
+  auto move = [&](float to) {
+    mass *= lm_exp2(fminf((ref - to) * sl.inv2, 0.f));
+    ref = to;
+    best.score = best.index == NONE ? -INFINITY : fmaxf(x2(best.logit) - best_lq, -INFINITY);
+  };
+  auto one = [&](int i) {  // an element by itself: a row's ends, and what the vectors leave
+    if (!sl.is_allowed(i)) return;
+    const float l = lm_float(sl.row[i]);
+    top = max_nan(top, l);
+    if (!(l > -INFINITY)) return;
+    if (l > ref) move(l);
+    mass += lm_exp2(x2(l));
+    const float lq = lm_log2(noise[i]), score = fmaxf(x2(l) - lq, -INFINITY);  // NaN noise is never ahead
+    if (score > best.score || best.index == NONE || (score == best.score && static_cast<unsigned>(i) < best.index)) {
+      best = Best{score, l, static_cast<unsigned>(i)};
+      best_lq = isnan(lq) ? INFINITY : lq;
+    }
+  };
+#pragma unroll 1
+  for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
+    uint4 bits[AHEAD];
+    float q[AHEAD][VEC];
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+      const int u = v + g * THREADS;
+      if (!sl.inside(u)) continue;
+      bits[g] = sl.whole(u);
+      const float* from = noise + sl.element(u);
+      if (vec) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+          const float4 f = __ldcs(reinterpret_cast<const float4*>(from + j));
+          q[g][j] = f.x;
+          q[g][j + 1] = f.y;
+          q[g][j + 2] = f.z;
+          q[g][j + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) q[g][j] = __ldcs(from + j);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+      const int u = v + g * THREADS;
+      if (!sl.inside(u)) continue;
+      float x[VEC], most = -INFINITY, least_q = FLT_MAX, peak = -INFINITY;
+      sl.unpack(bits[g], x);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        peak = max_nan(peak, x[j]);
+        least_q = fminf(least_q, q[g][j]);
+      }
+      top = max_nan(top, peak);
+      if (peak > ref) move(peak);
+      if (ref == -INFINITY) continue;
+      float w[VEC], score[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float y = x2(x[j]);
+        w[j] = lm_exp2(y);
+        score[j] = y - lm_log2_normal(q[g][j]);
+        most = fmaxf(most, score[j]);
+      }
+#pragma unroll
+      for (int d = VEC / 2; d; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < d; ++j) w[j] += w[j + d];
+      if (least_q < FLT_MIN || (best.index == NONE && most == -INFINITY)) {
+        // Noise below the normal range, or a first token that is behind all others.
+#pragma unroll 1
+        for (int j = 0; j < VEC; ++j) one(sl.element(u) + j);
+        continue;
+      }
+      mass += w[0];
+      if (most > best.score) {
+        int at = VEC - 1;
+        float l = x[VEC - 1], noise_there = q[g][VEC - 1];
+#pragma unroll
+        for (int j = VEC - 2; j >= 0; --j)
+          if (score[j] == most) {
+            at = j;
+            l = x[j];
+            noise_there = q[g][j];
+          }
+        best = Best{most, l, static_cast<unsigned>(sl.element(u) + at)};
+        best_lq = lm_log2_normal(noise_there);
+      }
+    }
+  }
+  if (threadIdx.x < 2 * VEC) {
+    const int which = threadIdx.x / VEC, v = which ? sl.nv - 1 : 0, i = sl.element(v) + static_cast<int>(threadIdx.x % VEC);
+    if (sl.nv > 0 && !sl.inside(v) && (which == 0 ? sl.element(v) < 0 : sl.element(v) >= 0) && i >= 0 && i < sl.n) one(i);
+  }
+  // The row's maximum.
+  top = warp_max_nan(top);
+  if (lane == 0) s.redf[warp] = top;
+  __syncthreads();
+  top = warp_max_nan(s.redf[lane & (WARPS - 1)]);
+  cluster.barrier_wait(std::move(started));
+  if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->part[rank] = Part{top, 0.f};
+  cluster.sync();
+#pragma unroll 1
+  for (int i = 0; i < C; ++i) top = max_nan(top, s.part[i].top);
+  const bool bad = refused || isnan(top) || !(temperature >= 0.f);
+  if (bad || top == -INFINITY) {
+    if (rank == 0 && threadIdx.x == 0) {
+      *token = -1;
+      *logprob = bad ? __int_as_float(0x7fc00000) : -INFINITY;
+    }
+    return;
+  }
+  sl.m = top;
+  if (ref > -INFINITY) move(top);
+  finish(sl, s, cluster, best, __float2ull_rn(mass * sl.scale), false, token, logprob);
+}
+
 // Only: a launch that finishes every row.  First: one that finishes those that
 // step 3 can, and marks the others.  Second: the one that finishes those.
 enum class Phase : int { Only, First, Second };
@@ -1145,17 +1284,12 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   sl.scale = __int_as_float((127 + e) << 23);
   sl.unit = __int_as_float((127 - e) << 23);
   const float* noise = a.noise + r * a.noise_ld;
-  const bool free = !greedy && !by_k && !by_p && !(min_p > 0.f);  // no filter
-  if (free) {
-    // Every token's noise will be read: L2 fetches it meanwhile.
-    const int first = max(sl.element(0), 0), last = max(min(sl.element(sl.nv), sl.n), first);
-    const uintptr_t from = (reinterpret_cast<uintptr_t>(noise + first) + 15) & ~uintptr_t(15),
-                    to = reinterpret_cast<uintptr_t>(noise + last) & ~uintptr_t(15);
-    constexpr unsigned PIECE = 4096;
-#pragma unroll 1
-    for (uintptr_t at = from + threadIdx.x * PIECE; at < to; at += THREADS * PIECE)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at),
-                   "r"(static_cast<unsigned>(to - at < PIECE ? to - at : PIECE)) : "memory");
+  if constexpr (phase != Phase::Second) {
+    if (!greedy && !by_k && !by_p && !(min_p > 0.f)) {
+      free_row(sl, s, cluster, std::move(started), noise, temperature, isnan(p) || isnan(min_p), a.out_tokens + r,
+               a.out_logprobs + r);
+      return;
+    }
   }
 
   // 1. The slice's largest logit (NaN if it holds one) and, for top-p, its
@@ -1224,14 +1358,10 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
     }
   }
   const float ref = top;
-  float widest = top;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
+  float widest = warp_max_nan(top);
   if (lane == 0) s.redf[warp] = widest;
   __syncthreads();
-  widest = s.redf[lane & (WARPS - 1)];
-#pragma unroll
-  for (int d = WARPS / 2; d; d >>= 1) widest = max_nan(widest, __shfl_xor_sync(FULL_MASK, widest, d));
+  widest = warp_max_nan(s.redf[lane & (WARPS - 1)]);
   sl.m = widest;
   cluster.barrier_wait(std::move(started));
   u64 Z = 0;
@@ -1396,7 +1526,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   }
   sl.m = top;
   const float floor_w = fminf(min_p, 1.f);
-  if constexpr (phase != Phase::Second) if (!free) {
+  if constexpr (phase != Phase::Second) {
     const bool decide = !by_k && !greedy;  // whether these keys are enough is not known beforehand
     bool enough = false;
     if (want && found >= 0) {
@@ -1425,7 +1555,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
       return;
     }
   }
-  if constexpr (phase != Phase::First) if (!free) {
+  if constexpr (phase != Phase::First) {
     if (threadIdx.x == 0) {
       *reinterpret_cast<S*>(s.slice) = sl;
       s.late = Late{noise, a.out_tokens + r, a.out_logprobs + r, Z, k, p, temperature, floor_w, tau, by_k, by_p};
@@ -1433,13 +1563,6 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
     __syncthreads();
     late_row<S>(s);
     return;
-  }
-
-  if constexpr (phase != Phase::Second) {  // no filter: a race among all
-    Best best{-INFINITY, 0.f, NONE};
-    u64 kept = 0;
-    race_all<false>(sl, noise, 0, 0.f, best, kept);
-    finish(sl, s, cluster, best, kept, false, a.out_tokens + r, a.out_logprobs + r);
   }
 }
 
