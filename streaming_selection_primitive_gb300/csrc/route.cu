@@ -76,6 +76,23 @@ __device__ __forceinline__ void load_part(const T* row, int E, bool vec, float (
   }
 }
 
+// The lane's part, laid out as for T, of 32 R floats in shared memory.
+template <typename T, int R>
+__device__ __forceinline__ void load_shared(const float* from, float (&z)[R]) {
+  using P = Part<T, R>;
+  constexpr int V = P::VEC < 4 ? P::VEC : 4;
+#pragma unroll
+  for (int g = 0; g < R; g += V) {
+    union {
+      typename Bits<4 * V>::type bits;
+      float v[V];
+    } u;
+    u.bits = *reinterpret_cast<const decltype(u.bits)*>(from + P::expert(g));
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[g + j] = u.v[j];
+  }
+}
+
 template <typename T, int R>
 __device__ __forceinline__ void store_part(T* row, int E, bool vec, const float (&d)[R]) {
   using P = Part<T, R>;
@@ -165,13 +182,13 @@ __device__ __forceinline__ float sigmoid(float z) { return lm_rcp(1.f + lm_exp2(
 // Softmax: s = exp(z - ref).  Sigmoid: s = sigmoid(z), or, where that could
 // underflow for every expert (ref below -60) or a value is not finite, the
 // careful form: s = sigmoid(z) exp(-c) with c = min(max z, 0).
-template <int R>
-__device__ __forceinline__ float token_scores(const float (&z)[R], float (&s)[R], bool sig, float ref) {
+template <bool SIG, int R>
+__device__ __forceinline__ float token_scores(const float (&z)[R], float (&s)[R], float ref) {
   float sum = 0.f;
-  if (sig && ref > -60.f) {
+  if (SIG && ref > -60.f) {
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r] = sigmoid(z[r]);
-  } else if (!sig && fabsf(ref) < INFINITY) {
+  } else if (!SIG && fabsf(ref) < INFINITY) {
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r] = lm_exp2((z[r] - ref) * LOG2E);
   } else {
@@ -182,7 +199,7 @@ __device__ __forceinline__ float token_scores(const float (&z)[R], float (&s)[R]
     const float c = fminf(m, 0.f), ec = expf(c);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (sig) {
+      if constexpr (SIG) {
         const bool pos = z[r] >= 0.f;
         const float u = z[r] == -INFINITY ? 0.f : expf(pos ? -z[r] : z[r] - c);
         s[r] = (pos ? 1.f : u) / (1.f + (pos ? u : u * ec));
@@ -202,29 +219,24 @@ __device__ __forceinline__ float slots_sum(float v, int width) {
   return v;
 }
 
-// The gate of the lane's slot (logit zc; ok: the slot is filled).  ref, sum:
-// the token's softmax reference and sum, for the form that needs them.  width:
-// the power of two not below k.
-__device__ __forceinline__ float slot_gate(float zc, bool ok, int width, bool sig, bool normalize, float ref, float sum) {
-  float e;
-  if (!normalize && !sig) {
-    e = (zc == ref ? 1.f : lm_exp2((zc - ref) * LOG2E)) / sum;
-    return ok ? e : 0.f;
+// The gate of the lane's slot (logit zc; ok: the slot is filled).  ref: the
+// token's largest logit (sigmoid: unused); sum: of its experts' scores.  width: the power of two not
+// below k.
+template <bool SIG>
+__device__ __forceinline__ float slot_gate(float zc, bool ok, int width, bool normalize, float ref, float sum) {
+  float e = SIG ? sigmoid(zc) : zc == ref ? 1.f : lm_exp2((zc - ref) * LOG2E);
+  e = ok ? e : 0.f;
+  if (!normalize) return SIG ? e : e * lm_rcp(sum);
+  float all = slots_sum(e, width);
+  const float first = __shfl_sync(FULL_MASK, all, 0);
+  if (!(first > 1e-20f)) {
+    // The chosen are far below the largest (a bias chose them), or underflow:
+    // by their logarithms.
+    const float y = ok ? (SIG ? log_sigmoid(zc) : zc) : -INFINITY;
+    const float top = key_to_float(__reduce_max_sync(FULL_MASK, ord_key(y)));
+    e = ok ? (y == top ? 1.f : lm_exp2((y - top) * LOG2E)) : 0.f;
+    all = slots_sum(e, width);
   }
-  if (sig) {
-    e = ok ? sigmoid(zc) : 0.f;
-    if (!normalize) return e;
-    // Scores that may underflow are compared by their logarithms.
-    if (!__any_sync(FULL_MASK, ok && zc < -60.f)) {
-      const float all = slots_sum(e, width);
-      return ok ? e * lm_rcp(all) : 0.f;
-    }
-    zc = log_sigmoid(zc);
-  }
-  const float y = ok ? zc : -INFINITY;
-  const float top = key_to_float(__reduce_max_sync(FULL_MASK, ord_key(y)));
-  e = ok ? (y == top ? 1.f : lm_exp2((y - top) * LOG2E)) : 0.f;
-  const float all = slots_sum(e, width);
   return ok ? e * lm_rcp(all) : 0.f;
 }
 
@@ -337,13 +349,13 @@ __device__ __noinline__ int pick_exact(const float (&c)[R], int k) {
 // The tokens of this CTA.  Leaves the CTA's slots per expert in cnt and the
 // sums of n_t p_te in psum (both E entries of shared memory; psum through
 // `stage`, WARPS x E), complete after the block barrier that ends it.
-template <typename T, int R>
+template <typename T, int R, bool SIG>
 __device__ __forceinline__ void route_tokens(const RouteArgs& a, unsigned* cnt, float* psum, float* stage,
                                              unsigned char* ring_smem) {
   using P = Part<T, R>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts, k = a.k;
   const bool exact = sizeof(T) == 2 && !a.bias;
-  const bool need_p = a.loss || (!a.normalize && !a.sigmoid);
+  const bool need_p = a.loss || (!a.normalize && !SIG);
   int width = 1;
   while (width < k) width <<= 1;
   const T* logits = static_cast<const T*>(a.logits);
@@ -362,15 +374,20 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, unsigned* cnt, 
 #pragma unroll
   for (int i = 0; i + 1 < S; ++i) ring.fetch(logits + (t + i * step) * a.ld, E, t + i * step < a.tokens, i);
   bool used = t < a.tokens && (!a.mask || a.mask[t]);
+  // Where this token's row, the row to fetch and the outputs are; each moves by a step.
+  const T* here = logits + t * a.ld;
+  const T* ahead = here + (S - 1) * step * a.ld;
+  const int64_t row_step = step * a.ld, slot_step = step * k;
+  float* gate_at = a.gates + t * k + lane;
+  int64_t* chosen_at = a.chosen + t * k + lane;
   for (int at = 0; t < a.tokens; t += step, at = at + 1 < S ? at + 1 : 0) {
     int mine = -1;  // lane j: the expert of slot j
     float gate = 0.f;
-    const int64_t ahead = t + (S - 1) * step;
-    if constexpr (S > 0) ring.fetch(logits + ahead * a.ld, E, ahead < a.tokens, at > 0 ? at - 1 : S - 1);
+    if constexpr (S > 0) ring.fetch(ahead, E, t + (S - 1) * step < a.tokens, at > 0 ? at - 1 : S - 1);
     const bool use_next = !a.mask || (t + step < a.tokens && a.mask[t + step]);
     ring.wait();
     if (used) {
-      const T* row = ring.row(logits + t * a.ld, at);
+      const T* row = ring.row(here, at);
       float z[R];
       load_part<T, R>(row, E, vec, z);
       uint32_t key[R];
@@ -400,34 +417,38 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, unsigned* cnt, 
         zc = mine >= 0 ? lm_float(row[mine]) : -INFINITY;
       }
       const bool ok = mine >= 0;
-      float ref = 0.f, sum = 1.f;
+      // The largest logit: that of the first slot, unless a bias chose it.
+      float ref = __shfl_sync(FULL_MASK, zc, 0), sum = 1.f;
+      if (!SIG && a.bias) {
+        ref = z[0];
+#pragma unroll
+        for (int r = 1; r < R; ++r) ref = fmaxf(ref, z[r]);
+        ref = key_to_float(__reduce_max_sync(FULL_MASK, ord_key(ref)));
+      }
       if (need_p) {
         const int filled = __popc(__ballot_sync(FULL_MASK, ok));
         if (filled) {
           float s[R];
-          ref = __shfl_sync(FULL_MASK, zc, 0);
-          if (!a.sigmoid && a.bias) {
-            ref = z[0];
-#pragma unroll
-            for (int r = 1; r < R; ++r) ref = fmaxf(ref, z[r]);
-            ref = key_to_float(__reduce_max_sync(FULL_MASK, ord_key(ref)));
-          }
-          sum = token_scores<R>(z, s, a.sigmoid, ref);
+          sum = token_scores<SIG, R>(z, s, ref);
           const float scale = __fdividef(static_cast<float>(filled), sum);
 #pragma unroll
           for (int r = 0; r < R; ++r) acc[r] = fmaf(s[r], scale, acc[r]);
         }
       }
-      gate = slot_gate(zc, ok, width, a.sigmoid, a.normalize, ref, sum);
+      gate = slot_gate<SIG>(zc, ok, width, a.normalize, ref, sum);
       if (ok) {
         if (nan) gate = __int_as_float(0x7fc00000);
         atomicAdd(cnt + mine, 1u);
       }
     }
     if (lane < k) {
-      a.gates[t * k + lane] = gate;
-      a.chosen[t * k + lane] = mine;
+      *gate_at = gate;
+      *chosen_at = mine;
     }
+    here += row_step;
+    ahead += row_step;
+    gate_at += slot_step;
+    chosen_at += slot_step;
     used = use_next;
     __syncwarp();  // the stage is free to be filled
   }
@@ -492,7 +513,7 @@ constexpr size_t route_smem(int E) {
 
 // Few tokens: one cluster, the CTAs' sums joined through distributed shared
 // memory; one launch and no workspace.
-template <typename T, int R>
+template <typename T, int R, bool SIG>
 __global__ void __launch_bounds__(WARPS<R> * 32) __cluster_dims__(CLUSTER, 1, 1) k_route_one(RouteArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int NW = WARPS<R>;
@@ -504,7 +525,7 @@ __global__ void __launch_bounds__(WARPS<R> * 32) __cluster_dims__(CLUSTER, 1, 1)
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  route_tokens<T, R>(a, cnt, psum, stage, smem);
+  route_tokens<T, R, SIG>(a, cnt, psum, stage, smem);
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   unsigned long long n = 0;
@@ -527,7 +548,7 @@ __global__ void __launch_bounds__(WARPS<R> * 32) __cluster_dims__(CLUSTER, 1, 1)
 }
 
 // Many tokens: each CTA writes its sums, and k_route_join adds them up.
-template <typename T, int R>
+template <typename T, int R, bool SIG>
 __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route(RouteArgs a, float* part_p, unsigned* part_c) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int NW = WARPS<R>;
@@ -539,7 +560,7 @@ __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route(RouteArgs a,
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  route_tokens<T, R>(a, cnt, psum, stage, smem);
+  route_tokens<T, R, SIG>(a, cnt, psum, stage, smem);
   for (int e = threadIdx.x; e < E; e += NW * 32) {
     part_c[int64_t(blockIdx.x) * E + e] = cnt[e];
     if (a.loss) part_p[int64_t(blockIdx.x) * E + e] = psum[e];
@@ -596,7 +617,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) __cluster_dims__(CLUSTER, 1, 1)
 //   + p_i ([i chosen] dg_i - sum_j p_j dg_j)         softmax
 //   + g_j dg_j                                       sigmoid
 // and dz = dy (softmax) or dy sigmoid(-z).
-template <typename T, int R>
+template <typename T, int R, bool SIG>
 __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route_backward(RouteBackwardArgs a) {
   using P = Part<T, R>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -637,17 +658,31 @@ __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route_backward(Rou
 #pragma unroll
     for (int r = 0; r < R; ++r) share[r] = f * static_cast<float>(c[r]);
   }
-  int64_t next_mine = t < a.tokens && lane < k ? a.chosen[t * k + lane] : -1;
-  float next_dg = a.grad_gates && t < a.tokens && lane < k ? a.grad_gates[t * k + lane] : 0.f;
+  // A slot's expert as 32 bits, -1 for what is outside [0, E).
+  auto slot = [&](int64_t e) { return e >= 0 && e < E ? static_cast<int>(e) : -1; };
+  const int64_t* chosen_at = a.chosen + t * k + lane;
+  const float* dg_at = a.grad_gates ? a.grad_gates + t * k + lane : nullptr;
+  const T* here = logits + t * a.ld;
+  const T* ahead = here + (S - 1) * step * a.ld;
+  T* out_at = grad + t * a.grad_ld;
+  const int64_t row_step = step * a.ld, out_step = step * a.grad_ld, slot_step = step * k;
+  int next_mine = t < a.tokens && lane < k ? slot(*chosen_at) : -1;
+  float next_dg = dg_at && t < a.tokens && lane < k ? *dg_at : 0.f;
   for (int at = 0; t < a.tokens; t += step, at = at + 1 < S ? at + 1 : 0) {
-    const int64_t mine = next_mine;
-    const bool ok = mine >= 0 && mine < E;
+    const int mine = next_mine;
+    const bool ok = mine >= 0;
     const float dg = ok ? next_dg : 0.f;
-    const int64_t ahead = t + (S - 1) * step;
-    if constexpr (S > 0) ring.fetch(logits + ahead * a.ld, E, ahead < a.tokens, at > 0 ? at - 1 : S - 1);
+    const T* const this_row = here;
+    T* const out = out_at;
+    if constexpr (S > 0) ring.fetch(ahead, E, t + (S - 1) * step < a.tokens, at > 0 ? at - 1 : S - 1);
+    here += row_step;
+    ahead += row_step;
+    out_at += out_step;
+    chosen_at += slot_step;
+    if (dg_at) dg_at += slot_step;
     if (lane < k && t + step < a.tokens) {
-      next_mine = a.chosen[(t + step) * k + lane];
-      if (a.grad_gates) next_dg = a.grad_gates[(t + step) * k + lane];
+      next_mine = slot(*chosen_at);
+      if (dg_at) next_dg = *dg_at;
     }
     const int filled = __popc(__ballot_sync(FULL_MASK, ok));
     float z[R], s[R];
@@ -655,17 +690,17 @@ __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route_backward(Rou
     if (!filled) {  // masked, or nothing to choose: no gradient
 #pragma unroll
       for (int r = 0; r < R; ++r) s[r] = 0.f;
-      store_part<T, R>(grad + t * a.grad_ld, E, out_vec, s);
+      store_part<T, R>(out, E, out_vec, s);
       __syncwarp();
       continue;
     }
-    const T* row = ring.row(logits + t * a.ld, at);
+    const T* row = ring.row(this_row, at);
     load_part<T, R>(row, E, vec, z);
     float m = -INFINITY;
 #pragma unroll
     for (int r = 0; r < R; ++r) m = fmaxf(m, z[r]);
     m = key_to_float(__reduce_max_sync(FULL_MASK, ord_key(m)));
-    const float sum = token_scores<R>(z, s, a.sigmoid, m), inv = __fdividef(1.f, sum);
+    const float sum = token_scores<SIG, R>(z, s, m), inv = lm_rcp(sum);
     const float n_t = static_cast<float>(filled);
     float dot = 0.f;
     if (a.grad_loss) {
@@ -675,9 +710,9 @@ __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route_backward(Rou
     }
     if (a.grad_gates) {
       const float zc = ok ? lm_float(row[mine]) : -INFINITY;
-      const float g = slot_gate(zc, ok, width, a.sigmoid, a.normalize, m, sum);
+      const float g = slot_gate<SIG>(zc, ok, width, a.normalize, m, sum);
       float d = g * dg;
-      if (a.normalize || !a.sigmoid) {
+      if (a.normalize || !SIG) {
         const float gd = __shfl_sync(FULL_MASK, slots_sum(d, width), 0);
         if (a.normalize)
           d = g * (dg - gd);
@@ -687,17 +722,27 @@ __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route_backward(Rou
       if (ok) extra[mine] = d;
       __syncwarp();
     }
+    float chosen_part[R];
+    load_shared<T, R>(extra, chosen_part);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float dy = fmaf(s[r] * inv, fmaf(share[r], n_t, -dot), extra[P::expert(r)]);
-      if (a.sigmoid) dy *= sigmoid(-z[r]);
+      float dy = fmaf(s[r] * inv, fmaf(share[r], n_t, -dot), chosen_part[r]);
+      if constexpr (SIG) {  // sigmoid(-z) = e^-z sigmoid(z), with e^-z kept finite
+        const float u = fminf(lm_exp2(-LOG2E * z[r]), 1e30f);
+        dy *= u * lm_rcp(1.f + u);
+      }
       s[r] = dy;
     }
-    store_part<T, R>(grad + t * a.grad_ld, E, out_vec, s);
+    store_part<T, R>(out, E, out_vec, s);
     __syncwarp();
     if (a.grad_gates && ok) extra[mine] = 0.f;
     __syncwarp();
   }
+}
+
+template <typename F>
+cudaError_t by_score(bool sig, F&& f) {
+  return sig ? f(std::true_type{}) : f(std::false_type{});
 }
 
 template <typename F>
@@ -746,39 +791,44 @@ constexpr int64_t ONE_TOKENS = 2 * CLUSTER * WARPS<R>;
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   return by_type(a.type, [&](auto type) {
-    return by_width(a.experts, [&](auto w) {
-      using T = decltype(type);
-      constexpr int R = decltype(w)::value;
-      if (a.tokens <= ONE_TOKENS<R>)
-        return launch_with(k_route_one<T, R>, CLUSTER, WARPS<R> * 32, route_smem<T, R>(a.experts),
-                           stream, a);
-      const int grid = route_grid(a.tokens, WARPS<R>, PER_SM<R>);
-      cudaMemPool_t pool;
-      cudaError_t err = library_pool(&pool);
-      if (err != cudaSuccess) return err;
-      void* part = nullptr;
-      const size_t each = size_t(grid) * a.experts * 4;
-      err = cudaMallocFromPoolAsync(&part, (a.loss ? 2 : 1) * each, pool, stream);
-      if (err != cudaSuccess) return err;
-      unsigned* part_c = static_cast<unsigned*>(part);
-      float* part_p = reinterpret_cast<float*>(static_cast<char*>(part) + each);
-      err = launch_with(k_route<T, R>, grid, WARPS<R> * 32, route_smem<T, R>(a.experts), stream, a, part_p, part_c);
-      if (err == cudaSuccess)
-        err = launch_kernel(k_route_join, dim3(CLUSTER), dim3(JOIN_THREADS), 0, stream, grid, a.experts, part_p, part_c,
-                            a.counts, a.loss);
-      const cudaError_t freed = cudaFreeAsync(part, stream);
-      return err != cudaSuccess ? err : freed;
+    return by_width(a.experts, [&](auto width) {
+      return by_score(a.sigmoid, [&](auto sig) {
+        using T = decltype(type);
+        constexpr int R = decltype(width)::value;
+        constexpr bool SIG = decltype(sig)::value;
+        const size_t smem = route_smem<T, R>(a.experts);
+        if (a.tokens <= ONE_TOKENS<R>)
+          return launch_with(k_route_one<T, R, SIG>, CLUSTER, WARPS<R> * 32, smem, stream, a);
+        const int grid = route_grid(a.tokens, WARPS<R>, PER_SM<R>);
+        cudaMemPool_t pool;
+        cudaError_t err = library_pool(&pool);
+        if (err != cudaSuccess) return err;
+        void* part = nullptr;
+        const size_t each = size_t(grid) * a.experts * 4;
+        err = cudaMallocFromPoolAsync(&part, (a.loss ? 2 : 1) * each, pool, stream);
+        if (err != cudaSuccess) return err;
+        unsigned* part_c = static_cast<unsigned*>(part);
+        float* part_p = reinterpret_cast<float*>(static_cast<char*>(part) + each);
+        err = launch_with(k_route<T, R, SIG>, grid, WARPS<R> * 32, smem, stream, a, part_p, part_c);
+        if (err == cudaSuccess)
+          err = launch_kernel(k_route_join, dim3(CLUSTER), dim3(JOIN_THREADS), 0, stream, grid, a.experts, part_p, part_c,
+                              a.counts, a.loss);
+        const cudaError_t freed = cudaFreeAsync(part, stream);
+        return err != cudaSuccess ? err : freed;
+      });
     });
   });
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
   return by_type(a.type, [&](auto type) {
-    return by_width(a.experts, [&](auto w) {
-      using T = decltype(type);
-      constexpr int R = decltype(w)::value;
-      return launch_with(k_route_backward<T, R>, route_grid(a.tokens, WARPS<R>, PER_SM<R>), WARPS<R> * 32,
-                         size_t(WARPS<R>) * (Ring<T, R>::BYTES + 32 * R * 4), stream, a);
+    return by_width(a.experts, [&](auto width) {
+      return by_score(a.sigmoid, [&](auto sig) {
+        using T = decltype(type);
+        constexpr int R = decltype(width)::value;
+        return launch_with(k_route_backward<T, R, decltype(sig)::value>, route_grid(a.tokens, WARPS<R>, PER_SM<R>),
+                           WARPS<R> * 32, size_t(WARPS<R>) * (Ring<T, R>::BYTES + 32 * R * 4), stream, a);
+      });
     });
   });
 }
