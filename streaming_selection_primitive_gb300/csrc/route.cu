@@ -727,10 +727,7 @@ __global__ void __launch_bounds__(WARPS<R> * 32, PER_SM<R>) k_route_backward(Rou
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float dy = fmaf(s[r] * inv, fmaf(share[r], n_t, -dot), chosen_part[r]);
-      if constexpr (SIG) {  // sigmoid(-z) = e^-z sigmoid(z), with e^-z kept finite
-        const float u = fminf(lm_exp2(-LOG2E * z[r]), 1e30f);
-        dy *= u * lm_rcp(1.f + u);
-      }
+      if constexpr (SIG) dy *= sigmoid(-z[r]);
       s[r] = dy;
     }
     store_part<T, R>(out, E, out_vec, s);
