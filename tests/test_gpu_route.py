@@ -113,6 +113,20 @@ def test_strides_and_alignment(pk, cuda_device, dtype, E, ld, offset):
     assert torch.equal(got, pk.route_backward(z, r, grad_gates=dg)) and (wide[:, :3] == 7).all() and (wide[:, 3 + E:] == 7).all()
 
 
+def test_rows_far_apart(pk, cuda_device):
+    # Offsets of logits and their gradient past 2^31 elements.
+    E, far = 100, (1 << 30) + 512
+    z = torch.randn((4, E), device=cuda_device).to(torch.bfloat16)
+    store, grad = (torch.empty(3 * far + E, dtype=torch.bfloat16, device=cuda_device).as_strided((4, E), (far, 1))
+                   for _ in range(2))
+    store.copy_(z)
+    want, got = pk.route(z, 5), pk.route(store, 5)
+    assert all(torch.equal(getattr(got, f), getattr(want, f)) for f in ("gates", "experts", "counts", "loss"))
+    dg, dl = torch.randn_like(got.gates), torch.ones((), device=cuda_device)
+    pk.route_backward(store, got, grad_gates=dg, grad_loss=dl, out=grad)
+    assert torch.equal(grad, pk.route_backward(z, want, grad_gates=dg, grad_loss=dl))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("normalize", [True, False])
 @pytest.mark.parametrize("dtype", TYPES)

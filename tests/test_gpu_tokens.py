@@ -91,6 +91,61 @@ def test_batches(pk, cuda_device, rows, n):
     check(pk, logits, noise, T=0.9)
 
 
+@pytest.mark.parametrize("how", ["k2000", "p.9", "p.999 hot", "min_p", "all cold", "kp"])
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 9001), (torch.bfloat16, 20004), (torch.float16, 3000)])
+def test_more_rows_than_processors(pk, cuda_device, dtype, n, how):
+    # Rows that a CTA alone cannot finish are left to clusters.
+    logits, noise = inputs(320, n, dtype, 31, cuda_device)
+    logits[::7] *= 0.02  # flat: thousands of tokens are kept
+    logits[3::31] = float("-inf")
+    logits[5, 17] = float("nan")
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(2)
+    mask = torch.randint(-(1 << 31), 1 << 31, (320, (n + 31) // 32), generator=g, device=cuda_device).to(torch.int32)
+    mask[9::40] = 0
+    got, lp = check(pk, logits, noise, **FILTERS[how])
+    assert (got[3::31] == -1).all() and (lp[3::31] == -np.inf).all() and got[5] == -1 and np.isnan(lp[5])
+    got, lp = check(pk, logits, noise, mask=mask, **FILTERS[how])
+    assert (got[9::40] == -1).all()
+
+
+@pytest.mark.parametrize("rows", [30, 76, 320])
+@pytest.mark.parametrize("k", [63, 64, 65, 128, 129, 255, 256, 257, 511, 600])
+def test_list_lengths(pk, cuda_device, k, rows):
+    # Around the lengths where the ranked lists end, with ties across the cut.
+    logits, noise = inputs(rows, 6000, torch.float32, k, cuda_device)
+    logits[::2] = (logits[::2] * 8).round() / 8
+    check(pk, logits, noise, k=k, most_unclear=0.03)
+    check(pk, logits, noise, k=k, p=0.97, min_p=0.004, most_unclear=0.03)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 18, 37, 75])
+def test_clusters(pk, cuda_device, rows, dtype):
+    # 8, 8, 4 and 2 CTAs a row; flat and steep rows, kept tokens side by side or apart.
+    logits, noise = inputs(rows, 40009, dtype, 41, cuda_device)
+    logits[::3] *= 0.1
+    logits[1::5] = torch.sort(logits[1::5], dim=1).values
+    for how in ("k2000", "p.9", "p.999 hot", "kp", "min_p", "none"):
+        check(pk, logits, noise, most_unclear=0.05, **FILTERS[how])
+
+
+def test_rows_far_apart(pk, cuda_device):
+    # Offsets of logits and noise past 2^31 elements.
+    n, far = 5000, (1 << 30) + 1024
+    store = torch.empty(2 * far + n, dtype=torch.bfloat16, device=cuda_device)
+    numbers = torch.empty(2 * far + n, device=cuda_device)
+    logits, noise = (t.as_strided((3, n), (far, 1)) for t in (store, numbers))
+    a, b = inputs(3, n, torch.bfloat16, 51, cuda_device)
+    logits.copy_(a)
+    noise.copy_(b)
+    for how in ({"k": 40}, {"p": 0.95}, {}):
+        want = pk.sample_tokens(a, b, top_k=how.get("k", 0), top_p=how.get("p", 1.0))
+        got = pk.sample_tokens(logits, noise, top_k=how.get("k", 0), top_p=how.get("p", 1.0))
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        check(pk, a, b, **how)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("ld,offset", [(10007, 0), (10008, 0), (10016, 1), (10011, 3), (12000, 8)])
 def test_strides_and_alignment(pk, cuda_device, dtype, ld, offset):
