@@ -135,6 +135,8 @@ struct Shared {
   unsigned slot, merged, hits, marks[WARPS];
   unsigned captured;  // keys that the first level found, in `candidates` unless there are more than fit
   unsigned short hit[THREADS];
+  alignas(16) uint32_t maxima[THREADS];
+  float tau;
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
@@ -190,6 +192,23 @@ __device__ __forceinline__ float lm_log2_normal(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two floats at a time.
+__device__ __forceinline__ u64 pair_of(float a, float b) {
+  return u64(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float pair_low(u64 a) { return __uint_as_float(static_cast<unsigned>(a)); }
+__device__ __forceinline__ float pair_high(u64 a) { return __uint_as_float(static_cast<unsigned>(a >> 32)); }
+__device__ __forceinline__ u64 pair_add(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 pair_mul(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // One row as a CTA of its cluster sees it.  Positions are counted from the
@@ -326,6 +345,21 @@ struct Slice {
 #pragma unroll
       for (int j = 0; j < d; ++j) w[j] += w[j + d];
     return w[0];
+  }
+  // The same where neither m nor 1 / T is infinite, two at a time.
+  __device__ __forceinline__ float finite_weights(const float (&x)[VEC]) const {
+    const u64 less = pair_of(-m, -m), by = pair_of(inv2, inv2);
+    u64 w[VEC / 2];
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+      const u64 y = pair_mul(pair_add(pair_of(x[2 * j], x[2 * j + 1]), less), by);
+      w[j] = pair_of(lm_exp2(pair_low(y)), lm_exp2(pair_high(y)));
+    }
+#pragma unroll
+    for (int d = VEC / 4; d; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < d; ++j) w[j] = pair_add(w[j], w[j + d]);
+    return pair_low(w[0]) + pair_high(w[0]);
   }
   __device__ __forceinline__ u64 fixed(float w) const { return __float2ull_rn(w * scale); }
 
@@ -631,29 +665,48 @@ __device__ __forceinline__ u64 mass_target(float p, u64 Z) {
 }
 
 // A value that at least `want` of the block's thread maxima reach, and not many
-// more: bisection over the keys between the least maximum and the largest
-// (each under a count over the block).  -inf if there are no more than `want`.
+// more: bisection over the keys between the least maximum and the largest, by
+// one warp (a count over the block would be a barrier a step: 6 us a row where
+// this takes MEASURE).  -inf if there are no more than `want`.
 __device__ __forceinline__ float block_tau(float top, float widest, int want, Shared& s) {
-  const uint32_t key = choice_key(top);
-  const uint32_t least = __reduce_min_sync(FULL_MASK, key ? key : ~0u);
-  if ((threadIdx.x & 31) == 0) s.redk[threadIdx.x >> 5] = least;
-  int count = __syncthreads_count(key != 0u);
-  if (count <= want) return -INFINITY;
-  uint32_t lo = s.redk[0], hi = choice_key(widest) + 1u;
+  s.maxima[threadIdx.x] = choice_key(top);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    uint4 key[WARPS / 4];
 #pragma unroll
-  for (int w = 1; w < WARPS; ++w) lo = min(lo, s.redk[w]);
-#pragma unroll 1
-  while (hi - lo > 1u && count > want + want / 8 + 4) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int c = __syncthreads_count(key >= mid);
-    if (c >= want) {
-      lo = mid;
-      count = c;
+    for (int i = 0; i < WARPS / 4; ++i) key[i] = reinterpret_cast<const uint4*>(s.maxima)[i * 32 + threadIdx.x];
+    auto reach = [&](uint32_t least) {
+      unsigned c = 0;
+#pragma unroll
+      for (int i = 0; i < WARPS / 4; ++i)
+        c += (key[i].x >= least) + (key[i].y >= least) + (key[i].z >= least) + (key[i].w >= least);
+      return static_cast<int>(__reduce_add_sync(FULL_MASK, c));
+    };
+    uint32_t lo = ~0u, hi = choice_key(widest) + 1u;
+#pragma unroll
+    for (int i = 0; i < WARPS / 4; ++i)  // (a key of 0, less 1, is the largest number)
+      lo = min(min(min(lo, key[i].x - 1u), min(key[i].y - 1u, key[i].z - 1u)), key[i].w - 1u);
+    lo = __reduce_min_sync(FULL_MASK, lo) + 1u;
+    int count = reach(1u);
+    if (count <= want) {
+      lo = KEY_NEG_INF;
     } else {
-      hi = mid;
+#pragma unroll 1
+      while (hi - lo > 1u && count > want + want / 8 + 4) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int c = reach(mid);
+        if (c >= want) {
+          lo = mid;
+          count = c;
+        } else {
+          hi = mid;
+        }
+      }
     }
+    if (threadIdx.x == 0) s.tau = key_to_float(lo);
   }
-  return key_to_float(lo);
+  __syncthreads();
+  return s.tau;
 }
 
 // body(i, rank) for every candidate, rank being the number of larger ones (they
@@ -1034,45 +1087,46 @@ __device__ __forceinline__ void merge_keys(Shared& s, int C, int want) {
   __syncthreads();
 }
 
-// Mass of the list s.sorted[0 .. got) (one warp).
+// The race over the list s.sorted[0 .. got) (one warp): the tokens before which
+// the mass is below the target, and whose weight is at least floor_w.  False,
+// without a race, if the list does not hold all of them: `whole` says that
+// it does in any case; otherwise it has to reach the mass or to fall below
+// floor_w.  by_k: the mass is the list's.
 template <typename S>
-__device__ __forceinline__ u64 list_mass(const S& sl, const Shared& s, int got) {
-  u64 sum = 0;
+__device__ __forceinline__ bool race_list(const S& sl, const Shared& s, int got, bool whole, bool by_k, bool by_p, float p,
+                                          u64 Z, float floor_w, bool greedy, int64_t* token, float* logprob) {
+  // A lane takes neighbouring keys, so that one scan over the lanes does.
+  const int lane = threadIdx.x & 31, each = (got + 31) >> 5, first = lane * each, end = min(first + each, got);
+  u64 mine = 0;
 #pragma unroll 1
-  for (int at = threadIdx.x & 31; at < got; at += 32) sum += sl.fixed(sl.weight(sl.logit_of(s.sorted[at])));
-  return warp_sum64(sum);
-}
-
-// The race over a list that holds all that can be kept: the tokens before which
-// the mass is below `target` and whose weight is at least floor_w (one warp).
-template <typename S>
-__device__ __forceinline__ void race_list(const S& sl, const Shared& s, int got, u64 target, float floor_w, bool greedy,
-                                          int64_t* token, float* logprob) {
-  const int lane = threadIdx.x & 31;
-  u64 kept = 0, above = 0;
+  for (int at = first; at < end; ++at) mine += sl.fixed(sl.weight(sl.logit_of(s.sorted[at])));
+  u64 above = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 o = __shfl_up_sync(FULL_MASK, above, d);
+    if (lane >= d) above += o;
+  }
+  const u64 total = __shfl_sync(FULL_MASK, above, 31);
+  above -= mine;
+  const u64 target = by_p ? mass_target(p, by_k ? total : Z) : ~u64(0);
+  const float last = got ? sl.weight(sl.logit_of(s.sorted[got - 1])) : 0.f;
+  if (!whole && !(by_p && total >= target) && !(last < floor_w)) return false;
+  u64 kept = 0;
   Best best{-INFINITY, 0.f, NONE};
 #pragma unroll 1
-  for (int base = 0; base < got && above < target; base += 32) {
-    const int at = base + lane;
-    const bool some = at < got;
-    const u64 key = some ? s.sorted[at] : 0;
-    const float l = some ? sl.logit_of(key) : -INFINITY, w = some ? sl.weight(l) : 0.f;
+  for (int at = first; at < end && (above < target || at == 0); ++at) {
+    const u64 key = s.sorted[at];
+    const float l = sl.logit_of(key), w = sl.weight(l), x = sl.x(l);
     const u64 part = sl.fixed(w);
-    u64 with = part;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const u64 o = __shfl_up_sync(FULL_MASK, with, d);
-      if (lane >= d) with += o;
-    }
-    if (some && (above + with - part < target || at == 0) && w >= floor_w && sl.x(l) > -INFINITY) {
-      kept += part;
-      better(best, Best{greedy ? 0.f : race(sl.x(l), s.sorted_q[at]), l, static_cast<unsigned>(sl.index_of(key))});
-    }
-    above += __shfl_sync(FULL_MASK, with, 31);
+    above += part;
+    if (!(w >= floor_w) || x == -INFINITY) continue;
+    kept += part;
+    better(best, Best{greedy ? 0.f : race(x, s.sorted_q[at]), l, static_cast<unsigned>(sl.index_of(key))});
   }
   kept = warp_sum64(kept);
   warp_best(best);
   if (lane == 0) write_row(sl, best, kept, greedy, token, logprob);
+  return true;
 }
 
 // Running maximum (NaN if there is one) over whole vectors of logits.
@@ -1318,24 +1372,18 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
         for (int i = 0; i < AHEAD; ++i)
           if (in[i]) packed.take(bits[i]);
       } else {
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-          if (in[0]) {
-            float x[VEC];
-            sl.unpack(bits[0], x);
-            const float before = top;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) top = max_nan(top, x[j]);
-            if (top > -INFINITY) {
-              rescale(before);
-              mass += sl.weights(x);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j + 1 < AHEAD; ++j) {
-            bits[j] = bits[j + 1];
-            in[j] = in[j + 1];
-          }
+          if (!in[i]) continue;
+          VectorMax<T> peak;
+          peak.take(bits[i]);
+          const float before = top;
+          top = max_nan(top, peak.get());
+          if (top != before) rescale(before);
+          if (top == -INFINITY) continue;
+          float x[VEC];
+          sl.unpack(bits[i], x);
+          mass += top < INFINITY && sl.inv2 < INFINITY ? sl.finite_weights(x) : sl.weights(x);
         }
       }
     }
@@ -1534,13 +1582,8 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
         const int got = found < want ? found : want;
         if (!alone) merge_keys(s, C, want);
         if (warp == 0) {
-          // Enough: the list holds everything, or reaches the mass, or falls below min-p.
-          const u64 total = list_mass(sl, s, got);
-          if (by_k) Z = total;
-          const u64 target = by_p ? mass_target(p, Z) : ~u64(0);
-          const float last = got ? sl.weight(sl.logit_of(s.sorted[got - 1])) : 0.f;
-          enough = !decide || found < want || (by_p && total >= target) || last < floor_w;
-          if (enough) race_list(sl, s, got, target, floor_w, greedy, a.out_tokens + r, a.out_logprobs + r);
+          enough = race_list(sl, s, got, !decide || found < want, by_k, by_p, p, Z, floor_w, greedy, a.out_tokens + r,
+                             a.out_logprobs + r);
           if (phase == Phase::Only && decide && lane < C) cluster.map_shared_rank(&s, lane)->enough = enough;
         }
       }
