@@ -56,6 +56,7 @@ constexpr int TOP = 256;        // keys that step 2 can sort in a CTA that has t
 constexpr int TOP_SHARED = 128; // and in a cluster's
 constexpr int TOP_MIN_P = 64;   // and those that min-p seldom leaves more of
 constexpr int CANDIDATES = 1024;
+constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds the cut
 constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
@@ -98,6 +99,12 @@ struct Late {
   bool by_k, by_p;
 };
 
+// What scan_row tells: the best of the tokens above the list, their mass, and that of those which min-p keeps.
+struct Scan {
+  Best best;
+  u64 mass, kept;
+};
+
 struct Shared {
   // Written by other CTAs of the cluster.
   union {
@@ -117,13 +124,19 @@ struct Shared {
   int enough;
   Best ex_best[MAX_CLUSTER];
   u64 ex_kept[MAX_CLUSTER];
-  u64 beyond[MAX_CLUSTER];
+  u64 beyond[MAX_CLUSTER];  // mass above the list
+  unsigned lists[MAX_CLUSTER];
   // This CTA's own.
   alignas(16) unsigned count[BINS];
   alignas(16) unsigned lo[BINS];  // 64-bit masses in two words
   alignas(16) unsigned hi[BINS];
-  alignas(16) u64 candidates[CANDIDATES + 2];
-  float candidates_q[CANDIDATES];
+  union {
+    struct {
+      alignas(16) u64 candidates[CANDIDATES + 2];
+      float candidates_q[CANDIDATES];
+    };
+    int list_at[LISTED];  // step 4: their indices
+  };
   unsigned own_sample[SAMPLE_BINS];
   alignas(16) float row_sample[SAMPLE_BINS];
   u64 sorted[TOP];  // of step 3's list, or step 4's
@@ -133,7 +146,7 @@ struct Shared {
   uint32_t redk[WARPS];
   Best best[WARPS];
   unsigned slot, merged, hits, marks[WARPS];
-  unsigned captured;  // keys that the first level found, in `candidates` unless there are more than fit
+  unsigned listed;  // tokens that scan_row found for the list (which holds them unless there are more than fit)
   unsigned short hit[THREADS];
   alignas(16) uint32_t maxima[THREADS];
   float tau;
@@ -238,6 +251,9 @@ struct Slice {
 
   __device__ __forceinline__ bool inside(int v) const { return v >= in0 && v < in1; }
 
+  // -inf, in each element of a packed word.
+  static constexpr unsigned NOTHING = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+
   // Elements that are not allowed become -inf, in the packed vector.
   __device__ __forceinline__ uint4 hide(int i, uint4 bits) const {
     const int at = i & 31;
@@ -247,11 +263,10 @@ struct Slice {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (sizeof(T) == 4) {
-        b[j] = ok >> j & 1u ? b[j] : 0xff800000u;
+        b[j] = ok >> j & 1u ? b[j] : NOTHING;
       } else {
-        constexpr unsigned low = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
         const unsigned keep = (ok >> 2 * j & 1u) * 0xffffu | (ok >> (2 * j + 1) & 1u) * 0xffff0000u;
-        b[j] = (b[j] & keep) | (low * 0x10001u & ~keep);
+        b[j] = (b[j] & keep) | (NOTHING & ~keep);
       }
     }
     return bits;
@@ -273,6 +288,17 @@ struct Slice {
     for (int j = 0; j < VEC; ++j) x[j] = lm_float(u.t[j]);
   }
 
+  // The first four elements of packed ones.
+  __device__ __forceinline__ void unpack4(uint4 bits, float (&x)[4]) const {
+    union {
+      uint4 bits;
+      T t[VEC];
+    } u;
+    u.bits = bits;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = lm_float(u.t[j]);
+  }
+
   // Any vector; elements outside the row or not allowed are -inf.
   __device__ __forceinline__ void load(int v, float (&x)[VEC]) const {
     unpack(inside(v) ? whole(v) : edge[v < in0 ? 0 : 1], x);
@@ -281,14 +307,11 @@ struct Slice {
   // Element j of a vector (inside the row, allowed).
   __device__ __forceinline__ float one(int v, int j) const { return lm_float(row[element(v) + j]); }
 
-  // body(l, i, given(i), place) for every element of the slice in [floor, ceil]
-  // (floor finite or +inf).  A lane first marks those of several vectors and
-  // then takes BATCH of them at a time, so that the lanes' hits meet in the same
-  // turns and what `given` reads for them is under way together.  each(x) sees every
-  // vector that is looked at.  place: the element's own in a list of the given
-  // length (null: none is kept).
-  template <int BATCH, typename E, typename G, typename F>
-  __device__ __forceinline__ void among(float floor, float ceil, unsigned* length, E&& each, G&& given, F&& body) const {
+  // body(l, i) for every element of the slice in [floor, ceil] (floor finite or
+  // +inf).  A lane first marks those of several vectors and then takes them one
+  // by one, so that the lanes' hits meet in the same turns.
+  template <typename F>
+  __device__ __forceinline__ void among(float floor, float ceil, F&& body) const {
     constexpr int GROUP = 32 / VEC;
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -300,7 +323,6 @@ struct Slice {
         if (u < nv) {
           float x[VEC];
           load(u, x);
-          each(x);
           unsigned some = 0;
 #pragma unroll
           for (int j = 0; j < VEC; ++j) some |= x[j] >= floor && x[j] <= ceil ? 1u << j : 0u;
@@ -308,26 +330,11 @@ struct Slice {
         }
       }
 #pragma unroll 1
-      while (__any_sync(FULL_MASK, hits != 0u)) {
-        float l[BATCH];
-        int at[BATCH];
-        decltype(given(0)) what[BATCH];
-        const int some = min(__popc(hits), BATCH);
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-          if (i < some) {
-            const int b = __ffs(hits) - 1, u = base + lane + b / VEC * THREADS;
-            hits &= hits - 1;
-            at[i] = element(u) + b % VEC;
-            l[i] = one(u, b % VEC);
-            what[i] = given(at[i]);
-          }
-        const unsigned place = length ? warp_reserve(length, some) : 0u;
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-          if (i < some) body(l[i], at[i], what[i], place + i);
-        __syncwarp();
+      for (; hits; hits &= hits - 1) {
+        const int b = __ffs(hits) - 1, u = base + lane + b / VEC * THREADS;
+        body(one(u, b % VEC), element(u) + b % VEC);
       }
+      __syncwarp();
     }
   }
 
@@ -449,46 +456,32 @@ struct Level {
 // The histogram, joined over the cluster, and the bin where the running count
 // (or mass) from the top first reaches `target`: s.bin, s.above_*, s.in_c;
 // s.bin = BINS where it does not.  What lies above the first level's ceil
-// counts as above (its mass only).  fresh: the joined histogram is in place.
+// counts as above (its mass only, s.beyond).  fresh: the joined histogram is in
+// place.  listed: s.list_at holds all that the first level counts.
 template <typename S>
 __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const Level& lv, bool by_mass,
-                                      u64 target, bool fresh) {
-  const bool over = lv.bin0 < 0 && lv.ceil < sl.m, capture = lv.bin0 < 0;
+                                      u64 target, bool fresh, bool listed) {
   if (!fresh) {
 #pragma unroll 1
     for (int b = threadIdx.x; b < BINS; b += THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0u;
-    if (capture && threadIdx.x == 0) s.captured = 0;
     __syncthreads();
-    u64 beyond = 0;
-    float partial = 0.f;
-    int vectors = 0;
-    sl.template among<1>(
-        lv.floor, lv.ceil, capture ? &s.captured : nullptr,
-        [&](const float (&x)[S::VEC]) {
-          if (!over) return;
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < S::VEC; ++j) sum += x[j] > lv.ceil ? sl.weight(x[j]) : 0.f;
-          partial += sum;
-          if (++vectors % 16 == 0) {
-            beyond += sl.fixed(partial);
-            partial = 0.f;
-          }
-        },
-        [](int) { return 0; },
-        [&](float l, int i, int, unsigned place) {
-          const int b = lv.bin_of(sl, l, i);
-          if (b < 0) return;
-          if (capture && place < CANDIDATES) s.candidates[place] = sl.key(l, i);
-          const u64 mass = sl.fixed(sl.weight(l));
-          atomicAdd(&s.count[b], 1u);
-          const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
-          const unsigned mh = static_cast<unsigned>(mass >> 32) + (old + ml < old ? 1u : 0u);
-          if (mh) atomicAdd(&s.hi[b], mh);
-        });
-    if (over) {
-      beyond = block_sum64(beyond + sl.fixed(partial), s);
-      if (threadIdx.x < cluster.num_blocks()) cluster.map_shared_rank(&s, threadIdx.x)->beyond[cluster.block_rank()] = beyond;
+    auto add = [&](float l, int i) {
+      const int b = lv.bin_of(sl, l, i);
+      if (b < 0) return;
+      const u64 mass = sl.fixed(sl.weight(l));
+      atomicAdd(&s.count[b], 1u);
+      const unsigned ml = static_cast<unsigned>(mass), old = atomicAdd(&s.lo[b], ml);
+      const unsigned mh = static_cast<unsigned>(mass >> 32) + (old + ml < old ? 1u : 0u);
+      if (mh) atomicAdd(&s.hi[b], mh);
+    };
+    if (listed) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < static_cast<int>(s.listed); i += THREADS) {
+        const int at = s.list_at[i];
+        add(lm_float(sl.row[at]), at);
+      }
+    } else {
+      sl.among(lv.floor, lv.ceil, add);
     }
     cluster.sync();
     // This CTA joins its share of the bins: of C neighbouring threads each reads
@@ -525,7 +518,7 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
     cluster.sync();
   }
   u64 base = 0;
-  if (over)
+  if (lv.bin0 < 0 && lv.ceil < sl.m)
 #pragma unroll 1
     for (int i = 0; i < static_cast<int>(cluster.num_blocks()); ++i) base += s.beyond[i];
   // Thread t takes bin t.
@@ -550,11 +543,11 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
 // it (then s.total_m is its mass).
 template <typename S>
 __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level lv, bool by_mass, u64 target, int which,
-                       bool& fresh) {
+                       bool& fresh, bool listed) {
   u64 above_c = 0, above_m = 0;
 #pragma unroll 1
   for (int level = 0;; ++level) {
-    cross(sl, s, cluster, lv, by_mass, target - (by_mass ? above_m : above_c), fresh && level == 0);
+    cross(sl, s, cluster, lv, by_mass, target - (by_mass ? above_m : above_c), fresh && level == 0, listed);
     fresh = level == 0;
     if (s.bin == BINS) return false;
     above_c += s.above_c;
@@ -594,18 +587,17 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
         for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->list[which][at] = key;
     };
     if (s.count[bin] != 0u) {
-      if (s.captured <= CANDIDATES) {
+      if (listed) {
 #pragma unroll 1
-        for (int i = threadIdx.x; i < static_cast<int>(s.captured); i += THREADS) {
-          const u64 key = s.candidates[i];
-          if (lv.bin_of(sl, sl.logit_of(key), sl.index_of(key)) == bin) send(key);
+        for (int i = threadIdx.x; i < static_cast<int>(s.listed); i += THREADS) {
+          const int at = s.list_at[i];
+          const float l = lm_float(sl.row[at]);
+          if (lv.bin_of(sl, l, at) == bin) send(sl.key(l, at));
         }
       } else {
-        sl.template among<1>(
-            floor, ceil, nullptr, [](const float (&)[S::VEC]) {}, [](int) { return 0; },
-            [&](float l, int i, int, unsigned) {
-              if (lv.bin_of(sl, l, i) == bin) send(sl.key(l, i));
-            });
+        sl.among(floor, ceil, [&](float l, int i) {
+          if (lv.bin_of(sl, l, i) == bin) send(sl.key(l, i));
+        });
       }
     }
     cluster.sync();
@@ -769,12 +761,14 @@ __device__ __forceinline__ void finish(const S& sl, Shared& s, cg::cluster_group
   warp_best(best);
   if ((threadIdx.x & 31) == 0) s.best[threadIdx.x >> 5] = best;
   __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll 1
-    for (int w = 1; w < WARPS; ++w) better(best, s.best[w]);
-    Shared* leader = cluster.map_shared_rank(&s, 0);
-    leader->ex_best[rank] = best;
-    leader->ex_kept[rank] = kept;
+  if (threadIdx.x < 32) {
+    best = s.best[threadIdx.x & (WARPS - 1)];
+    warp_best(best);
+    if (threadIdx.x == 0) {
+      Shared* leader = cluster.map_shared_rank(&s, 0);
+      leader->ex_best[rank] = best;
+      leader->ex_kept[rank] = kept;
+    }
   }
   cluster.sync();
   if (rank == 0 && threadIdx.x == 0) {
@@ -867,7 +861,7 @@ __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left)
 #pragma unroll
         for (int i = 0; i < j; ++i) above += count[i];
         above *= every;
-        near = above > 4096.f ? fmaxf(point - blur, 0.f) : 0.f;
+        near = above > static_cast<float>(C * LISTED / 2) ? fmaxf(point - blur, 0.f) : 0.f;
       }
       tail += mass[j];
       var += mass[j] * weight[j];
@@ -883,127 +877,217 @@ __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left)
   __syncthreads();
 }
 
-// The race where many tokens take part: every vector of the slice beside its
-// noise; keys from thr up and weights from floor_w up.  Scores are in units of
-// log 2; a vector's best is looked for where it beats the thread's.
+// The slice's tokens in [floor, inf], to the list (s.listed counts them, and is 0
+// before).  The lanes first mark those of several vectors.
 template <typename S>
-__device__ __forceinline__ void race_all(const S& sl, const float* noise, u64 thr, float floor_w, Best& best, u64& kept) {
-  constexpr int VEC = S::VEC;
-  const bool vec = reinterpret_cast<uintptr_t>(noise + sl.element(0)) % 16 == 0;
-  // Kept: above the cut's logit, or its copies up to the cut's index.
-  const float cut = thr ? sl.logit_of(thr) : -FLT_MAX;
-  const int cut_index = thr ? sl.index_of(thr) : sl.n;
-  auto kept_here = [&](float x, int i, float w) {
-    return x > -INFINITY && (x > cut || (x == cut && i <= cut_index)) && w >= floor_w;
-  };
-  float sum = 0.f;
-  int turn = 0;
-  constexpr int AHEAD = 16 / VEC;  // vectors under way a thread
+__device__ __forceinline__ void list_row(const S& sl, Shared& s, float floor) {
+  constexpr int VEC = S::VEC, GROUP = 32 / VEC;
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int v = threadIdx.x; v < sl.nv; v += AHEAD * THREADS) {
-    float x[AHEAD][VEC], q[AHEAD][VEC];
-#pragma unroll
-    for (int g = 0; g < AHEAD; ++g) {
-      const int u = v + g * THREADS, first = sl.element(u);
-      const bool in = u < sl.nv && sl.inside(u);
-      if (in && vec) {
-#pragma unroll
-        for (int j = 0; j < VEC; j += 4) {
-          const float4 f = __ldcs(reinterpret_cast<const float4*>(noise + first + j));
-          q[g][j] = f.x;
-          q[g][j + 1] = f.y;
-          q[g][j + 2] = f.z;
-          q[g][j + 3] = f.w;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          q[g][j] = in || (u < sl.nv && first + j >= 0 && first + j < sl.n) ? noise[first + j] : 1.f;
-      }
+  for (int base = threadIdx.x - lane; base < sl.nv; base += GROUP * THREADS) {
+    unsigned hits = 0;
+#pragma unroll 2
+    for (int g = 0; g < GROUP; ++g) {
+      const int u = base + lane + g * THREADS;
       if (u < sl.nv) {
-        sl.load(u, x[g]);
-      } else {
+        float x[VEC];
+        sl.load(u, x);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) x[g][j] = -INFINITY;
+        for (int j = 0; j < VEC; ++j) hits |= x[j] >= floor ? 1u << (g * VEC + j) : 0u;
       }
     }
-#pragma unroll
-    for (int g = 0; g < AHEAD; ++g) {
-      const int first = sl.element(v + g * THREADS);
-      float w[VEC], score[VEC], most = -INFINITY, least_q = FLT_MAX;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float x2 = fminf((x[g][j] - sl.m) * sl.inv2, 0.f);
-        w[j] = lm_exp2(x2);
-        score[j] = x2 - lm_log2_normal(q[g][j]);
-        const bool some = kept_here(x[g][j], first + j, w[j]);
-        w[j] = some ? w[j] : 0.f;
-        score[j] = some ? score[j] : -INFINITY;
-        most = fmaxf(most, score[j]);  // (NaN noise is never ahead)
-        least_q = fminf(least_q, q[g][j]);
-      }
-#pragma unroll
-      for (int d = VEC / 2; d; d >>= 1)
-#pragma unroll
-        for (int j = 0; j < d; ++j) w[j] += w[j + d];
-      sum += w[0];
-      if (least_q < FLT_MIN || (best.index == NONE && most == -INFINITY)) {
-        // Noise below the normal range, or a first token that is behind all others.
+    unsigned at = warp_reserve(&s.listed, __popc(hits));
 #pragma unroll 1
-        for (int j = 0; j < VEC; ++j) {
-          const int i = first + j;
-          if (i < 0 || i >= sl.n || v + g * THREADS >= sl.nv || !sl.is_allowed(i)) continue;
-          const float l = lm_float(sl.row[i]), x2 = fminf((l - sl.m) * sl.inv2, 0.f);
-          const float exact = fmaxf(x2 - lm_log2(noise[i]), -INFINITY);
-          if (x2 > -INFINITY && kept_here(l, i, lm_exp2(x2)) && (exact > best.score || best.index == NONE))
-            best = Best{exact, l, static_cast<unsigned>(i)};
-        }
-      } else if (most > best.score) {
-        int at = VEC - 1;
-        float l = x[g][VEC - 1];
-#pragma unroll
-        for (int j = VEC - 2; j >= 0; --j)
-          if (score[j] == most) {
-            at = j;
-            l = x[g][j];
-          }
-        best = Best{most, l, static_cast<unsigned>(first + at)};
-      }
+    for (; hits; hits &= hits - 1, ++at) {
+      const int b = __ffs(hits) - 1, u = base + lane + b / VEC * THREADS;
+      if (at < LISTED) s.list_at[at] = sl.element(u) + b % VEC;
     }
-    if (++turn % 16 == 0) {
-      kept += sl.fixed(sum);
-      sum = 0.f;
-    }
+    __syncwarp();
   }
-  kept += sl.fixed(sum);
 }
 
-// 4. The cuts, over everything above a value that is not kept: for top-k one
-// that k keys of one slice reach; for top-p the sample's, or the one at which n
-// tokens together weigh less than what may be left out.  Then the race.  (A
-// function of its own: the registers that it needs would be spilled by rows
-// that never come here, at a microsecond a row.)
+// One pass over the slice and its noise: the race of the tokens above `cut` (its
+// copies up to cut_index included) with a weight of floor_w or more, and a
+// list of those in [floor, cut] that are not above.  The noise is read for
+// all, not to wait for the logits first: where a tenth is kept every sector of
+// it is touched anyway.  Scores are in units of log 2; the best of four
+// elements is looked for where it beats the thread's.  (Four at a time: eight
+// need more registers than there are.)
+template <typename S>
+__device__ __noinline__ Scan scan_row(Shared& s, float cut, int cut_index, float floor) {
+  constexpr int VEC = S::VEC, PARTS = VEC / 4;
+  const S sl = *reinterpret_cast<const S*>(s.slice);
+  const float* noise = s.late.noise + sl.first;
+  const float floor_w = s.late.floor_w;
+  const bool draw = s.late.temperature != 0.f;
+  const bool vec = reinterpret_cast<uintptr_t>(noise) % 16 == 0;
+  const int lane = threadIdx.x & 31;
+  const float next = key_to_float(ord_key(cut) + 1u);  // (NaN above +inf)
+  if (cut == -INFINITY) cut_index = -1;                // what is not allowed
+  Best best{-INFINITY, 0.f, NONE};
+  u64 mass = 0, kept = 0;
+  float sum = 0.f, sum_kept = 0.f;
+  int turn = 0;
+#pragma unroll 1
+  for (int base = threadIdx.x - lane; base < sl.nv; base += THREADS) {
+    const int v = base + lane, at = v * VEC;
+    const bool some_here = v < sl.nv, in = some_here && sl.inside(v);
+    float4 q[PARTS];
+    uint4 bits;
+    if (!draw) {
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) q[h] = make_float4(1.f, 1.f, 1.f, 1.f);
+    } else if (in && vec) {
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) q[h] = __ldcs(reinterpret_cast<const float4*>(noise + at) + h);
+    } else {
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        float* to = &q[h].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = sl.first + at + 4 * h + j;
+          to[j] = some_here && i >= 0 && i < sl.n ? noise[at + 4 * h + j] : 1.f;
+        }
+      }
+    }
+    if (some_here) bits = in ? sl.whole(v) : sl.edge[v < sl.in0 ? 0 : 1];
+    unsigned list = 0;
+    if (!some_here) bits = make_uint4(S::NOTHING, S::NOTHING, S::NOTHING, S::NOTHING);
+#pragma unroll 1
+    for (int h = 0; h < PARTS; ++h) {
+      float x[4];
+      sl.unpack4(bits, x);
+      const float qs[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+      const int first = sl.first + at + 4 * h;
+      // Above: from the cut on up to its index, from the next value on after it.
+      const float least = first <= cut_index ? cut : next;
+      float y[4], w[4], score[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = x[j] >= least ? fminf((x[j] - sl.m) * sl.inv2, 0.f) : -INFINITY;
+        list |= x[j] >= floor && !(x[j] >= least) ? 1u << (4 * h + j) : 0u;
+      }
+      if (first <= cut_index && cut_index < first + 3) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (first + j > cut_index && x[j] == cut) y[j] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = lm_exp2(y[j]);
+        score[j] = y[j] - lm_log2_normal(qs[j]);
+      }
+      sum += (w[0] + w[1]) + (w[2] + w[3]);
+      if (floor_w > 0.f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum_kept += w[j] >= floor_w ? w[j] : 0.f;
+          if (w[j] < floor_w) y[j] = score[j] = -INFINITY;
+        }
+      }
+      const float most = fmaxf(fmaxf(score[0], score[1]), fmaxf(score[2], score[3]));  // (NaN noise is never ahead)
+      const float least_q = fminf(fminf(qs[0], qs[1]), fminf(qs[2], qs[3]));
+      if (least_q < FLT_MIN || (most == -INFINITY && best.index == NONE)) {
+        // Noise below the normal range, or a first token that is behind all others.
+        if (fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float exact = fmaxf(y[j] - lm_log2(qs[j]), -INFINITY);
+            if (y[j] > -INFINITY && (exact > best.score || best.index == NONE))
+              best = Best{exact, x[j], static_cast<unsigned>(first + j)};
+          }
+        }
+      } else if (most > best.score) {
+        int which = 3;
+        float l = x[3];
+#pragma unroll
+        for (int j = 2; j >= 0; --j)
+          if (score[j] == most) {
+            which = j;
+            l = x[j];
+          }
+        best = Best{most, l, static_cast<unsigned>(first + which)};
+      }
+      if constexpr (PARTS > 1) {
+        bits.x = bits.z;
+        bits.y = bits.w;
+        q[0] = q[PARTS - 1];
+      }
+    }
+    if (__any_sync(FULL_MASK, list != 0u)) {
+      unsigned place = warp_reserve(&s.listed, __popc(list));
+#pragma unroll 1
+      for (; list; list &= list - 1, ++place)
+        if (place < LISTED) s.list_at[place] = sl.first + at + __ffs(list) - 1;
+      __syncwarp();
+    }
+    if (++turn % 16 == 0) {
+      mass += sl.fixed(sum);
+      kept += sl.fixed(sum_kept);
+      sum = sum_kept = 0.f;
+    }
+  }
+  mass += sl.fixed(sum);
+  return Scan{best, mass, floor_w > 0.f ? kept + sl.fixed(sum_kept) : mass};
+}
+
+// 4. A list of the tokens among which the cuts lie: for top-k from a value that
+// k keys of one slice reach; for top-p from the sample's, or from the one at
+// which n tokens together weigh less than what may be left out.  The cuts are
+// found in it, and what they leave joins the race.  Where the sample says that
+// the tokens above its point are too many for a list, the pass that makes it
+// races over them at once.  A list that is too long all the same is done
+// without: then each step reads the slice.  (A function of its own: the
+// registers that it needs would be spilled by rows that never come here, at a
+// microsecond a row.)
 template <typename S>
 __device__ __noinline__ void late_row(Shared& s) {
   static_assert(sizeof(S) <= sizeof(s.slice), "room for the slice");
   const S sl = *reinterpret_cast<const S*>(s.slice);
   const Late& late = s.late;
   cg::cluster_group cluster = cg::this_cluster();
-  const float temperature = late.temperature, top = sl.m;
-  const bool greedy = temperature == 0.f;
+  const int C = cluster.num_blocks();
+  const float temperature = late.temperature, top = sl.m, floor_w = late.floor_w;
+  const bool greedy = temperature == 0.f, cuts = late.by_k || late.by_p, sampled = late.by_p && !late.by_k;
   u64 Z = late.Z;
-  u64 thr = greedy ? sl.value_key(top) : 0;  // copies of the maximum; the lowest index wins the race
-  // Whether one token in 16 or more is kept, by the sample: then every sector of
-  // the noise is read anyway.
-  bool many = false, captured = false;
-  if (late.by_k || late.by_p) {
-    const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) * sl.unit);
-    const float sure = late.by_k ? late.tau : top - temperature * __logf(__fdividef(static_cast<float>(sl.n), 0.99f * left));
-    many = !late.by_k && s.likely[2] * 16.f >= static_cast<float>(sl.n);
-    const float far = late.by_k ? sure : top - temperature * s.likely[0];
-    const float ceil = late.by_k || s.likely[1] <= 0.f ? top : top - temperature * s.likely[1];
-    // From the narrowest range to the widest, tried one after another.
-    Level lv = far <= top && far > sure ? level_between(sl, far, ceil) : level_between(sl, sure, top);
+  u64 thr = 0;
+  // The least logit that min-p can keep (with room for its and the weights' roundings).
+  const float lowest = greedy          ? top
+                       : floor_w > 0.f ? fminf(top, top + temperature * (1.001f * __logf(floor_w) - 1e-3f))
+                                       : -INFINITY;
+  const float left = (1.f - fmaxf(late.p, 0.f)) * (static_cast<float>(Z) * sl.unit);
+  const float sure = !cuts ? lowest
+                     : !sampled
+                         ? late.tau
+                         : top - temperature * __logf(__fdividef(static_cast<float>(sl.n), 0.99f * left));
+  const float far = sampled ? top - temperature * s.likely[0] : sure;
+  const float ceil = sampled && s.likely[1] > 0.f ? top - temperature * s.likely[1] : top;
+  // From the narrowest range to the widest, tried one after another.
+  Level lv = far <= top && far > sure ? level_between(sl, far, ceil) : level_between(sl, sure, top);
+  if (lv.floor == -FLT_MAX) lv = level_between(sl, -INFINITY, top);
+  const bool dense = greedy || lv.ceil < top, list = !greedy && lv.floor > -FLT_MAX;
+  if (threadIdx.x == 0) s.listed = 0;
+  __syncthreads();
+  Scan scan{Best{-INFINITY, 0.f, NONE}, 0, 0};
+  if (dense) {
+    scan = scan_row<S>(s, greedy ? top : lv.ceil, greedy ? sl.n : -1, greedy ? INFINITY : lv.floor);
+  } else if (list) {  // (from the row's bottom on it would be too long)
+    list_row(sl, s, lv.floor);
+  }
+  bool listed = list;
+  if (list) {
+    const u64 mass = block_sum64(scan.mass, s);
+    if (threadIdx.x < C) {
+      Shared* to = cluster.map_shared_rank(&s, threadIdx.x);
+      to->beyond[cluster.block_rank()] = mass;
+      to->lists[cluster.block_rank()] = s.listed;
+    }
+    cluster.sync();
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) listed = listed && s.lists[c] <= LISTED;
+  }
+  if (cuts) {
     bool fresh = false;
 #pragma unroll 1
     for (int turn = late.by_k ? 0 : 1; turn < (late.by_p ? 2 : 1); ++turn) {  // the first k, then their share p
@@ -1012,46 +1096,34 @@ __device__ __noinline__ void late_row(Shared& s) {
 #pragma unroll 1
       for (;;) {
         __syncthreads();  // what the turn before left in s has been read
-        cut = select(sl, s, cluster, lv, turn == 1, target, turn, fresh);
+        cut = select(sl, s, cluster, lv, turn == 1, target, turn, fresh, listed);
         if (cut || turn == 0 || lv.floor == -FLT_MAX) break;
         // The sample's answer was wrong, or roundings used up what the sure floor
         // leaves out.
         lv = level_between(sl, lv.floor > sure ? sure : -INFINITY, top);
-        fresh = false;
+        fresh = listed = false;
       }
       // Without a cut: there are no more than k, or Z's rounding asks for more
       // mass than there is, so that everything stays.
       if (turn == 0) Z = cut ? s.z : s.total_m;
       if (cut && s.thr > thr) thr = s.thr;
-      captured = cut && lv.ceil >= top;  // the first level's keys hold all that are kept
     }
   }
-  // (ln min_p: with room for its and the weights' roundings.)
-  const float floor_w = late.floor_w;
-  float floor = thr ? sl.logit_of(thr) : -FLT_MAX;
-  if (floor_w > 0.f) floor = fmaxf(floor, fminf(top, top + temperature * (1.001f * __logf(floor_w) - 1e-3f)));
-  Best best{-INFINITY, 0.f, NONE};
-  u64 kept = 0;
-  const float* noise = late.noise;
-  auto run = [&](float l, int i, float q, unsigned) {
-    const float w = sl.weight(l), x = sl.x(l);
-    if (sl.key(l, i) < thr || w < floor_w || x == -INFINITY) return;
-    kept += sl.fixed(w);
-    better(best, Best{greedy ? 0.f : race(x, q), l, static_cast<unsigned>(i)});
-  };
-  if (many) {
-    race_all(sl, noise, thr, floor_w, best, kept);
-  } else if (captured && s.captured <= CANDIDATES) {
-#pragma unroll 1
-    for (int i = threadIdx.x; i < static_cast<int>(s.captured); i += THREADS) {
-      const u64 key = s.candidates[i];
-      if (key >= thr) run(sl.logit_of(key), sl.index_of(key), noise[sl.index_of(key)], 0);
+  if (listed) {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < static_cast<int>(s.listed); i += THREADS) {
+      const int at = s.list_at[i];
+      const float l = lm_float(sl.row[at]), q = late.noise[at], w = sl.weight(l), x2 = fminf((l - sl.m) * sl.inv2, 0.f);
+      if (sl.key(l, at) < thr || w < floor_w || x2 == -INFINITY) continue;
+      scan.kept += sl.fixed(w);
+      better(scan.best, Best{fmaxf(x2 - lm_log2(q), -INFINITY), l, static_cast<unsigned>(at)});
     }
-  } else {
-    sl.template among<4>(
-        floor, INFINITY, nullptr, [](const float (&)[S::VEC]) {}, [&](int i) { return greedy ? 1.f : noise[i]; }, run);
+  } else if (!greedy) {
+    const float end = thr ? sl.logit_of(thr) : -INFINITY;
+    const bool by_thr = end >= lowest;
+    scan = scan_row<S>(s, by_thr ? end : lowest, by_thr && thr ? sl.index_of(thr) : sl.n, INFINITY);
   }
-  finish(sl, s, cluster, best, kept, greedy, late.token, late.logprob);
+  finish(sl, s, cluster, scan.best, scan.kept, greedy, late.token, late.logprob);
 }
 
 // The first `want` keys of the cluster's lists into s.sorted.  (The lists'
