@@ -60,7 +60,6 @@ constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds th
 constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
-constexpr int SECOND = 76, SECOND_CTAS = 4;  // clusters of the second launch (two CTAs an SM)
 constexpr int LIST = 128;       // keys of a bin that are ranked directly
 constexpr int SLICE_LEAST = 4 << 10;   // bytes of a row that are worth a CTA of a cluster
 using u64 = unsigned long long;
@@ -154,6 +153,8 @@ struct Shared {
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
   float likely[3];
+  int taken;
+  int64_t row;  // of the second launch
   uint4 edge[2];
   Late late;
   alignas(8) unsigned char slice[96];  // the row's Slice
@@ -1367,7 +1368,7 @@ __device__ __forceinline__ void free_row(S& sl, Shared& s, cg::cluster_group& cl
 // Only: a launch that finishes every row.  First: one that finishes those that
 // step 3 can, and marks the others.  Second: the one that finishes those.
 enum class Phase : int { Only, First, Second };
-constexpr int64_t LEFT = -2;  // the mark, in out_tokens
+constexpr int64_t LEFT = -2, TAKEN = -3;  // the marks, in out_tokens
 
 template <typename T, Phase phase>
 __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int per_cta, Shared& s) {
@@ -1681,31 +1682,59 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   }
 }
 
+// The next row at or after `from` (around the end) that is marked LEFT, marked
+// TAKEN now; -1 if there is none.  Called by a whole CTA.
+__device__ __forceinline__ int64_t take_row(const TokenArgs& a, int64_t from, Shared& s) {
+#pragma unroll 1
+  for (int64_t base = 0; base < a.rows;) {
+    const int64_t i = base + threadIdx.x, r = from + i < a.rows ? from + i : from + i - a.rows;
+    const unsigned marks = __ballot_sync(FULL_MASK, i < a.rows && __ldcg(a.out_tokens + r) == LEFT);
+    if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = marks;
+    __syncthreads();
+    int first = -1;
+#pragma unroll 1
+    for (int w = 0; w < WARPS && first < 0; ++w)
+      if (s.marks[w]) first = 32 * w + __ffs(s.marks[w]) - 1;
+    if (first < 0) {
+      base += THREADS;
+      __syncthreads();
+      continue;
+    }
+    const int64_t it = from + base + first < a.rows ? from + base + first : from + base + first - a.rows;
+    if (threadIdx.x == 0)
+      s.taken = atomicCAS(reinterpret_cast<u64*>(a.out_tokens + it), static_cast<u64>(LEFT), static_cast<u64>(TAKEN)) ==
+                static_cast<u64>(LEFT);
+    __syncthreads();
+    if (s.taken) return it;
+  }
+  return -1;
+}
+
 template <typename T, Phase phase>
 __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int per_cta) {
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
-  const int log_c = __ffs(cluster.num_blocks()) - 1;
+  const int C = cluster.num_blocks(), log_c = __ffs(C) - 1;
   const int64_t first = blockIdx.x >> log_c, clusters = gridDim.x >> log_c;
   pdl_wait();
   pdl_trigger();
   if constexpr (phase != Phase::Second) {
     sample_row<T, phase>(a, first, per_cta, s);
   } else {
-    // This cluster's rows, THREADS at a time: which of them are marked.  (A row's
-    // mark goes only after every CTA of its cluster has taken it up.)
+    // Clusters take marked rows as they become free: rows differ in their time by
+    // three, and 64 of 256 fixed shares held three of them where others held none.
+    cluster.sync();
 #pragma unroll 1
-    for (int64_t base = first; base < a.rows; base += clusters * THREADS) {
-      const int64_t mine = base + clusters * threadIdx.x;
-      const unsigned marks = __ballot_sync(FULL_MASK, mine < a.rows && a.out_tokens[mine] == LEFT);
-      if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = marks;
-      __syncthreads();
-#pragma unroll 1
-      for (int w = 0; w < WARPS; ++w)
-#pragma unroll 1
-        for (unsigned left = s.marks[w]; left; left &= left - 1)
-          sample_row<T, phase>(a, base + clusters * (32 * w + __ffs(left) - 1), per_cta, s);
-      __syncthreads();
+    for (int64_t from = first * a.rows / clusters;;) {
+      if (cluster.block_rank() == 0) {
+        const int64_t r = take_row(a, from, s);
+        if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->row = r;
+      }
+      cluster.sync();
+      const int64_t r = s.row;
+      if (r < 0) return;
+      sample_row<T, phase>(a, r, per_cta, s);
+      from = r;
     }
   }
 }
@@ -1718,6 +1747,13 @@ int cluster_of(int64_t rows, int64_t bytes) {
   return c;
 }
 
+// CTAs of a cluster of the second launch, which has two CTAs an SM.  A quarter of
+// the rows or more come there under top-p; with fewer of them than clusters a
+// row's own time counts, with more the number that are under way.  (256 rows of
+// 131072 bfloat16, 64 left: 84 us with 4 CTAs, 106 with 2; 512 of 65536 float32:
+// 226 and 198.)
+int second_of(int64_t rows, int64_t bytes) { return std::min(cluster_of(1, bytes), rows > 2 * sms() ? 2 : 4); }
+
 template <typename T>
 cudaError_t launch_typed(const TokenArgs& a, cudaStream_t stream) {
   constexpr int VEC = 16 / int(sizeof(T));
@@ -1725,11 +1761,11 @@ cudaError_t launch_typed(const TokenArgs& a, cudaStream_t stream) {
   auto launch = [&](auto kernel, int64_t rows, int c) {
     return launch_clusters(kernel, rows * c, THREADS, c, 0, stream, a, static_cast<int>((vectors + c - 1) / c));
   };
-  const int c = cluster_of(a.rows, vectors * 16), second = std::min(cluster_of(1, vectors * 16), SECOND_CTAS);
+  const int c = cluster_of(a.rows, vectors * 16), second = second_of(a.rows, vectors * 16);
   if (c > 1 || second == 1) return launch(k_sample_tokens<T, Phase::Only>, a.rows, c);
   const cudaError_t e = launch(k_sample_tokens<T, Phase::First>, a.rows, c);
   if (e != cudaSuccess) return e;
-  return launch(k_sample_tokens<T, Phase::Second>, a.rows < SECOND ? a.rows : SECOND, second);
+  return launch(k_sample_tokens<T, Phase::Second>, std::min<int64_t>(a.rows, 2 * sms() / second), second);
 }
 
 }  // namespace
