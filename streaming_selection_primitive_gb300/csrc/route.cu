@@ -118,15 +118,17 @@ __device__ __forceinline__ void store_part(T* row, int E, bool vec, const float 
 // A warp's ring of STAGES token rows in shared memory, filled by asynchronous
 // copies: each lane copies what it reads itself, so that the next tokens'
 // rows are on their way while one is worked on, without holding registers.
-// (131072 x 256 f32, forward and backward: 228 us with plain loads.)  Taken
-// for rows whose groups of VEC values are whole and aligned; others are loaded
-// when their turn comes.
+// Taken for rows of 1 to 2 KB whose groups of VEC values are whole and aligned
+// (32768 x 512 bfloat16: 44.8 us forward and 28.3 backward, against 46.0 and 31.7
+// with plain loads).  Shorter ones are loaded when their turn comes, which the
+// other warps hide (32768 x 128 bfloat16: 19.2 and 12.3 us, against 21.0 and 13.6
+// through a ring); longer ones would need more shared memory than there is.
 template <typename T, int R>
 struct Ring {
   using P = Part<T, R>;
   static constexpr int CHUNK = P::VEC * int(sizeof(T));
   static constexpr int ROW = 32 * R * int(sizeof(T));
-  static constexpr int STAGES = CHUNK < 4 || ROW > 2048 ? 0 : ROW > 1024 ? 2 : 4;
+  static constexpr int STAGES = ROW < 1024 || ROW > 2048 ? 0 : ROW > 1024 ? 2 : 4;
   static constexpr int BYTES = STAGES * ROW;  // per warp
   unsigned char* base;  // this warp's
   bool on;

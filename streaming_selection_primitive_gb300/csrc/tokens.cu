@@ -9,8 +9,8 @@
 // rates w_i); its log-probability is x_i - log sum kept w.
 //
 // One CTA takes a row, or a cluster of up to 8 where there are few rows (then
-// each takes a slice); rows that need step 4 are left to a second launch, with
-// clusters of 8, unless the first one has these:
+// each takes a slice); rows that need step 4 are left to a second launch, of
+// clusters, unless the first one has these:
 //   1. one read of the slice gives its maximum and, for top-p, its mass.
 //      What is needed of the slice again comes from the caches;
 //   2. its first keys, sorted: of the threads' maxima a value is taken that at
@@ -20,16 +20,27 @@
 //      up to TOP, and for most rows under top-p and min-p, they are all that can
 //      be kept: one warp cuts them and runs the race, which reads the noise of
 //      these tokens only;
-//   4. otherwise the cuts are found by histograms of counts and masses over
-//      equal ranges of x, then of keys, repeated inside the range where the
-//      count or the mass crosses its target until that holds at most LIST
-//      keys; then every CTA races over its kept tokens.  For top-p the sample
-//      tells between which values the crossing should lie, so that the
-//      histogram touches little else; where it does not, it is made again from
-//      a value that surely is below.
+//   4. otherwise the tokens among which the cut lies are listed (for top-p those
+//      between two values that the sample gives; what is above them joins the
+//      race in the same pass), and a histogram of the list's counts and masses
+//      over equal ranges of x, then of keys, is repeated inside the range
+//      where the count or the mass crosses its target until that holds at most
+//      LIST keys.  Where the sample was wrong or the list is too long, the
+//      same is done over the slice.
 //
 // A row without filters is one pass over its logits and noise together
 // (free_row).
+//
+// What bounds it: with many rows without filters the instructions of a
+// token's exponential and logarithm (512 rows of 65536 float32: 268 MB in 56
+// us, 4.8 TB/s, seven tenths of a copy's rate); under top-k the read (256 rows
+// of 131072 bfloat16, k = 50: 67 MB in 27 us, of which a second launch that
+// finds nothing is 6); under top-p the weights of the first pass, and then
+// the latency of the rows of step 4, some forty steps between barriers of 1000 to
+// 3000 cycles each (the same rows, p = 0.9, slopes from 1 to 2 against the
+// logarithm of the rank: 84 us, of which the first launch has 33).  One row is a chain
+// of such steps whatever its length: 1 x 32768 takes 5.5 us without filters,
+// 7 greedily, 10.5 with k = 50.
 //
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
@@ -60,8 +71,9 @@ constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds th
 constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
+constexpr int SECOND_CTAS = 4;  // of a cluster of the second launch, which has two CTAs an SM
 constexpr int LIST = 128;       // keys of a bin that are ranked directly
-constexpr int SLICE_LEAST = 4 << 10;   // bytes of a row that are worth a CTA of a cluster
+constexpr int SLICE_LEAST = 16 << 10;   // bytes of a row that are worth a CTA of a cluster
 using u64 = unsigned long long;
 
 // The race's state: the best score, its logit and index (NONE: none yet).
@@ -147,8 +159,6 @@ struct Shared {
   unsigned slot, merged, hits, marks[WARPS];
   unsigned listed;  // tokens that scan_row found for the list (which holds them unless there are more than fit)
   unsigned short hit[THREADS];
-  alignas(16) uint32_t maxima[THREADS];
-  float tau;
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
@@ -658,48 +668,29 @@ __device__ __forceinline__ u64 mass_target(float p, u64 Z) {
 }
 
 // A value that at least `want` of the block's thread maxima reach, and not many
-// more: bisection over the keys between the least maximum and the largest, by
-// one warp (a count over the block would be a barrier a step: 6 us a row where
-// this takes MEASURE).  -inf if there are no more than `want`.
+// more: bisection over the keys between the least maximum and the largest
+// (each under a count over the block).  -inf if there are no more than `want`.
 __device__ __forceinline__ float block_tau(float top, float widest, int want, Shared& s) {
-  s.maxima[threadIdx.x] = choice_key(top);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    uint4 key[WARPS / 4];
+  const uint32_t key = choice_key(top);
+  const uint32_t least = __reduce_min_sync(FULL_MASK, key ? key : ~0u);
+  if ((threadIdx.x & 31) == 0) s.redk[threadIdx.x >> 5] = least;
+  int count = __syncthreads_count(key != 0u);
+  if (count <= want) return -INFINITY;
+  uint32_t lo = s.redk[0], hi = choice_key(widest) + 1u;
 #pragma unroll
-    for (int i = 0; i < WARPS / 4; ++i) key[i] = reinterpret_cast<const uint4*>(s.maxima)[i * 32 + threadIdx.x];
-    auto reach = [&](uint32_t least) {
-      unsigned c = 0;
-#pragma unroll
-      for (int i = 0; i < WARPS / 4; ++i)
-        c += (key[i].x >= least) + (key[i].y >= least) + (key[i].z >= least) + (key[i].w >= least);
-      return static_cast<int>(__reduce_add_sync(FULL_MASK, c));
-    };
-    uint32_t lo = ~0u, hi = choice_key(widest) + 1u;
-#pragma unroll
-    for (int i = 0; i < WARPS / 4; ++i)  // (a key of 0, less 1, is the largest number)
-      lo = min(min(min(lo, key[i].x - 1u), min(key[i].y - 1u, key[i].z - 1u)), key[i].w - 1u);
-    lo = __reduce_min_sync(FULL_MASK, lo) + 1u;
-    int count = reach(1u);
-    if (count <= want) {
-      lo = KEY_NEG_INF;
-    } else {
+  for (int w = 1; w < WARPS; ++w) lo = min(lo, s.redk[w]);
 #pragma unroll 1
-      while (hi - lo > 1u && count > want + want / 8 + 4) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int c = reach(mid);
-        if (c >= want) {
-          lo = mid;
-          count = c;
-        } else {
-          hi = mid;
-        }
-      }
+  while (hi - lo > 1u && count > want + want / 8 + 4) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int c = __syncthreads_count(key >= mid);
+    if (c >= want) {
+      lo = mid;
+      count = c;
+    } else {
+      hi = mid;
     }
-    if (threadIdx.x == 0) s.tau = key_to_float(lo);
   }
-  __syncthreads();
-  return s.tau;
+  return key_to_float(lo);
 }
 
 // body(i, rank) for every candidate, rank being the number of larger ones (they
@@ -1520,12 +1511,16 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
       sample_point(sl, s, (1.f - fmaxf(p, 0.f)) * (static_cast<float>(Z) * sl.unit));
       if (want) {
         // How many keys should reach the mass: three standard deviations of a
-        // count of one in 2^sample_shift more, and a few.
-        const float tokens = s.likely[2];
-        const float most = 32.f + tokens + 3.f * lm_sqrt(static_cast<float>(1 << sl.sample_shift) * (tokens + 16.f));
-        const int limit = alone ? TOP : TOP_SHARED;
+        // count of one in 2^sample_shift more, and a few.  Worth a try where one
+        // of them more does not pass the limit.  (With the limit at the count
+        // itself rows are tried that then need step 4: 64 x 131072, p = 0.9, took 55 us
+        // against 52; at three of them too few are tried: 256 rows took 94 us
+        // against 85.)
+        const float tokens = s.likely[2], deviation = lm_sqrt(static_cast<float>(1 << sl.sample_shift) * (tokens + 16.f));
+        const float limit = alone ? TOP : TOP_SHARED;
         // (With min-p the tokens may end long before the mass.)
-        want = tokens > limit ? (min_p > 0.f ? TOP_MIN_P : 0) : static_cast<int>(fminf(most, static_cast<float>(limit)));
+        want = tokens + deviation > limit ? (min_p > 0.f ? TOP_MIN_P : 0)
+                                          : static_cast<int>(fminf(32.f + tokens + 3.f * deviation, limit));
       }
     } else {
       want = 0;  // a NaN, or nothing to choose
@@ -1747,13 +1742,6 @@ int cluster_of(int64_t rows, int64_t bytes) {
   return c;
 }
 
-// CTAs of a cluster of the second launch, which has two CTAs an SM.  A quarter of
-// the rows or more come there under top-p; with fewer of them than clusters a
-// row's own time counts, with more the number that are under way.  (256 rows of
-// 131072 bfloat16, 64 left: 84 us with 4 CTAs, 106 with 2; 512 of 65536 float32:
-// 226 and 198.)
-int second_of(int64_t rows, int64_t bytes) { return std::min(cluster_of(1, bytes), rows > 2 * sms() ? 2 : 4); }
-
 template <typename T>
 cudaError_t launch_typed(const TokenArgs& a, cudaStream_t stream) {
   constexpr int VEC = 16 / int(sizeof(T));
@@ -1761,8 +1749,8 @@ cudaError_t launch_typed(const TokenArgs& a, cudaStream_t stream) {
   auto launch = [&](auto kernel, int64_t rows, int c) {
     return launch_clusters(kernel, rows * c, THREADS, c, 0, stream, a, static_cast<int>((vectors + c - 1) / c));
   };
-  const int c = cluster_of(a.rows, vectors * 16), second = second_of(a.rows, vectors * 16);
-  if (c > 1 || second == 1) return launch(k_sample_tokens<T, Phase::Only>, a.rows, c);
+  const int c = cluster_of(a.rows, vectors * 16), second = std::min(cluster_of(1, vectors * 16), SECOND_CTAS);
+  if (c > 1 || second == 1 || a.rows > 2 * sms()) return launch(k_sample_tokens<T, Phase::Only>, a.rows, c);
   const cudaError_t e = launch(k_sample_tokens<T, Phase::First>, a.rows, c);
   if (e != cudaSuccess) return e;
   return launch(k_sample_tokens<T, Phase::Second>, std::min<int64_t>(a.rows, 2 * sms() / second), second);
