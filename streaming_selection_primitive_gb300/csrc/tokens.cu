@@ -67,11 +67,11 @@ constexpr int TOP = 256;        // keys that step 2 can sort in a CTA that has t
 constexpr int TOP_SHARED = 128; // and in a cluster's
 constexpr int TOP_MIN_P = 64;   // and those that min-p seldom leaves more of
 constexpr int CANDIDATES = 1024;
-constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds the cut
+constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds the cut,
+constexpr int LISTED_ALONE = 8192;  // and of a long row in one CTA (in dynamic shared memory)
 constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
-constexpr int SECOND_CTAS = 4;  // of a cluster of the second launch, which has two CTAs an SM
 constexpr int LIST = 128;       // keys of a bin that are ranked directly
 constexpr int SLICE_LEAST = 16 << 10;   // bytes of a row that are worth a CTA of a cluster
 using u64 = unsigned long long;
@@ -146,7 +146,7 @@ struct Shared {
       alignas(16) u64 candidates[CANDIDATES + 2];
       float candidates_q[CANDIDATES];
     };
-    int list_at[LISTED];  // step 4: their indices
+    int list_at[LISTED];  // step 4: their indices (unless they are in dynamic shared memory)
   };
   unsigned own_sample[SAMPLE_BINS];
   alignas(16) float row_sample[SAMPLE_BINS];
@@ -156,15 +156,15 @@ struct Shared {
   float redf[WARPS], mass[WARPS];
   uint32_t redk[WARPS];
   Best best[WARPS];
-  unsigned slot, merged, hits, marks[WARPS];
+  unsigned slot, merged, hits;
+  int* list_to;     // the list, and its length at most
+  unsigned room;
   unsigned listed;  // tokens that scan_row found for the list (which holds them unless there are more than fit)
   unsigned short hit[THREADS];
   unsigned bin;  // the crossing found by a pass: BINS if there is none
   u64 above_c, above_m, in_c, total_m;
   u64 thr, z;
   float likely[3];
-  int taken;
-  int64_t row;  // of the second launch
   uint4 edge[2];
   Late late;
   alignas(8) unsigned char slice[96];  // the row's Slice
@@ -468,7 +468,7 @@ struct Level {
 // (or mass) from the top first reaches `target`: s.bin, s.above_*, s.in_c;
 // s.bin = BINS where it does not.  What lies above the first level's ceil
 // counts as above (its mass only, s.beyond).  fresh: the joined histogram is in
-// place.  listed: s.list_at holds all that the first level counts.
+// place.  listed: the list holds all that the first level counts.
 template <typename S>
 __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group& cluster, const Level& lv, bool by_mass,
                                       u64 target, bool fresh, bool listed) {
@@ -488,7 +488,7 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
     if (listed) {
 #pragma unroll 1
       for (int i = threadIdx.x; i < static_cast<int>(s.listed); i += THREADS) {
-        const int at = s.list_at[i];
+        const int at = s.list_to[i];
         add(lm_float(sl.row[at]), at);
       }
     } else {
@@ -601,7 +601,7 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
       if (listed) {
 #pragma unroll 1
         for (int i = threadIdx.x; i < static_cast<int>(s.listed); i += THREADS) {
-          const int at = s.list_at[i];
+          const int at = s.list_to[i];
           const float l = lm_float(sl.row[at]);
           if (lv.bin_of(sl, l, at) == bin) send(sl.key(l, at));
         }
@@ -853,7 +853,7 @@ __device__ __forceinline__ void sample_point(const S& sl, Shared& s, float left)
 #pragma unroll
         for (int i = 0; i < j; ++i) above += count[i];
         above *= every;
-        near = above > static_cast<float>(C * LISTED / 2) ? fmaxf(point - blur, 0.f) : 0.f;
+        near = above > static_cast<float>(C * (s.room / 2)) ? fmaxf(point - blur, 0.f) : 0.f;
       }
       tail += mass[j];
       var += mass[j] * weight[j];
@@ -892,7 +892,7 @@ __device__ __forceinline__ void list_row(const S& sl, Shared& s, float floor) {
 #pragma unroll 1
     for (; hits; hits &= hits - 1, ++at) {
       const int b = __ffs(hits) - 1, u = base + lane + b / VEC * THREADS;
-      if (at < LISTED) s.list_at[at] = sl.element(u) + b % VEC;
+      if (at < s.room) s.list_to[at] = sl.element(u) + b % VEC;
     }
     __syncwarp();
   }
@@ -1011,7 +1011,7 @@ __device__ __noinline__ Scan scan_row(Shared& s, float cut, int cut_index, float
       unsigned place = warp_reserve(&s.listed, __popc(list));
 #pragma unroll 1
       for (; list; list &= list - 1, ++place)
-        if (place < LISTED) s.list_at[place] = sl.first + at + __ffs(list) - 1;
+        if (place < s.room) s.list_to[place] = sl.first + at + __ffs(list) - 1;
       __syncwarp();
     }
     if (++turn % 16 == 0) {
@@ -1077,7 +1077,7 @@ __device__ __noinline__ void late_row(Shared& s) {
     }
     cluster.sync();
 #pragma unroll 1
-    for (int c = 0; c < C; ++c) listed = listed && s.lists[c] <= LISTED;
+    for (int c = 0; c < C; ++c) listed = listed && s.lists[c] <= s.room;
   }
   if (cuts) {
     bool fresh = false;
@@ -1104,7 +1104,7 @@ __device__ __noinline__ void late_row(Shared& s) {
   if (listed) {
 #pragma unroll 2
     for (int i = threadIdx.x; i < static_cast<int>(s.listed); i += THREADS) {
-      const int at = s.list_at[i];
+      const int at = s.list_to[i];
       const float l = lm_float(sl.row[at]), q = late.noise[at], w = sl.weight(l), x2 = fminf((l - sl.m) * sl.inv2, 0.f);
       if (sl.key(l, at) < thr || w < floor_w || x2 == -INFINITY) continue;
       scan.kept += sl.fixed(w);
@@ -1356,12 +1356,7 @@ __device__ __forceinline__ void free_row(S& sl, Shared& s, cg::cluster_group& cl
   finish(sl, s, cluster, best, __float2ull_rn(mass * sl.scale), false, token, logprob);
 }
 
-// Only: a launch that finishes every row.  First: one that finishes those that
-// step 3 can, and marks the others.  Second: the one that finishes those.
-enum class Phase : int { Only, First, Second };
-constexpr int64_t LEFT = -2, TAKEN = -3;  // the marks, in out_tokens
-
-template <typename T, Phase phase>
+template <typename T>
 __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int per_cta, Shared& s) {
   using S = Slice<T>;
   constexpr int VEC = S::VEC;
@@ -1379,7 +1374,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   const bool by_k = !greedy && k > 0 && k < a.n, by_p = !greedy && p < 1.f;
   const bool need_mass = by_p && !by_k, alone = C == 1;
   // Keys that step 2 sorts (0: it would not help); for top-p in a CTA alone the sample may say otherwise.
-  int want = phase == Phase::Second ? 0 : greedy ? 1 : by_k ? (k <= (alone ? TOP : TOP_SHARED) ? k : 0) : min_p > 0.f ? TOP_MIN_P : by_p ? TOP_SHARED : 0;
+  int want = greedy ? 1 : by_k ? (k <= (alone ? TOP : TOP_SHARED) ? k : 0) : min_p > 0.f ? TOP_MIN_P : by_p ? TOP_SHARED : 0;
   S sl;
   sl.row = static_cast<const T*>(a.logits) + r * a.ld;
   sl.mask = a.mask ? a.mask + r * a.mask_ld : nullptr;
@@ -1402,12 +1397,10 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   sl.scale = __int_as_float((127 + e) << 23);
   sl.unit = __int_as_float((127 - e) << 23);
   const float* noise = a.noise + r * a.noise_ld;
-  if constexpr (phase != Phase::Second) {
-    if (!greedy && !by_k && !by_p && !(min_p > 0.f)) {
-      free_row(sl, s, cluster, std::move(started), noise, temperature, isnan(p) || isnan(min_p), a.out_tokens + r,
-               a.out_logprobs + r);
-      return;
-    }
+  if (!greedy && !by_k && !by_p && !(min_p > 0.f)) {
+    free_row(sl, s, cluster, std::move(started), noise, temperature, isnan(p) || isnan(min_p), a.out_tokens + r,
+             a.out_logprobs + r);
+    return;
   }
 
   // 1. The slice's largest logit (NaN if it holds one) and, for top-p, its
@@ -1556,7 +1549,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
 
   // 2. The slice's first keys.
   int keys = 0;
-  if (phase != Phase::Second && want && !isnan(widest)) {
+  if (want && !isnan(widest)) {
     // The threads whose maximum reaches tau; their vectors are shared out over all.
     if (!flat && own >= fmaxf(tau, -FLT_MAX)) s.hit[atomicAdd(&s.hits, 1u)] = static_cast<unsigned short>(threadIdx.x);
     __syncthreads();
@@ -1642,96 +1635,41 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   }
   sl.m = top;
   const float floor_w = fminf(min_p, 1.f);
-  if constexpr (phase != Phase::Second) {
+  if (want && found >= 0) {
     const bool decide = !by_k && !greedy;  // whether these keys are enough is not known beforehand
-    bool enough = false;
-    if (want && found >= 0) {
-      if (rank == 0) {
-        const int got = found < want ? found : want;
-        if (!alone) merge_keys(s, C, want);
-        if (warp == 0) {
-          enough = race_list(sl, s, got, !decide || found < want, by_k, by_p, p, Z, floor_w, greedy, a.out_tokens + r,
-                             a.out_logprobs + r);
-          if (phase == Phase::Only && decide && lane < C) cluster.map_shared_rank(&s, lane)->enough = enough;
-        }
-      }
-      if (phase == Phase::Only) {
-        if (!decide) return;
-        cluster.sync();  // the first CTA has written `enough`
-        if (s.enough) return;
+    if (rank == 0) {
+      const int got = found < want ? found : want;
+      if (!alone) merge_keys(s, C, want);
+      if (warp == 0) {
+        const bool enough = race_list(sl, s, got, !decide || found < want, by_k, by_p, p, Z, floor_w, greedy,
+                                      a.out_tokens + r, a.out_logprobs + r);
+        if (decide && lane < C) cluster.map_shared_rank(&s, lane)->enough = enough;
       }
     }
-    if (phase == Phase::First) {
-      if (rank == 0 && threadIdx.x == 0 && !enough) a.out_tokens[r] = LEFT;
-      return;
-    }
+    if (!decide) return;
+    cluster.sync();  // the first CTA has written `enough`
+    if (s.enough) return;
   }
-  if constexpr (phase != Phase::First) {
-    if (threadIdx.x == 0) {
-      *reinterpret_cast<S*>(s.slice) = sl;
-      s.late = Late{noise, a.out_tokens + r, a.out_logprobs + r, Z, k, p, temperature, floor_w, tau, by_k, by_p};
-    }
-    __syncthreads();
-    late_row<S>(s);
-    return;
+  if (threadIdx.x == 0) {
+    *reinterpret_cast<S*>(s.slice) = sl;
+    s.late = Late{noise, a.out_tokens + r, a.out_logprobs + r, Z, k, p, temperature, floor_w, tau, by_k, by_p};
   }
+  __syncthreads();
+  late_row<S>(s);
 }
 
-// The next row at or after `from` (around the end) that is marked LEFT, marked
-// TAKEN now; -1 if there is none.  Called by a whole CTA.
-__device__ __forceinline__ int64_t take_row(const TokenArgs& a, int64_t from, Shared& s) {
-#pragma unroll 1
-  for (int64_t base = 0; base < a.rows;) {
-    const int64_t i = base + threadIdx.x, r = from + i < a.rows ? from + i : from + i - a.rows;
-    const unsigned marks = __ballot_sync(FULL_MASK, i < a.rows && __ldcg(a.out_tokens + r) == LEFT);
-    if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = marks;
-    __syncthreads();
-    int first = -1;
-#pragma unroll 1
-    for (int w = 0; w < WARPS && first < 0; ++w)
-      if (s.marks[w]) first = 32 * w + __ffs(s.marks[w]) - 1;
-    if (first < 0) {
-      base += THREADS;
-      __syncthreads();
-      continue;
-    }
-    const int64_t it = from + base + first < a.rows ? from + base + first : from + base + first - a.rows;
-    if (threadIdx.x == 0)
-      s.taken = atomicCAS(reinterpret_cast<u64*>(a.out_tokens + it), static_cast<u64>(LEFT), static_cast<u64>(TAKEN)) ==
-                static_cast<u64>(LEFT);
-    __syncthreads();
-    if (s.taken) return it;
-  }
-  return -1;
-}
-
-template <typename T, Phase phase>
-__global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int per_cta) {
+template <typename T>
+__global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int per_cta, bool long_lists) {
   __shared__ Shared s;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int C = cluster.num_blocks(), log_c = __ffs(C) - 1;
-  const int64_t first = blockIdx.x >> log_c, clusters = gridDim.x >> log_c;
+  extern __shared__ int long_list[];
+  const int log_c = __ffs(cg::this_cluster().num_blocks()) - 1;
+  if (threadIdx.x == 0) {  // (read after many barriers)
+    s.list_to = long_lists ? long_list : s.list_at;
+    s.room = long_lists ? LISTED_ALONE : LISTED;
+  }
   pdl_wait();
   pdl_trigger();
-  if constexpr (phase != Phase::Second) {
-    sample_row<T, phase>(a, first, per_cta, s);
-  } else {
-    // Clusters take marked rows as they become free: rows differ in their time by
-    // three, and 64 of 256 fixed shares held three of them where others held none.
-    cluster.sync();
-#pragma unroll 1
-    for (int64_t from = first * a.rows / clusters;;) {
-      if (cluster.block_rank() == 0) {
-        const int64_t r = take_row(a, from, s);
-        if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->row = r;
-      }
-      cluster.sync();
-      const int64_t r = s.row;
-      if (r < 0) return;
-      sample_row<T, phase>(a, r, per_cta, s);
-      from = r;
-    }
-  }
+  sample_row<T>(a, blockIdx.x >> log_c, per_cta, s);
 }
 
 // CTAs of a row's cluster: as many as the SMs have room for at once, while
@@ -1746,14 +1684,17 @@ template <typename T>
 cudaError_t launch_typed(const TokenArgs& a, cudaStream_t stream) {
   constexpr int VEC = 16 / int(sizeof(T));
   const int64_t vectors = (a.n + 2 * VEC - 2) / VEC;  // at any alignment of the row
-  auto launch = [&](auto kernel, int64_t rows, int c) {
-    return launch_clusters(kernel, rows * c, THREADS, c, 0, stream, a, static_cast<int>((vectors + c - 1) / c));
-  };
-  const int c = cluster_of(a.rows, vectors * 16), second = std::min(cluster_of(1, vectors * 16), SECOND_CTAS);
-  if (c > 1 || second == 1 || a.rows > 2 * sms()) return launch(k_sample_tokens<T, Phase::Only>, a.rows, c);
-  const cudaError_t e = launch(k_sample_tokens<T, Phase::First>, a.rows, c);
-  if (e != cudaSuccess) return e;
-  return launch(k_sample_tokens<T, Phase::Second>, std::min<int64_t>(a.rows, 2 * sms() / second), second);
+  const int c = cluster_of(a.rows, vectors * 16);
+  // One CTA for a row whose slice would be worth several.
+  const bool long_lists = c == 1 && vectors * 16 > 2 * SLICE_LEAST;
+  size_t dynamic = 0;
+  if (long_lists) {
+    dynamic = LISTED_ALONE * sizeof(int);
+    const cudaError_t e = cudaFuncSetAttribute(k_sample_tokens<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dynamic));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_clusters(k_sample_tokens<T>, a.rows * c, THREADS, c, dynamic, stream, a,
+                         static_cast<int>((vectors + c - 1) / c), long_lists);
 }
 
 }  // namespace
