@@ -1392,7 +1392,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
   sl.inv = fmaxf(lm_rcp(temperature), __int_as_float(1));
   sl.inv2 = sl.inv * LOG2E;
   sl.index_bits = 32 - __clz(sl.n - 1);
-  sl.sample_shift = min(max(sl.index_bits - 13, 0), 6);  // 4096 to 8192 elements of the row, where it has them
+  sl.sample_shift = min(max(sl.index_bits - 14, 0), 6);  // 8192 to 16384 elements of the row, where it has them
   const int e = min(62 - sl.index_bits, 44);
   sl.scale = __int_as_float((127 + e) << 23);
   sl.unit = __int_as_float((127 - e) << 23);
