@@ -12,6 +12,13 @@
 // One warp takes a token: R = E / 32 logits a lane (rounded up to a power of
 // two), in registers, read once.  The choice runs on 32-bit keys that end in
 // the expert's index (sort_key), so that a round is one warp-wide maximum.
+//
+// What bounds it: a token's instructions, 549 forward and 438 backward for 256
+// experts of float32, 344 and 270 for 128 of bfloat16, of which the SMs issue
+// two to three a cycle.  131072 x 256 float32, k = 8: 78 us forward (147 MB, 1.9
+// TB/s) and 69 backward (281 MB, 4.1 TB/s); 32768 x 128 bfloat16: 19 and 12 us.  Up to a few thousand tokens the
+// launches and the join of the CTAs' sums count: 4096 of 64 take 7.4 and 3.4 us,
+// 16 of 128 take 4.1 and 3.0.
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -28,7 +35,9 @@ namespace {
 constexpr int CLUSTER = 8;  // CTAs of the one-launch form and of the join
 
 // Warps of a CTA, and resident CTAs per SM of the forms for many tokens (which
-// size their grids): what the registers of R values a lane allow.
+// size their grids): what the registers of R values a lane allow.  (131072 x 256
+// float32, forward and backward: 78 and 69 us; with one CTA an SM 86 and 98, with
+// eight warps a CTA 90 and 98.)
 template <int R>
 constexpr int WARPS = R <= 16 ? 16 : 8;
 template <int R>
@@ -780,9 +789,9 @@ cudaError_t launch_with(void (*kernel)(KArgs...), int grid, int threads, size_t 
   return launch_kernel(kernel, dim3(grid), dim3(threads), smem, stream, args...);
 }
 
-// One launch up to this many tokens (two a warp of the cluster): 16 x 128
-// takes 4.4 us, where the grid and the join take 7.4 us (1025 tokens); every
-// further token of a warp adds 1.6 us.
+// One launch up to this many tokens (two a warp of the cluster).  (x 128 bfloat16,
+// k = 8: 16 tokens take 4.1 us, and 5.3 by the grid and the join; 512 take 5.8 by
+// the grid and 8.4 in one launch.)
 template <int R>
 constexpr int64_t ONE_TOKENS = 2 * CLUSTER * WARPS<R>;
 

@@ -9,8 +9,7 @@
 // rates w_i); its log-probability is x_i - log sum kept w.
 //
 // One CTA takes a row, or a cluster of up to 8 where there are few rows (then
-// each takes a slice); rows that need step 4 are left to a second launch, of
-// clusters, unless the first one has these:
+// each takes a slice):
 //   1. one read of the slice gives its maximum and, for top-p, its mass.
 //      What is needed of the slice again comes from the caches;
 //   2. its first keys, sorted: of the threads' maxima a value is taken that at
@@ -31,16 +30,18 @@
 // A row without filters is one pass over its logits and noise together
 // (free_row).
 //
-// What bounds it: with many rows without filters the instructions of a
-// token's exponential and logarithm (512 rows of 65536 float32: 268 MB in 56
-// us, 4.8 TB/s, seven tenths of a copy's rate); under top-k the read (256 rows
-// of 131072 bfloat16, k = 50: 67 MB in 27 us, of which a second launch that
-// finds nothing is 6); under top-p the weights of the first pass, and then
-// the latency of the rows of step 4, some forty steps between barriers of 1000 to
-// 3000 cycles each (the same rows, p = 0.9, slopes from 1 to 2 against the
-// logarithm of the rank: 84 us, of which the first launch has 33).  One row is a chain
-// of such steps whatever its length: 1 x 32768 takes 5.5 us without filters,
-// 7 greedily, 10.5 with k = 50.
+// What bounds it, with the times of a call on the device (bfloat16, noise and
+// logits in or out of L2 as they come; L: logits that fall by 1 to 2 per unit
+// of the logarithm of their rank):
+//   many rows without filters: the instructions of a token's exponential and
+//     logarithm.  512 x 65536 float32: 268 MB in 51 us, 5.2 TB/s, 0.77 of a copy's rate;
+//   many rows under top-k or greedily: the read, and step 2.  256 x 131072, 67 MB:
+//     16 us greedily, 22 us with k = 50;
+//   top-p: the weights of the first pass, and then the rows of step 4, thirty
+//     steps between barriers of 1000 to 4000 cycles each, beside the slices' scan.
+//     64 x 131072, p = 0.9, L: 48 us, and 25 us at T = 0.7, where fewer rows get there;
+//   one row: the same chain of steps, whatever its length.  1 x 32768: 5.5 us
+//     without filters, 7 greedily, 8.6 with k = 50, 14 with p = 0.9.
 //
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
@@ -63,17 +64,27 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int TOP = 256;        // keys that step 2 can sort in a CTA that has the row to itself (half its threads),
-constexpr int TOP_SHARED = 128; // and in a cluster's
-constexpr int TOP_MIN_P = 64;   // and those that min-p seldom leaves more of
+// Keys that step 2 can sort in a CTA that has the row to itself (half its
+// threads; 256 x 131072, p = 0.9, T = 0.7: 78 us, and 99 us with 128), in a
+// cluster's (its lists of 128 just fit the first CTA's), and those that min-p
+// seldom leaves more of (64 x 131072, min-p = 0.01: 21.1 us, and 24.6 with 128;
+// 0.05 in 256 rows: 35 us, and 29 with 128).
+constexpr int TOP = 256;
+constexpr int TOP_SHARED = 128;
+constexpr int TOP_MIN_P = 64;
 constexpr int CANDIDATES = 1024;
 constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds the cut,
-constexpr int LISTED_ALONE = 8192;  // and of a long row in one CTA (in dynamic shared memory)
-constexpr int BINS = 256;       // of one histogram pass (the joining of 1024 took 6 us in a cluster of 8)
+constexpr int LISTED_ALONE = 8192;  // and of a long row in one CTA, in dynamic shared memory (256 x 131072,
+                                    // p = 0.9: 132 us, and 212 with 4096)
+constexpr int BINS = 256;       // of one histogram pass (64 x 131072, k = 1000: 68 us, and 75 with 128;
+                                // the joining of 1024 took 6 us in a cluster of 8)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
 constexpr int LIST = 128;       // keys of a bin that are ranked directly
-constexpr int SLICE_LEAST = 16 << 10;   // bytes of a row that are worth a CTA of a cluster
+// Bytes of a row that are worth a CTA of a cluster.  (1 x 32768 bfloat16, k = 50 and
+// p = 0.9: 8.8 and 14.4 us with four CTAs, 10.1 and 19.4 with eight; 1 x 4096, k = 50:
+// 6.7 us with one, 8.6 with two.)
+constexpr int SLICE_LEAST = 16 << 10;
 using u64 = unsigned long long;
 
 // The race's state: the best score, its logit and index (NONE: none yet).
@@ -1474,7 +1485,8 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
     // (A thread without a logit has no mass; nor has a slice, and its maximum is -inf.)
     mass = warp_sum(mass > 0.f ? mass * sl.weight(ref) : 0.f);
     if (lane == 0) s.mass[warp] = mass;
-    // The sample: one vector in 2^sample_shift.  (What lies beyond the bins weighs nothing.)
+    // The sample: one vector in 2^sample_shift.  (What lies beyond the bins weighs
+    // nothing.  64 x 131072, p = 0.9: 48 us; 53 with half as many elements, 48 with twice.)
 #pragma unroll 1
     for (int q = threadIdx.x; q < sl.nv >> sl.sample_shift; q += THREADS) {
       float x[VEC];
@@ -1672,8 +1684,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
   sample_row<T>(a, blockIdx.x >> log_c, per_cta, s);
 }
 
-// CTAs of a row's cluster: as many as the SMs have room for at once, while
-// each still has a slice of some size.
+// CTAs of a row's cluster: as many as the SMs have room for at once (two an SM),
+// while each still has a slice of some size.  (64 x 131072 bfloat16 without filters
+// and with p = 0.9: 14 and 52 us with four CTAs, 18 and 63 with two, 29 and 158 with one,
+// 19 and 63 with eight, whose CTAs do not all fit.  304 x 65536, p = 0.9, T = 0.7: 37
+// us with one, 57 with two.  The rows that a CTA alone could not finish were once left to
+// a second launch with clusters: 304 x 65536, p = 0.9, took 134 us where this takes 77.)
 int cluster_of(int64_t rows, int64_t bytes) {
   int c = 1;
   while (c < MAX_CLUSTER && rows * c * 2 <= 2 * sms() && bytes / (2 * c) >= SLICE_LEAST) c *= 2;
