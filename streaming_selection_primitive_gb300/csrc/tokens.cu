@@ -39,7 +39,7 @@
 //     16 us greedily, 22 us with k = 50;
 //   top-p: the weights of the first pass, and then the rows of step 4, thirty
 //     steps between barriers of 1000 to 4000 cycles each, beside the slices' scan.
-//     64 x 131072, p = 0.9, L: 48 us, and 25 us at T = 0.7, where fewer rows get there;
+//     64 x 131072, p = 0.9, L: 46 us, and 24 us at T = 0.7, where fewer rows get there;
 //   one row: the same chain of steps, whatever its length.  1 x 32768: 5.5 us
 //     without filters, 7 greedily, 8.6 with k = 50, 14 with p = 0.9.
 //
@@ -543,18 +543,47 @@ __device__ __forceinline__ void cross(const S& sl, Shared& s, cg::cluster_group&
   if (lv.bin0 < 0 && lv.ceil < sl.m)
 #pragma unroll 1
     for (int i = 0; i < static_cast<int>(cluster.num_blocks()); ++i) base += s.beyond[i];
-  // Thread t takes bin t.
-  const bool mine = threadIdx.x < BINS;
-  const u64 nc = mine ? s.merged_c[threadIdx.x] : 0, nm = mine ? s.merged_m[threadIdx.x] : 0;
-  if (threadIdx.x == 0) s.bin = BINS;
-  const u64 bc = block_before64(nc, s.wc), bm = base + block_before64(nm, s.wm);
-  if (threadIdx.x == BINS - 1) s.total_m = bm + nm;
-  const u64 before = by_mass ? bm : bc, with = before + (by_mass ? nm : nc);
-  if (before < target && target <= with) {
-    s.bin = threadIdx.x;
-    s.above_c = bc;
-    s.above_m = bm;
-    s.in_c = nc;
+  // One warp, eight neighbouring bins a lane.
+  if (threadIdx.x < 32) {
+    constexpr int EACH = BINS / 32;
+    static_assert(EACH == 8, "eight bins a lane");
+    const int first = EACH * static_cast<int>(threadIdx.x);
+    u64 nc = 0, nm = 0;
+#pragma unroll 1
+    for (int j = 0; j < EACH; ++j) {
+      nc += s.merged_c[first + j];
+      nm += s.merged_m[first + j];
+    }
+    u64 bc = nc, bm = nm;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const u64 oc = __shfl_up_sync(FULL_MASK, bc, d), om = __shfl_up_sync(FULL_MASK, bm, d);
+      if (static_cast<int>(threadIdx.x) >= d) {
+        bc += oc;
+        bm += om;
+      }
+    }
+    bm += base;
+    if (threadIdx.x == 31) s.total_m = bm;
+    const u64 with = by_mass ? bm : bc;
+    bc -= nc;
+    bm -= nm;
+    const bool here = (by_mass ? bm : bc) < target && target <= with;
+    if (here) {
+      int j = 0;
+#pragma unroll 1
+      for (; j + 1 < EACH; ++j) {
+        const u64 c = s.merged_c[first + j], m = s.merged_m[first + j];
+        if ((by_mass ? bm + m : bc + c) >= target) break;
+        bc += c;
+        bm += m;
+      }
+      s.bin = first + j;
+      s.above_c = bc;
+      s.above_m = bm;
+      s.in_c = s.merged_c[first + j];
+    }
+    if (!__any_sync(FULL_MASK, here) && threadIdx.x == 0) s.bin = BINS;
   }
   __syncthreads();
 }
@@ -596,10 +625,11 @@ __device__ bool select(const S& sl, Shared& s, cg::cluster_group& cluster, Level
     // Few enough: every CTA sends the keys that it has to all, after those
     // of the CTAs before it.
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
-    unsigned base = 0;
-#pragma unroll 1
-    for (int i = 0; i < rank; ++i) base += cluster.map_shared_rank(&s, i)->count[bin];
-    if (threadIdx.x == 0) s.slot = base;
+    if (threadIdx.x < 32) {
+      const unsigned base = __reduce_add_sync(
+          FULL_MASK, static_cast<int>(threadIdx.x) < rank ? cluster.map_shared_rank(&s, threadIdx.x)->count[bin] : 0u);
+      if (threadIdx.x == 0) s.slot = base;
+    }
     __syncthreads();
     const float floor = lv.bin0 < 0 ? lv.low(sl, bin) : lv.floor, ceil = lv.bin0 < 0 ? lv.high(sl, bin) : lv.ceil;
     auto send = [&](u64 key) {
@@ -1074,6 +1104,12 @@ __device__ __noinline__ void late_row(Shared& s) {
   __syncthreads();
   Scan scan{Best{-INFINITY, 0.f, NONE}, 0, 0};
   if (dense) {
+    // The noise is on its way to L2 before the loads ask for it.  (512 x 65536 float32,
+    // p = 0.9: 123 us, and 127 without.)
+    const float* noise = late.noise;
+#pragma unroll 1
+    for (int i = max(sl.first, 0) + 32 * static_cast<int>(threadIdx.x); i < min(sl.first + sl.nv * S::VEC, sl.n); i += 32 * THREADS)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + i));
     scan = scan_row<S>(s, greedy ? top : lv.ceil, greedy ? sl.n : -1, greedy ? INFINITY : lv.floor);
   } else if (list) {  // (from the row's bottom on it would be too long)
     list_row(sl, s, lv.floor);
@@ -1474,6 +1510,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
     }
   }
   const float ref = top;
+  float all_top = -INFINITY;  // the row's maximum, where it is known before step 3
   float widest = warp_max_nan(top);
   if (lane == 0) s.redf[warp] = widest;
   __syncthreads();
@@ -1509,6 +1546,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
     float m = s.part[0].top;
 #pragma unroll 1
     for (int i = 1; i < C; ++i) m = max_nan(m, s.part[i].top);
+    all_top = m;
     if (m > -INFINITY) {
       sl.m = m;
 #pragma unroll 1
@@ -1624,18 +1662,24 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
         });
     keys = keys < want ? keys : want;
   }
-  if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->sent[rank] = Sent{widest, tau, keys};
-  cluster.sync();
 
-  // 3. The row's maximum and first keys.
-  top = s.sent[0].top;
-  tau = s.sent[0].tau;
-  int found = s.sent[0].keys;  // keys of all CTAs, or -1
+  // 3. The row's maximum and first keys (nothing to tell where step 2 was left out
+  // and the maximum is known).
+  int found = 0;  // keys of all CTAs, or -1
+  if (want || !need_mass) {
+    if (threadIdx.x < C) cluster.map_shared_rank(&s, threadIdx.x)->sent[rank] = Sent{widest, tau, keys};
+    cluster.sync();
+    top = s.sent[0].top;
+    tau = s.sent[0].tau;
+    found = s.sent[0].keys;
 #pragma unroll 1
-  for (int i = 1; i < C; ++i) {
-    top = max_nan(top, s.sent[i].top);
-    tau = fmaxf(tau, s.sent[i].tau);
-    found = found < 0 || s.sent[i].keys < 0 ? -1 : found + s.sent[i].keys;
+    for (int i = 1; i < C; ++i) {
+      top = max_nan(top, s.sent[i].top);
+      tau = fmaxf(tau, s.sent[i].tau);
+      found = found < 0 || s.sent[i].keys < 0 ? -1 : found + s.sent[i].keys;
+    }
+  } else {
+    top = all_top;
   }
   const bool bad = isnan(top) || !(temperature >= 0.f) || isnan(p) || isnan(min_p);
   if (bad || top == -INFINITY) {
