@@ -130,6 +130,54 @@ def test_clusters(pk, cuda_device, rows, dtype):
         check(pk, logits, noise, most_unclear=0.05, **FILTERS[how])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [3, 40, 160])
+def test_rows_that_keep_much(pk, cuda_device, rows, dtype):
+    # Tens of thousands of tokens are kept: odd rows, noise off the 16-byte grid, masks, min-p after top-p.
+    n = 45001 if rows > 100 else 90001
+    logits, noise = inputs(rows, n, dtype, rows, cuda_device, ld=n + 3, offset=1, spread=0.4)
+    shifted = torch.cat([noise, noise[:, :1]], 1)[:, 1:]
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(3)
+    mask = torch.randint(-(1 << 31), 1 << 31, (rows, (n + 31) // 32), generator=g, device=cuda_device).to(torch.int32)
+    few = 12  # the definition sorts every row
+    for how in ({"p": 0.9}, {"p": 0.97, "min_p": 0.05}, {"p": 0.6, "T": 0.3, "mask": mask}, {"k": 20000, "p": 0.8}, {"min_p": 0.1}):
+        m = how.get("mask")
+        args = {"temperature": how.get("T", 1.0), "top_k": how.get("k", 0), "top_p": how.get("p", 1.0), "min_p": how.get("min_p", 0.0)}
+        all_tokens, all_logprobs = pk.sample_tokens(logits, shifted, mask=m, **args)
+        at = torch.arange(0, rows, max(1, rows // few), device=cuda_device)
+        got, lp = check(pk, logits[at], shifted[at], most_unclear=0.2,
+                        **{**how, **({"mask": m[at].contiguous()} if m is not None else {})})
+        # A row's choice does not depend on how many CTAs shared it (its log-probability by the masses' roundings).
+        assert (all_tokens[at].cpu().numpy() == got).mean() > 0.8
+        assert np.allclose(all_logprobs[at].cpu().numpy()[all_tokens[at].cpu().numpy() == got],
+                           lp[all_tokens[at].cpu().numpy() == got], rtol=0, atol=2e-5)
+
+
+@pytest.mark.parametrize("rows", [2, 160])
+def test_noise_extremes_where_much_is_kept(pk, cuda_device, rows):
+    n = 40000
+    logits, noise = inputs(rows, n, torch.float32, 61, cuda_device, spread=0.1)
+    top = logits.argmax(1)
+    noise[0, top[0]] = 0.0              # ahead of everything
+    noise[1, :] = float("nan")          # never ahead
+    noise[1, top[1]] = 5.0
+    if rows > 2:
+        noise[2, :] = -1.0
+        noise[2, top[2]] = float("inf")
+        noise[3, top[3]] = 1e-42        # below the normal range: 97 ahead of an ordinary number
+        noise[4, ::2] = float("inf")
+    for how in ({"p": 0.9}, {"p": 0.9, "min_p": 0.5}, {"k": 30000}):
+        got, _ = check(pk, logits[:8], noise[:8], **how)
+        for _ in range(2):
+            args = {"top_k": how.get("k", 0), "top_p": how.get("p", 1.0), "min_p": how.get("min_p", 0.0)}
+            every, _ = pk.sample_tokens(logits, noise, **args)
+        want = [0, 1, 3] if rows > 2 else [0, 1]
+        assert all(every[r] == top[r] == int(got[r]) for r in want)
+        if rows > 2:
+            assert every[4] % 2 == 1
+
+
 def test_rows_far_apart(pk, cuda_device):
     # Offsets of logits and noise past 2^31 elements.
     n, far = 5000, (1 << 30) + 1024
