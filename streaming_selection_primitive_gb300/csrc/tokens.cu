@@ -1610,7 +1610,10 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
       const int vectors = flat ? sl.nv : static_cast<int>(s.hits) << shift;
 #pragma unroll 1
       for (int base = threadIdx.x - lane; base < vectors; base += THREADS) {
-        if (*reinterpret_cast<volatile unsigned*>(&s.slot) > CANDIDATES) break;  // (the count only says so)
+        // Too many already: the count alone says so.  (Other warps add to it: one
+        // lane reads, so that the warp leaves as a whole.)
+        const unsigned so_far = lane == 0 ? *reinterpret_cast<volatile unsigned*>(&s.slot) : 0u;
+        if (__shfl_sync(FULL_MASK, so_far, 0) > CANDIDATES) break;
         const int i = base + lane, v = i >= vectors ? sl.nv : flat ? i : s.hit[i >> shift] + (i & ((1 << shift) - 1)) * THREADS;
         unsigned some = 0;
         if (v < sl.nv) {

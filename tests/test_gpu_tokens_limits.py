@@ -1,0 +1,45 @@
+"""sample_tokens at the limits of its lists, cuts and sums, against the definition in float64.
+
+Tolerances are those of test_gpu_tokens.py (its check and inputs are used here).
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_tokens import check, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def few_threads_hold_the_top(rows, n, dtype, device, threads, vectors, seed):
+    """Rows whose largest logits lie in few threads' vectors: element (t + 512 j) VEC + c of thread t.
+
+    A thread's logits are alike and its level is its own, so that the best of `threads` of them bring all that
+    these threads hold."""
+    logits, noise = inputs(rows, n, dtype, seed, device)
+    g = torch.Generator(device=device)
+    g.manual_seed(seed + 1)
+    vec = 16 // logits.element_size()
+    t = torch.randperm(512, generator=g, device=device)[:threads]
+    at = ((t[:, None] + 512 * torch.arange(vectors, device=device))[:, :, None] * vec + torch.arange(vec, device=device))
+    level = 10.0 + torch.arange(threads, device=device) / threads
+    value = level[:, None, None] + torch.rand(at.shape, generator=g, device=device) / threads
+    logits[:, at.flatten()] = value.flatten().to(dtype)
+    return logits, noise
+
+
+@pytest.mark.parametrize("rows", [3, 40, 160, 320])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_more_keys_than_can_be_ranked(pk, cuda_device, rows, dtype):
+    # 1024 keys of a slice can be ranked: copies of one value (no choice of a limit leaves fewer), and many
+    # distinct values in few threads (a higher limit does).
+    n = 40000
+    logits, noise = few_threads_hold_the_top(rows, n, dtype, cuda_device, 120, n // (512 * 16 // (4 if dtype == torch.float32 else 2)), 71)
+    logits[::3] = torch.where(torch.arange(n, device=cuda_device) % 7 == 3, 20.0, logits[::3].float()).to(dtype)
+    at = torch.arange(0, rows, max(1, rows // 10), device=cuda_device)
+    for how in ({"k": 1}, {"k": 50}, {"k": 50, "p": 0.7}, {"T": 0.0}, {"min_p": 0.3}):
+        args = {"temperature": how.get("T", 1.0), "top_k": how.get("k", 0), "top_p": how.get("p", 1.0), "min_p": how.get("min_p", 0.0)}
+        every, _ = pk.sample_tokens(logits, noise, **args)
+        got, _ = check(pk, logits[at], noise[at], most_unclear=0.2, **how)
+        if "k" in how or "T" in how:
+            assert np.array_equal(every[at].cpu().numpy(), got)
