@@ -48,6 +48,7 @@
 // the same whatever order the atomics take.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -940,12 +941,13 @@ __device__ __forceinline__ void list_row(const S& sl, Shared& s, float floor) {
 }
 
 // One pass over the slice and its noise: the race of the tokens above `cut` (its
-// copies up to cut_index included) with a weight of floor_w or more, and a
+// copies up to cut_index included: none if that is NO_COPY) with a weight of floor_w or more, and a
 // list of those in [floor, cut] that are not above.  The noise is read for
 // all, not to wait for the logits first: where a tenth is kept every sector of
 // it is touched anyway.  Scores are in units of log 2; the best of four
 // elements is looked for where it beats the thread's.  (Four at a time: eight
 // need more registers than there are.)
+constexpr int NO_COPY = INT_MIN;  // below every position: a row that starts off the 16-byte boundary has some below 0
 template <typename S>
 __device__ __noinline__ Scan scan_row(Shared& s, float cut, int cut_index, float floor) {
   constexpr int VEC = S::VEC, PARTS = VEC / 4;
@@ -956,7 +958,7 @@ __device__ __noinline__ Scan scan_row(Shared& s, float cut, int cut_index, float
   const bool vec = reinterpret_cast<uintptr_t>(noise) % 16 == 0;
   const int lane = threadIdx.x & 31;
   const float next = key_to_float(ord_key(cut) + 1u);  // (NaN above +inf)
-  if (cut == -INFINITY) cut_index = -1;                // what is not allowed
+  if (cut == -INFINITY) cut_index = NO_COPY;           // what is not allowed
   Best best{-INFINITY, 0.f, NONE};
   u64 mass = 0, kept = 0;
   float sum = 0.f, sum_kept = 0.f;
@@ -1110,7 +1112,7 @@ __device__ __noinline__ void late_row(Shared& s) {
 #pragma unroll 1
     for (int i = max(sl.first, 0) + 32 * static_cast<int>(threadIdx.x); i < min(sl.first + sl.nv * S::VEC, sl.n); i += 32 * THREADS)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + i));
-    scan = scan_row<S>(s, greedy ? top : lv.ceil, greedy ? sl.n : -1, greedy ? INFINITY : lv.floor);
+    scan = scan_row<S>(s, greedy ? top : lv.ceil, greedy ? sl.n : NO_COPY, greedy ? INFINITY : lv.floor);
   } else if (list) {  // (from the row's bottom on it would be too long)
     list_row(sl, s, lv.floor);
   }

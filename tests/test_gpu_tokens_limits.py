@@ -43,3 +43,24 @@ def test_more_keys_than_can_be_ranked(pk, cuda_device, rows, dtype):
         got, _ = check(pk, logits[at], noise[at], most_unclear=0.2, **how)
         if "k" in how or "T" in how:
             assert np.array_equal(every[at].cpu().numpy(), got)
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_tokens_at_the_sampled_ceiling(pk, cuda_device, offset):
+    # Float32 logits on a grid of 1/8 (the spacing near 2^20), so that the value above which tokens are raced
+    # without a list is on the grid too.  Row r's first three logits are r steps below the largest and
+    # have the noise to win: token 0 wherever it is kept.
+    rows, n, T, p = 48, 40001, 4.0, 0.5
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(81)
+    store = torch.zeros(rows * n + offset, device=cuda_device)
+    logits = store[offset:].view(rows, n)
+    steps = torch.randint(0, 65, (n,), generator=g, device=cuda_device)
+    steps[100] = 0
+    logits.copy_((2.0 ** 20 + 8 - 0.125 * steps.float()).expand(rows, n))
+    logits[:, :3] = 2.0 ** 20 + 8 - 0.125 * torch.arange(rows, device=cuda_device)[:, None].float()
+    noise = torch.empty((rows, n), device=cuda_device).exponential_(generator=g)
+    noise[:, :3] = torch.tensor([1e-30, 1e-29, 1e-28], device=cuda_device)
+    got, _ = check(pk, logits, noise, T=T, p=p, most_unclear=0.1)
+    # Half of the mass of levels 0 .. 64 that fall by exp(-1/32) each lies above level 18 or so.
+    assert (got[:15] == 0).all() and (got[22:] != 0).all()
