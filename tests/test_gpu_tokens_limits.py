@@ -64,3 +64,29 @@ def test_tokens_at_the_sampled_ceiling(pk, cuda_device, offset):
     got, _ = check(pk, logits, noise, T=T, p=p, most_unclear=0.1)
     # Half of the mass of levels 0 .. 64 that fall by exp(-1/32) each lies above level 18 or so.
     assert (got[:15] == 0).all() and (got[22:] != 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_of_2_to_the_28(pk, cuda_device, dtype):
+    # Logits of 0 at the start of each eighth of the row (a CTA's slice: every thread meets its maximum at
+    # once), and otherwise x: the mass is zeros + (n - zeros) exp(x).  A thread adds up 65536 weights below 1.
+    n = 1 << 28
+    logits = torch.zeros((1, n), dtype=dtype, device=cuda_device)
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(91)
+    noise = torch.empty((1, n), device=cuda_device).exponential_(generator=g)
+    zeros = 8 * 8192
+    off = []
+    for x in (-0.15234375, -0.203125, -0.5, -1.5546875, -2.5, -3.0):
+        logits.view(8, n // 8)[:, 8192:] = x
+        mass = zeros + (n - zeros) * np.exp(x)
+        for p in (1.0, 0.5):
+            token, lp = (t.item() for t in pk.sample_tokens(logits, noise, top_p=p))
+            l = logits[0, token].item()
+            off.append(abs(lp - (l - np.log(p * mass))) / (1e-5 + 4e-7 * abs(lp)))
+            # The token is the best of those that are surely kept, or one at the cut.
+            cut = n if p == 1 else int(n * (p - 2.0 ** -12))
+            score = logits[0, :cut].double() - noise[0, :cut].double().log()
+            assert l - np.log(noise[0, token].double().item()) >= score.max().item() - 2.0 ** -15
+            del score
+    assert max(off) < 1, off
