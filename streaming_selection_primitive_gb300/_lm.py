@@ -92,7 +92,9 @@ def route(logits, k: int, *, score: str = "softmax", normalize: bool = True, bia
     its slots hold expert -1 and gate 0.  A -inf logit is never chosen.  Equal
     values are chosen by lower index.
 
-    Where logits requires a gradient, gates and loss carry it (route_backward)."""
+    Where logits requires a gradient, gates and loss carry it (route_backward).
+    There is no second derivative: going back through a gradient that was taken
+    with create_graph raises."""
     code = _SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
@@ -139,6 +141,14 @@ def _autograd():
     if _function is None:
         torch = _torch()
 
+        def gradient(logits, experts, counts, grad_gates, grad_loss, score, normalize):
+            r = Routing(None, experts, counts, None, score, normalize)
+            if grad_gates is not None:
+                grad_gates = grad_gates.detach().float().contiguous()
+            if grad_loss is not None:
+                grad_loss = grad_loss.detach().float().contiguous()
+            return route_backward(logits.detach(), r, grad_gates=grad_gates, grad_loss=grad_loss)
+
         class Route(torch.autograd.Function):
             @staticmethod
             def forward(ctx, logits, k, score, normalize, bias, mask, balance):
@@ -151,13 +161,19 @@ def _autograd():
 
             @staticmethod
             def backward(ctx, grad_gates, _experts, _counts, grad_loss):
-                logits, experts, counts = ctx.saved_tensors
-                r = Routing(None, experts, counts, None, *ctx.how)
-                if grad_gates is not None:
-                    grad_gates = grad_gates.float().contiguous()
-                if grad_loss is not None:
-                    grad_loss = grad_loss.float().contiguous()
-                grad = route_backward(logits.detach(), r, grad_gates=grad_gates, grad_loss=grad_loss)
-                return (grad,) + (None,) * 6
+                of = RouteGradient.apply if torch.is_grad_enabled() else gradient
+                return (of(*ctx.saved_tensors, grad_gates, grad_loss, *ctx.how),) + (None,) * 6
+
+        class RouteGradient(torch.autograd.Function):
+            """The gradient under create_graph: what is made of it leads back here, to the logits and to the
+            gradients of gates and loss, instead of counting as a constant."""
+
+            @staticmethod
+            def forward(ctx, *args):
+                return gradient(*args)
+
+            @staticmethod
+            def backward(ctx, _grad):
+                raise NotImplementedError("route has no second derivative")
         _function = Route
     return _function
