@@ -48,7 +48,11 @@ def sample_tokens(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     token i is allowed.  The filters are applied in that order, each to what the
     one before kept; temperature 0 takes the largest logit.  A row with nothing
     to choose gives (-1, -inf), one with an allowed NaN (-1, nan).  The same
-    inputs give the same token and log-probability."""
+    inputs give the same token and log-probability.
+
+    Not differentiable: the log-probabilities come without a graph, also where
+    logits or temperature require a gradient (what of either has a forward-mode
+    tangent raises).  For a loss take them anew from the logits."""
     r = (_ext or _native()).sample_tokens(logits, noise, temperature, top_k, top_p, min_p, mask, out,
                                           None if stream is None else stream.cuda_stream)
     if type(r) is int:
@@ -94,7 +98,8 @@ def route(logits, k: int, *, score: str = "softmax", normalize: bool = True, bia
 
     Where logits requires a gradient, gates and loss carry it (route_backward).
     There is no second derivative: going back through a gradient that was taken
-    with create_graph raises."""
+    with create_graph raises.  Nor is there one in forward mode: logits with a
+    tangent raise."""
     code = _SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
@@ -119,7 +124,8 @@ def route_backward(logits, routing: Routing, *, grad_gates=None, grad_loss=None,
 
     grad_gates: (tokens, k) float32, or None.  grad_loss: a float32 tensor of one
     element on the device, or None.  routing.counts may have been replaced by
-    the sum over several devices.  out: where to write, unit column stride."""
+    the sum over several devices.  out: where to write, unit column stride.
+    The result comes without a graph; a forward-mode tangent raises."""
     code = _SCORES.get(routing.score)
     if code is None:
         raise ValueError(f"routing.score must be one of {sorted(_SCORES)}")

@@ -39,6 +39,12 @@ std::string text(const Tensor& t) {
   return s + ")";
 }
 
+// A forward-mode tangent of what the outputs are a function of would be lost.
+const Tensor& without_tangent(const Tensor& t, const char* name) {
+  if (t._fw_grad(0).defined()) refuse(PyExc_NotImplementedError, "%s has a forward-mode derivative, which this call has not", name);
+  return t;
+}
+
 struct Logits {
   const Tensor* t;
   int64_t rows, n, ld;
@@ -52,6 +58,7 @@ Logits logits_of(PyObject* o) {
   if (!t.is_cuda() || (s != at::kFloat && s != at::kBFloat16 && s != at::kHalf))
     refuse(PyExc_TypeError, "logits must be a float32, bfloat16 or float16 CUDA tensor");
   if (t.dim() != 2) refuse(PyExc_ValueError, "logits must be 2-D");
+  without_tangent(t, "logits");
   const int64_t rows = t.size(0), n = t.size(1);
   if (n > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "logits must have unit column stride");
   return {&t, rows, n, rows > 1 ? t.stride(0) : n, s == at::kFloat ? PROFK_F32 : s == at::kBFloat16 ? PROFK_BF16 : PROFK_F16};
@@ -126,10 +133,12 @@ PyObject* sample_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int64_t noise_ld = rows_of(noise, "noise", x.rows, x.n);
   profk_sampling how{};
   const int64_t rows[1] = {x.rows};
-  if (THPVariable_Check(arg[2]))
+  if (THPVariable_Check(arg[2])) {
+    without_tangent(THPVariable_Unpack(arg[2]), "temperature");
     how.temperature = static_cast<float*>(array(arg[2], "temperature", at::kFloat, like, rows));
-  else
+  } else {
     how.all_temperature = static_cast<float>(number(arg[2]));
+  }
   if (THPVariable_Check(arg[3]))
     how.top_k = static_cast<int32_t*>(array(arg[3], "top_k", at::kInt, like, rows));
   else
@@ -205,9 +214,12 @@ PyObject* route_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const profk_routing how{static_cast<int>(whole(arg[3])), arg[4] == Py_True, nullptr, nullptr};
   const float *grad_gates = nullptr, *grad_loss = nullptr;
   const int64_t* counts = nullptr;
-  if (arg[5] != Py_None) grad_gates = static_cast<float*>(array(arg[5], "grad_gates", at::kFloat, like, {x.rows, k}));
+  if (arg[5] != Py_None) {
+    grad_gates = static_cast<float*>(array(arg[5], "grad_gates", at::kFloat, like, {x.rows, k}));
+    without_tangent(THPVariable_Unpack(arg[5]), "grad_gates");
+  }
   if (arg[6] != Py_None) {
-    const Tensor& g = on_device(arg[6], "grad_loss", at::kFloat, like);
+    const Tensor& g = without_tangent(on_device(arg[6], "grad_loss", at::kFloat, like), "grad_loss");
     if (g.numel() != 1) refuse(PyExc_ValueError, "grad_loss must hold one element");
     grad_loss = static_cast<float*>(g.data_ptr());
     counts = static_cast<int64_t*>(array(arg[2], "routing.counts", at::kLong, like, {x.n}));
