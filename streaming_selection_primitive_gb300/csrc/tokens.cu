@@ -789,6 +789,88 @@ __device__ __forceinline__ void rank_candidates(const Shared& s, int keys, B&& b
   }
 }
 
+// A higher limit for the slice's keys from `least` on, of which there are more
+// than can be ranked: the want-th largest of an even share of them, one in so
+// many in the order of the threads with a hit (flat: of the vectors).  (What the
+// count that found them too many has stored by then depends on the order of the
+// warps, and so would the limit.  64 x 131072 bfloat16 in ascending order, k = 50:
+// 103 us, and 151 with the first that were stored.)
+template <typename S>
+__device__ __noinline__ float higher_limit(Shared& s, float least, bool flat, int shift, int want) {
+  const S sl = *reinterpret_cast<const S*>(s.slice);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!flat) {  // s.hit in the threads' order
+    if (threadIdx.x < WARPS) s.redk[threadIdx.x] = 0u;
+    const int hits = static_cast<int>(s.hits), mine = static_cast<int>(threadIdx.x) < hits ? s.hit[threadIdx.x] : 0;
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < hits) atomicOr(&s.redk[mine >> 5], 1u << (mine & 31));
+    __syncthreads();
+    const unsigned before = s.redk[warp] & ((1u << lane) - 1u);
+    if (s.redk[warp] >> lane & 1u) {
+      unsigned at = __popc(before);
+#pragma unroll 1
+      for (int w = 0; w < warp; ++w) at += __popc(s.redk[w]);
+      s.hit[at] = static_cast<unsigned short>(threadIdx.x);
+    }
+    __syncthreads();
+  }
+  const int vectors = flat ? sl.nv : static_cast<int>(s.hits) << shift;
+  auto vector = [&](int i) {
+    return i >= vectors ? sl.nv : flat ? i : s.hit[i >> shift] + (i & ((1 << shift) - 1)) * THREADS;
+  };
+  auto marks = [&](int v) {
+    unsigned some = 0;
+    if (v < sl.nv) {
+      float x[S::VEC];
+      sl.load(v, x);
+#pragma unroll
+      for (int j = 0; j < S::VEC; ++j) some |= x[j] >= least ? 1u << j : 0u;
+    }
+    return some;
+  };
+  int mine = 0;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < vectors; i += THREADS) mine += __popc(marks(vector(i)));
+  mine = __reduce_add_sync(FULL_MASK, mine);
+  if (lane == 0) s.redk[warp] = mine;
+  __syncthreads();
+  unsigned rank = 0, all = 0;
+#pragma unroll 1
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) rank += s.redk[w];
+    all += s.redk[w];
+  }
+  const unsigned step = (all + CANDIDATES - 1) / CANDIDATES;
+#pragma unroll 1
+  for (int base = threadIdx.x - lane; base < vectors; base += THREADS) {
+    const int v = vector(base + lane);
+    unsigned some = marks(v);
+    const int n = __popc(some);
+    int with = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(FULL_MASK, with, d);
+      if (lane >= d) with += o;
+    }
+    unsigned at = rank + with - n;
+    rank += __shfl_sync(FULL_MASK, with, 31);
+#pragma unroll 1
+    for (; some; some &= some - 1, ++at)
+      if (at % step == 0) s.candidates[at / step] = sl.key(sl.one(v, __ffs(some) - 1), sl.element(v) + __ffs(some) - 1);
+    __syncwarp();
+  }
+  const int stored = static_cast<int>((all + step - 1) / step);
+  if (threadIdx.x == 0) s.candidates[stored] = 0;
+  __syncthreads();
+  rank_candidates(
+      s, stored, [](bool, int, u64) { return 0; },
+      [&](u64 key, int place, int) {
+        if (place == want - 1) s.thr = key;
+      });
+  __syncthreads();
+  return sl.logit_of(s.thr);
+}
+
 // x - log q; NaN noise is never ahead.
 __device__ __forceinline__ float race(float x, float q) { return fmaxf(fmaf(lm_log2(q), -LN2, x), -INFINITY); }
 
@@ -1672,15 +1754,13 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
       __syncthreads();
       keys = static_cast<int>(s.slot);
       if (keys <= CANDIDATES || turn == 2) break;
-      // Too many (neighbours are alike, so that a thread holds several):
-      // again from the want-th largest of those that were stored.
-      rank_candidates(
-          s, CANDIDATES, [](bool, int, u64) { return 0; },
-          [&](u64 key, int rank, int) {
-            if (rank == want - 1) s.thr = key;
-          });
+      // Too many (neighbours are alike, so that a thread holds several): again
+      // from a higher limit, if there is one.
+      if (threadIdx.x == 0) *reinterpret_cast<S*>(s.slice) = sl;
       __syncthreads();
-      tau = sl.logit_of(s.thr);
+      const float higher = higher_limit<S>(s, least, flat, shift, want);
+      if (!(higher > least)) break;
+      tau = higher;
       if (threadIdx.x == 0) s.slot = 0;
       __syncthreads();
     }

@@ -90,3 +90,19 @@ def test_rows_of_2_to_the_28(pk, cuda_device, dtype):
             assert l - np.log(noise[0, token].double().item()) >= score.max().item() - 2.0 ** -15
             del score
     assert max(off) < 1, off
+
+
+@pytest.mark.parametrize("rows,k", [(320, 256), (70, 128)])
+def test_the_same_call_gives_the_same_bits_past_the_lists(pk, cuda_device, rows, k):
+    # More keys reach the limit than can be ranked, twice, and the third limit lets through about as many as can:
+    # which of them a limit is taken from must not depend on the order of the threads.  All scores of a row
+    # are equal but for their roundings, so that another way through the kernel shows.
+    n, threads, vectors = 65536, k + 40, 16 if k == 256 else 32
+    logits, _ = few_threads_hold_the_top(rows, n, torch.float32, cuda_device, threads, vectors if rows > 300 else 8, 101)
+    logits[:] = logits[torch.arange(rows, device=cuda_device) % 8]
+    noise = torch.exp(logits - logits.amax(1, keepdim=True)) * torch.linspace(0.5, 2.0, rows, device=cuda_device)[:, None]
+    for how in ({}, {"top_p": 0.99}):
+        want = pk.sample_tokens(logits, noise, top_k=k, **how)
+        for _ in range(60):
+            got = pk.sample_tokens(logits, noise, top_k=k, **how)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1].view(torch.int32), want[1].view(torch.int32))
