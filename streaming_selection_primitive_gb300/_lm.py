@@ -6,8 +6,10 @@
 
 As in the rest of the package, everything runs in the library's kernels on the
 current stream (or ``stream``), and a tensor that the kernels cannot read as
-it is raises instead of being copied.  A call given ``stream`` marks the
-outputs that it makes as used there; the inputs' lifetime is the caller's.
+it is raises instead of being copied.  A call given ``stream`` makes its outputs
+on that stream, so that it waits for nothing on the current one, and marks them as
+used on the current stream as well; the caller orders the two where they meet, and
+the inputs' lifetime is the caller's.
 """
 from __future__ import annotations
 
@@ -37,6 +39,14 @@ def _native():
     return _ext
 
 
+def _used_here(outputs):
+    """Outputs made on another stream: their memory is not given back before the current stream is done with them."""
+    current = _torch().cuda.current_stream(outputs[0].device)
+    for t in outputs:
+        if t is not None:
+            t.record_stream(current)
+
+
 def sample_tokens(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, mask=None, out=None, stream=None):
     """One token per row of logits: (tokens int64, logprobs float32).
 
@@ -58,8 +68,7 @@ def sample_tokens(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     if type(r) is int:
         _abi.check(r)
     if stream is not None and out is None:
-        for t in r:
-            t.record_stream(stream)
+        _used_here(r)
     return r
 
 
@@ -112,9 +121,7 @@ def route(logits, k: int, *, score: str = "softmax", normalize: bool = True, bia
     if type(r) is int:
         _abi.check(r)
     if stream is not None:
-        for t in r:
-            if t is not None:
-                t.record_stream(stream)
+        _used_here(r)
     return Routing(*r, score, normalize)
 
 
@@ -134,7 +141,7 @@ def route_backward(logits, routing: Routing, *, grad_gates=None, grad_loss=None,
     if type(r) is int:
         _abi.check(r)
     if stream is not None and out is None:
-        r.record_stream(stream)
+        _used_here((r,))
     return r
 
 

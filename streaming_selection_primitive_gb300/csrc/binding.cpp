@@ -105,11 +105,23 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
   return at::detail::empty_cuda(shape, like.options().dtype(type));
 }
 
-// The stream's address where one is given, else the device's current stream.
-cudaStream_t stream_of(PyObject* o, const Tensor& like) {
-  if (o != Py_None) return reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(o));
-  return c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
-}
+// The tensors' device, and the call's stream where one is given, made current for the
+// call: its outputs come from that stream's blocks.  (A block of the current
+// stream's may still be in use by work queued there.)
+class Place {
+ public:
+  Place(PyObject* o, const Tensor& like) : device_(like.device()) {
+    if (o == Py_None) return;
+    void* given = PyLong_AsVoidPtr(o);
+    if (!given && PyErr_Occurred()) throw python_error();
+    side_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(given), like.device().index()));
+  }
+  cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream().stream(); }
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard side_;
+};
 
 PyObject* tuple_of(std::initializer_list<Tensor> tensors) {
   PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
@@ -158,7 +170,7 @@ PyObject* sample_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
     mask_ld = rows_of(m, "mask", x.rows, (x.n + 31) / 32);
     mask = static_cast<const uint32_t*>(m.data_ptr());
   }
-  const c10::cuda::CUDAGuard guard(like.device());
+  const Place place(arg[8], like);
   Tensor tokens, logprobs;
   if (arg[7] == Py_None) {
     tokens = empty(rows, at::kLong, like);
@@ -173,7 +185,7 @@ PyObject* sample_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   }
   const int code = profk_sample_tokens(like.data_ptr(), x.type, x.rows, x.n, x.ld, static_cast<float*>(noise.data_ptr()),
                                        noise_ld, mask, mask_ld, &how, static_cast<int64_t*>(tokens.data_ptr()),
-                                       static_cast<float*>(logprobs.data_ptr()), stream_of(arg[8], like));
+                                       static_cast<float*>(logprobs.data_ptr()), place.stream());
   return code == PROFK_OK ? tuple_of({tokens, logprobs}) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
@@ -189,14 +201,14 @@ PyObject* route(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   if (arg[4] != Py_None) how.bias = static_cast<float*>(array(arg[4], "bias", at::kFloat, like, {x.n}));
   if (arg[5] != Py_None) how.mask = static_cast<uint8_t*>(array(arg[5], "mask", at::kBool, like, {x.rows}));
   if (k < 1 || k > x.n) refuse(PyExc_ValueError, "k must be in 1 .. experts");
-  const c10::cuda::CUDAGuard guard(like.device());
+  const Place place(arg[7], like);
   const Tensor gates = empty({x.rows, k}, at::kFloat, like), experts = empty({x.rows, k}, at::kLong, like),
                counts = empty({x.n}, at::kLong, like);
   Tensor loss;
   if (arg[6] == Py_True) loss = empty({}, at::kFloat, like);
   const int code = profk_route(like.data_ptr(), x.type, x.rows, x.n, x.ld, k, &how, static_cast<float*>(gates.data_ptr()),
                                static_cast<int64_t*>(experts.data_ptr()), static_cast<int64_t*>(counts.data_ptr()),
-                               loss.defined() ? static_cast<float*>(loss.data_ptr()) : nullptr, stream_of(arg[7], like));
+                               loss.defined() ? static_cast<float*>(loss.data_ptr()) : nullptr, place.stream());
   return code == PROFK_OK ? tuple_of({gates, experts, counts, loss}) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
@@ -224,7 +236,7 @@ PyObject* route_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
     grad_loss = static_cast<float*>(g.data_ptr());
     counts = static_cast<int64_t*>(array(arg[2], "routing.counts", at::kLong, like, {x.n}));
   }
-  const c10::cuda::CUDAGuard guard(like.device());
+  const Place place(arg[8], like);
   Tensor out;
   int64_t out_ld = x.n;
   if (arg[7] == Py_None) {
@@ -234,7 +246,7 @@ PyObject* route_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
     out_ld = rows_of(out, "out", x.rows, x.n);
   }
   const int code = profk_route_backward(like.data_ptr(), x.type, x.rows, x.n, x.ld, k, &how, chosen, counts, grad_gates,
-                                        grad_loss, out.data_ptr(), out_ld, stream_of(arg[8], like));
+                                        grad_loss, out.data_ptr(), out_ld, place.stream());
   return code == PROFK_OK ? THPVariable_Wrap(out) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }

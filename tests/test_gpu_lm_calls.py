@@ -64,3 +64,80 @@ def test_log_probabilities_come_without_a_graph(pk, cuda_device):
     want = pk.sample_tokens(z, noise)
     got = pk.sample_tokens(z.clone().requires_grad_(), noise)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and not got[1].requires_grad
+
+
+@pytest.mark.parametrize("call", ["sample_tokens", "route", "route_backward"])
+def test_outputs_on_another_stream_leave_freed_blocks_alone(pk, cuda_device, call):
+    # Inputs made on the side stream, which therefore has no reason to wait for the current one; there, work is
+    # queued on tensors of the outputs' sizes that have been let go.  Outputs made from their memory would be
+    # written before it is read.
+    tokens, E, k = 4096, 64, 4
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        z, g = rows(cuda_device, tokens, E)
+        noise = torch.empty_like(z).exponential_(generator=g)
+        r = pk.route(z, k)
+        dg = torch.ones_like(r.gates).cumsum(1)
+        want = {"sample_tokens": lambda: pk.sample_tokens(z, noise), "route": lambda: pk.route(z, k)[:4],
+                "route_backward": lambda: (pk.route_backward(z, r, grad_gates=dg),)}[call]()
+    torch.cuda.synchronize()
+    freed = [torch.full(t.shape, 7, dtype=t.dtype, device=cuda_device) for t in want]
+    kept = [torch.zeros_like(t) for t in freed]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for a, b in zip(kept, freed):
+        a.copy_(b)
+    blocks = {t.data_ptr() for t in freed}
+    del freed, a, b
+    got = {"sample_tokens": lambda: pk.sample_tokens(z, noise, stream=side), "route": lambda: pk.route(z, k, stream=side)[:4],
+           "route_backward": lambda: (pk.route_backward(z, r, grad_gates=dg, stream=side),)}[call]()
+    assert not blocks & {t.data_ptr() for t in got}
+    side.synchronize()
+    assert all(torch.equal(x.cpu(), y.cpu()) for x, y in zip(got, want))
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in kept)
+
+
+def test_outputs_of_another_stream_outlive_their_use_here(pk, cuda_device):
+    # Let go while the current stream still has work on them: the side stream must not get the memory yet.
+    z, _ = rows(cuda_device, 4096, 64)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r = pk.route(z, 4, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    kept, want = torch.zeros_like(r.gates), r.gates.clone()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    kept.copy_(r.gates)
+    block = r.gates.data_ptr()
+    del r
+    again = pk.route(z, 4, stream=side)
+    assert block not in {t.data_ptr() for t in again[:4]}
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want)
+
+
+def test_streams_given_and_current_agree(pk, cuda_device):
+    z, g = rows(cuda_device, 500, 64)
+    noise = torch.empty_like(z).exponential_(generator=g)
+    want, lp = pk.sample_tokens(z, noise, top_k=5)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.default_stream(), torch.cuda.current_stream(), torch.cuda.Stream(),
+                   torch.cuda.ExternalStream(torch.cuda.Stream().cuda_stream)):
+        before = torch.cuda.current_stream()
+        got = pk.sample_tokens(z, noise, top_k=5, stream=stream)
+        assert torch.cuda.current_stream() == before
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want) and torch.equal(got[1], lp)
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = pk.sample_tokens(z, noise, top_k=5, stream=side)
+        r = pk.route(z, 3, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    z.copy_(z.flip(0))
+    graph.replay()
+    want = pk.sample_tokens(z, noise, top_k=5)
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(r.experts, pk.route(z, 3).experts)
