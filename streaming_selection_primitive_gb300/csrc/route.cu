@@ -779,11 +779,15 @@ int route_grid(int64_t tokens, int warps, int per_sm) {
   return static_cast<int>(need < most ? need : most);
 }
 
-// Sets a kernel's dynamic shared memory (above the default limit once) and launches it.
+// Launches a kernel with `smem` bytes of dynamic shared memory, `most` being what any
+// call of it asks for.  The limit is the kernel's, for all host threads: it is
+// set to the same number whatever the call, so that none of them takes it back
+// below what another is about to launch with.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_with(void (*kernel)(KArgs...), int grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t launch_with(void (*kernel)(KArgs...), int grid, int threads, size_t smem, size_t most, cudaStream_t stream,
+                        Args... args) {
+  if (most > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(kernel, dim3(grid), dim3(threads), smem, stream, args...);
@@ -804,9 +808,9 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
         using T = decltype(type);
         constexpr int R = decltype(width)::value;
         constexpr bool SIG = decltype(sig)::value;
-        const size_t smem = route_smem<T, R>(a.experts);
+        const size_t smem = route_smem<T, R>(a.experts), most = route_smem<T, R>(32 * R);
         if (a.tokens <= ONE_TOKENS<R>)
-          return launch_with(k_route_one<T, R, SIG>, CLUSTER, WARPS<R> * 32, smem, stream, a);
+          return launch_with(k_route_one<T, R, SIG>, CLUSTER, WARPS<R> * 32, smem, most, stream, a);
         const int grid = route_grid(a.tokens, WARPS<R>, PER_SM<R>);
         cudaMemPool_t pool;
         cudaError_t err = library_pool(&pool);
@@ -817,7 +821,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         unsigned* part_c = static_cast<unsigned*>(part);
         float* part_p = reinterpret_cast<float*>(static_cast<char*>(part) + each);
-        err = launch_with(k_route<T, R, SIG>, grid, WARPS<R> * 32, smem, stream, a, part_p, part_c);
+        err = launch_with(k_route<T, R, SIG>, grid, WARPS<R> * 32, smem, most, stream, a, part_p, part_c);
         if (err == cudaSuccess)
           err = launch_kernel(k_route_join, dim3(CLUSTER), dim3(JOIN_THREADS), 0, stream, grid, a.experts, part_p, part_c,
                               a.counts, a.loss);
@@ -834,8 +838,9 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t strea
       return by_score(a.sigmoid, [&](auto sig) {
         using T = decltype(type);
         constexpr int R = decltype(width)::value;
+        constexpr size_t smem = size_t(WARPS<R>) * (Ring<T, R>::BYTES + 32 * R * 4);
         return launch_with(k_route_backward<T, R, decltype(sig)::value>, route_grid(a.tokens, WARPS<R>, PER_SM<R>),
-                           WARPS<R> * 32, size_t(WARPS<R>) * (Ring<T, R>::BYTES + 32 * R * 4), stream, a);
+                           WARPS<R> * 32, smem, smem, stream, a);
       });
     });
   });

@@ -1,4 +1,7 @@
 """How the language-model selections are called: derivatives, streams, host threads, messages."""
+import ctypes as C
+import threading
+
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
@@ -141,3 +144,45 @@ def test_streams_given_and_current_agree(pk, cuda_device):
     graph.replay()
     want = pk.sample_tokens(z, noise, top_k=5)
     assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(r.experts, pk.route(z, 3).experts)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("wide,narrow", [(256, 130), (512, 260), (1024, 600)])
+def test_host_threads_with_different_numbers_of_experts(pk, cuda_device, dtype, wide, narrow):
+    # Both counts take the same kernels with different amounts of shared memory.  Through the C-ABI, whose calls
+    # run side by side (ctypes gives up the interpreter's lock), each thread on a stream of its own.
+    from streaming_selection_primitive_gb300 import _abi
+    lib = pk.lib()
+
+    def arrays(E):
+        z, g = rows(cuda_device, 300, E, seed=E)
+        z = z.to(dtype)
+        out = [torch.empty((300, 4), device=cuda_device), torch.empty((300, 4), dtype=torch.int64, device=cuda_device),
+               torch.empty(E, dtype=torch.int64, device=cuda_device), torch.empty((), device=cuda_device), torch.empty_like(z)]
+        return z, out, torch.cuda.Stream()
+
+    def work(E, z, out, stream, failed):
+        how = _abi.Routing(_abi.SCORE_SIGMOID, 1)
+        kind = _abi.F32 if dtype == torch.float32 else _abi.BF16
+        gates, experts, counts, loss, grad = (t.data_ptr() for t in out)
+        for i in range(3000):
+            a = lib.profk_route(z.data_ptr(), kind, 300, E, E, 4, C.byref(how), gates, experts, counts, loss, stream.cuda_stream)
+            b = lib.profk_route_backward(z.data_ptr(), kind, 300, E, E, 4, C.byref(how), experts, counts, gates, loss, grad, E,
+                                         stream.cuda_stream)
+            if a or b:
+                failed.append((E, i, a, b))
+                return
+
+    sets = {E: arrays(E) for E in (wide, narrow)}
+    torch.cuda.synchronize()
+    failed = []
+    threads = [threading.Thread(target=work, args=(E, *sets[E], failed)) for E in (wide, narrow)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for E, (z, out, _) in sets.items():
+        r = pk.route(z, 4, score="sigmoid")
+        assert torch.equal(out[0], r.gates) and torch.equal(out[1], r.experts) and torch.equal(out[2], r.counts)
