@@ -5,7 +5,8 @@ Each translation unit is compiled by nvcc in parallel, then linked with
 driver at run time).  Objects go to ``_build/``; the library to ``lib/``.
 A unit is recompiled when it or any header is newer than its object.  The
 language-model selections' Python half (csrc/binding.cpp) is compiled by g++
-against the installed torch and linked to the library.
+against the installed torch and linked to the library, which needs neither: it
+is linked first, and without torch it is all that is built.
 """
 from __future__ import annotations
 
@@ -88,40 +89,54 @@ def _run(cmd, what: str, verbose: bool) -> None:
         raise RuntimeError(f"building {what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _binding_jobs(force: bool):
+    """(object, library, whether the object is stale) of the binding; None without torch."""
+    try:
+        out = binding_path()
+    except ModuleNotFoundError:
+        return None
+    obj = BUILD / (out.stem + ".o")
+    stale = force or not obj.exists() or obj.stat().st_mtime < max(BINDING_SOURCE.stat().st_mtime, _headers_mtime())
+    return obj, out, stale
+
+
 def build(verbose: bool = False, force: bool = False) -> Path:
-    """Compiles what is stale and links lib/libprofk.so; returns its path."""
+    """Compiles what is stale and links lib/libprofk.so; returns its path.  A
+    binding that does not compile raises after that."""
     BUILD.mkdir(exist_ok=True)
     LIBDIR.mkdir(exist_ok=True)
     hdr = _headers_mtime()
-    binding = binding_path()
-    binding_obj = BUILD / (binding.stem + ".o")
-    binding_stale = force or not binding_obj.exists() or \
-        binding_obj.stat().st_mtime < max(BINDING_SOURCE.stat().st_mtime, hdr)
+    binding = _binding_jobs(force)
     jobs = []
     for name in SOURCES:
         src = CSRC / name
         obj = BUILD / (name + ".o")
         if force or not obj.exists() or obj.stat().st_mtime < max(src.stat().st_mtime, hdr):
             jobs.append((src, obj))
-    if jobs or binding_stale:
-        with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
-            extra = ex.submit(_compile_binding, binding_obj, verbose) if binding_stale else None
-            list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
-            if extra is not None:
-                extra.result()
-    objs = [BUILD / (n + ".o") for n in SOURCES]
-    newest = max(o.stat().st_mtime for o in objs)
-    if force or jobs or not LIB.exists() or LIB.stat().st_mtime < newest:
-        tmp = LIB.with_suffix(".so.tmp")
-        cmd = [_nvcc(), "-shared"] + ARCH + ["-o", str(tmp)] + [str(o) for o in objs]
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+        # (Among the library's units, not to be waited for by itself.)
+        extra = ex.submit(_compile_binding, binding[0], verbose) if binding and binding[2] else None
+        list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
+        objs = [BUILD / (n + ".o") for n in SOURCES]
+        newest = max(o.stat().st_mtime for o in objs)
+        if force or jobs or not LIB.exists() or LIB.stat().st_mtime < newest:
+            tmp = LIB.with_suffix(".so.tmp")
+            cmd = [_nvcc(), "-shared"] + ARCH + ["-o", str(tmp)] + [str(o) for o in objs]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
+        if extra is not None:
+            extra.result()
+    if binding is None:
         if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB)
-    if force or not binding.exists() or binding.stat().st_mtime < binding_obj.stat().st_mtime:
-        _link_binding(binding_obj, binding, verbose)
+            print("no torch: the library alone", flush=True)
+        return LIB
+    obj, out, _ = binding
+    if force or not out.exists() or out.stat().st_mtime < obj.stat().st_mtime:
+        _link_binding(obj, out, verbose)
     return LIB
 
 
