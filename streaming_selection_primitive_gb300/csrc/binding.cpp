@@ -33,10 +33,10 @@ template <typename... A>
   throw python_error();
 }
 
-std::string text(const Tensor& t) {
+std::string text(at::IntArrayRef shape) {
   std::string s = "(";
-  for (int64_t d : t.sizes()) s += std::to_string(d) + ", ";
-  return s + ")";
+  for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
+  return s + (shape.size() == 1 ? ",)" : ")");
 }
 
 // A forward-mode tangent of what the outputs are a function of would be lost.
@@ -76,16 +76,18 @@ const Tensor& on_device(PyObject* o, const char* name, at::ScalarType type, cons
 // The same, contiguous and of the given shape: its address.
 void* array(PyObject* o, const char* name, at::ScalarType type, const Tensor& like, at::IntArrayRef shape) {
   const Tensor& t = on_device(o, name, type, like);
-  if (t.sizes() != shape || !t.is_contiguous())
-    refuse(PyExc_ValueError, "%s must be contiguous and of another shape than %s", name, text(t).c_str());
+  if (t.sizes() != shape)
+    refuse(PyExc_ValueError, "%s must have shape %s, not %s", name, text(shape).c_str(), text(t.sizes()).c_str());
+  if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
   return t.data_ptr();
 }
 
 // A 2-D tensor of the given shape with unit column stride: its row stride.
 int64_t rows_of(const Tensor& t, const char* name, int64_t rows, int64_t n) {
-  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != n || (n > 1 && t.stride(1) != 1))
-    refuse(PyExc_ValueError, "%s must have shape (%lld, %lld) and unit column stride, not %s", name,
-                            static_cast<long long>(rows), static_cast<long long>(n), text(t).c_str());
+  const int64_t shape[2] = {rows, n};
+  if (t.sizes() != at::IntArrayRef(shape))
+    refuse(PyExc_ValueError, "%s must have shape %s, not %s", name, text(shape).c_str(), text(t.sizes()).c_str());
+  if (n > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "%s must have unit column stride", name);
   return rows > 1 ? t.stride(0) : n;
 }
 

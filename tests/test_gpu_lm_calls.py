@@ -186,3 +186,25 @@ def test_host_threads_with_different_numbers_of_experts(pk, cuda_device, dtype, 
     for E, (z, out, _) in sets.items():
         r = pk.route(z, 4, score="sigmoid")
         assert torch.equal(out[0], r.gates) and torch.equal(out[1], r.experts) and torch.equal(out[2], r.counts)
+
+
+def test_messages_say_what_is_wanted(pk, cuda_device):
+    z, g = rows(cuda_device)  # 10 x 16
+    noise = torch.empty_like(z).exponential_(generator=g)
+    r = pk.route(z, 2)
+    wide = torch.ones((10, 4), device=cuda_device)
+    for call, error, words in (
+            (lambda: pk.sample_tokens(z, noise, top_p=torch.ones(3, device=cuda_device)), ValueError, r"top_p must have shape \(10,\), not \(3,\)"),
+            (lambda: pk.sample_tokens(z, noise, top_p=wide[:, 0]), ValueError, "top_p must be contiguous"),
+            (lambda: pk.sample_tokens(z, noise[:, :5]), ValueError, r"noise must have shape \(10, 16\), not \(10, 5\)"),
+            (lambda: pk.sample_tokens(z, noise.t().contiguous().t()), ValueError, "noise must have unit column stride"),
+            (lambda: pk.sample_tokens(z, noise, mask=torch.ones((10, 2), dtype=torch.int32, device=cuda_device)), ValueError,
+             r"mask must have shape \(10, 1\), not \(10, 2\)"),
+            (lambda: pk.route(z, 2, bias=torch.ones(15, device=cuda_device)), ValueError, r"bias must have shape \(16,\), not \(15,\)"),
+            (lambda: pk.route(z, 2, mask=torch.ones((10, 1), dtype=torch.bool, device=cuda_device)), ValueError,
+             r"mask must have shape \(10,\), not \(10, 1\)"),
+            (lambda: pk.route_backward(z, r, grad_gates=wide[:, :2]), ValueError, "grad_gates must be contiguous"),
+            (lambda: pk.route_backward(z, r, grad_gates=wide), ValueError, r"grad_gates must have shape \(10, 2\), not \(10, 4\)"),
+            (lambda: pk.route_backward(z[:5], r), ValueError, r"routing.experts must have shape \(5, 2\), not \(10, 2\)")):
+        with pytest.raises(error, match=words):
+            call()
