@@ -394,18 +394,24 @@ int profk_sample_tokens(const void* logits, int type, int64_t rows, int64_t n, i
 /* How profk_route scores and gates. */
 #define PROFK_SCORE_SOFTMAX 0
 #define PROFK_SCORE_SIGMOID 1
+#define PROFK_BIAS_ON_SCORES 0x100 /* added to `score`: what the bias is added to (without a bias: no matter) */
 typedef struct profk_routing {
-  int score;           /* PROFK_SCORE_SOFTMAX or PROFK_SCORE_SIGMOID */
+  int score;           /* PROFK_SCORE_SOFTMAX or PROFK_SCORE_SIGMOID, and perhaps PROFK_BIAS_ON_SCORES */
   int normalize;       /* nonzero: the gates of a token sum to 1 */
-  const float* bias;   /* device, `experts` floats added to the logits for the choice only, or NULL */
+  const float* bias;   /* device, `experts` floats for the choice only, or NULL: added to the logits, or, with
+                        * PROFK_BIAS_ON_SCORES, to the scores (sigmoid(z), or p of the softmax) */
   const uint8_t* mask; /* device, `tokens` bytes, 0 for a token that is not routed (padding), or NULL */
 } profk_routing;
 
 /* Top-k experts of each token.  A token's choice is the first k experts in
  * the library order of c = z + bias (float32), z its logits; c = -inf and NaN
  * are never chosen, and slots left over (or all slots of a masked token) hold
- * expert -1 and gate 0.  With y = z (softmax) or log sigmoid(z) (sigmoid) and
- * p = softmax(y) over the experts, a chosen expert's gate is
+ * expert -1 and gate 0.  With PROFK_BIAS_ON_SCORES c = sigmoid(z) + bias
+ * (sigmoid) or p + bias (softmax) instead, scores to a few units of float32's
+ * last place, and -inf where z is; the two orders differ: z = (2, 0) and bias =
+ * (0, 0.6) choose expert 0 by z + bias, expert 1 by sigmoid(z) + bias.  With
+ * y = z (softmax) or log sigmoid(z) (sigmoid) and p = softmax(y) over the
+ * experts, a chosen expert's gate is
  *   normalize:  exp(y) / sum of exp(y) over the token's chosen experts
  *   otherwise:  p (softmax) or sigmoid(z) (sigmoid).
  * counts[e] is the number of slots that hold e.  The balance loss is

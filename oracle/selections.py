@@ -1,7 +1,7 @@
 """The selections of a language model by their definitions, in float64 numpy.
 
-``token`` and ``routing`` restate the formulas one row or one batch at a time, by
-full sorts and plain sums; ``routing_gradient`` is the derivative written out
+``token``, ``routing`` and ``routed`` restate the formulas one row or one batch at a time,
+by full sorts and plain sums; ``routing_gradient`` is the derivative written out
 per token from the Jacobians.  Used by tests only.
 """
 from __future__ import annotations
@@ -106,28 +106,43 @@ def _softmax(y):
 def routing(z32, k, score, normalize, bias=None, mask=None):
     """gates, experts, counts, loss of float32 logits z32 (tokens, experts)."""
     z32 = np.asarray(z32, np.float32)
-    tokens, E = z32.shape
     with np.errstate(invalid="ignore"):
         c = z32 if bias is None else z32 + np.asarray(bias, np.float32)  # a float32 sum, by definition
-    z = z32.astype(np.float64)
-    gates = np.zeros((tokens, k))
-    experts = np.full((tokens, k), -1, np.int64)
+    experts = np.full((len(z32), k), -1, np.int64)
+    for t in range(len(z32)):
+        if mask is None or mask[t]:
+            chosen = order_of(c[t])[:k]
+            experts[t, :chosen.size] = chosen
+    gates, counts, loss = routed(z32, experts, score, normalize)
+    return gates, experts, counts, loss
+
+
+def scores_and_bias(z32, score, bias):
+    """What the choice is by where the bias is added to the scores, in float64 (-inf where the logit is)."""
+    z = np.asarray(z32, np.float32).astype(np.float64)
+    y = _log_scores(z, score)
+    s = np.exp(y) if score == "sigmoid" else np.stack([_softmax(row) if row.max() > -np.inf else 0 * np.exp(row) for row in y])
+    return np.where(z == -np.inf, -np.inf, s + np.asarray(bias, np.float64))
+
+
+def routed(z32, experts, score, normalize):
+    """gates, counts, loss of float32 logits z32 (tokens, experts) for a choice (-1: an empty slot, the last ones)."""
+    z = np.asarray(z32, np.float32).astype(np.float64)
+    E = z.shape[1]
+    gates = np.zeros(experts.shape)
     P = np.zeros(E)
-    for t in range(tokens):
-        if mask is not None and not mask[t]:
-            continue
-        chosen = order_of(c[t])[:k]
+    for t in range(len(z)):
+        chosen = experts[t][experts[t] >= 0]
         if not chosen.size:
             continue
         y = _log_scores(z[t], score)
         p = np.full(E, np.nan) if np.isnan(z[t]).any() else _softmax(y)
         g = _softmax(y[chosen]) if normalize else p[chosen] if score == "softmax" else np.exp(y[chosen])
         gates[t, :chosen.size] = np.nan if np.isnan(z[t]).any() else g
-        experts[t, :chosen.size] = chosen
         P += chosen.size * p
     counts = np.bincount(experts[experts >= 0], minlength=E)
     N = max(int(counts.sum()), 1)
-    return gates, experts, counts, float(E * ((counts / N) * (P / N)).sum())
+    return gates, counts, float(E * ((counts / N) * (P / N)).sum())
 
 
 def routing_gradient(z32, experts, counts, score, normalize, grad_gates=None, grad_loss=None):

@@ -53,7 +53,7 @@ class ProfkStats(C.Structure):
 
 
 F32, BF16, F16 = 0, 1, 2
-SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID, BIAS_ON_SCORES = 0, 1, 0x100
 
 
 class Sampling(C.Structure):

@@ -85,6 +85,7 @@ class Routing(NamedTuple):
 
 
 _SCORES = {"softmax": _abi.SCORE_SOFTMAX, "sigmoid": _abi.SCORE_SIGMOID}
+_BIAS_ON = {"logits": 0, "scores": _abi.BIAS_ON_SCORES}
 
 
 def _torch():
@@ -93,15 +94,17 @@ def _torch():
 
 
 def route(logits, k: int, *, score: str = "softmax", normalize: bool = True, bias=None, mask=None, balance: bool = True,
-          stream=None) -> Routing:
+          bias_on: str = "logits", stream=None) -> Routing:
     """Top-k experts of each token with their gates, the count of tokens per
     expert and, with ``balance``, the balance loss (1 for an even choice).
 
     logits: (tokens, experts), float32, bfloat16 or float16, unit column
     stride, at most 1024 experts.  k: at most 32.  score "softmax": gates from
     the softmax of the logits; "sigmoid": from their sigmoids.  normalize: a
-    token's gates sum to 1.  bias: (experts,) float32, added to the logits for
-    the choice only.  mask: (tokens,) bool, False where a token is not routed:
+    token's gates sum to 1.  bias: (experts,) float32, for the choice only.
+    bias_on "logits": the choice is by z + bias; "scores": by sigmoid(z) + bias or
+    softmax(z) + bias, another order (balancing rules that correct a bias step
+    by step are mostly stated so, for sigmoid scores above all).  mask: (tokens,) bool, False where a token is not routed:
     its slots hold expert -1 and gate 0.  A -inf logit is never chosen.  Equal
     values are chosen by lower index.
 
@@ -112,11 +115,14 @@ def route(logits, k: int, *, score: str = "softmax", normalize: bool = True, bia
     code = _SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    on = _BIAS_ON.get(bias_on)
+    if on is None:
+        raise ValueError(f"bias_on must be one of {sorted(_BIAS_ON)}")
     if getattr(logits, "requires_grad", False) and _torch().is_grad_enabled():
         if stream is not None:
             raise ValueError("a call that records a gradient runs on the current stream: use torch.cuda.stream")
-        return Routing(*_autograd().apply(logits, k, score, normalize, bias, mask, balance), score, normalize)
-    r = (_ext or _native()).route(logits, k, code, bool(normalize), bias, mask, bool(balance),
+        return Routing(*_autograd().apply(logits, k, score, normalize, bias, mask, balance, bias_on), score, normalize)
+    r = (_ext or _native()).route(logits, k, code + on, bool(normalize), bias, mask, bool(balance),
                                   None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _abi.check(r)
@@ -164,8 +170,9 @@ def _autograd():
 
         class Route(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, logits, k, score, normalize, bias, mask, balance):
-                r = route(logits.detach(), k, score=score, normalize=normalize, bias=bias, mask=mask, balance=balance)
+            def forward(ctx, logits, k, score, normalize, bias, mask, balance, bias_on):
+                r = route(logits.detach(), k, score=score, normalize=normalize, bias=bias, mask=mask, balance=balance,
+                          bias_on=bias_on)
                 ctx.save_for_backward(logits, r.experts, r.counts)
                 ctx.how = score, normalize
                 ctx.mark_non_differentiable(r.experts, r.counts)
@@ -175,7 +182,7 @@ def _autograd():
             @staticmethod
             def backward(ctx, grad_gates, _experts, _counts, grad_loss):
                 of = RouteGradient.apply if torch.is_grad_enabled() else gradient
-                return (of(*ctx.saved_tensors, grad_gates, grad_loss, *ctx.how),) + (None,) * 6
+                return (of(*ctx.saved_tensors, grad_gates, grad_loss, *ctx.how),) + (None,) * 7
 
         class RouteGradient(torch.autograd.Function):
             """The gradient under create_graph: what is made of it leads back here, to the logits and to the

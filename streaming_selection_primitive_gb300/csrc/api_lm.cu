@@ -1,5 +1,5 @@
 // C-ABI of the language-model selections: argument checks, then one launcher
-// (tokens.cu, route.cu).  Nothing here waits for the device.
+// (tokens.cu, route.cu, route_scores.cu).  Nothing here waits for the device.
 #include <cmath>
 
 #include "../../include/profk.h"
@@ -27,12 +27,15 @@ int guarded(F&& f) {
   }
 }
 
+bool sigmoid(const profk_routing* how) { return (how->score & ~PROFK_BIAS_ON_SCORES) == PROFK_SCORE_SIGMOID; }
+
 // The limits that routing and its gradient share.
 int check_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t ld, int64_t k,
                 const profk_routing* how) {
   if (!how || !type_ok(type) || tokens < 0 || experts < 1 || ld < experts || k < 1 || k > experts)
     return PROFK_ERR_INVALID;
-  if (how->score != PROFK_SCORE_SOFTMAX && how->score != PROFK_SCORE_SIGMOID) return PROFK_ERR_INVALID;
+  const int score = how->score & ~PROFK_BIAS_ON_SCORES;
+  if (score != PROFK_SCORE_SOFTMAX && score != PROFK_SCORE_SIGMOID) return PROFK_ERR_INVALID;
   if (tokens > 0 && !logits) return PROFK_ERR_INVALID;
   if (experts > ROUTE_MAX_EXPERTS || k > ROUTE_MAX_K || tokens >= (int64_t(1) << 32)) return PROFK_ERR_UNSUPPORTED;
   if (!aligned(logits, type_size(type))) return PROFK_ERR_UNSUPPORTED;
@@ -77,7 +80,7 @@ int profk_route(const void* logits, int type, int64_t tokens, int64_t experts, i
       !aligned(how->bias, 4))
     return PROFK_ERR_UNSUPPORTED;
   const RouteArgs a{logits, type, tokens, static_cast<int>(experts), ld, static_cast<int>(k),
-                    how->score == PROFK_SCORE_SIGMOID, how->normalize != 0, how->bias, how->mask, out_gates,
+                    sigmoid(how), how->normalize != 0, (how->score & PROFK_BIAS_ON_SCORES) != 0, how->bias, how->mask, out_gates,
                     out_experts, out_counts, out_loss};
   return guarded([&] { return launch_route(a, stream); });
 }
@@ -95,7 +98,7 @@ int profk_route_backward(const void* logits, int type, int64_t tokens, int64_t e
       !aligned(grad_logits, type_size(type)))
     return PROFK_ERR_UNSUPPORTED;
   const RouteBackwardArgs a{logits, type, tokens, static_cast<int>(experts), ld, static_cast<int>(k),
-                            how->score == PROFK_SCORE_SIGMOID, how->normalize != 0, chosen, counts, grad_gates,
+                            sigmoid(how), how->normalize != 0, chosen, counts, grad_gates,
                             grad_loss, grad_logits, grad_ld};
   return guarded([&] { return launch_route_backward(a, stream); });
 }

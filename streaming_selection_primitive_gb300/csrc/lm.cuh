@@ -1,4 +1,4 @@
-// Shared device pieces of the language-model selections (tokens.cu, route.cu).
+// Shared device pieces of the language-model selections (tokens.cu, route.cuh).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -32,7 +32,7 @@ struct TokenArgs {
 };
 cudaError_t launch_sample_tokens(const TokenArgs& a, cudaStream_t stream);
 
-// Choice of k experts per token (route.cu).
+// Choice of k experts per token (route.cuh).
 constexpr int ROUTE_MAX_EXPERTS = 1024;
 constexpr int ROUTE_MAX_K = 32;
 struct RouteArgs {
@@ -42,7 +42,7 @@ struct RouteArgs {
   int experts;
   int64_t ld;
   int k;
-  bool sigmoid, normalize;
+  bool sigmoid, normalize, on_scores;  // on_scores: the bias is added to the scores, not to the logits
   const float* bias;    // experts, or null
   const uint8_t* mask;  // tokens, or null
   float* gates;         // tokens x k
@@ -51,6 +51,7 @@ struct RouteArgs {
   float* loss;          // one float, or null
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route_scores(const RouteArgs& a, cudaStream_t stream);  // on_scores, with a bias
 
 struct RouteBackwardArgs {
   const void* logits;

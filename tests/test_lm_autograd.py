@@ -66,3 +66,26 @@ def test_first_derivative_of_gates_and_loss(lm):
     np.testing.assert_allclose(z.grad.numpy(), want, rtol=0, atol=1e-6)
     with torch.no_grad():
         assert not lm.route(z, 2).gates.requires_grad
+
+
+def test_what_a_bias_is_added_to(pk, lm, monkeypatch):
+    # The code that reaches the native half, and the C-ABI's refusal of other ones.
+    import ctypes as C
+
+    from streaming_selection_primitive_gb300 import _abi
+    seen = []
+    real = StandIn.route
+    monkeypatch.setattr(StandIn, "route", lambda self, logits, k, score, *rest: (seen.append(score), real(self, logits, k, score & 1, *rest))[1])
+    for score in ("softmax", "sigmoid"):
+        for on in ("logits", "scores"):
+            lm.route(leaf().detach(), 2, score=score, bias_on=on)
+            lm.route(leaf(), 2, score=score, bias_on=on)
+    assert seen == [0, 0, 0x100, 0x100, 1, 1, 0x101, 0x101]
+    with pytest.raises(ValueError):
+        lm.route(leaf(), 2, bias_on="gates")
+    p = C.c_void_p(256)
+    for code in (2, 0x102, 0x200, 0x201, -1):
+        how = _abi.Routing(code, 1)
+        assert pk.lib().profk_route(p, _abi.F32, 4, 16, 16, 2, how, p, p, p, None, None) == _abi.PROFK_ERR_INVALID
+        assert pk.lib().profk_route_backward(p, _abi.F32, 0, 16, 16, 2, how, p, p, p, None, p, 16, None) == _abi.PROFK_ERR_INVALID
+    assert pk.lib().profk_route_backward(p, _abi.F32, 0, 16, 16, 2, _abi.Routing(0x101, 1), p, p, p, None, p, 16, None) == 0
