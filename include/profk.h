@@ -380,7 +380,8 @@ typedef struct profk_sampling {
  *   out_tokens   device, rows int64
  *   out_logprobs device, rows float: x_token - log(sum w over the kept); 0
  *                when T = 0
- * A logit of -inf is never kept.  A row in which nothing can be kept gives
+ * A logit of -inf is never kept, nor is one whose x_i is -inf (beside +inf, or
+ * where its distance over T passes float32).  A row in which nothing can be kept gives
  * the token -1 and -inf; an allowed NaN, a negative or NaN temperature, or a
  * NaN top_p or min_p gives -1 and NaN (the call does not wait for the device,
  * so it cannot return PROFK_ERR_NAN).  Sums of w are exact 64-bit integer

@@ -1403,7 +1403,9 @@ __device__ __forceinline__ void free_row(S& sl, Shared& s, cg::cluster_group& cl
   auto move = [&](float to) {
     mass.scale(lm_exp2(fminf((ref - to) * sl.inv2, 0.f)));
     ref = to;
-    best.score = best.index == NONE ? -INFINITY : fmaxf(x2(best.logit) - best_lq, -INFINITY);
+    const float y = x2(best.logit);
+    if (y == -INFINITY) best.index = NONE;  // it weighs nothing beside `to`
+    best.score = best.index == NONE ? -INFINITY : fmaxf(y - best_lq, -INFINITY);
   };
   auto one = [&](int i) {  // an element by itself: a row's ends, and what the vectors leave
     if (!sl.is_allowed(i)) return;
@@ -1411,8 +1413,10 @@ __device__ __forceinline__ void free_row(S& sl, Shared& s, cg::cluster_group& cl
     top = max_nan(top, l);
     if (!(l > -INFINITY)) return;
     if (l > ref) move(l);
-    mass.add(lm_exp2(x2(l)));
-    const float lq = lm_log2(noise[i]), score = fmaxf(x2(l) - lq, -INFINITY);  // NaN noise is never ahead
+    const float y = x2(l);
+    if (y == -INFINITY) return;  // it weighs nothing
+    mass.add(lm_exp2(y));
+    const float lq = lm_log2(noise[i]), score = fmaxf(y - lq, -INFINITY);  // NaN noise is never ahead
     if (score > best.score || best.index == NONE || (score == best.score && static_cast<unsigned>(i) < best.index)) {
       best = Best{score, l, static_cast<unsigned>(i)};
       best_lq = isnan(lq) ? INFINITY : lq;

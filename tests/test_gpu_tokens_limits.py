@@ -106,3 +106,19 @@ def test_the_same_call_gives_the_same_bits_past_the_lists(pk, cuda_device, rows,
         for _ in range(60):
             got = pk.sample_tokens(logits, noise, top_k=k, **how)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1].view(torch.int32), want[1].view(torch.int32))
+
+
+@pytest.mark.parametrize("n", [2, 9, 700, 40000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_token_without_weight_is_never_given(pk, cuda_device, n, dtype):
+    # Beside +inf (or at a temperature near 0) every other logit weighs nothing, also where the noise of the tokens
+    # with weight is never ahead.
+    inf, nan = float("inf"), float("nan")
+    logits, noise = inputs(6, n, dtype, 111, cuda_device)
+    at = n // 2
+    for r, (q, l) in enumerate([(nan, inf), (inf, inf), (-1.0, inf), (nan, 30.0), (inf, 30.0), (1.0, inf)]):
+        logits[r, at], noise[r, at] = l, q
+    T = torch.tensor([1.0, 1.0, 1.0, 1e-39, 1e-39, 1.0], device=cuda_device)
+    for how in ({}, {"top_k": 5}, {"top_p": 0.9}, {"min_p": 0.01}):
+        got, lp = pk.sample_tokens(logits, noise, temperature=T, **how)
+        assert (got == at).all() and (lp == 0).all(), how
