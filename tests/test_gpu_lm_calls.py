@@ -208,3 +208,30 @@ def test_messages_say_what_is_wanted(pk, cuda_device):
             (lambda: pk.route_backward(z[:5], r), ValueError, r"routing.experts must have shape \(5, 2\), not \(10, 2\)")):
         with pytest.raises(error, match=words):
             call()
+
+
+def test_host_threads_through_python(pk, cuda_device):
+    # Four threads, each with inputs and a stream of its own, sample, route and go backward.
+    def work(i, out):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            z, g = rows(cuda_device, 200 + 50 * i, 40 + 30 * i, seed=i)
+            noise = torch.empty_like(z).exponential_(generator=g)
+            leaf = z.clone().requires_grad_()
+            for _ in range(50):
+                token, lp = pk.sample_tokens(z, noise, top_k=7, top_p=0.9)
+                r = pk.route(leaf, 3)
+                leaf.grad = None
+                (r.gates.square().sum() + r.loss).backward()
+            stream.synchronize()
+            out[i] = [t.cpu() for t in (token, lp, r.gates.detach(), r.experts, r.counts, r.loss.detach(), leaf.grad)]
+
+    alone, together = {}, {}
+    for i in range(4):
+        work(i, alone)
+    threads = [threading.Thread(target=work, args=(i, together)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(a, b) for i in range(4) for a, b in zip(alone[i], together[i]))

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_tokens import check, inputs
+from oracle import selections as ref
+from test_gpu_tokens import MASS_BLUR, SCORE_BLUR, TYPES, check, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +123,70 @@ def test_a_token_without_weight_is_never_given(pk, cuda_device, n, dtype):
     for how in ({}, {"top_k": 5}, {"top_p": 0.9}, {"min_p": 0.01}):
         got, lp = pk.sample_tokens(logits, noise, temperature=T, **how)
         assert (got == at).all() and (lp == 0).all(), how
+
+
+def cluster_of(rows, n, size, processors):
+    """CTAs of a row: up to 8 while they have room at once (two a processor) and each has 16 KB."""
+    vec, c = 16 // size, 1
+    nbytes = (n + 2 * vec - 2) // vec * 16
+    while c < 8 and rows * c * 2 <= 2 * processors and nbytes // (2 * c) >= 16384:
+        c *= 2
+    return c
+
+
+def check_some(pk, logits, noise, at, T=1.0, k=0, p=1.0, min_p=0.0):
+    """The call over all rows, and the rows `at` against the definition: tokens, and what the others may be."""
+    got, lp = pk.sample_tokens(logits, noise, temperature=T, top_k=k, top_p=p, min_p=min_p)
+    l, q = logits[at].double().cpu().numpy(), noise[at].double().cpu().numpy()
+    numbers = [np.float32(x).item() for x in (p, min_p)]
+    may = []
+    for i, r in enumerate(at):
+        want = ref.tokens_within(l[i], q[i], np.ones(l.shape[1], bool), np.float32(T).item(), k, *numbers, SCORE_BLUR, MASS_BLUR)
+        assert got[r].item() in want, (r, got[r].item(), want)
+        lo, hi = want[got[r].item()]
+        room = 1e-5 + 4e-7 * abs(lo)
+        assert lo - room <= lp[r].item() <= hi + room, (r, lp[r].item(), lo, hi)
+        may.append(want)
+    return got[at], lp[at], may
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("c", [1, 2, 4, 8])
+def test_lists_that_clusters_join(pk, cuda_device, c, dtype):
+    # Around the 128 keys that a CTA of a cluster may send (256 of a CTA alone): ties across the cut and across the
+    # slices' borders, and slices that all hold the same values, so that each sends all that it may.
+    processors = torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    size, n = dtype.itemsize, 135000 // dtype.itemsize
+    vec = 16 // size
+    rows = {1: 2 * processors, 2: processors, 4: processors // 2, 8: processors // 4}[c]
+    assert cluster_of(rows, n, size, processors) == c
+    logits, noise = inputs(rows, n, dtype, 121 + c, cuda_device)
+    per = -(-((n + 2 * vec - 2) // vec) // c) * vec  # elements of a slice (rows on the 16-byte boundary)
+    logits[::2] = (logits[::2].float() * 8).round().to(dtype) / 8
+    logits[1::4] = logits[1::4, :per].repeat(1, c)[:, :n]
+    logits[3::8] = torch.sort(logits[3::8], dim=1, descending=True).values
+    at = list(range(0, rows, max(1, rows // 12)))[:12] + [1, 3, 5]
+    for k in (2, 17, 127, 128, 129, 130, 255, 256, 257):
+        check_some(pk, logits, noise, at, k=k)
+    for how in ({"k": 128, "p": 0.95}, {"k": 127, "p": 0.9, "min_p": 0.2}, {"p": 0.02}, {"p": 0.3, "T": 0.4}, {"min_p": 0.2}, {"T": 0.0}):
+        check_some(pk, logits, noise, at, **how)
+
+
+@pytest.mark.parametrize("n", [33333, 90001])
+def test_rows_shared_out_otherwise_agree_but_for_near_ties(pk, cuda_device, n):
+    # The same rows by one, two, four and eight CTAs each: a token that differs is one of several within the
+    # scores' or the masses' roundings.
+    rows = 320
+    logits, noise = inputs(rows, n, torch.float32, 131, cuda_device, spread=0.4)
+    at = list(range(0, 12))
+    for how in ({"p": 0.9}, {"p": 0.97, "min_p": 0.05}, {"k": 20000, "p": 0.8}, {"k": 100}, {"min_p": 0.1}, {}):
+        first = None
+        for some in (320, 100, 50, 20):
+            got, lp, may = check_some(pk, logits[:some], noise[:some], at, **how)
+            if first is None:
+                first = got, lp
+            for i in range(len(at)):
+                if got[i] != first[0][i]:
+                    assert len(may[i]) > 1 and first[0][i].item() in may[i]
+                else:
+                    assert abs(lp[i] - first[1][i]).item() < 2e-5
