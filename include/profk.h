@@ -426,8 +426,9 @@ typedef struct profk_routing {
  *   out_experts device, tokens*k int64
  *   out_counts  device, `experts` int64
  *   out_loss    device, one float, or NULL
- * A NaN among the logits of a token that is not masked makes its gates and
- * the loss NaN; its experts are still valid.  The call only enqueues work on
+ * A NaN among the logits of a token that fills a slot makes its gates and the
+ * loss NaN; its experts are still valid.  (A token of NaN and -inf alone fills
+ * none, like a masked one.)  The call only enqueues work on
  * `stream`, with a workspace from the library's pool; the same call gives the
  * same bits.  tokens = 0 is allowed. */
 int profk_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t ld, int64_t k,

@@ -1,7 +1,7 @@
 // Native half of the Python calls in _lm.py: checks the tensors, makes the
 // outputs and calls the C-ABI (libprofk.so) on the current stream.  A call of
 // a few microseconds spends most of them here if this is done in Python: one
-// decoding step's route took 23 us through ctypes, 9 us with this file.
+// decoding step's route takes 19.5 us through ctypes, 6.5 us with this file.
 //
 // Functions take positional arguments only (the keyword forms are in _lm.py)
 // and return the outputs, or the library's status where it is not PROFK_OK.

@@ -44,7 +44,8 @@ __device__ __forceinline__ float lm_sqrt(float x) {
 }
 
 // 1 / x by the hardware's approximation (one ulp; x or results below the
-// normal range count as zero).  An exact division is 120 instructions.
+// normal range count as zero).  What it divides carries two ulps of an
+// exponential already.
 __device__ __forceinline__ float lm_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

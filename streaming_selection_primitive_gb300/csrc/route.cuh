@@ -16,12 +16,17 @@
 // two), in registers, read once.  The choice runs on 32-bit keys that end in
 // the expert's index (sort_key), so that a round is one warp-wide maximum.
 //
-// What bounds it: a token's instructions, 549 forward and 438 backward for 256
-// experts of float32, 344 and 270 for 128 of bfloat16, of which the SMs issue
-// two to three a cycle.  131072 x 256 float32, k = 8: 78 us forward (147 MB, 1.9
-// TB/s) and 69 backward (281 MB, 4.1 TB/s); 32768 x 128 bfloat16: 19 and 12 us.  Up to a few thousand tokens the
-// launches and the join of the CTAs' sums count: 4096 of 64 take 7.4 and 3.4 us,
-// 16 of 128 take 4.1 and 3.0.
+// What bounds it (several sets of inputs in turn, beyond L2):
+//   256 experts of float32: a token's instructions, 551 forward and 438 backward, of
+//     which the SMs issue 3.2 and 2.8 a cycle of 4.  131072 tokens, k = 8: 79 us
+//     forward (147 MB, 1.9 TB/s) and 69 backward (281 MB, 4.1 TB/s);
+//   128 of bfloat16: 344 and 271 instructions, 2.5 and 2.0 a cycle (2.8 and 2.6 with
+//     the inputs in L2): a token begins with its load, which the other warps do not
+//     hide in full, and the backward pass with its choice and gates too.  32768
+//     tokens: 20 and 16 us, 12 for a backward pass that finds the logits in L2;
+//   few tokens: the launches, one token's chain of rounds and exchanges, and the
+//     join of the CTAs' sums.  4096 of 64 take 7.7 and 3.5 us, 16 of 128 take 4.4
+//     with the loss, 3.4 without, and 3.2 backward.
 #pragma once
 
 #include <type_traits>
@@ -41,8 +46,8 @@ constexpr int CLUSTER = 8;  // CTAs of the one-launch form and of the join
 
 // Warps of a CTA, and resident CTAs per SM of the forms for many tokens (which
 // size their grids): what the registers of R values a lane allow.  (131072 x 256
-// float32, forward and backward: 78 and 69 us; with one CTA an SM 86 and 98, with
-// eight warps a CTA 90 and 98.)
+// float32, forward and backward: 79 and 69 us; with one CTA an SM 86 and 97, with
+// eight warps a CTA 90 and 97.)
 template <int R>
 constexpr int WARPS = R <= 16 ? 16 : 8;
 template <int R>
@@ -133,10 +138,11 @@ __device__ __forceinline__ void store_part(T* row, int E, bool vec, const float 
 // copies: each lane copies what it reads itself, so that the next tokens'
 // rows are on their way while one is worked on, without holding registers.
 // Taken for rows of 1 to 2 KB whose groups of VEC values are whole and aligned
-// (32768 x 512 bfloat16: 44.8 us forward and 28.3 backward, against 46.0 and 31.7
-// with plain loads).  Shorter ones are loaded when their turn comes, which the
-// other warps hide (32768 x 128 bfloat16: 19.2 and 12.3 us, against 21.0 and 13.6
-// through a ring); longer ones would need more shared memory than there is.
+// (32768 x 512 bfloat16: 45.5 us forward and 32.8 backward, against 49.5 and 41.3
+// with plain loads; 131072 x 256 float32 79.0 and 69.1, against 77.0 and 69.5).
+// Shorter ones are loaded when their turn comes (32768 x 128 bfloat16: 20.0 and 16.4
+// us, against 21.3 and 15.5 through a ring); longer ones would need more shared
+// memory than there is.
 template <typename T, int R>
 struct Ring {
   using P = Part<T, R>;
@@ -827,8 +833,8 @@ cudaError_t launch_with(void (*kernel)(KArgs...), int grid, int threads, size_t 
 }
 
 // One launch up to this many tokens (two a warp of the cluster).  (x 128 bfloat16,
-// k = 8: 16 tokens take 4.1 us, and 5.3 by the grid and the join; 512 take 5.8 by
-// the grid and 8.4 in one launch.)
+// k = 8: 16 tokens take 4.4 us, and 5.5 by the grid and the join; 512 take 6.0 by
+// the grid and 8.3 in one launch.)
 template <int R>
 constexpr int64_t ONE_TOKENS = 2 * CLUSTER * WARPS<R>;
 

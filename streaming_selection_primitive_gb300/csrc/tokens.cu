@@ -30,18 +30,20 @@
 // A row without filters is one pass over its logits and noise together
 // (free_row).
 //
-// What bounds it, with the times of a call on the device (bfloat16, noise and
-// logits in or out of L2 as they come; L: logits that fall by 1 to 2 per unit
-// of the logarithm of their rank):
-//   many rows without filters: the instructions of a token's exponential and
-//     logarithm.  512 x 65536 float32: 268 MB in 51 us, 5.2 TB/s, 0.77 of a copy's rate;
+// What bounds it, with the times of a call on the device (bfloat16, several sets
+// of inputs in turn, beyond L2 where they are that large; logits that fall by 1 to
+// 2 per unit of the logarithm of their rank):
+//   many rows without filters: loads and the instructions of a token's exponential
+//     and logarithm, which take turns.  512 x 65536 float32: 268 MB in 51.6 us, 5.2
+//     TB/s, 0.78 of a copy's rate; 64 x 131072: 50 MB in 15.6 us;
 //   many rows under top-k or greedily: the read, and step 2.  256 x 131072, 67 MB:
 //     16 us greedily, 22 us with k = 50;
-//   top-p: the weights of the first pass, and then the rows of step 4, thirty
-//     steps between barriers of 1000 to 4000 cycles each, beside the slices' scan.
-//     64 x 131072, p = 0.9, L: 46 us, and 24 us at T = 0.7, where fewer rows get there;
-//   one row: the same chain of steps, whatever its length.  1 x 32768: 5.5 us
-//     without filters, 7 greedily, 8.6 with k = 50, 14 with p = 0.9.
+//   top-p: the weights of the first pass, and then the slowest row of step 4,
+//     some thirty steps between barriers beside the slices' scans.  64 x 131072,
+//     p = 0.9: 47 us, and 27 us at T = 0.7, where fewer rows get there;
+//   top-k above what step 2 sorts: step 4 for every row.  64 x 131072, k = 1000: 68 us;
+//   one row: the same chain of steps, whatever its length.  1 x 32768: 5.8 us
+//     without filters, 6.7 greedily, 8.7 with k = 50, 15 with p = 0.9.
 //
 // Masses are summed as 64-bit integers (w scaled by a power of two up to
 // 2^44, the largest that n of them cannot overflow), so that every sum is
@@ -66,25 +68,25 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
 // Keys that step 2 can sort in a CTA that has the row to itself (half its
-// threads; 256 x 131072, p = 0.9, T = 0.7: 78 us, and 99 us with 128), in a
+// threads; 256 x 131072, p = 0.9, T = 0.7, 24 inputs: 61 us in the median and 82 at
+// most, with 128 as much in the median and 145 at most), in a
 // cluster's (its lists of 128 just fit the first CTA's), and those that min-p
-// seldom leaves more of (64 x 131072, min-p = 0.01: 21.1 us, and 24.6 with 128;
-// 0.05 in 256 rows: 35 us, and 29 with 128).
+// seldom leaves more of (64 x 131072, min-p = 0.01: 23.3 us, and 26.9 with 128;
+// 0.05 in 256 rows: 35.4 us, and 29.9 with 128).
 constexpr int TOP = 256;
 constexpr int TOP_SHARED = 128;
 constexpr int TOP_MIN_P = 64;
 constexpr int CANDIDATES = 1024;
 constexpr int LISTED = 4096;    // tokens of a slice among which step 4 finds the cut,
 constexpr int LISTED_ALONE = 8192;  // and of a long row in one CTA, in dynamic shared memory (256 x 131072,
-                                    // p = 0.9: 132 us, and 212 with 4096)
-constexpr int BINS = 256;       // of one histogram pass (64 x 131072, k = 1000: 68 us, and 75 with 128;
-                                // the joining of 1024 took 6 us in a cluster of 8)
+                                    // p = 0.9: 119 us, and 196 with 4096)
+constexpr int BINS = 256;       // of one histogram pass (64 x 131072, k = 1000: 68 us, and 73 with 128)
 constexpr int SAMPLE_BINS = 128;       // of the sample of a slice,
 constexpr float SAMPLE_SCALE = 8.f;    // so many a unit of x
 constexpr int LIST = 128;       // keys of a bin that are ranked directly
 // Bytes of a row that are worth a CTA of a cluster.  (1 x 32768 bfloat16, k = 50 and
-// p = 0.9: 8.8 and 14.4 us with four CTAs, 10.1 and 19.4 with eight; 1 x 4096, k = 50:
-// 6.7 us with one, 8.6 with two.)
+// p = 0.9: 8.7 and 15.0 us with these four CTAs, 8.0 and 19.3 with one, 8.8 and 16.5
+// with two, 10.3 and 16.8 with eight; 1 x 4096, k = 50: 7.2 us with one, 8.9 with two.)
 constexpr int SLICE_LEAST = 16 << 10;
 using u64 = unsigned long long;
 
@@ -1215,7 +1217,7 @@ __device__ __noinline__ void late_row(Shared& s) {
   Scan scan{Best{-INFINITY, 0.f, NONE}, 0, 0};
   if (dense) {
     // The noise is on its way to L2 before the loads ask for it.  (512 x 65536 float32,
-    // p = 0.9: 123 us, and 127 without.)
+    // p = 0.9: 125 us, and 128 without.)
     const float* noise = late.noise;
 #pragma unroll 1
     for (int i = max(sl.first, 0) + 32 * static_cast<int>(threadIdx.x); i < min(sl.first + sl.nv * S::VEC, sl.n); i += 32 * THREADS)
@@ -1648,7 +1650,7 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
     mass = warp_sum(mass > 0.f ? mass * sl.weight(ref) : 0.f);
     if (lane == 0) s.mass[warp] = mass;
     // The sample: one vector in 2^sample_shift.  (What lies beyond the bins weighs
-    // nothing.  64 x 131072, p = 0.9: 48 us; 53 with half as many elements, 48 with twice.)
+    // nothing.  64 x 131072, p = 0.9: 47 us; 52 with half as many elements, 48 with twice.)
 #pragma unroll 1
     for (int q = threadIdx.x; q < sl.nv >> sl.sample_shift; q += THREADS) {
       float x[VEC];
@@ -1681,9 +1683,9 @@ __device__ __forceinline__ void sample_row(const TokenArgs& a, int64_t r, int pe
         // How many keys should reach the mass: three standard deviations of a
         // count of one in 2^sample_shift more, and a few.  Worth a try where one
         // of them more does not pass the limit.  (With the limit at the count
-        // itself rows are tried that then need step 4: 64 x 131072, p = 0.9, took 55 us
-        // against 52; at three of them too few are tried: 256 rows took 94 us
-        // against 85.)
+        // itself rows are tried that then need step 4: 256 x 131072, p = 0.9, T = 0.7, took
+        // 74 us in the median of 24 inputs, against 61; at three of them 59, but too few
+        // are tried at T = 1: 64 rows took 54 us, against 53.)
         const float tokens = s.likely[2], deviation = lm_sqrt(static_cast<float>(1 << sl.sample_shift) * (tokens + 16.f));
         const float limit = alone ? TOP : TOP_SHARED;
         // (With min-p the tokens may end long before the mass.)
@@ -1856,10 +1858,9 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample_tokens(TokenArgs a, int p
 
 // CTAs of a row's cluster: as many as the SMs have room for at once (two an SM),
 // while each still has a slice of some size.  (64 x 131072 bfloat16 without filters
-// and with p = 0.9: 14 and 52 us with four CTAs, 18 and 63 with two, 29 and 158 with one,
-// 19 and 63 with eight, whose CTAs do not all fit.  304 x 65536, p = 0.9, T = 0.7: 37
-// us with one, 57 with two.  The rows that a CTA alone could not finish were once left to
-// a second launch with clusters: 304 x 65536, p = 0.9, took 134 us where this takes 77.)
+// and with p = 0.9: 15.6 and 47 us with four CTAs, 18 and 60 with two, 27 and 92 with
+// one, 21 and 62 with eight, whose CTAs do not all fit.  304 x 65536, p = 0.9: 72 us
+// with one and 79 with two, at T = 0.7 40 and 49.)
 int cluster_of(int64_t rows, int64_t bytes) {
   int c = 1;
   while (c < MAX_CLUSTER && rows * c * 2 <= 2 * sms() && bytes / (2 * c) >= SLICE_LEAST) c *= 2;
