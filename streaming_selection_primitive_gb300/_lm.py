@@ -39,14 +39,6 @@ def _native():
     return _ext
 
 
-def _used_here(outputs):
-    """Outputs made on another stream: their memory is not given back before the current stream is done with them."""
-    current = _torch().cuda.current_stream(outputs[0].device)
-    for t in outputs:
-        if t is not None:
-            t.record_stream(current)
-
-
 def sample_tokens(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, mask=None, out=None, stream=None):
     """One token per row of logits: (tokens int64, logprobs float32).
 
@@ -67,8 +59,6 @@ def sample_tokens(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0
                                           None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _abi.check(r)
-    if stream is not None and out is None:
-        _used_here(r)
     return r
 
 
@@ -126,8 +116,6 @@ def route(logits, k: int, *, score: str = "softmax", normalize: bool = True, bia
                                   None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _abi.check(r)
-    if stream is not None:
-        _used_here(r)
     return Routing(*r, score, normalize)
 
 
@@ -146,8 +134,6 @@ def route_backward(logits, routing: Routing, *, grad_gates=None, grad_loss=None,
                                            grad_gates, grad_loss, out, None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _abi.check(r)
-    if stream is not None and out is None:
-        _used_here((r,))
     return r
 
 

@@ -103,26 +103,35 @@ int64_t whole(PyObject* o) {
   return v;
 }
 
-Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
-  return at::detail::empty_cuda(shape, like.options().dtype(type));
-}
-
-// The tensors' device, and the call's stream where one is given, made current for the
-// call: its outputs come from that stream's blocks.  (A block of the current
-// stream's may still be in use by work queued there.)
+// The tensors' device, and the call's stream: the one given, made current for the
+// call, else the device's current one.  Outputs come from the stream's own blocks
+// (one of the current stream's may still be in use by work queued there), and
+// where a stream is given they are marked as used on the current one as well, so
+// that what the caller queues on them there outlives them.
 class Place {
  public:
-  Place(PyObject* o, const Tensor& like) : device_(like.device()) {
+  Place(PyObject* o, const Tensor& like)
+      : like_(like), device_(like.device()), stream_(c10::cuda::getCurrentCUDAStream(like.device().index())) {
     if (o == Py_None) return;
     void* given = PyLong_AsVoidPtr(o);
     if (!given && PyErr_Occurred()) throw python_error();
-    side_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(given), like.device().index()));
+    callers_ = stream_;
+    stream_ = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(given), like.device().index());
+    side_.emplace(stream_);
   }
-  cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream().stream(); }
+  cudaStream_t stream() const { return stream_.stream(); }
+  Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    Tensor t = at::detail::empty_cuda(shape, like_.options().dtype(type));
+    if (callers_) t.record_stream(*callers_);
+    return t;
+  }
 
  private:
+  const Tensor& like_;
   c10::cuda::CUDAGuard device_;
-  c10::cuda::OptionalCUDAStreamGuard side_;
+  c10::cuda::CUDAStream stream_;
+  std::optional<c10::cuda::CUDAStream> callers_;
+  std::optional<c10::cuda::CUDAStreamGuard> side_;
 };
 
 PyObject* tuple_of(std::initializer_list<Tensor> tensors) {
@@ -175,8 +184,8 @@ PyObject* sample_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const Place place(arg[8], like);
   Tensor tokens, logprobs;
   if (arg[7] == Py_None) {
-    tokens = empty(rows, at::kLong, like);
-    logprobs = empty(rows, at::kFloat, like);
+    tokens = place.empty(rows, at::kLong);
+    logprobs = place.empty(rows, at::kFloat);
   } else {
     if (!PyTuple_Check(arg[7]) || PyTuple_GET_SIZE(arg[7]) != 2)
       refuse(PyExc_TypeError, "out must be a tuple of two tensors");
@@ -204,10 +213,10 @@ PyObject* route(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   if (arg[5] != Py_None) how.mask = static_cast<uint8_t*>(array(arg[5], "mask", at::kBool, like, {x.rows}));
   if (k < 1 || k > x.n) refuse(PyExc_ValueError, "k must be in 1 .. experts");
   const Place place(arg[7], like);
-  const Tensor gates = empty({x.rows, k}, at::kFloat, like), experts = empty({x.rows, k}, at::kLong, like),
-               counts = empty({x.n}, at::kLong, like);
+  const Tensor gates = place.empty({x.rows, k}, at::kFloat), experts = place.empty({x.rows, k}, at::kLong),
+               counts = place.empty({x.n}, at::kLong);
   Tensor loss;
-  if (arg[6] == Py_True) loss = empty({}, at::kFloat, like);
+  if (arg[6] == Py_True) loss = place.empty({}, at::kFloat);
   const int code = profk_route(like.data_ptr(), x.type, x.rows, x.n, x.ld, k, &how, static_cast<float*>(gates.data_ptr()),
                                static_cast<int64_t*>(experts.data_ptr()), static_cast<int64_t*>(counts.data_ptr()),
                                loss.defined() ? static_cast<float*>(loss.data_ptr()) : nullptr, place.stream());
@@ -242,7 +251,7 @@ PyObject* route_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   Tensor out;
   int64_t out_ld = x.n;
   if (arg[7] == Py_None) {
-    out = empty({x.rows, x.n}, like.scalar_type(), like);
+    out = place.empty({x.rows, x.n}, like.scalar_type());
   } else {
     out = on_device(arg[7], "out", like.scalar_type(), like);
     out_ld = rows_of(out, "out", x.rows, x.n);
