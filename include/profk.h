@@ -451,6 +451,120 @@ int profk_route_backward(const void* logits, int type, int64_t tokens, int64_t e
                          const float* grad_gates, const float* grad_loss, void* grad_logits, int64_t grad_ld,
                          cudaStream_t stream);
 
+/* ---- log-probabilities of given tokens, and the losses that train on them ---- */
+
+/* What these calls share.  `logits` is a device array, row r at r*ld elements,
+ * n values of `type` (1 <= n < 2^30, rows < 2^28, else PROFK_ERR_UNSUPPORTED).
+ * With m the row's largest logit, T the temperature, x_i = (l_i - m) / T and
+ * s = sum exp(x_i), a token's log-probability is x_token - log s, and the row's
+ * entropy is log s - sum x_i exp(x_i) / s: of the softmax over the whole row at
+ * that temperature (a token that profk_sample_tokens drew without a filter has
+ * the same).
+ *   tokens       device, rows int64.  A negative token leaves its row out: its
+ *                logits are not read (they may hold anything), its outputs are 0,
+ *                and so is its gradient.  A token from n on gives NaN
+ *   temperature  device, rows float, or NULL: all_temperature for every row.
+ *                It has to be above 0 and finite, and log2(e) / T finite
+ *                (all_temperature: else PROFK_ERR_INVALID; a row's: NaN)
+ *   out_logprobs, out_entropies (or NULL)  device, rows float
+ *   out_stats    device, rows pairs of floats (or NULL): m and s, for the backward
+ *                pass; 8-byte aligned
+ * A logit of -inf has probability 0.  A row of nothing but -inf gives -inf, the
+ * entropy 0 and the gradient 0; one with a NaN or +inf gives NaN.  Sums are
+ * float32 with their losses carried along, or double, in a fixed order: the same
+ * call gives the same bits.  The calls only enqueue work on `stream`, may be
+ * captured in a graph, and allow rows = 0. */
+int profk_token_logprobs(const void* logits, int type, int64_t rows, int64_t n, int64_t ld, const int64_t* tokens,
+                         const float* temperature, float all_temperature, float* out_logprobs, float* out_entropies,
+                         float* out_stats, cudaStream_t stream);
+
+/* Gradient with respect to the logits: with p_i = exp(x_i) / s
+ *   grad_i = scale * [g (1[i = token] - p_i) - h p_i (x_i - log s + H)] / T,
+ * g and h the row's entries of grad_logprobs and grad_entropies.  A row whose
+ * entries are both 0 gets the gradient 0 without being read.
+ *   stats, entropies  as the forward call gave them (entropies: NULL when
+ *                     grad_entropies is)
+ *   grad_logprobs, grad_entropies  device, rows float, or NULL
+ *   scale        device, one float, or NULL: 1
+ *   grad_logits  device, row r at r*grad_ld elements, n values of `type`; it may
+ *                be the logits themselves (grad_ld = ld) */
+int profk_token_logprobs_backward(const void* logits, int type, int64_t rows, int64_t n, int64_t ld,
+                                  const int64_t* tokens, const float* temperature, float all_temperature,
+                                  const float* stats, const float* entropies, const float* grad_logprobs,
+                                  const float* grad_entropies, const float* scale, void* grad_logits, int64_t grad_ld,
+                                  cudaStream_t stream);
+
+/* The same log-probabilities from hidden states and the output matrix, whose
+ * product (the logits) stays on the chip in float32:
+ *   hidden  device, row r at r*hidden_ld elements, `width` values of `type`
+ *   weight  device, token i's row at i*weight_ld elements
+ * type is PROFK_BF16 or PROFK_F16; both arrays begin at 16-byte boundaries and
+ * their row strides are multiples of 16 bytes (else PROFK_ERR_UNSUPPORTED), width
+ * itself may be odd.  1 <= width < 2^20, n < 2^30 and rows < 2^24.  The values behind a row's width
+ * are not looked at.  There is no gradient.  The call takes a workspace from the library's
+ * pool (12 to 16 bytes for every row and 256 tokens of the vocabulary). */
+int profk_head_logprobs(const void* hidden, const void* weight, int type, int64_t rows, int64_t n, int64_t width,
+                        int64_t hidden_ld, int64_t weight_ld, const int64_t* tokens, const float* temperature,
+                        float all_temperature, float* out_logprobs, float* out_entropies, cudaStream_t stream);
+
+/* How profk_policy_loss weighs.  Each array is on the device, `rows` floats. */
+typedef struct profk_policy {
+  const float* old_logprobs;  /* the tokens' log-probabilities when they were drawn */
+  const float* advantages;
+  const float* ref_logprobs;  /* of the reference policy, or NULL: no KL term */
+  const float* weights;       /* each token's factor in the loss; 0 leaves it out.  NULL: 1 / rows for all */
+  float clip_low, clip_high;  /* the ratio's bounds are 1 - clip_low and 1 + clip_high; both >= 0 */
+  float kl;                   /* factor of the KL term */
+  float entropy;              /* factor of the entropy (which the loss is lowered by) */
+} profk_policy;
+
+/* The clipped policy loss.  With lp a token's log-probability, r = exp(lp - old),
+ * A its advantage, q = ref - lp:
+ *   term = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(q) - 1 - q) - entropy H,
+ *   loss = sum of weight * term over the tokens that are not left out.
+ * The gradient of the first part is -A r where the clipped product is not the
+ * smaller one, else 0.  old, advantages, ref and weights are constants.
+ *   out_loss           device, one float
+ *   out_sums           device, three floats: the sums of weight * (exp(q) - 1 - q), of the
+ *                      weights of clipped tokens, and of weight * H (0 without entropies)
+ *   out_entropies      device, rows floats; NULL only if how->entropy is 0
+ *   out_slopes         device, rows floats: d loss / d logprob (for the backward call)
+ *   out_entropy_slopes device, rows floats: d loss / d entropy, or NULL
+ *   grad_logits        device, or NULL: the gradient of the loss with respect to the logits,
+ *                      from the same launch; as in profk_token_logprobs_backward, which gives
+ *                      the same from out_slopes.  It may be the logits themselves */
+int profk_policy_loss(const void* logits, int type, int64_t rows, int64_t n, int64_t ld, const int64_t* tokens,
+                      const float* temperature, float all_temperature, const profk_policy* how, float* out_loss,
+                      float* out_sums, float* out_logprobs, float* out_entropies, float* out_stats, float* out_slopes,
+                      float* out_entropy_slopes, void* grad_logits, int64_t grad_ld, cudaStream_t stream);
+
+/* How profk_preference_loss compares. */
+typedef struct profk_preference {
+  const float* ref_logprobs; /* device, rows floats: of the reference policy, or NULL: 0 */
+  float beta;                /* factor of the ratios, finite */
+  float label_smoothing;     /* 0 .. 1: the share of pairs taken to be labelled the wrong way round */
+  float margin;              /* taken from each pair's difference, finite */
+  int average;               /* nonzero: a sequence counts by the mean over its tokens, not by their sum */
+} profk_preference;
+
+/* The preference loss of pairs of sequences.  Sequence j is the rows
+ * offsets[j] .. offsets[j + 1] - 1; 2i is pair i's preferred one, 2i + 1 the other.
+ * With D_j the sum (or mean) of lp - ref over the rows of j that are not left
+ * out (0 where there are none), e the label smoothing and
+ *   d = beta (D_2i - D_2i+1) - margin,
+ * a pair's term is -(1 - e) log sigmoid(d) - e log sigmoid(-d); the loss is
+ * the mean of the pairs' terms (0 without a pair).
+ *   offsets      device, 2*pairs + 1 int64, not falling, within 0 .. rows.  Rows before
+ *                the first and from the last on are left out.  A sequence whose offsets are
+ *                not so makes its pair's margin and the loss NaN
+ *   out_loss     device, one float
+ *   out_margins  device, pairs floats: d
+ *   out_slopes   device, rows floats: d loss / d logprob (for the backward call) */
+int profk_preference_loss(const void* logits, int type, int64_t rows, int64_t n, int64_t ld, const int64_t* tokens,
+                          const float* temperature, float all_temperature, const int64_t* offsets, int64_t pairs,
+                          const profk_preference* how, float* out_loss, float* out_margins, float* out_logprobs,
+                          float* out_stats, float* out_slopes, cudaStream_t stream);
+
 /* ---- calls that allocate nothing --------------------------------------- */
 
 /* Bytes of the fixed device scratch array behind profk_topk_noalloc.  Every

@@ -18,10 +18,13 @@ from ._abi import (OPT_FILTER_CTAS_PER_SM, OPT_FORCE_M, OPT_FORCE_S, OPT_FORCE_T
                    PARAMS_DEFAULT, PARAMS_EXACT, SAMPLER_AUTO, SAMPLER_GRID, SAMPLER_LISTS, SAMPLER_STEPS,
                    PARAMS_OLD, PATH_EXACT, PATH_FALLBACK, PATH_FILTER, PATH_TIE, ProfkError, ProfkStats)
 from ._lm import Routing, route, route_backward, sample_tokens
+from ._losses import (PolicyLoss, PreferenceLoss, TokenLogprobs, policy_loss, policy_loss_backward, preference_loss,
+                      preference_loss_backward, token_logprobs, token_logprobs_backward)
 
 __all__ = ["topk", "topk_batched", "topk_noalloc", "params", "workspace_size", "set_option", "get_option", "reset_options",
            "sample", "threshold", "filter_pass", "refine", "exact", "last_stage_ms", "ProfkError", "ProfkStats",
-           "lib", "sample_tokens", "route", "route_backward", "Routing"]
+           "lib", "sample_tokens", "route", "route_backward", "Routing", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
+           "policy_loss", "policy_loss_backward", "PolicyLoss", "preference_loss", "preference_loss_backward", "PreferenceLoss"]
 
 
 def lib():

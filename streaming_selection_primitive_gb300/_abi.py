@@ -67,6 +67,18 @@ class Routing(C.Structure):
     _fields_ = [("score", C.c_int), ("normalize", C.c_int), ("bias", C.c_void_p), ("mask", C.c_void_p)]
 
 
+class Policy(C.Structure):
+    _fields_ = [
+        ("old_logprobs", C.c_void_p), ("advantages", C.c_void_p), ("ref_logprobs", C.c_void_p), ("weights", C.c_void_p),
+        ("clip_low", C.c_float), ("clip_high", C.c_float), ("kl", C.c_float), ("entropy", C.c_float),
+    ]
+
+
+class Preference(C.Structure):
+    _fields_ = [("ref_logprobs", C.c_void_p), ("beta", C.c_float), ("label_smoothing", C.c_float), ("margin", C.c_float),
+                ("average", C.c_int)]
+
+
 _STATS_NAMES = tuple(name for name, _ in ProfkStats._fields_)
 _STATS_FMT = __import__("struct").Struct("=7q2f4iQfi")
 assert _STATS_FMT.size == C.sizeof(ProfkStats)
@@ -116,6 +128,19 @@ _SIGS = {
     "profk_route_backward": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
                                        C.POINTER(Routing), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                        C.c_int64, C.c_void_p]),
+    "profk_token_logprobs": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                       C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "profk_token_logprobs_backward": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                                C.c_void_p, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                                C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "profk_head_logprobs": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                      C.c_int64, C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "profk_policy_loss": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                    C.c_float, C.POINTER(Policy), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "profk_preference_loss": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                        C.c_float, C.c_void_p, C.c_int64, C.POINTER(Preference), C.c_void_p,
+                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
 }
 
 

@@ -27,7 +27,7 @@ BINDING_SOURCE = CSRC / "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", str(INCLUDE)] + ARCH
 SOURCES = ["sample.cu", "select.cu", "sort.cu", "refine.cu", "tie.cu", "rows.cu", "filter.cu", "segments.cu", "api.cu", "params.cpp", "noalloc.cu", "tokens.cu", "route.cu", "route_scores.cu",
-           "api_lm.cu"]
+           "api_lm.cu", "logprobs.cu", "head.cu", "api_logprobs.cu"]
 
 
 def _nvcc() -> str:

@@ -1,15 +1,16 @@
-// Native half of the Python calls in _lm.py: checks the tensors, makes the
+// Native half of the Python calls in _lm.py and _losses.py: checks the tensors, makes the
 // outputs and calls the C-ABI (libprofk.so) on the current stream.  A call of
 // a few microseconds spends most of them here if this is done in Python: one
 // decoding step's route takes 19.5 us through ctypes, 6.5 us with this file.
 //
-// Functions take positional arguments only (the keyword forms are in _lm.py)
+// Functions take positional arguments only (the keyword forms are in those files)
 // and return the outputs, or the library's status where it is not PROFK_OK.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <optional>
 #include <string>
 
@@ -17,6 +18,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -262,10 +264,207 @@ PyObject* route_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- log-probabilities of given tokens, and the losses on them ----
+
+// What a loss takes as it is: no derivative reaches it, and one that was asked for is refused.
+const float* constant(PyObject* o, const char* name, const Tensor& like, int64_t rows) {
+  if (o == Py_None) return nullptr;
+  const int64_t shape[1] = {rows};
+  const auto* p = static_cast<const float*>(array(o, name, at::kFloat, like, shape));
+  const Tensor& t = without_tangent(THPVariable_Unpack(o), name);
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    refuse(PyExc_ValueError, "%s counts as a constant, but requires a gradient: detach it", name);
+  return p;
+}
+
+struct Temperature {
+  const float* rows = nullptr;
+  float all = 1.f;
+  Temperature(PyObject* o, const Tensor& like, int64_t n) {
+    if (THPVariable_Check(o)) {
+      rows = constant(o, "temperature", like, n);
+      return;
+    }
+    all = static_cast<float>(number(o));
+    if (!(all > 0.f && all < INFINITY && 1.4426950f / all < INFINITY && 1.4426950f / all > 0.f))
+      refuse(PyExc_ValueError, "temperature must be above 0 and finite");
+  }
+};
+
+const int64_t* tokens_of(PyObject* o, const Tensor& like, int64_t rows) {
+  return static_cast<const int64_t*>(array(o, "tokens", at::kLong, like, {rows}));
+}
+
+float* data(const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
+
+// Where a gradient of the logits goes: a tensor of the caller's, or a new one.  The C-ABI
+// refuses one that lies across the logits' memory.
+struct GradientOut {
+  Tensor t;
+  int64_t ld;
+  GradientOut(PyObject* o, const Logits& x, const Place& place) : ld(x.n) {
+    if (o == Py_None) {
+      t = place.empty({x.rows, x.n}, x.t->scalar_type());
+    } else {
+      t = on_device(o, "out", x.t->scalar_type(), *x.t);
+      ld = rows_of(t, "out", x.rows, x.n);
+      if (ld < x.n) refuse(PyExc_ValueError, "the rows of out must not share memory");
+    }
+  }
+};
+
+// logits, tokens, temperature, entropy, stream
+PyObject* token_logprobs(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  expect(count, 5);
+  const Logits x = logits_of(arg[0]);
+  const Tensor& like = *x.t;
+  const int64_t* tokens = tokens_of(arg[1], like, x.rows);
+  const Temperature T(arg[2], like, x.rows);
+  const Place place(arg[4], like);
+  const Tensor logprobs = place.empty({x.rows}, at::kFloat), stats = place.empty({x.rows, 2}, at::kFloat);
+  Tensor entropies;
+  if (arg[3] == Py_True) entropies = place.empty({x.rows}, at::kFloat);
+  const int code = profk_token_logprobs(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, data(logprobs),
+                                        data(entropies), data(stats), place.stream());
+  return code == PROFK_OK ? tuple_of({logprobs, entropies, stats}) : PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
+// logits, tokens, temperature, stats, entropies, grad_logprobs, grad_entropies, scale, out, stream
+PyObject* token_logprobs_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  expect(count, 10);
+  const Logits x = logits_of(arg[0]);
+  const Tensor& like = *x.t;
+  const int64_t* tokens = tokens_of(arg[1], like, x.rows);
+  const Temperature T(arg[2], like, x.rows);
+  const auto* stats = static_cast<const float*>(array(arg[3], "stats", at::kFloat, like, {x.rows, 2}));
+  const auto row_floats = [&](PyObject* o, const char* name) -> const float* {
+    if (o == Py_None) return nullptr;
+    const auto* p = static_cast<const float*>(array(o, name, at::kFloat, like, {x.rows}));
+    without_tangent(THPVariable_Unpack(o), name);
+    return p;
+  };
+  const float *entropies = row_floats(arg[4], "entropies"), *g = row_floats(arg[5], "grad_logprobs"),
+              *h = row_floats(arg[6], "grad_entropies"), *scale = nullptr;
+  if (h && !entropies) refuse(PyExc_ValueError, "grad_entropies needs the entropies of a call with entropy=True");
+  if (arg[7] != Py_None) {
+    const Tensor& t = without_tangent(on_device(arg[7], "grad_loss", at::kFloat, like), "grad_loss");
+    if (t.numel() != 1) refuse(PyExc_ValueError, "grad_loss must hold one element");
+    scale = data(t);
+  }
+  const Place place(arg[9], like);
+  const GradientOut out(arg[8], x, place);
+  const int code = profk_token_logprobs_backward(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, stats,
+                                                 entropies, g, h, scale, out.t.data_ptr(), out.ld, place.stream());
+  return code == PROFK_OK ? THPVariable_Wrap(out.t) : PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
+// hidden, weight, tokens, temperature, entropy, stream
+PyObject* head_logprobs(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  expect(count, 6);
+  if (!THPVariable_Check(arg[0]) || !THPVariable_Check(arg[1])) refuse(PyExc_TypeError, "hidden states and weight must be CUDA tensors");
+  const Tensor& hidden = without_tangent(THPVariable_Unpack(arg[0]), "x");
+  const at::ScalarType s = hidden.scalar_type();
+  if (!hidden.is_cuda() || (s != at::kBFloat16 && s != at::kHalf))
+    refuse(PyExc_TypeError, "with a weight, x must be a bfloat16 or float16 CUDA tensor of hidden states");
+  const Tensor& weight = without_tangent(on_device(arg[1], "weight", s, hidden), "weight");
+  if (hidden.dim() != 2 || weight.dim() != 2) refuse(PyExc_ValueError, "x and weight must be 2-D");
+  const int64_t rows = hidden.size(0), width = hidden.size(1), n = weight.size(0);
+  if (at::GradMode::is_enabled() && (hidden.requires_grad() || weight.requires_grad()))
+    refuse(PyExc_ValueError, "there is no gradient from hidden states: give logits, or call under torch.no_grad()");
+  const int64_t hidden_ld = rows_of(hidden, "x", rows, width), weight_ld = rows_of(weight, "weight", n, width);
+  const int64_t* tokens = tokens_of(arg[2], hidden, rows);
+  const Temperature T(arg[3], hidden, rows);
+  if (width < 1 || n < 1) refuse(PyExc_ValueError, "x and weight must not be empty");
+  if (reinterpret_cast<uintptr_t>(hidden.data_ptr()) % 16 || reinterpret_cast<uintptr_t>(weight.data_ptr()) % 16 ||
+      (rows > 1 && hidden_ld % 8) || (n > 1 && weight_ld % 8))
+    refuse(PyExc_ValueError, "x and weight must begin at 16-byte boundaries, with row strides that are multiples of 16 bytes");
+  const Place place(arg[5], hidden);
+  const Tensor logprobs = place.empty({rows}, at::kFloat);
+  Tensor entropies;
+  if (arg[4] == Py_True) entropies = place.empty({rows}, at::kFloat);
+  // (The stride of a single row is never used.)
+  const int64_t whole_rows = (width + 7) / 8 * 8;
+  const int code = profk_head_logprobs(hidden.data_ptr(), weight.data_ptr(), s == at::kHalf ? PROFK_F16 : PROFK_BF16, rows, n,
+                                       width, rows > 1 ? hidden_ld : whole_rows, n > 1 ? weight_ld : whole_rows, tokens, T.rows,
+                                       T.all, data(logprobs), data(entropies), place.stream());
+  return code == PROFK_OK ? tuple_of({logprobs, entropies, Tensor()}) : PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
+// logits, tokens, old_logprobs, advantages, ref_logprobs, weights, temperature, clip_low, clip_high, kl, entropy, gradient, out, stream
+PyObject* policy_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  expect(count, 14);
+  const Logits x = logits_of(arg[0]);
+  const Tensor& like = *x.t;
+  const int64_t* tokens = tokens_of(arg[1], like, x.rows);
+  if (arg[2] == Py_None || arg[3] == Py_None) refuse(PyExc_TypeError, "old_logprobs and advantages must be tensors");
+  profk_policy how{constant(arg[2], "old_logprobs", like, x.rows), constant(arg[3], "advantages", like, x.rows),
+                   constant(arg[4], "ref_logprobs", like, x.rows), constant(arg[5], "weights", like, x.rows),
+                   static_cast<float>(number(arg[7])), static_cast<float>(number(arg[8])), static_cast<float>(number(arg[9])), 0.f};
+  const Temperature T(arg[6], like, x.rows);
+  const bool entropy = arg[10] != Py_None, gradient = arg[11] == Py_True;
+  if (entropy) how.entropy = static_cast<float>(number(arg[10]));
+  const Place place(arg[13], like);
+  const Tensor loss = place.empty({}, at::kFloat), sums = place.empty({3}, at::kFloat), logprobs = place.empty({x.rows}, at::kFloat),
+               stats = place.empty({x.rows, 2}, at::kFloat), slopes = place.empty({x.rows}, at::kFloat);
+  Tensor entropies, entropy_slopes, grad;
+  int64_t grad_ld = 0;
+  if (entropy) entropies = place.empty({x.rows}, at::kFloat);
+  if (how.entropy != 0.f) entropy_slopes = place.empty({x.rows}, at::kFloat);
+  if (gradient) {
+    const GradientOut out(arg[12], x, place);
+    grad = out.t;
+    grad_ld = out.ld;
+  } else if (arg[12] != Py_None) {
+    refuse(PyExc_ValueError, "out is for gradient=True");
+  }
+  const int code = profk_policy_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, &how, data(loss),
+                                     data(sums), data(logprobs), data(entropies), data(stats), data(slopes),
+                                     data(entropy_slopes), grad.defined() ? grad.data_ptr() : nullptr, grad_ld, place.stream());
+  return code == PROFK_OK ? tuple_of({loss, sums, logprobs, entropies, stats, slopes, entropy_slopes, grad}) : PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
+// logits, tokens, offsets, ref_logprobs, beta, label_smoothing, margin, average, temperature, stream
+PyObject* preference_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  expect(count, 10);
+  const Logits x = logits_of(arg[0]);
+  const Tensor& like = *x.t;
+  const int64_t* tokens = tokens_of(arg[1], like, x.rows);
+  const Tensor& o = on_device(arg[2], "offsets", at::kLong, like);
+  if (o.dim() != 1 || o.size(0) % 2 != 1 || !o.is_contiguous())
+    refuse(PyExc_ValueError, "offsets must be contiguous, 1-D and of an odd length: two sequences for each pair, and the end");
+  const int64_t pairs = o.size(0) / 2;
+  const profk_preference how{constant(arg[3], "ref_logprobs", like, x.rows), static_cast<float>(number(arg[4])),
+                             static_cast<float>(number(arg[5])), static_cast<float>(number(arg[6])), arg[7] == Py_True};
+  const Temperature T(arg[8], like, x.rows);
+  const Place place(arg[9], like);
+  const Tensor loss = place.empty({}, at::kFloat), margins = place.empty({pairs}, at::kFloat),
+               logprobs = place.empty({x.rows}, at::kFloat), stats = place.empty({x.rows, 2}, at::kFloat),
+               slopes = place.empty({x.rows}, at::kFloat);
+  const int code = profk_preference_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all,
+                                         static_cast<const int64_t*>(o.data_ptr()), pairs, &how, data(loss), data(margins),
+                                         data(logprobs), data(stats), data(slopes), place.stream());
+  return code == PROFK_OK ? tuple_of({loss, margins, logprobs, stats, slopes}) : PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"sample_tokens", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(sample_tokens)), METH_FASTCALL, nullptr},
     {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(route)), METH_FASTCALL, nullptr},
     {"route_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(route_backward)), METH_FASTCALL, nullptr},
+    {"token_logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(token_logprobs)), METH_FASTCALL, nullptr},
+    {"token_logprobs_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(token_logprobs_backward)), METH_FASTCALL, nullptr},
+    {"head_logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(head_logprobs)), METH_FASTCALL, nullptr},
+    {"policy_loss", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(policy_loss)), METH_FASTCALL, nullptr},
+    {"preference_loss", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(preference_loss)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "profk_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -70,4 +70,82 @@ struct RouteBackwardArgs {
 };
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream);
 
+// Log-probabilities of given tokens, their gradient, and the losses on them (logprobs.cu).
+struct LogprobArgs {
+  const void* logits;  // rows of n values, row stride ld
+  int type;            // a profk_type
+  int64_t rows, n, ld;
+  const int64_t* tokens;     // negative: the row is left out
+  const float* temperature;  // per row, or null: all_temperature
+  float all_temperature;
+  float* logprobs;
+  float* entropies;        // or null
+  float2* stats;           // or null: largest logit, sum of exp((l - largest) / T)
+  float* zeros;            // or null: every row gets 0
+  const float* weights;    // or null; a row of weight 0 is left out
+  const int64_t* offsets;  // or null; sequences + 1 of them: rows before the first and from the last on are left out
+  int64_t sequences;
+  void* grad_logits;  // with the policy loss, or null: rows of n values, row stride grad_ld
+  int64_t grad_ld;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream);
+
+struct LogprobBackwardArgs {
+  const void* logits;
+  int type;
+  int64_t rows, n, ld;
+  const int64_t* tokens;
+  const float* temperature;
+  float all_temperature;
+  const float2* stats;
+  const float* entropies;       // null when grad_entropies is
+  const float* grad_logprobs;   // or null
+  const float* grad_entropies;  // or null
+  const float* scale;           // one float for both, or null
+  void* grad_logits;
+  int64_t grad_ld;
+};
+cudaError_t launch_token_logprobs_backward(const LogprobBackwardArgs& a, cudaStream_t stream);
+
+struct PolicyHow {
+  const float* old_logprobs;
+  const float* advantages;
+  const float* ref_logprobs;  // or null: no KL term
+  const float* weights;       // or null: all_weight
+  float all_weight, clip_low, clip_high, kl, entropy;
+};
+struct PolicyOut {
+  float* loss;
+  float* sums;  // three floats: weighted sums of KL terms, of clipped tokens, of entropies
+  float* slopes;
+  float* entropy_slopes;  // or null
+};
+cudaError_t launch_policy_loss(const LogprobArgs& a, const PolicyHow& how, const PolicyOut& out, cudaStream_t stream);
+
+struct PreferenceHow {
+  const float* ref_logprobs;  // or null
+  float beta, smoothing, margin;
+  bool average;
+};
+struct PreferenceOut {
+  float* loss;
+  float* margins;
+  float* slopes;
+};
+cudaError_t launch_preference_loss(const LogprobArgs& a, const PreferenceHow& how, const PreferenceOut& out, cudaStream_t stream);
+
+// The same log-probabilities from hidden states and the output matrix (head.cu).
+struct HeadArgs {
+  const void* hidden;  // rows of `width` values, row stride hidden_ld
+  const void* weight;  // n rows of `width` values, row stride weight_ld
+  int type;            // PROFK_BF16 or PROFK_F16
+  int64_t rows, n, width, hidden_ld, weight_ld;
+  const int64_t* tokens;
+  const float* temperature;
+  float all_temperature;
+  float* logprobs;
+  float* entropies;  // or null
+};
+cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream);
+
 }  // namespace profk

@@ -1,0 +1,106 @@
+// A row of logits under the softmax: running maximum and sums of one pass (logprobs.cu),
+// their joins, and what the losses make of a row.
+#pragma once
+
+#include "lm.cuh"
+#include "lm.h"
+
+namespace profk {
+
+// Below this, 2^x is zero in float32 whatever it is; as the smallest exponent it keeps
+// x 2^x from becoming inf * 0 where a logit is -inf.
+constexpr float NO_MASS = -300.f;
+
+// What has been seen of a row: its largest logit m, s = sum 2^x and t = sum x 2^x with
+// x = (l - m) c, c = log2(e) / T.  s and t are sums of many terms (a thread of a long
+// row adds millions): each carries what its additions lost in a second float.  A NaN or
+// +inf logit makes s NaN (inf - inf), and it stays so; s = 0 says that nothing but -inf came.
+struct Running {
+  float m, s, t, s_lost, t_lost;
+};
+
+// m as the point that others are taken from: any finite number while all are -inf.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+
+// sum + v exactly, as a float and what it lost.
+__device__ __forceinline__ void add_exact(float& sum, float& lost, float v) {
+  const float r = sum + v, back = r - sum;
+  lost += (sum - (r - back)) + (v - back);
+  sum = r;
+}
+
+// The exponent by which sums relative to `from` shrink when taken relative to `to`.
+// (fmaxf gives NO_MASS where both are infinite: what is NaN already stays it, what is zero too.)
+__device__ __forceinline__ float shrink(float from, float to, float c) { return fmaxf((from - to) * c, NO_MASS); }
+
+// Row results that the kernels exchange.
+struct RowSum {
+  float m, s, t;
+};
+
+__device__ __forceinline__ RowSum total(const Running& r) { return {r.m, r.s + r.s_lost, r.t + r.t_lost}; }
+
+// Joins over the warp: all lanes get the same, in the same order every time.
+template <bool ENTROPY>
+__device__ __forceinline__ RowSum warp_join(RowSum r, float c) {
+  const float m = warp_max(r.m);
+  const float d = shrink(r.m, m, c), f = lm_exp2(d);
+  const float s = warp_sum(r.s * f);
+  const float t = ENTROPY ? warp_sum(f * (r.t + d * r.s)) : 0.f;
+  return {m, s, t};
+}
+
+// Two parts of a row as one.
+__device__ __forceinline__ RowSum joined(const RowSum& y, const RowSum& z, float c) {
+  const float m = fmaxf(y.m, z.m), dy = shrink(y.m, m, c), dz = shrink(z.m, m, c);
+  const float fy = lm_exp2(dy), fz = lm_exp2(dz);
+  return {m, fy * y.s + fz * z.s, fy * (y.t + dy * y.s) + fz * (z.t + dz * z.s)};
+}
+
+// A token's log-probability from its logit and the row's sums: -inf where the row holds
+// nothing, NaN where it holds a NaN or +inf.
+__device__ __forceinline__ float row_logprob(const RowSum& r, float logit, float T) {
+  return r.s == 0.f ? -INFINITY : (logit - reference(r.m)) / T - logf(r.s);
+}
+
+// log s - (sum x exp x) / s; 0 for a row that holds nothing.
+__device__ __forceinline__ float row_entropy(const RowSum& r) {
+  return r.s == 0.f ? 0.f : logf(r.s) - r.t * LN2 / r.s;
+}
+
+// log2(e) / T; NaN where T is no positive number, or so near to zero (or infinity) that
+// this is none.
+__device__ __forceinline__ float inverse_temperature(float T) {
+  const float c = LOG2E / T;
+  return c > 0.f && c < INFINITY ? c : NAN;
+}
+
+// One token's part of the clipped policy loss, by its log-probability.
+struct PolicyTerm {
+  float loss;     // without the entropy
+  float kl;       // exp(q) - 1 - q, q = reference - log-probability
+  bool clipped;   // the clipped ratio is what counts: no gradient of the ratio
+  float slope;    // d loss / d log-probability
+};
+
+__device__ __forceinline__ PolicyTerm policy_term(float lp, float old_lp, float A, bool with_ref, float ref_lp,
+                                                  const PolicyHow& how) {
+  PolicyTerm y;
+  const float ratio = expf(lp - old_lp), low = 1.f - how.clip_low, high = 1.f + how.clip_high;
+  y.clipped = (A > 0.f && ratio > high) || (A < 0.f && ratio < low);
+  // A ratio that is not a number, or an infinite one times nothing, shows in the loss.
+  y.loss = y.clipped ? -A * (A > 0.f ? high : low) : -A * ratio;
+  y.slope = y.clipped ? 0.f : -A * ratio;
+  y.kl = 0.f;
+  if (with_ref) {
+    const float q = ref_lp - lp, e = expm1f(q);
+    y.kl = e == INFINITY ? e : e - q;
+    if (how.kl != 0.f) {
+      y.loss += how.kl * y.kl;
+      y.slope -= how.kl * e;
+    }
+  }
+  return y;
+}
+
+}  // namespace profk
