@@ -252,7 +252,10 @@ typedef enum profk_option {
                                   candidates share; its first pass finds a key outside that prefix and
                                   every CTA of the row starts the passes again from the key's top bit.
                                   Results and statistics are those of the default */
-  PROFK_OPT__COUNT = 14
+  PROFK_OPT_HEAD_WAIT_TEST = 14, /* the same test for profk_head_logprobs [0]: 1 makes its waits for a finished
+                                  tile expect one arrival more than comes, with a bound of 4096 polls.  Its
+                                  outputs are then NaN (0 for rows left out); the next call is unaffected */
+  PROFK_OPT__COUNT = 15
 } profk_option;
 #define PROFK_WAIT_TEST_OFF 0
 #define PROFK_WAIT_TEST_SAMPLER 1
@@ -501,8 +504,9 @@ int profk_token_logprobs_backward(const void* logits, int type, int64_t rows, in
  * type is PROFK_BF16 or PROFK_F16; both arrays begin at 16-byte boundaries and
  * their row strides are multiples of 16 bytes (else PROFK_ERR_UNSUPPORTED), width
  * itself may be odd.  1 <= width < 2^20, n < 2^30 and rows < 2^24.  The values behind a row's width
- * are not looked at.  There is no gradient.  The call takes a workspace from the library's
- * pool (12 to 16 bytes for every row and 256 tokens of the vocabulary). */
+ * are not looked at.  rows * n is limited to some 2^45.  There is no gradient.  The call takes a
+ * workspace from the library's pool: at most 32 bytes for each row and 256 tokens of the
+ * vocabulary.  Its waits on the device are bounded; where one runs out, outputs are NaN. */
 int profk_head_logprobs(const void* hidden, const void* weight, int type, int64_t rows, int64_t n, int64_t width,
                         int64_t hidden_ld, int64_t weight_ld, const int64_t* tokens, const float* temperature,
                         float all_temperature, float* out_logprobs, float* out_entropies, cudaStream_t stream);

@@ -30,18 +30,20 @@ namespace {
 // Options.
 std::atomic<int64_t> g_opt[PROFK_OPT__COUNT] = {
     {PROFK_PARAMS_DEFAULT}, {6}, {1}, {0}, {0}, {0}, {0}, {0}, {1}, {0}, {PROFK_SAMPLER_AUTO}, {PROFK_WAIT_TEST_OFF}, {0},
-    {0}};
+    {0}, {0}};
 
 // PROFK_OPT_WAIT_TEST: the wait setting of the persistent kernel it names
 // (one arrival more than the launch has at its first grid barrier, and a
 // short bound), the default setting for every other kernel.
-WaitCfg wait_cfg_for(int64_t kernel) {
-  const int64_t t = g_opt[PROFK_OPT_WAIT_TEST].load();
-  if (t == PROFK_WAIT_TEST_OFF || t != kernel) return WaitCfg{};
+WaitCfg wait_test() {
   WaitCfg w;
   w.skew = 1u;
   w.polls = 1 << 12;
   return w;
+}
+WaitCfg wait_cfg_for(int64_t kernel) {
+  const int64_t t = g_opt[PROFK_OPT_WAIT_TEST].load();
+  return t == PROFK_WAIT_TEST_OFF || t != kernel ? WaitCfg{} : wait_test();
 }
 
 // Longest row handled as one (PROFK_OPT_MAX_SEGMENT; 0 = 2^32, the reach of a
@@ -1061,6 +1063,8 @@ bool pdl_enabled() { return g_opt[PROFK_OPT_PDL].load(std::memory_order_relaxed)
 
 cudaError_t library_pool(cudaMemPool_t* out) { return pool_for_current_device(out); }
 
+WaitCfg head_wait() { return g_opt[PROFK_OPT_HEAD_WAIT_TEST].load() ? wait_test() : WaitCfg{}; }
+
 }  // namespace profk
 
 using namespace profk;
@@ -1364,6 +1368,7 @@ int profk_set_option(int option, int64_t value) {
   if (option == PROFK_OPT_WAIT_TEST && (value < PROFK_WAIT_TEST_OFF || value > PROFK_WAIT_TEST_SORT))
     return PROFK_ERR_INVALID;
   if (option == PROFK_OPT_SPECULATIVE && value > 8) return PROFK_ERR_INVALID;
+  if (option == PROFK_OPT_HEAD_WAIT_TEST && value > 1) return PROFK_ERR_INVALID;
   if (option == PROFK_OPT_PREFIX_TEST && value > 33) return PROFK_ERR_INVALID;
   if (option == PROFK_OPT_MAX_SEGMENT && value != 0 && (value < (1 << 16) || value > (int64_t(1) << 32) || (value & 3)))
     return PROFK_ERR_INVALID;

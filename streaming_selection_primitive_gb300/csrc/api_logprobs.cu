@@ -118,6 +118,7 @@ int profk_head_logprobs(const void* hidden, const void* weight, int type, int64_
       !temperature_ok(temperature, all_temperature))
     return PROFK_ERR_INVALID;
   if (n >= (int64_t(1) << 30) || rows >= (int64_t(1) << 24) || width >= (int64_t(1) << 20)) return PROFK_ERR_UNSUPPORTED;
+  if ((rows / 128 + 1) * (n / 256 + 1) >= (int64_t(1) << 30)) return PROFK_ERR_UNSUPPORTED;
   if (hidden_ld >= (int64_t(1) << 38) || weight_ld >= (int64_t(1) << 38)) return PROFK_ERR_UNSUPPORTED;
   if (!aligned(hidden, 16) || !aligned(weight, 16) || hidden_ld % 8 || weight_ld % 8 || !aligned(tokens, 8) ||
       !floats(temperature, out_logprobs, out_entropies))

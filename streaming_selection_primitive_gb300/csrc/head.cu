@@ -1,70 +1,269 @@
 // Log-probabilities of given tokens from hidden states and the output matrix: a product
-// whose result, the logits, is turned into row maxima and sums tile by tile and never
-// leaves the chip.
+// on the tensor cores whose result, the logits, is turned into row maxima and sums tile
+// by tile and never leaves the chip.
+//
+// A tile is 128 rows of hidden states by 256 tokens of the vocabulary.  A CTA (one an SM)
+// has a warp that copies pieces of both, 64 deep, into a ring in shared memory, a warp
+// that issues the products into one half of the tensor memory, and eight warps that
+// meanwhile take the finished tile in the other half: a thread has a row's 128 of the
+// tokens, and carries the row's running maximum and sums over a run of tiles.  The runs'
+// sums are joined by a second kernel.
+//
+// Every wait is bounded; a CTA whose wait ends without its barrier writes NaN for all rows of
+// its remaining work.
+#include <cuda.h>
+
+#include <algorithm>
+
 #include "../../include/profk.h"
 #include "lm.h"
 #include "logprobs.cuh"
+#include "tcgen05.cuh"
 
 namespace profk {
 namespace {
 
-constexpr int TILE = 64;        // rows and tokens of a tile
-constexpr int DEPTH = 32;       // of the product at a time
-constexpr int THREADS = 256;
+constexpr int TILE_ROWS = 128;
+constexpr int TILE_TOKENS = 256;
+constexpr int DEPTH = 64;   // of a piece: 128 bytes a row, the widest swizzle
+constexpr int STAGES = 4;   // pieces in the ring
+constexpr int TAKERS = 8;   // warps that take tiles: two for each quarter of the lanes
+constexpr int COPIER = TAKERS, MULTIPLIER = TAKERS + 1;  // the other two warps
+constexpr int THREADS = 32 * (TAKERS + 2);
+constexpr int TENSOR_COLUMNS = 2 * TILE_TOKENS;  // all there are: two accumulators
+constexpr int PARTS = 2;    // a run's columns are taken by two threads a row
 
-template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(THREADS) k_head(HeadArgs a, float4* parts, float* logits) {
-  pdl_wait();
-  __shared__ float h[DEPTH][TILE + 1], w[DEPTH][TILE + 1], l[TILE][TILE + 1];
-  const int64_t row0 = int64_t(blockIdx.y) * TILE, col0 = int64_t(blockIdx.x) * TILE;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.width; k0 += DEPTH) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < TILE * DEPTH; i += THREADS) {
-      const int k = i % DEPTH, r = i / DEPTH;
-      const bool in = k0 + k < a.width;
-      h[k][r] = in && row0 + r < a.rows ? lm_float(static_cast<const T*>(a.hidden)[(row0 + r) * a.hidden_ld + k0 + k]) : 0.f;
-      w[k][r] = in && col0 + r < a.n ? lm_float(static_cast<const T*>(a.weight)[(col0 + r) * a.weight_ld + k0 + k]) : 0.f;
-    }
-    __syncthreads();
-    for (int k = 0; k < DEPTH; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(h[k][ty + 16 * i], w[k][tx + 16 * j], acc[i][j]);
+constexpr size_t ROWS_BYTES = TILE_ROWS * DEPTH * 2, TOKENS_BYTES = TILE_TOKENS * DEPTH * 2;
+constexpr size_t STAGE_BYTES = ROWS_BYTES + TOKENS_BYTES;
+constexpr size_t SHARED_BYTES = STAGES * STAGE_BYTES + 1024;  // (the ring begins at a multiple of 1024 bytes)
+
+// How the work is cut: run r is row tile r % row_tiles and the vocabulary's tiles
+// (r / row_tiles) * run and on, `run` of them, so that CTAs that work at the same time share
+// their tiles of the matrix in L2.
+struct Plan {
+  int row_tiles, token_tiles, run, runs, pieces;
+};
+
+struct Barriers {
+  uint64_t full[STAGES], empty[STAGES];  // of the ring
+  uint64_t done[2], taken[2];            // of the accumulators
+  uint32_t tensor;                       // address of the tensor memory
+  int given_up;
+};
+
+template <bool ENTROPY>
+__device__ __forceinline__ void take_columns(RowSum& r, float (&v)[32], float c) {
+  float m = r.m;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
+  const float d = shrink(r.m, reference(m), c), f = lm_exp2(d);
+  const Pair minus = pair(-reference(m), -reference(m)), cc = pair(c, c);
+  Pair s[2] = {0, 0}, t[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float x0, x1;
+    split(mul2(add2(pair(v[i], v[i + 1]), minus), cc), x0, x1);
+    const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
+    s[i / 2 & 1] = add2(s[i / 2 & 1], e);
+    if (ENTROPY) t[i / 2 & 1] = fma2(pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i / 2 & 1]);
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) l[ty + 16 * i][tx + 16 * j] = acc[i][j];
+  float a, b;
+  if (ENTROPY) {
+    split(add2(t[0], t[1]), a, b);
+    r.t = f * (r.t + d * r.s) + (a + b);
+  }
+  split(add2(s[0], s[1]), a, b);
+  r.s = f * r.s + (a + b);
+  r.m = m;
+}
+
+template <bool ENTROPY>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_head(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, HeadArgs a, Plan plan, uint32_t product,
+           float4* parts, float* logits, WaitCfg waits) {
+  extern __shared__ uint8_t raw[];
+  __shared__ Barriers sync;
+  uint8_t* ring = raw + (1024 - shared_address(raw) % 1024) % 1024;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int limit = wait_limit(waits);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      barrier_init(&sync.full[i], 1);
+      barrier_init(&sync.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      barrier_init(&sync.done[i], 1 + waits.skew);
+      barrier_init(&sync.taken[i], TAKERS);
+    }
+    barrier_init_done();
+    sync.given_up = 0;
+  }
+  if (warp == MULTIPLIER) tensor_alloc<TENSOR_COLUMNS>(&sync.tensor);
+  before_barrier();
   __syncthreads();
-  const int64_t row = row0 + threadIdx.x;
-  if (threadIdx.x < TILE && row < a.rows) {
-    const float c = inverse_temperature(a.temperature ? a.temperature[row] : a.all_temperature);
-    const int64_t token = a.tokens[row];
-    const int cols = static_cast<int>(min(int64_t(TILE), a.n - col0));
-    float m = -INFINITY, s = 0.f, t = 0.f;
-    for (int j = 0; j < cols; ++j) m = fmaxf(m, l[threadIdx.x][j]);
-    for (int j = 0; j < cols; ++j) {
-      const float x = (l[threadIdx.x][j] - reference(m)) * c, e = lm_exp2(x);
-      s += e;
-      t = fmaf(fmaxf(x, NO_MASS), e, t);
+  after_barrier();
+  const uint32_t tensor = sync.tensor;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == COPIER) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      unsigned parity = 1;  // (the ring begins empty)
+      for (int run = blockIdx.x; run < plan.runs && !sync.given_up; run += gridDim.x) {
+        const int row0 = run % plan.row_tiles * TILE_ROWS, first = run / plan.row_tiles * plan.run;
+        const int last = min(first + plan.run, plan.token_tiles);
+        bool ok = true;
+        for (int tile = first; tile < last && ok; ++tile)
+          for (int piece = 0; piece < plan.pieces; ++piece) {
+            ok = barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit);
+            if (!ok) break;
+            uint8_t* to = ring + stage * STAGE_BYTES;
+            barrier_arrive_expect(&sync.full[stage], STAGE_BYTES);
+            copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[stage]);
+            copy_tile(to + ROWS_BYTES, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[stage]);
+            issued = min(issued + 1, STAGES);
+            if (++stage == STAGES) {
+              stage = 0;
+              parity ^= 1;
+            }
+          }
+      }
+      // The last products' arrivals on the ring.
+      for (int i = 0; i < STAGES && !sync.given_up; ++i) {
+        if (!barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit)) break;
+        if (++stage == STAGES) {
+          stage = 0;
+          parity ^= 1;
+        }
+        issued = 0;
+      }
+      if (sync.given_up && issued > 0) {
+        // Nobody may be reading any more, but copies may still be writing: the last turn of each
+        // stage is waited for.  (Whoever has given up has set the flag, which these waits are not to look at.)
+        int nobody = 0;
+        for (int i = 0; i < issued; ++i) {
+          if (stage == 0) parity ^= 1;
+          stage = stage ? stage - 1 : STAGES - 1;
+          nobody = 0;
+          barrier_wait(&sync.full[stage], parity ^ 1, &nobody, WAIT_POLLS);
+        }
+      }
     }
-    parts[int64_t(blockIdx.x) * a.rows + row] = make_float4(m, s, t, 0.f);
-    if (token >= col0 && token < col0 + cols) logits[row] = l[threadIdx.x][token - col0];
+  } else if (warp == MULTIPLIER) {
+    if (lane == 0) {
+      int stage = 0, half = 0;
+      unsigned parity = 0, taken = 1;  // (both accumulators begin free)
+      bool ok = true;
+      for (int run = blockIdx.x; run < plan.runs && ok; run += gridDim.x) {
+        const int first = run / plan.row_tiles * plan.run, last = min(first + plan.run, plan.token_tiles);
+        for (int tile = first; tile < last && ok; ++tile) {
+          ok = barrier_wait(&sync.taken[half], taken, &sync.given_up, limit);
+          if (!ok) break;
+          after_barrier();
+          const uint32_t to = tensor + half * TILE_TOKENS;
+          for (int piece = 0; piece < plan.pieces; ++piece) {
+            ok = barrier_wait(&sync.full[stage], parity, &sync.given_up, limit);
+            if (!ok) break;
+            after_barrier();
+            const uint64_t x = tile_descriptor(ring + stage * STAGE_BYTES), w = tile_descriptor(ring + stage * STAGE_BYTES + ROWS_BYTES);
+#pragma unroll
+            for (int k = 0; k < DEPTH / 16; ++k)  // 32 bytes on along the rows: 2 in the descriptor's units
+              multiply(to, x + 2 * k, w + 2 * k, product, piece + k > 0);
+            products_arrive(&sync.empty[stage]);
+            if (++stage == STAGES) {
+              stage = 0;
+              parity ^= 1;
+            }
+          }
+          if (!ok) break;
+          products_arrive(&sync.done[half]);
+          half ^= 1;
+          if (half == 0) taken ^= 1;
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3, side = warp >> 2;
+    int half = 0;
+    unsigned done = 0;
+    bool ok = true;
+    for (int run = blockIdx.x; run < plan.runs; run += gridDim.x) {
+      const int index = run / plan.row_tiles, first = index * plan.run, last = min(first + plan.run, plan.token_tiles);
+      const int64_t row = int64_t(run % plan.row_tiles) * TILE_ROWS + quarter * 32 + lane;
+      const bool in = row < a.rows;
+      const float c = inverse_temperature(in && a.temperature ? a.temperature[row] : a.all_temperature);
+      const int64_t token = in ? a.tokens[row] : -1;
+      RowSum sum{-INFINITY, 0.f, 0.f};
+      for (int tile = first; tile < last && ok; ++tile) {
+        ok = __all_sync(FULL_MASK, barrier_wait(&sync.done[half], done, &sync.given_up, limit));
+        if (!ok) break;
+        after_barrier();
+        constexpr int EACH = TILE_TOKENS / PARTS;
+        const uint32_t from = tensor + (uint32_t(quarter * 32) << 16) + half * TILE_TOKENS + side * EACH;
+        const int64_t column0 = int64_t(tile) * TILE_TOKENS + side * EACH;
+#pragma unroll 1
+        for (int i = 0; i < EACH; i += 32) {
+          float v[32];
+          tensor_load(v, from + i);
+          tensor_loaded();
+          const int64_t column = column0 + i;
+          if (column + 32 > a.n) {  // behind the vocabulary
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (column + j >= a.n) v[j] = -INFINITY;
+          }
+          const int64_t at = token - column;
+          if (__any_sync(FULL_MASK, at >= 0 && at < 32)) {
+            float logit = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (at == j) logit = v[j];
+            if (at >= 0 && at < 32 && token < a.n) logits[row] = logit;
+          }
+          take_columns<ENTROPY>(sum, v, c);
+        }
+        before_barrier();
+        __syncwarp();
+        if (lane == 0) barrier_arrive(&sync.taken[half]);
+        half ^= 1;
+        if (half == 0) done ^= 1;
+      }
+      if (!ok) sum.s = NAN;
+      if (in) parts[(int64_t(index) * PARTS + side) * a.rows + row] = make_float4(sum.m, sum.s, sum.t, 0.f);
+    }
   }
+  // The products in flight are done: what came before a taken tile is, and on giving up
+  // the multiplier's own are waited for.
+  if (warp == MULTIPLIER && lane == 0 && sync.given_up) {
+    int nobody = 0;
+    __shared__ uint64_t last;
+    barrier_init(&last, 1);
+    barrier_init_done();
+    products_arrive(&last);
+    barrier_wait(&last, 0, &nobody, WAIT_POLLS);
+  }
+  __syncwarp();
+  before_barrier();
+  __syncthreads();
+  after_barrier();
+  if (warp == MULTIPLIER) tensor_free<TENSOR_COLUMNS>(tensor);
 }
 
 constexpr int JOIN_ROWS = 32, JOIN_WARPS = 16;
 
 // A row's parts joined: a lane has a row, a warp every JOIN_WARPS-th part.
-__global__ void __launch_bounds__(JOIN_ROWS * JOIN_WARPS) k_head_join(HeadArgs a, const float4* parts, const float* logits, int tiles) {
+__global__ void __launch_bounds__(JOIN_ROWS * JOIN_WARPS) k_head_join(HeadArgs a, const float4* parts, const float* logits, int count) {
+  pdl_trigger();
   pdl_wait();
   __shared__ RowSum sums[JOIN_WARPS][JOIN_ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = int64_t(blockIdx.x) * JOIN_ROWS + lane;
-  const float temperature = row < a.rows ? (a.temperature ? a.temperature[row] : a.all_temperature) : 1.f;
+  const float temperature = row < a.rows && a.temperature ? a.temperature[row] : a.all_temperature;
   const float c = inverse_temperature(temperature);
   RowSum y{-INFINITY, 0.f, 0.f};
   if (row < a.rows)
-    for (int i = warp; i < tiles; i += JOIN_WARPS) {
+    for (int i = warp; i < count; i += JOIN_WARPS) {
       const float4 z = parts[int64_t(i) * a.rows + row];
       y = joined(y, RowSum{z.x, z.y, z.z}, c);
     }
@@ -79,25 +278,66 @@ __global__ void __launch_bounds__(JOIN_ROWS * JOIN_WARPS) k_head_join(HeadArgs a
   if (a.entropies) a.entropies[row] = live ? row_entropy(y) : 0.f;
 }
 
+// A matrix of `rows` rows as the copies see it: tiles of 64 values by `tile_rows`, zero outside.
+bool describe(CUtensorMap* map, const void* p, bool bf16, int64_t rows, int64_t width, int64_t ld, int tile_rows) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t size[2] = {cuuint64_t(width), cuuint64_t(rows)}, stride[1] = {cuuint64_t(ld) * 2};
+  const cuuint32_t box[2] = {DEPTH, cuuint32_t(tile_rows)}, step[2] = {1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), size, stride, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+Plan plan_for(const HeadArgs& a) {
+  Plan p;
+  p.row_tiles = static_cast<int>((a.rows + TILE_ROWS - 1) / TILE_ROWS);
+  p.token_tiles = static_cast<int>((a.n + TILE_TOKENS - 1) / TILE_TOKENS);
+  p.pieces = static_cast<int>((a.width + DEPTH - 1) / DEPTH);
+  // Runs of up to 4 tiles, while there are 8 runs or more for each SM.
+  const int64_t tiles = int64_t(p.row_tiles) * p.token_tiles;
+  p.run = static_cast<int>(std::clamp<int64_t>(tiles / (8 * sms()), 1, 4));
+  p.runs = p.row_tiles * ((p.token_tiles + p.run - 1) / p.run);
+  return p;
+}
+
 }  // namespace
 
 cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
+  const bool bf16 = a.type == PROFK_BF16;
+  CUtensorMap hidden, weight;
+  if (!describe(&hidden, a.hidden, bf16, a.rows, a.width, a.hidden_ld, TILE_ROWS) ||
+      !describe(&weight, a.weight, bf16, a.n, a.width, a.weight_ld, TILE_TOKENS))
+    return cudaErrorInvalidValue;
+  const Plan plan = plan_for(a);
+  const int count = (plan.token_tiles + plan.run - 1) / plan.run * PARTS;
   cudaMemPool_t pool;
   cudaError_t err = library_pool(&pool);
   if (err != cudaSuccess) return err;
-  const int tiles = static_cast<int>((a.n + TILE - 1) / TILE);
-  const size_t part_bytes = size_t(tiles) * a.rows * sizeof(float4);
+  const size_t part_bytes = size_t(count) * a.rows * sizeof(float4);
   char* work = nullptr;
-  err = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&work), part_bytes + a.rows * 4, pool, stream);
+  err = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&work), part_bytes + a.rows * sizeof(float), pool, stream);
   if (err != cudaSuccess) return err;
   float4* parts = reinterpret_cast<float4*>(work);
   float* logits = reinterpret_cast<float*>(work + part_bytes);
-  const dim3 grid(tiles, static_cast<unsigned>((a.rows + TILE - 1) / TILE));
-  err = a.type == PROFK_BF16 ? launch_kernel(k_head<__nv_bfloat16, true>, grid, dim3(THREADS), 0, stream, a, parts, logits)
-                             : launch_kernel(k_head<__half, true>, grid, dim3(THREADS), 0, stream, a, parts, logits);
+  const auto kernel = a.entropies ? k_head<true> : k_head<false>;
+  const unsigned grid = std::min(plan.runs, sms());
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SHARED_BYTES));
+  if (err == cudaSuccess)
+    err = launch_kernel(kernel, dim3(grid), dim3(THREADS), SHARED_BYTES, stream, hidden, weight, a, plan,
+                        product_descriptor(bf16, TILE_ROWS, TILE_TOKENS), parts, logits, head_wait());
   if (err == cudaSuccess)
     err = launch_kernel(k_head_join, dim3(static_cast<unsigned>((a.rows + JOIN_ROWS - 1) / JOIN_ROWS)), dim3(JOIN_ROWS * JOIN_WARPS), 0, stream,
-                        a, parts, logits, tiles);
+                        a, parts, logits, count);
   const cudaError_t freed = cudaFreeAsync(work, stream);
   return err != cudaSuccess ? err : freed;
 }

@@ -9,6 +9,8 @@ namespace profk {
 // The library's stream-ordered memory pool of the current device (api.cu).
 cudaError_t library_pool(cudaMemPool_t* out);
 int sms();  // SMs of the current device
+struct WaitCfg;
+WaitCfg head_wait();  // test setting of head.cu's waits (PROFK_OPT_HEAD_WAIT_TEST)
 
 // Choice of one token per row (tokens.cu).
 struct TokenArgs {

@@ -118,6 +118,20 @@ def test_no_rows_and_refusals(pk, cuda_device):
         assert torch.equal(pk.token_logprobs(hidden, tokens, weight=weight).logprobs, r.logprobs)
 
 
+def test_a_wait_that_runs_out(pk, cuda_device):
+    # A barrier that waits for one arrival more than comes, with a bound of 4096 polls: the kernel gives up and says so.
+    hidden, weight, tokens = inputs(300, 200, 9000, torch.bfloat16)
+    tokens[5] = -1
+    want = pk.token_logprobs(hidden, tokens, weight=weight)
+    pk.set_option(pk.OPT_HEAD_WAIT_TEST, 1)
+    got = pk.token_logprobs(hidden, tokens, weight=weight, entropy=True)
+    torch.cuda.synchronize()
+    pk.set_option(pk.OPT_HEAD_WAIT_TEST, 0)
+    live = tokens >= 0
+    assert got.logprobs[live].isnan().all() and got.entropies[live].isnan().all() and got.logprobs[5] == 0
+    assert torch.equal(pk.token_logprobs(hidden, tokens, weight=weight).logprobs, want.logprobs)
+
+
 def test_streams_graphs_and_equal_bits(pk, cuda_device):
     hidden, weight, tokens = inputs(200, 512, 5000, torch.bfloat16)
     want = pk.token_logprobs(hidden, tokens, weight=weight, entropy=True)
