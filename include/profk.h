@@ -505,7 +505,7 @@ int profk_token_logprobs_backward(const void* logits, int type, int64_t rows, in
  * their row strides are multiples of 16 bytes (else PROFK_ERR_UNSUPPORTED), width
  * itself may be odd.  1 <= width < 2^20, n < 2^30 and rows < 2^24.  The values behind a row's width
  * are not looked at.  rows * n is limited to some 2^45.  There is no gradient.  The call takes a
- * workspace from the library's pool: at most 32 bytes for each row and 256 tokens of the
+ * workspace from the library's pool: at most 32 bytes for each row and 128 tokens of the
  * vocabulary.  Its waits on the device are bounded; where one runs out, outputs are NaN. */
 int profk_head_logprobs(const void* hidden, const void* weight, int type, int64_t rows, int64_t n, int64_t width,
                         int64_t hidden_ld, int64_t weight_ld, const int64_t* tokens, const float* temperature,

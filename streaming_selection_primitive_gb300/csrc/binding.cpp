@@ -291,6 +291,26 @@ struct Temperature {
   }
 };
 
+// Several float32 outputs in one piece of memory: a small call's time is spent in making its
+// tensors, and most of that in asking for their memory (a policy loss FILL).  They are
+// tensors of their own to autograd, and the memory lives as long as any of them.
+class Floats {
+ public:
+  Floats(const Place& place, int64_t rows, int64_t arrays) : each_((rows + 3) / 4 * 4), all_(place.empty({each_ * arrays}, at::kFloat)) {}
+  // The next `arrays` of the arrays as one tensor (each begins at a multiple of 16 bytes).
+  Tensor take(at::IntArrayRef shape, int64_t arrays = 1) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all_.storage()), all_.key_set(), all_.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(at_);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    at_ += each_ * arrays;
+    return t;
+  }
+
+ private:
+  int64_t each_, at_ = 0;
+  Tensor all_;
+};
+
 const int64_t* tokens_of(PyObject* o, const Tensor& like, int64_t rows) {
   return static_cast<const int64_t*>(array(o, "tokens", at::kLong, like, {rows}));
 }
@@ -322,9 +342,10 @@ PyObject* token_logprobs(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int64_t* tokens = tokens_of(arg[1], like, x.rows);
   const Temperature T(arg[2], like, x.rows);
   const Place place(arg[4], like);
-  const Tensor logprobs = place.empty({x.rows}, at::kFloat), stats = place.empty({x.rows, 2}, at::kFloat);
+  Floats floats(place, x.rows, arg[3] == Py_True ? 4 : 3);
+  const Tensor logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2);
   Tensor entropies;
-  if (arg[3] == Py_True) entropies = place.empty({x.rows}, at::kFloat);
+  if (arg[3] == Py_True) entropies = floats.take({x.rows});
   const int code = profk_token_logprobs(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, data(logprobs),
                                         data(entropies), data(stats), place.stream());
   return code == PROFK_OK ? tuple_of({logprobs, entropies, stats}) : PyLong_FromLong(code);
@@ -411,12 +432,14 @@ PyObject* policy_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const bool entropy = arg[10] != Py_None, gradient = arg[11] == Py_True;
   if (entropy) how.entropy = static_cast<float>(number(arg[10]));
   const Place place(arg[13], like);
-  const Tensor loss = place.empty({}, at::kFloat), sums = place.empty({3}, at::kFloat), logprobs = place.empty({x.rows}, at::kFloat),
-               stats = place.empty({x.rows, 2}, at::kFloat), slopes = place.empty({x.rows}, at::kFloat);
+  // (What is kept for the record, the loss and its sums, does not hold the rows' memory.)
+  Floats few(place, 4, 2), floats(place, x.rows, 4 + entropy + (how.entropy != 0.f));
+  const Tensor loss = few.take({}), sums = few.take({3}), logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2),
+               slopes = floats.take({x.rows});
   Tensor entropies, entropy_slopes, grad;
   int64_t grad_ld = 0;
-  if (entropy) entropies = place.empty({x.rows}, at::kFloat);
-  if (how.entropy != 0.f) entropy_slopes = place.empty({x.rows}, at::kFloat);
+  if (entropy) entropies = floats.take({x.rows});
+  if (how.entropy != 0.f) entropy_slopes = floats.take({x.rows});
   if (gradient) {
     const GradientOut out(arg[12], x, place);
     grad = out.t;
@@ -446,9 +469,9 @@ PyObject* preference_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
                              static_cast<float>(number(arg[5])), static_cast<float>(number(arg[6])), arg[7] == Py_True};
   const Temperature T(arg[8], like, x.rows);
   const Place place(arg[9], like);
-  const Tensor loss = place.empty({}, at::kFloat), margins = place.empty({pairs}, at::kFloat),
-               logprobs = place.empty({x.rows}, at::kFloat), stats = place.empty({x.rows, 2}, at::kFloat),
-               slopes = place.empty({x.rows}, at::kFloat);
+  Floats few(place, std::max<int64_t>(pairs, 1), 2), floats(place, x.rows, 4);
+  const Tensor loss = few.take({}), margins = few.take({pairs}), logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2),
+               slopes = floats.take({x.rows});
   const int code = profk_preference_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all,
                                          static_cast<const int64_t*>(o.data_ptr()), pairs, &how, data(loss), data(margins),
                                          data(logprobs), data(stats), data(slopes), place.stream());

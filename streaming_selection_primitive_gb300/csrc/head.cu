@@ -2,10 +2,10 @@
 // on the tensor cores whose result, the logits, is turned into row maxima and sums tile
 // by tile and never leaves the chip.
 //
-// A tile is 128 rows of hidden states by 256 tokens of the vocabulary.  A CTA (one an SM)
+// A tile is 128 rows of hidden states by up to 256 tokens of the vocabulary.  A CTA (one an SM)
 // has a warp that copies pieces of both, 64 deep, into a ring in shared memory, a warp
 // that issues the products into one half of the tensor memory, and eight warps that
-// meanwhile take the finished tile in the other half: a thread has a row's 128 of the
+// meanwhile take the finished tile in the other half: a thread has half of a row's
 // tokens, and carries the row's running maximum and sums over a run of tiles.  The runs'
 // sums are joined by a second kernel.
 //
@@ -14,6 +14,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "../../include/profk.h"
 #include "lm.h"
@@ -24,28 +25,30 @@ namespace profk {
 namespace {
 
 constexpr int TILE_ROWS = 128;
-constexpr int TILE_TOKENS = 256;
+constexpr int TILE_TOKENS = 256;  // at most: the width is chosen for each call (plan_for)
 constexpr int DEPTH = 64;   // of a piece: 128 bytes a row, the widest swizzle
-constexpr int STAGES = 4;   // pieces in the ring
+constexpr int MAX_STAGES = 6;  // pieces in the ring
 constexpr int TAKERS = 8;   // warps that take tiles: two for each quarter of the lanes
 constexpr int COPIER = TAKERS, MULTIPLIER = TAKERS + 1;  // the other two warps
 constexpr int THREADS = 32 * (TAKERS + 2);
 constexpr int TENSOR_COLUMNS = 2 * TILE_TOKENS;  // all there are: two accumulators
-constexpr int PARTS = 2;    // a run's columns are taken by two threads a row
+constexpr int PARTS = 2;    // a row's columns are taken by two threads, 32 by 32 in turn
 
-constexpr size_t ROWS_BYTES = TILE_ROWS * DEPTH * 2, TOKENS_BYTES = TILE_TOKENS * DEPTH * 2;
-constexpr size_t STAGE_BYTES = ROWS_BYTES + TOKENS_BYTES;
-constexpr size_t SHARED_BYTES = STAGES * STAGE_BYTES + 1024;  // (the ring begins at a multiple of 1024 bytes)
+constexpr int ROWS_BYTES = TILE_ROWS * DEPTH * 2;
+constexpr int RING_BYTES = 4 * (ROWS_BYTES + TILE_TOKENS * DEPTH * 2);
+constexpr int SHARED_BYTES = RING_BYTES + 1024;  // (the ring begins at a multiple of 1024 bytes)
 
 // How the work is cut: run r is row tile r % row_tiles and the vocabulary's tiles
 // (r / row_tiles) * run and on, `run` of them, so that CTAs that work at the same time share
 // their tiles of the matrix in L2.
 struct Plan {
-  int row_tiles, token_tiles, run, runs, pieces;
+  int width;  // tokens of a tile: a multiple of 32
+  int row_tiles, token_tiles, run, runs, pieces, stages;
+  __host__ __device__ int stage_bytes() const { return ROWS_BYTES + width * DEPTH * 2; }
 };
 
 struct Barriers {
-  uint64_t full[STAGES], empty[STAGES];  // of the ring
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // of the ring
   uint64_t done[2], taken[2];            // of the accumulators
   uint32_t tensor;                       // address of the tensor memory
   int given_up;
@@ -56,38 +59,49 @@ __device__ __forceinline__ void take_columns(RowSum& r, float (&v)[32], float c)
   float m = r.m;
 #pragma unroll
   for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
-  const float d = shrink(r.m, reference(m), c), f = lm_exp2(d);
-  const Pair minus = pair(-reference(m), -reference(m)), cc = pair(c, c);
+  if (m > r.m) {
+    const float d = shrink(r.m, m, c), f = lm_exp2(d);
+    if (ENTROPY) r.t = f * (r.t + d * r.s);
+    r.s *= f;
+    r.m = m;
+  }
+  const Centre at(m, c);
   Pair s[2] = {0, 0}, t[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  const Pair by = pair(at.by, at.by), cc = pair(c, c);
+  const auto add = [&](Pair x, int i) {
     float x0, x1;
-    split(mul2(add2(pair(v[i], v[i + 1]), minus), cc), x0, x1);
+    split(x, x0, x1);
     const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
-    s[i / 2 & 1] = add2(s[i / 2 & 1], e);
-    if (ENTROPY) t[i / 2 & 1] = fma2(pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i / 2 & 1]);
+    s[i & 1] = add2(s[i & 1], e);
+    if (ENTROPY) t[i & 1] = fma2(pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i & 1]);
+  };
+  if (at.fused) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) add(fma2(pair(v[2 * i], v[2 * i + 1]), cc, by), i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) add(mul2(add2(pair(v[2 * i], v[2 * i + 1]), by), cc), i);
   }
   float a, b;
   if (ENTROPY) {
     split(add2(t[0], t[1]), a, b);
-    r.t = f * (r.t + d * r.s) + (a + b);
+    r.t += a + b;
   }
   split(add2(s[0], s[1]), a, b);
-  r.s = f * r.s + (a + b);
-  r.m = m;
+  r.s += a + b;
 }
 
 template <bool ENTROPY>
 __global__ void __launch_bounds__(THREADS, 1)
     k_head(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, HeadArgs a, Plan plan, uint32_t product,
-           float4* parts, float* logits, WaitCfg waits) {
+           float4* parts, int count, float* logits, WaitCfg waits) {
   extern __shared__ uint8_t raw[];
   __shared__ Barriers sync;
   uint8_t* ring = raw + (1024 - shared_address(raw) % 1024) % 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int limit = wait_limit(waits);
+  const int limit = wait_limit(waits), stages = plan.stages, stage_bytes = plan.stage_bytes();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < plan.stages; ++i) {
       barrier_init(&sync.full[i], 1);
       barrier_init(&sync.empty[i], 1);
     }
@@ -103,8 +117,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   after_barrier();
   const uint32_t tensor = sync.tensor;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (behind it: what follows may read what this reads)
 
   if (warp == COPIER) {
     if (lane == 0) {
@@ -118,21 +132,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int piece = 0; piece < plan.pieces; ++piece) {
             ok = barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit);
             if (!ok) break;
-            uint8_t* to = ring + stage * STAGE_BYTES;
-            barrier_arrive_expect(&sync.full[stage], STAGE_BYTES);
+            uint8_t* to = ring + stage * stage_bytes;
+            barrier_arrive_expect(&sync.full[stage], stage_bytes);
             copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[stage]);
-            copy_tile(to + ROWS_BYTES, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[stage]);
-            issued = min(issued + 1, STAGES);
-            if (++stage == STAGES) {
+            copy_tile(to + ROWS_BYTES, &weight, piece * DEPTH, tile * plan.width, &sync.full[stage]);
+            issued = min(issued + 1, stages);
+            if (++stage == stages) {
               stage = 0;
               parity ^= 1;
             }
           }
       }
       // The last products' arrivals on the ring.
-      for (int i = 0; i < STAGES && !sync.given_up; ++i) {
+      for (int i = 0; i < stages && !sync.given_up; ++i) {
         if (!barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit)) break;
-        if (++stage == STAGES) {
+        if (++stage == stages) {
           stage = 0;
           parity ^= 1;
         }
@@ -144,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int nobody = 0;
         for (int i = 0; i < issued; ++i) {
           if (stage == 0) parity ^= 1;
-          stage = stage ? stage - 1 : STAGES - 1;
+          stage = stage ? stage - 1 : stages - 1;
           nobody = 0;
           barrier_wait(&sync.full[stage], parity ^ 1, &nobody, WAIT_POLLS);
         }
@@ -166,12 +180,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = barrier_wait(&sync.full[stage], parity, &sync.given_up, limit);
             if (!ok) break;
             after_barrier();
-            const uint64_t x = tile_descriptor(ring + stage * STAGE_BYTES), w = tile_descriptor(ring + stage * STAGE_BYTES + ROWS_BYTES);
+            const uint64_t x = tile_descriptor(ring + stage * stage_bytes), w = tile_descriptor(ring + stage * stage_bytes + ROWS_BYTES);
 #pragma unroll
             for (int k = 0; k < DEPTH / 16; ++k)  // 32 bytes on along the rows: 2 in the descriptor's units
               multiply(to, x + 2 * k, w + 2 * k, product, piece + k > 0);
             products_arrive(&sync.empty[stage]);
-            if (++stage == STAGES) {
+            if (++stage == stages) {
               stage = 0;
               parity ^= 1;
             }
@@ -199,11 +213,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = __all_sync(FULL_MASK, barrier_wait(&sync.done[half], done, &sync.given_up, limit));
         if (!ok) break;
         after_barrier();
-        constexpr int EACH = TILE_TOKENS / PARTS;
-        const uint32_t from = tensor + (uint32_t(quarter * 32) << 16) + half * TILE_TOKENS + side * EACH;
-        const int64_t column0 = int64_t(tile) * TILE_TOKENS + side * EACH;
+        const uint32_t from = tensor + (uint32_t(quarter * 32) << 16) + half * TILE_TOKENS;
+        const int64_t column0 = int64_t(tile) * plan.width;
 #pragma unroll 1
-        for (int i = 0; i < EACH; i += 32) {
+        for (int i = side * 32; i < plan.width; i += 32 * PARTS) {
           float v[32];
           tensor_load(v, from + i);
           tensor_loaded();
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (half == 0) done ^= 1;
       }
       if (!ok) sum.s = NAN;
-      if (in) parts[(int64_t(index) * PARTS + side) * a.rows + row] = make_float4(sum.m, sum.s, sum.t, 0.f);
+      if (in) parts[(row * count + index) * PARTS + side] = make_float4(sum.m, sum.s, sum.t, 0.f);
     }
   }
   // The products in flight are done: what came before a taken tile is, and on giving up
@@ -250,32 +263,34 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == MULTIPLIER) tensor_free<TENSOR_COLUMNS>(tensor);
 }
 
-constexpr int JOIN_ROWS = 32, JOIN_WARPS = 16;
+constexpr int JOIN_THREADS = 128;
 
-// A row's parts joined: a lane has a row, a warp every JOIN_WARPS-th part.
-__global__ void __launch_bounds__(JOIN_ROWS * JOIN_WARPS) k_head_join(HeadArgs a, const float4* parts, const float* logits, int count) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ RowSum sums[JOIN_WARPS][JOIN_ROWS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = int64_t(blockIdx.x) * JOIN_ROWS + lane;
+// A row's parts joined, by a warp.
+__global__ void __launch_bounds__(JOIN_THREADS) k_head_join(HeadArgs a, const float4* parts, const float* logits, int count) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
+  // (The kernel before lets this one start once all before it is done: what the user gave can be read.)
+  const int64_t token = row < a.rows ? a.tokens[row] : -1;
   const float temperature = row < a.rows && a.temperature ? a.temperature[row] : a.all_temperature;
   const float c = inverse_temperature(temperature);
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.rows) return;
+  const bool live = token >= 0;
+  const float logit = live && token < a.n ? logits[row] : NAN;
   RowSum y{-INFINITY, 0.f, 0.f};
-  if (row < a.rows)
-    for (int i = warp; i < count; i += JOIN_WARPS) {
-      const float4 z = parts[int64_t(i) * a.rows + row];
+  if (live)
+#pragma unroll 4
+    for (int i = lane; i < count; i += 32) {
+      const float4 z = parts[row * count + i];
       y = joined(y, RowSum{z.x, z.y, z.z}, c);
     }
-  sums[warp][lane] = y;
-  __syncthreads();
-  if (warp != 0 || row >= a.rows) return;
-  for (int i = 1; i < JOIN_WARPS; ++i) y = joined(y, sums[i][lane], c);
+  y = centred(warp_join<true>(y, c), c);
   if (!(c > 0.f)) y.s = NAN;
-  const int64_t token = a.tokens[row];
-  const bool live = token >= 0;
-  a.logprobs[row] = live ? row_logprob(y, token < a.n ? logits[row] : NAN, temperature) : 0.f;
-  if (a.entropies) a.entropies[row] = live ? row_entropy(y) : 0.f;
+  if (lane == 0) {
+    a.logprobs[row] = live ? row_logprob(y, logit, temperature) : 0.f;
+    if (a.entropies) a.entropies[row] = live ? row_entropy(y) : 0.f;
+  }
 }
 
 // A matrix of `rows` rows as the copies see it: tiles of 64 values by `tile_rows`, zero outside.
@@ -301,8 +316,21 @@ bool describe(CUtensorMap* map, const void* p, bool bf16, int64_t rows, int64_t 
 Plan plan_for(const HeadArgs& a) {
   Plan p;
   p.row_tiles = static_cast<int>((a.rows + TILE_ROWS - 1) / TILE_ROWS);
-  p.token_tiles = static_cast<int>((a.n + TILE_TOKENS - 1) / TILE_TOKENS);
   p.pieces = static_cast<int>((a.width + DEPTH - 1) / DEPTH);
+  // The width that leaves the SMs least idle: rounds of one tile an SM times the width (a narrow tile
+  // reads the hidden states more often, so it has to gain a sixteenth).
+  p.width = 0;
+  int64_t best = 0;
+  for (int width = TILE_TOKENS; width >= 128; width -= 32) {
+    const int64_t tiles = p.row_tiles * ((a.n + width - 1) / width), cost = (tiles + sms() - 1) / sms() * width;
+    if (!p.width || cost * 16 < best * 15) {
+      p.width = width;
+      best = cost;
+    }
+  }
+  if (getenv("HW")) p.width = atoi(getenv("HW"));
+  p.token_tiles = static_cast<int>((a.n + p.width - 1) / p.width);
+  p.stages = std::min(MAX_STAGES, RING_BYTES / p.stage_bytes());
   // Runs of up to 4 tiles, while there are 8 runs or more for each SM.
   const int64_t tiles = int64_t(p.row_tiles) * p.token_tiles;
   p.run = static_cast<int>(std::clamp<int64_t>(tiles / (8 * sms()), 1, 4));
@@ -314,12 +342,12 @@ Plan plan_for(const HeadArgs& a) {
 
 cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
   const bool bf16 = a.type == PROFK_BF16;
+  const Plan plan = plan_for(a);
   CUtensorMap hidden, weight;
   if (!describe(&hidden, a.hidden, bf16, a.rows, a.width, a.hidden_ld, TILE_ROWS) ||
-      !describe(&weight, a.weight, bf16, a.n, a.width, a.weight_ld, TILE_TOKENS))
+      !describe(&weight, a.weight, bf16, a.n, a.width, a.weight_ld, plan.width))
     return cudaErrorInvalidValue;
-  const Plan plan = plan_for(a);
-  const int count = (plan.token_tiles + plan.run - 1) / plan.run * PARTS;
+  const int runs = (plan.token_tiles + plan.run - 1) / plan.run, count = runs * PARTS;
   cudaMemPool_t pool;
   cudaError_t err = library_pool(&pool);
   if (err != cudaSuccess) return err;
@@ -331,12 +359,12 @@ cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
   float* logits = reinterpret_cast<float*>(work + part_bytes);
   const auto kernel = a.entropies ? k_head<true> : k_head<false>;
   const unsigned grid = std::min(plan.runs, sms());
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SHARED_BYTES));
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED_BYTES);
   if (err == cudaSuccess)
-    err = launch_kernel(kernel, dim3(grid), dim3(THREADS), SHARED_BYTES, stream, hidden, weight, a, plan,
-                        product_descriptor(bf16, TILE_ROWS, TILE_TOKENS), parts, logits, head_wait());
+    err = launch_kernel(kernel, dim3(grid), dim3(THREADS), size_t(SHARED_BYTES), stream, hidden, weight, a, plan,
+                        product_descriptor(bf16, TILE_ROWS, plan.width), parts, runs, logits, head_wait());
   if (err == cudaSuccess)
-    err = launch_kernel(k_head_join, dim3(static_cast<unsigned>((a.rows + JOIN_ROWS - 1) / JOIN_ROWS)), dim3(JOIN_ROWS * JOIN_WARPS), 0, stream,
+    err = launch_kernel(k_head_join, dim3(static_cast<unsigned>((a.rows + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32))), dim3(JOIN_THREADS), 0, stream,
                         a, parts, logits, count);
   const cudaError_t freed = cudaFreeAsync(work, stream);
   return err != cudaSuccess ? err : freed;

@@ -52,6 +52,9 @@ __device__ __forceinline__ float lm_rcp(float x) {
   return y;
 }
 
+// The line of p to L2.
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
@@ -64,13 +67,14 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Launches a kernel whose CTAs form clusters of `cluster`, with any amount of
-// dynamic shared memory, as launch_kernel does.
+// Launches a kernel whose CTAs form clusters of `cluster`, as launch_kernel does, with `smem`
+// bytes of dynamic shared memory, `most` being what any call of it asks for.  (The
+// limit is the kernel's, for all host threads: it is set to the same number whatever the call.)
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, size_t smem,
-                                   cudaStream_t stream, Args... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+inline cudaError_t launch_clusters_most(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, size_t smem,
+                                        size_t most, cudaStream_t stream, Args... args) {
+  if (most > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }
   ++launch_count();
@@ -88,6 +92,12 @@ inline cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int t
   cfg.attrs = at;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, size_t smem,
+                                   cudaStream_t stream, Args... args) {
+  return launch_clusters_most(kernel, grid, threads, cluster, smem, smem, stream, args...);
 }
 
 }  // namespace profk

@@ -10,21 +10,25 @@
 // A row is taken by a cluster of CTAs (k_logprobs) or, where it is short, by a warp
 // (k_logprobs_short): one pass with a running maximum and sums, one exchange.  For a
 // policy loss with its gradient the same CTAs then go over their part again.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "../../include/profk.h"
 #include "lm.h"
 #include "logprobs.cuh"
+#include "tcgen05.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace profk {
 namespace {
 
-constexpr int THREADS = 512;    // of a CTA that takes a row or a part of one
+constexpr int THREADS = 256;    // of a CTA that takes a row or a part of one
 constexpr int WARPS = THREADS / 32;
 constexpr int SHORT_THREADS = 256;  // of a CTA whose warps take a row each
 constexpr int LOADS = 4;        // 16-byte loads of a thread before it looks at what came
+constexpr int KEEP_LOADS = 4;   // the same from shared memory
 constexpr int MAX_CLUSTER = 8;
 
 // ---------------------------------------------------------------------------
@@ -54,19 +58,20 @@ __device__ __forceinline__ Pair element_pair<__half>(const uint4& v, int i) {
 }
 
 // The largest of all elements (NaN is passed over).
-__device__ __forceinline__ float largest(const uint4 (&v)[LOADS], float) {
+template <int COUNT>
+__device__ __forceinline__ float largest(const uint4 (&v)[COUNT], float) {
   float m = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < LOADS; ++u)
+  for (int u = 0; u < COUNT; ++u)
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = fmaxf(m, __uint_as_float(word(v[u], i)));
   return m;
 }
-template <typename H2, typename T>
-__device__ __forceinline__ float largest_half(const uint4 (&v)[LOADS]) {
+template <typename H2, int COUNT>
+__device__ __forceinline__ float largest_half(const uint4 (&v)[COUNT]) {
   H2 m;
 #pragma unroll
-  for (int u = 0; u < LOADS; ++u)
+  for (int u = 0; u < COUNT; ++u)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = word(v[u], i);
@@ -75,10 +80,14 @@ __device__ __forceinline__ float largest_half(const uint4 (&v)[LOADS]) {
     }
   return fmaxf(lm_float(m.x), lm_float(m.y));
 }
-__device__ __forceinline__ float largest(const uint4 (&v)[LOADS], __nv_bfloat16) {
-  return largest_half<__nv_bfloat162, __nv_bfloat16>(v);
+template <int COUNT>
+__device__ __forceinline__ float largest(const uint4 (&v)[COUNT], __nv_bfloat16) {
+  return largest_half<__nv_bfloat162>(v);
 }
-__device__ __forceinline__ float largest(const uint4 (&v)[LOADS], __half) { return largest_half<__half2, __half>(v); }
+template <int COUNT>
+__device__ __forceinline__ float largest(const uint4 (&v)[COUNT], __half) {
+  return largest_half<__half2>(v);
+}
 
 template <typename T>
 __device__ __forceinline__ uint4 nothing();  // elements of -inf
@@ -125,47 +134,68 @@ __device__ __forceinline__ int part_begin(int vectors, int rank, int parts) {
   return static_cast<int>(static_cast<int64_t>(vectors) * rank / parts);
 }
 
-// One chunk of elements joins what has been seen.
-template <typename T, bool ENTROPY>
-__device__ __forceinline__ void take(Running& r, const uint4 (&v)[LOADS], float c) {
+// One chunk of elements joins what has been seen.  LONG: what additions lose is kept.
+template <typename T, bool ENTROPY, bool LONG, int COUNT>
+__device__ __forceinline__ void take(Running& r, const uint4 (&v)[COUNT], float c) {
   const float m = fmaxf(r.m, largest(v, T{}));
-  const float d = shrink(r.m, reference(m), c), f = lm_exp2(d);
-  const Pair minus = pair(-reference(m), -reference(m)), cc = pair(c, c);
-  Pair s[2] = {0, 0}, t[2] = {0, 0};
-#pragma unroll
-  for (int u = 0; u < LOADS; ++u)
-#pragma unroll
-    for (int i = 0; i < PER_VECTOR<T> / 2; ++i) {
-      float x0, x1;
-      split(mul2(add2(element_pair<T>(v[u], i), minus), cc), x0, x1);
-      const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
-      s[i & 1] = add2(s[i & 1], e);
-      if (ENTROPY) t[i & 1] = fma2(pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i & 1]);
+  if (m > r.m) {
+    const float d = shrink(r.m, m, c), f = lm_exp2(d);
+    if (ENTROPY) {
+      r.t = f * (r.t + d * r.s);
+      if (LONG) r.t_lost = f * (r.t_lost + d * r.s_lost);
     }
+    r.s *= f;
+    if (LONG) r.s_lost *= f;
+    r.m = m;
+  }
+  const Centre at(m, c);
+  Pair s[2] = {0, 0}, t[2] = {0, 0};
+  const auto add = [&](Pair x, int i) {
+    float x0, x1;
+    split(x, x0, x1);
+    const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
+    s[i & 1] = add2(s[i & 1], e);
+    if (ENTROPY) t[i & 1] = fma2(pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i & 1]);
+  };
+  const Pair by = pair(at.by, at.by), cc = pair(c, c);
+  if (at.fused) {
+#pragma unroll
+    for (int u = 0; u < COUNT; ++u)
+#pragma unroll
+      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(fma2(element_pair<T>(v[u], i), cc, by), i);
+  } else {
+#pragma unroll
+    for (int u = 0; u < COUNT; ++u)
+#pragma unroll
+      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(mul2(add2(element_pair<T>(v[u], i), by), cc), i);
+  }
   float a, b;
   if (ENTROPY) {
     split(add2(t[0], t[1]), a, b);
-    r.t = f * (r.t + d * r.s);
-    r.t_lost = f * (r.t_lost + d * r.s_lost);
-    add_exact(r.t, r.t_lost, a + b);
+    if (LONG)
+      add_exact(r.t, r.t_lost, a + b);
+    else
+      r.t += a + b;
   }
   split(add2(s[0], s[1]), a, b);
-  r.s *= f;
-  r.s_lost *= f;
-  add_exact(r.s, r.s_lost, a + b);
-  r.m = m;
+  if (LONG)
+    add_exact(r.s, r.s_lost, a + b);
+  else
+    r.s += a + b;
 }
 
-// The pass over vectors [begin, end) and this thread's single element by `STEP` threads.
+// A single element (-inf: none).
+__device__ __forceinline__ Running seen(float l, float c) {
+  if (l == -INFINITY) return {-INFINITY, 0.f, 0.f, 0.f, 0.f};
+  const float x = Centre(l, c).off(), e = lm_exp2(x) + (l - l);  // (NaN of NaN and +inf)
+  return {fmaxf(l, -INFINITY), e, x * e, 0.f, 0.f};
+}
+
+// The pass over vectors [begin, end) of `body` by STEP threads, and this thread's single element
+// (-inf: it has none).
 template <typename T, bool ENTROPY, int STEP>
-__device__ __forceinline__ Running pass(const T* p, const Layout<T>& at, int begin, int end, int thread, int single, float c) {
-  const uint4* body = reinterpret_cast<const uint4*>(p + at.head);
-  Running r{-INFINITY, 0.f, 0.f, 0.f, 0.f};
-  if (single >= 0) {
-    const float v = lm_float(p[single]);
-    r.m = fmaxf(v, -INFINITY);
-    r.s = v == -INFINITY ? 0.f : v - v + 1.f;
-  }
+__device__ __forceinline__ Running pass(const uint4* body, int begin, int end, int thread, float single, float c) {
+  Running r = seen(single, c);
   uint4 v[LOADS], next[LOADS];
   const auto load = [&](uint4(&w)[LOADS], int i) {
 #pragma unroll
@@ -181,82 +211,144 @@ __device__ __forceinline__ Running pass(const T* p, const Layout<T>& at, int beg
     for (int u = 0; u < LOADS; ++u) v[u] = next[u];
     i += LOADS * STEP;
     if (i < end) load(next, i);
-    take<T, ENTROPY>(r, v, c);
+    take<T, ENTROPY, true>(r, v, c);
   }
   return r;
 }
 
-// What a row's gradient is made of: element i gets e (k0 + k1 x) with x = (l - m) c and
+// The same over all of `count` vectors in shared memory, whose loads need no prefetch and which
+// are few enough for sums in one float: KEEP_SHARED bytes are 7 additions a thread of four vectors' sums.
+template <typename T, bool ENTROPY, int STEP>
+__device__ __forceinline__ Running pass_shared(const uint4* body, int count, int thread, float single, float c) {
+  Running r = seen(single, c);
+  for (int i = thread; i < count; i += KEEP_LOADS * STEP) {
+    uint4 v[KEEP_LOADS];
+#pragma unroll
+    for (int u = 0; u < KEEP_LOADS; ++u) v[u] = i + u * STEP < count ? body[i + u * STEP] : nothing<T>();
+    take<T, ENTROPY, false>(r, v, c);
+  }
+  return r;
+}
+
+// What a row's gradient is made of: element i gets e (k0 + k1 x) with x by the row's centre and
 // e = 2^x, and the token's element `one` besides.
 struct Slopes {
-  float m, c, k0, k1, one;
+  Centre at;
+  float k0, k1, one;
 };
 
-// g and h: the derivatives of the result by the row's log-probability and its entropy.
+// g and h: the derivatives of the result by the row's log-probability and its entropy; mean_x =
+// t / s.
 template <bool ENTROPY>
 __device__ __forceinline__ Slopes slopes_of(float m, float s, float mean_x, float temperature, float c, float g, float h) {
   const float per_T = 1.f / temperature;
-  Slopes y{reference(m), c, 0.f, 0.f, g * per_T};
+  Slopes y{Centre(m, c), 0.f, 0.f, g * per_T};
   if (s == 0.f) {  // nothing to put on any token
     y.one = 0.f;
     return y;
   }
-  const float scale = per_T / s;
-  y.k0 = -(ENTROPY ? g - h * LN2 * mean_x : g) * scale;
+  const float r = y.at.off(), scale = per_T / (s * lm_exp2(r));
+  y.k0 = -(ENTROPY ? g - h * LN2 * (mean_x + r) : g) * scale;
   if (ENTROPY) y.k1 = -h * LN2 * scale;
   return y;
 }
 
 template <bool ENTROPY>
 __device__ __forceinline__ float slope_at(const Slopes& k, float l) {
-  const float x = (l - k.m) * k.c, e = lm_exp2(x);
+  const float x = k.at(l), e = lm_exp2(x);
   return e * (ENTROPY ? fmaf(k.k1, fmaxf(x, NO_MASS), k.k0) : k.k0);
 }
 
-// The gradient of vectors [begin, end) and of this thread's single element, by STEP threads.
-// `same`: logits and gradient stand alike to the 16-byte boundaries.
-template <typename T, bool ENTROPY, int STEP>
-__device__ __forceinline__ void write_gradient(const T* p, T* out, const Layout<T>& at, int begin, int end, int thread,
-                                               int single, int token, const Slopes& k, bool same) {
-  if (single >= 0) out[single] = lm_cast<T>(slope_at<ENTROPY>(k, lm_float(p[single])) + (single == token ? k.one : 0.f));
-  constexpr int N = PER_VECTOR<T>;
-  const uint4* body = reinterpret_cast<const uint4*>(p + at.head);
-  T* to = out + at.head;
-  const Pair minus = pair(-k.m, -k.m), cc = pair(k.c, k.c), k0 = pair(k.k0, k.k0), k1 = pair(k.k1, k.k1);
-  const int token_vector = token >= at.head ? (token - at.head) / N : -1;
-  for (int i = begin; i < end; i += LOADS * STEP) {
-    uint4 v[LOADS];
+// 16 bytes that begin `shift` bytes into the first of two vectors.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int shift) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (shift & 8)
 #pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int j = i + u * STEP + thread;
-      if (j < end) v[u] = body[j];
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (shift & 4)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  const int bits = (shift & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+
+// The gradient of `count` elements from `p` (in global or in shared memory) to `out`, by STEP
+// threads; `token` is the token's place among them, out of range where it is none.  Where p and
+// out stand differently to the 16-byte boundaries, 16 bytes of the gradient come from two
+// vectors of p.  (p may be out: an element is read by the thread that writes it.)
+template <typename T, bool ENTROPY, int STEP, int COUNT = LOADS>
+__device__ __forceinline__ void write_gradient(const T* p, T* out, int count, int thread, int token, const Slopes& k) {
+  constexpr int N = PER_VECTOR<T>, SIZE = sizeof(T);
+  int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / SIZE, count);
+  int vectors = (count - head) / N;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p + head) & 15);
+  if (shift) {  // (nothing outside the elements is read: the first or last vector may be left to single threads)
+    if (vectors > 0 && shift > head * SIZE) {
+      head += N;
+      --vectors;
+    }
+    if (vectors > 0 && head * SIZE - shift + (vectors + 1) * 16 > count * SIZE) --vectors;
+  }
+  const int tail = count - head - vectors * N;
+  const int single = thread < head ? thread : thread >= 16 && thread < 16 + tail ? head + vectors * N + thread - 16 : -1;
+  if (single >= 0) out[single] = lm_cast<T>(slope_at<ENTROPY>(k, lm_float(p[single])) + (single == token ? k.one : 0.f));
+  const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p + head) - shift);
+  uint4* to = reinterpret_cast<uint4*>(out + head);
+  // The token's element is written once more by the thread that has its vector.
+  const int place = token - head;
+  const bool has_token = place >= 0 && place < vectors * N && (place / N) % STEP == thread;
+  const float token_slope = has_token ? slope_at<ENTROPY>(k, lm_float(p[token])) + k.one : 0.f;
+  const Pair by = pair(k.at.by, k.at.by), cc = pair(k.at.c, k.at.c), k0 = pair(k.k0, k.k0), k1 = pair(k.k1, k.k1);
+  for (int i = thread; i < vectors; i += COUNT * STEP) {
+    uint4 v[COUNT];
+    if (shift) {
+#pragma unroll
+      for (int u = 0; u < COUNT; ++u)
+        if (i + u * STEP < vectors) v[u] = shifted(from[i + u * STEP], from[i + u * STEP + 1], shift);
+    } else {
+#pragma unroll
+      for (int u = 0; u < COUNT; ++u)
+        if (i + u * STEP < vectors) v[u] = from[i + u * STEP];
     }
 #pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int j = i + u * STEP + thread;
-      if (j >= end) break;
+    for (int u = 0; u < COUNT; ++u) {
+      const int j = i + u * STEP;
+      if (j >= vectors) break;
       alignas(16) T y[N];
-#pragma unroll
-      for (int q = 0; q < N / 2; ++q) {
+      const auto put = [&](Pair x, int q) {
         float x0, x1, y0, y1;
-        split(mul2(add2(element_pair<T>(v[u], q), minus), cc), x0, x1);
+        split(x, x0, x1);
         const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
         split(mul2(e, ENTROPY ? fma2(k1, pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), k0) : k0), y0, y1);
-        if (j == token_vector) {
-          const int q_token = token - at.head - j * N - 2 * q;
-          if (q_token == 0) y0 += k.one;
-          if (q_token == 1) y1 += k.one;
-        }
         put_pair(y + 2 * q, y0, y1);
-      }
-      if (same) {
-        reinterpret_cast<uint4*>(to)[j] = *reinterpret_cast<const uint4*>(y);
+      };
+      if (k.at.fused) {
+#pragma unroll
+        for (int q = 0; q < N / 2; ++q) put(fma2(element_pair<T>(v[u], q), cc, by), q);
       } else {
 #pragma unroll
-        for (int q = 0; q < N; ++q) to[j * N + q] = y[q];
+        for (int q = 0; q < N / 2; ++q) put(mul2(add2(element_pair<T>(v[u], q), by), cc), q);
       }
+      to[j] = *reinterpret_cast<const uint4*>(y);
     }
   }
+  if (has_token) out[token] = lm_cast<T>(token_slope);
+}
+
+// A part's elements: its vectors, and the row's first and last ones where it is the first or last part.
+template <typename T>
+struct Span {
+  int first, count;
+  __device__ __forceinline__ Span(const Layout<T>& at, int begin, int end, bool is_first, bool is_last) {
+    first = is_first ? 0 : at.head + begin * PER_VECTOR<T>;
+    count = at.head + end * PER_VECTOR<T> + (is_last ? at.tail : 0) - first;
+  }
+};
+
+// The place of a row's token in a span, -1 where the row has none.
+__device__ __forceinline__ int place_in(int64_t token, int64_t n, int first) {
+  return token < n ? static_cast<int>(token) - first : -1;
 }
 
 template <typename T, int STEP>
@@ -277,15 +369,20 @@ struct Row {
   bool live;
 };
 
+__device__ __forceinline__ bool row_live(const LogprobArgs& a, int64_t row) {
+  bool live = a.tokens[row] >= 0;
+  if (a.weights && a.weights[row] == 0.f) live = false;
+  if (a.offsets && (row < a.offsets[0] || row >= a.offsets[a.sequences])) live = false;
+  return live;
+}
+
 template <typename T, bool GRADIENT>
 __device__ __forceinline__ Row<GRADIENT> load_row(const LogprobArgs& a, const PolicyHow& how, int64_t row) {
   Row<GRADIENT> r;
   r.token = a.tokens[row];
   r.temperature = a.temperature ? a.temperature[row] : a.all_temperature;
   r.c = inverse_temperature(r.temperature);
-  r.live = r.token >= 0;
-  if (a.weights && a.weights[row] == 0.f) r.live = false;
-  if (a.offsets && (row < a.offsets[0] || row >= a.offsets[a.sequences])) r.live = false;
+  r.live = row_live(a, row);
   // A token that the vocabulary has not is no number.
   r.logit = NAN;
   if (r.live && r.token < a.n) r.logit = lm_float(static_cast<const T*>(a.logits)[row * a.ld + r.token]);
@@ -324,15 +421,47 @@ __device__ __forceinline__ Slopes policy_slopes(const Row<GRADIENT>& r, const Ro
 
 // ---------------------------------------------------------------------------
 // A row by a cluster of CTAs.
+
+// The exchange of the warps' sums within a cluster: each CTA has room for those of all, written
+// there by stores that count on its barrier.  (No fence over what threads have written
+// before, as a barrier of the cluster would be.)
+template <int COUNT>  // warps of a CTA
+struct Exchange {
+  RowSum sums[MAX_CLUSTER * COUNT];
+  uint64_t all;
+  int given_up;
+
+  // By one thread, before the cluster's first barrier.
+  __device__ __forceinline__ void begin(int parts) {
+    barrier_init(&all, 1);
+    given_up = 0;
+    barrier_init_done();
+    barrier_arrive_expect(&all, parts * COUNT * sizeof(RowSum));
+  }
+  // By all threads, once every CTA of the cluster has begun: the row's sums, the same in
+  // every warp; by m itself.
+  template <bool ENTROPY>
+  __device__ __forceinline__ RowSum join(RowSum y, float c, int parts, int rank) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane < parts) store_remote(&sums[rank * COUNT + warp], make_float4(y.m, y.s, y.t, 0.f), &all, lane);
+    if (!__all_sync(FULL_MASK, barrier_wait(&all, 0, &given_up, WAIT_POLLS))) return {0.f, NAN, NAN};
+    y = {-INFINITY, 0.f, 0.f};
+    for (int i = lane; i < parts * COUNT; i += 32) y = joined(y, sums[i], c);
+    y = centred(warp_join<ENTROPY>(y, c), c);
+    if (!(c > 0.f)) y.s = NAN;
+    return y;
+  }
+};
+
 template <typename T, bool ENTROPY, bool GRADIENT>
-__global__ void __launch_bounds__(THREADS, 2) k_logprobs(LogprobArgs a, PolicyHow how) {
-  pdl_trigger();
+__global__ void __launch_bounds__(THREADS, 4) k_logprobs(LogprobArgs a, PolicyHow how) {
   pdl_wait();
-  __shared__ RowSum sums[MAX_CLUSTER * WARPS];
+  pdl_trigger();  // (behind it: what follows may read what this reads)
+  __shared__ Exchange<WARPS> exchange;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int64_t row = blockIdx.x / parts;
-  const int thread = threadIdx.x, lane = thread & 31, warp = thread >> 5, n = static_cast<int>(a.n);
+  const int thread = threadIdx.x, n = static_cast<int>(a.n);
   const T* p = static_cast<const T*>(a.logits) + row * a.ld;
   T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
   const Row<GRADIENT> r = load_row<T, GRADIENT>(a, how, row);
@@ -345,38 +474,29 @@ __global__ void __launch_bounds__(THREADS, 2) k_logprobs(LogprobArgs a, PolicyHo
     }
     return;
   }
-  if (parts > 1) cluster.barrier_arrive();  // (a CTA's shared memory is written once it runs)
+  if (thread == 0) exchange.begin(parts);
+  __syncthreads();
+  cluster_begin();
   const Layout<T> at(p, n);
   const int begin = part_begin(at.vectors, rank, parts), end = part_begin(at.vectors, rank + 1, parts);
   const int single = at.single(thread, rank == 0, rank == parts - 1);
-  RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, THREADS>(p, at, begin, end, thread, single, r.c)), r.c);
-  if (parts > 1) {
-    cluster.barrier_wait();
-    if (lane < parts) cluster.map_shared_rank(sums, lane)[rank * WARPS + warp] = y;
-    cluster.sync();
-  } else {
-    if (lane == 0) sums[warp] = y;
-    __syncthreads();
-  }
-  // Every warp joins all parts, in the same order.
-  y = {-INFINITY, 0.f, 0.f};
-  for (int i = lane; i < parts * WARPS; i += 32) y = joined(y, sums[i], r.c);
-  y = warp_join<ENTROPY>(y, r.c);
-  if (!(r.c > 0.f)) y.s = NAN;
+  const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
+  RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, THREADS>(reinterpret_cast<const uint4*>(p + at.head), begin, end, thread, alone, r.c)), r.c);
+  cluster_begun();
+  y = exchange.template join<ENTROPY>(y, r.c, parts, rank);
   const float lp = store_row(a, row, y, r.logit, r.temperature, rank == 0 && thread == 0);
   if (GRADIENT) {
     const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
-    const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    write_gradient<T, ENTROPY, THREADS>(p, out, at, begin, end, thread, single,
-                                        static_cast<int>(r.token < a.n ? r.token : -1), k, same);
+    const Span<T> mine(at, begin, end, rank == 0, rank == parts - 1);
+    write_gradient<T, ENTROPY, THREADS>(p + mine.first, out + mine.first, mine.count, thread, place_in(r.token, a.n, mine.first), k);
   }
 }
 
 // A row by a warp.
 template <typename T, bool ENTROPY, bool GRADIENT>
 __global__ void __launch_bounds__(SHORT_THREADS) k_logprobs_short(LogprobArgs a, PolicyHow how) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (behind it: what follows may read what this reads)
   const int lane = threadIdx.x & 31, n = static_cast<int>(a.n);
   const int64_t row = int64_t(blockIdx.x) * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
   if (row >= a.rows) return;
@@ -393,13 +513,77 @@ __global__ void __launch_bounds__(SHORT_THREADS) k_logprobs_short(LogprobArgs a,
   }
   const Layout<T> at(p, n);
   const int single = at.single(lane, true, true);
-  RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, 32>(p, at, 0, at.vectors, lane, single, r.c)), r.c);
+  const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
+  RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, 32>(reinterpret_cast<const uint4*>(p + at.head), 0, at.vectors, lane, alone, r.c)), r.c);
+  y = centred(y, r.c);
   if (!(r.c > 0.f)) y.s = NAN;
   const float lp = store_row(a, row, y, r.logit, r.temperature, lane == 0);
   if (GRADIENT) {
     const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
-    const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    write_gradient<T, ENTROPY, 32>(p, out, at, 0, at.vectors, lane, single, static_cast<int>(r.token < a.n ? r.token : -1), k, same);
+    write_gradient<T, ENTROPY, 32>(p, out, n, lane, place_in(r.token, a.n, 0), k);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The policy loss with its gradient, a row by a cluster whose CTAs keep their parts of it in
+// shared memory: the row is read from memory once, and its sums and its gradient are both
+// made from the copy.  Many such CTAs share an SM, so that some copy while others work.
+constexpr int KEEP_THREADS = 256;
+constexpr int KEEP_WARPS = KEEP_THREADS / 32;
+constexpr int KEEP_SHARED = 112 * 1024;  // dynamic shared memory at most
+
+template <typename T, bool ENTROPY>
+__global__ void __launch_bounds__(KEEP_THREADS, 4) k_policy_keep(LogprobArgs a, PolicyHow how) {
+  extern __shared__ __align__(128) uint8_t room[];
+  __shared__ Exchange<KEEP_WARPS> exchange;
+  __shared__ uint64_t full;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int thread = threadIdx.x, n = static_cast<int>(a.n);
+  const int64_t row = blockIdx.x / parts;
+  pdl_wait();
+  pdl_trigger();  // (behind it: what follows may read what this reads)
+  const T* p = static_cast<const T*>(a.logits) + row * a.ld;
+  T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
+  if (!row_live(a, row)) {  // the same for the whole cluster: none of it waits
+    if (rank == 0 && thread == 0) store_left_out(a, row);
+    const Layout<T> to(out, n);
+    write_zeros<T, KEEP_THREADS>(out, to, part_begin(to.vectors, rank, parts), part_begin(to.vectors, rank + 1, parts), thread,
+                                 to.single(thread, rank == 0, rank == parts - 1));
+    return;
+  }
+  const Layout<T> at(p, n);
+  const int begin = part_begin(at.vectors, rank, parts), end = part_begin(at.vectors, rank + 1, parts);
+  if (thread == 0) {
+    barrier_init(&full, 1);
+    exchange.begin(parts);
+    if (end > begin) {
+      barrier_arrive_expect(&full, unsigned(end - begin) * 16);
+      copy_bytes(room + 16, p + at.head + begin * PER_VECTOR<T>, unsigned(end - begin) * 16, &full);
+    } else {
+      barrier_arrive(&full);
+    }
+  }
+  __syncthreads();
+  cluster_begin();
+  const Row<true> r = load_row<T, true>(a, how, row);
+  const Span<T> mine(at, begin, end, rank == 0, rank == parts - 1);
+  T* copy = reinterpret_cast<T*>(room + 16) - (rank == 0 ? at.head : 0);  // the span's first element
+  const int single = at.single(thread, rank == 0, rank == parts - 1);
+  const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
+  if (single >= 0) copy[single - mine.first] = p[single];
+  cluster_begun();  // (the barriers are there, in all CTAs)
+  const bool there = barrier_wait(&full, 0, &exchange.given_up, WAIT_POLLS);
+  RowSum y = warp_join<ENTROPY>(
+      total(pass_shared<T, ENTROPY, KEEP_THREADS>(reinterpret_cast<const uint4*>(room + 16), end - begin, thread, alone, r.c)), r.c);
+  if (!__all_sync(FULL_MASK, there)) y.s = NAN;
+  y = exchange.template join<ENTROPY>(y, r.c, parts, rank);
+  const float lp = store_row(a, row, y, r.logit, r.temperature, rank == 0 && thread == 0);
+  const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
+  write_gradient<T, ENTROPY, KEEP_THREADS, KEEP_LOADS>(copy, out + mine.first, mine.count, thread, place_in(r.token, a.n, mine.first), k);
+  if (thread == 0 && exchange.given_up) {  // a copy that was not waited for must not outlive the CTA
+    int nobody = 0;
+    barrier_wait(&full, 0, &nobody, WAIT_POLLS);
   }
 }
 
@@ -429,16 +613,15 @@ __device__ __forceinline__ void backward_row(const LogprobBackwardArgs& a, int64
   const float2 stats = a.stats[row];
   const float mean_x = ENTROPY ? (logf(stats.y) - a.entropies[row]) * LOG2E : 0.f;
   const Slopes k = slopes_of<ENTROPY>(stats.x, stats.y, mean_x, temperature, c, g, h);
-  const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-  write_gradient<T, ENTROPY, STEP>(p, out, at, part_begin(at.vectors, rank, parts), part_begin(at.vectors, rank + 1, parts), thread,
-                                   at.single(thread, rank == 0, rank == parts - 1), static_cast<int>(token < n ? token : -1), k, same);
+  const Span<T> mine(at, part_begin(at.vectors, rank, parts), part_begin(at.vectors, rank + 1, parts), rank == 0, rank == parts - 1);
+  write_gradient<T, ENTROPY, STEP>(p + mine.first, out + mine.first, mine.count, thread, place_in(token, n, mine.first), k);
 }
 
 template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(THREADS, 2) k_logprobs_backward(LogprobBackwardArgs a, int parts) {
+__global__ void __launch_bounds__(THREADS, 4) k_logprobs_backward(LogprobBackwardArgs a, int parts) {
   pdl_trigger();
   pdl_wait();
-  backward_row<T, ENTROPY, THREADS>(a, blockIdx.x / parts, static_cast<int>(blockIdx.x % parts), parts, threadIdx.x);
+  backward_row<T, ENTROPY, THREADS>(a, a.rows - 1 - blockIdx.x / parts, static_cast<int>(blockIdx.x % parts), parts, threadIdx.x);
 }
 
 template <typename T, bool ENTROPY>
@@ -450,131 +633,197 @@ __global__ void __launch_bounds__(SHORT_THREADS) k_logprobs_backward_short(Logpr
 }
 
 // ---------------------------------------------------------------------------
-// The sums over rows.  Doubles, in a fixed order: the same call gives the same bits.
+// The sums over rows: floats with their losses carried along (double precision takes
+// several times as long here), in a fixed order: the same call gives the same bits.
+//
+// These kernels follow the one that writes the log-probabilities, which lets them start
+// once it has begun itself, that is once all before it is done: what the user gave can be read
+// before pdl_wait, only what that kernel writes comes after it.
 
 constexpr int JOIN_THREADS = 512;
+constexpr int JOIN_WARPS = JOIN_THREADS / 32;
 constexpr int JOIN_CLUSTER = 8;
 
-__device__ __forceinline__ double warp_sum(double v) {
+struct Sum {
+  float v = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float x) { add_exact(v, lost, x); }
+  __device__ __forceinline__ void add(const Sum& x) {
+    add_exact(v, lost, x.v);
+    lost += x.lost;
+  }
+  // Of an infinite or NaN sum the losses are NaN, and do not count.
+  __device__ __forceinline__ float value() const { return fabsf(v) < INFINITY ? v + lost : v; }
+};
+
+__device__ __forceinline__ Sum warp_sum(Sum x) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
-  return v;
+  for (int d = 16; d; d >>= 1) {
+    Sum y;
+    y.v = __shfl_xor_sync(FULL_MASK, x.v, d);
+    y.lost = __shfl_xor_sync(FULL_MASK, x.lost, d);
+    x.add(y);
+  }
+  return x;
 }
 
 // Sums over the cluster of COUNT values a thread, to thread 0 of CTA 0.  All threads call it.
 template <int COUNT>
-__device__ __forceinline__ void cluster_sum(double (&v)[COUNT]) {
-  __shared__ double part[COUNT][JOIN_CLUSTER * (JOIN_THREADS / 32)];
+__device__ __forceinline__ void cluster_sum(Sum (&x)[COUNT]) {
+  __shared__ Sum part[COUNT][JOIN_CLUSTER * JOIN_WARPS];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), parts = static_cast<int>(cluster.num_blocks());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  cluster.sync();  // (a CTA's shared memory is written once it runs)
+  if (parts > 1) cluster.sync();  // (a CTA's shared memory is written once it runs)
 #pragma unroll
   for (int i = 0; i < COUNT; ++i) {
-    v[i] = warp_sum(v[i]);
-    if (lane == 0) cluster.map_shared_rank(&part[i][0], 0)[rank * (JOIN_THREADS / 32) + warp] = v[i];
+    x[i] = warp_sum(x[i]);
+    if (lane == 0) cluster.map_shared_rank(&part[i][0], 0)[rank * JOIN_WARPS + warp] = x[i];
   }
-  cluster.sync();
-  if (rank == 0 && warp < COUNT) {
-    double s = 0.;
-    for (int i = lane; i < parts * (JOIN_THREADS / 32); i += 32) s += part[warp][i];
-    s = warp_sum(s);
-    __syncwarp();
-    if (lane == 0) part[warp][0] = s;
-  }
-  __syncthreads();
+  if (parts > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  if (rank != 0 || warp != 0) return;
 #pragma unroll
-  for (int i = 0; i < COUNT; ++i) v[i] = part[i][0];
+  for (int i = 0; i < COUNT; ++i) {
+    x[i] = Sum{};
+    for (int k = lane; k < parts * JOIN_WARPS; k += 32) x[i].add(part[i][k]);
+    x[i] = warp_sum(x[i]);
+  }
+}
+
+// What the user gave for a token.
+struct TokenInputs {
+  float weight, old_lp, advantage, ref_lp;
+  bool live;
+};
+
+__device__ __forceinline__ TokenInputs token_inputs(const LogprobArgs& a, const PolicyHow& how, int64_t row) {
+  TokenInputs y;
+  y.weight = how.weights ? how.weights[row] : how.all_weight;
+  y.old_lp = how.old_logprobs[row];
+  y.advantage = how.advantages[row];
+  y.ref_lp = how.ref_logprobs ? how.ref_logprobs[row] : 0.f;
+  y.live = a.tokens[row] >= 0 && y.weight != 0.f;
+  return y;
 }
 
 __global__ void __launch_bounds__(JOIN_THREADS) k_policy_join(LogprobArgs a, PolicyHow how, PolicyOut out) {
-  pdl_trigger();
-  pdl_wait();
-  double v[4] = {0., 0., 0., 0.};
   const int64_t step = int64_t(gridDim.x) * JOIN_THREADS;
-  for (int64_t row = int64_t(blockIdx.x) * JOIN_THREADS + threadIdx.x; row < a.rows; row += step) {
-    const float w = how.weights ? how.weights[row] : how.all_weight;
-    const bool live = a.tokens[row] >= 0 && w != 0.f;
+  int64_t row = int64_t(blockIdx.x) * JOIN_THREADS + threadIdx.x;
+  TokenInputs next{};
+  if (row < a.rows) next = token_inputs(a, how, row);
+  pdl_wait();
+  pdl_trigger();
+  Sum sums[4];  // loss, KL terms, clipped weights, entropies
+  for (; row < a.rows; row += step) {
+    const TokenInputs in = next;
+    if (row + step < a.rows) next = token_inputs(a, how, row + step);
+    const float lp = a.logprobs[row], H = a.entropies ? a.entropies[row] : 0.f;
     float slope = 0.f, h = 0.f;
-    if (live) {
-      const PolicyTerm term = policy_term(a.logprobs[row], how.old_logprobs[row], how.advantages[row],
-                                          how.ref_logprobs != nullptr, how.ref_logprobs ? how.ref_logprobs[row] : 0.f, how);
-      const float H = a.entropies ? a.entropies[row] : 0.f;
-      v[0] += double(w) * (double(term.loss) - (how.entropy != 0.f ? double(how.entropy) * H : 0.));
-      v[1] += double(w) * term.kl;
-      v[2] += term.clipped ? double(w) : 0.;
-      v[3] += double(w) * H;
-      slope = w * term.slope;
-      h = -how.entropy * w;
+    if (in.live) {
+      const PolicyTerm term = policy_term(lp, in.old_lp, in.advantage, how.ref_logprobs != nullptr, in.ref_lp, how);
+      sums[0].add(in.weight * (how.entropy != 0.f ? fmaf(-how.entropy, H, term.loss) : term.loss));
+      sums[1].add(in.weight * term.kl);
+      sums[2].add(term.clipped ? in.weight : 0.f);
+      sums[3].add(in.weight * H);
+      slope = in.weight * term.slope;
+      h = -how.entropy * in.weight;
     }
     out.slopes[row] = slope;
     if (out.entropy_slopes) out.entropy_slopes[row] = h;
   }
-  cluster_sum(v);
+  cluster_sum(sums);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *out.loss = static_cast<float>(v[0]);
+    *out.loss = sums[0].value();
 #pragma unroll
-    for (int i = 0; i < 3; ++i) out.sums[i] = static_cast<float>(v[i + 1]);
+    for (int i = 0; i < 3; ++i) out.sums[i] = sums[i + 1].value();
   }
 }
 
 // log(1 + exp v)
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
-// A pair by a team of `team` threads (a warp, or the CTA): its margin, its term of the loss
+// A pair by a team of TEAM threads (a warp, or the CTA): its margin, its term of the loss
 // and its rows' slopes.
-__global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a, PreferenceHow how, PreferenceOut out, int team) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ double across[2][2][JOIN_THREADS / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, thread = threadIdx.x % team;
-  const int64_t pairs = a.sequences / 2, teams = int64_t(gridDim.x) * (JOIN_THREADS / team);
-  double loss[1] = {0.};
+template <int TEAM>
+__global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a, PreferenceHow how, PreferenceOut out) {
+  __shared__ Sum across[2][JOIN_WARPS];
+  __shared__ int across_live[2][JOIN_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, thread = threadIdx.x % TEAM;
+  const int64_t pairs = a.sequences / 2, teams = int64_t(gridDim.x) * (JOIN_THREADS / TEAM);
+  const int64_t first = int64_t(blockIdx.x) * (JOIN_THREADS / TEAM) + threadIdx.x / TEAM;
+  bool waited = a.rows == 0;  // (no kernel went before that let this one start)
+  if (waited) pdl_wait();
+  Sum loss[1];
   // (A team of the whole CTA goes round together: the bound is the same for all of it.)
-  for (int64_t pair = int64_t(blockIdx.x) * (JOIN_THREADS / team) + threadIdx.x / team; pair < pairs; pair += teams) {
-    double sum[2], count[2];
-    int64_t begin[2], end[2];
-    bool good = true;
+  for (int64_t pair = first; pair < pairs; pair += teams) {
+    Sum sum[2];
+    int live[2];
+    int64_t edge[3];
+    bool good[2];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) edge[i] = a.offsets[2 * pair + i];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      begin[side] = a.offsets[2 * pair + side];
-      end[side] = a.offsets[2 * pair + side + 1];
       // Offsets that fall or leave the rows: nothing of the sequence is looked at.
-      if (begin[side] < 0 || end[side] < begin[side] || end[side] > a.rows) {
-        good = false;
-        begin[side] = end[side] = 0;
-      }
-      double s = 0.;
-      int live = 0;
-      for (int64_t row = begin[side] + thread; row < end[side]; row += team)
-        if (a.tokens[row] >= 0) {
-          s += double(a.logprobs[row]) - (how.ref_logprobs ? double(how.ref_logprobs[row]) : 0.);
-          ++live;
-        }
-      sum[side] = warp_sum(s);
-      count[side] = __reduce_add_sync(FULL_MASK, live);
+      good[side] = edge[side] >= 0 && edge[side + 1] >= edge[side] && edge[side + 1] <= a.rows;
+      live[side] = 0;
     }
-    if (team > 32) {
+    if (!waited) {  // what is about to be read, on its way while the log-probabilities are not there yet
+#pragma unroll
+      for (int side = 0; side < 2; ++side)
+        if (good[side])
+          for (int64_t row = edge[side] + thread * 4; row < edge[side + 1]; row += TEAM * 4) {
+            prefetch(a.tokens + row);
+            if (how.ref_logprobs) prefetch(how.ref_logprobs + row);
+          }
+      pdl_wait();
+      waited = true;
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+      if (good[side])
+#pragma unroll 4
+        for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM) {
+          const float lp = a.logprobs[row], ref = how.ref_logprobs ? how.ref_logprobs[row] : 0.f;
+          if (a.tokens[row] >= 0) {
+            sum[side].add(lp - ref);
+            ++live[side];
+          }
+        }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      sum[side] = warp_sum(sum[side]);
+      live[side] = __reduce_add_sync(FULL_MASK, live[side]);
+    }
+    if (TEAM > 32) {
       __syncthreads();  // (of the pair before, all is read)
       if (lane == 0)
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-          across[side][0][warp] = sum[side];
-          across[side][1][warp] = count[side];
+          across[side][warp] = sum[side];
+          across_live[side][warp] = live[side];
         }
       __syncthreads();
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
-        sum[side] = warp_sum(lane < JOIN_THREADS / 32 ? across[side][0][lane] : 0.);
-        count[side] = warp_sum(lane < JOIN_THREADS / 32 ? across[side][1][lane] : 0.);
+        sum[side] = warp_sum(lane < JOIN_WARPS ? across[side][lane] : Sum{});
+        live[side] = __reduce_add_sync(FULL_MASK, lane < JOIN_WARPS ? across_live[side][lane] : 0);
       }
     }
-    double share[2] = {1., 1.};
-    if (how.average)
+    // The difference before anything is rounded to one float.
+    float share[2] = {1.f, 1.f}, apart;
+    if (how.average) {
 #pragma unroll
-      for (int side = 0; side < 2; ++side) share[side] = 1. / fmax(count[side], 1.);
-    float margin = static_cast<float>(how.beta * (sum[0] * share[0] - sum[1] * share[1]) - how.margin);
-    if (!good) margin = NAN;
+      for (int side = 0; side < 2; ++side) share[side] = 1.f / static_cast<float>(max(live[side], 1));
+      apart = sum[0].value() * share[0] - sum[1].value() * share[1];
+    } else {
+      Sum d = sum[0];
+      d.add(Sum{-sum[1].v, -sum[1].lost});
+      apart = d.value();
+    }
+    const float margin = good[0] && good[1] ? fmaf(how.beta, apart, -how.margin) : NAN;
     const float eps = how.smoothing, rest = 1.f - eps;
     // (A side without weight is left out: it may be infinite.)
     float term = 0.f, slope = 0.f;
@@ -587,19 +836,21 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a,
       slope += eps / (1.f + expf(-margin));
     }
     if (thread == 0) {
-      loss[0] += term;
+      loss[0].add(term);
       out.margins[pair] = margin;
     }
-    const double each = double(slope) * how.beta / double(pairs);
+    const float each = slope * (how.beta / static_cast<float>(pairs));
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const float y = static_cast<float>((side ? -each : each) * share[side]);
-      for (int64_t row = begin[side] + thread; row < end[side]; row += team)
-        if (a.tokens[row] >= 0) out.slopes[row] = y;
-    }
+    for (int side = 0; side < 2; ++side)
+      if (good[side])
+#pragma unroll 4
+        for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM)
+          if (a.tokens[row] >= 0) out.slopes[row] = (side ? -each : each) * share[side];
   }
+  if (!waited) pdl_wait();
+  pdl_trigger();
   cluster_sum(loss);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *out.loss = pairs ? static_cast<float>(loss[0] / double(pairs)) : 0.f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *out.loss = pairs ? loss[0].value() / static_cast<float>(pairs) : 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -619,6 +870,9 @@ cudaError_t by_flag(bool flag, F&& f) {
 
 int64_t row_bytes(int64_t n, int type) { return n * (type == PROFK_F32 ? 4 : 2); }
 
+// Shared memory of a CTA that keeps a part of a row: its vectors, and room for single elements before and behind.
+int64_t keep_bytes(int64_t n, int type, int parts) { return (row_bytes(n, type) / parts + 16 + 2 * 16 + 127) / 128 * 128; }
+
 bool is_short(int64_t n, int type) { return row_bytes(n, type) <= 8192; }
 
 // CTAs a row: as many as fit the SMs at once, of 8 KB or more each.
@@ -626,6 +880,17 @@ int cluster_for(int64_t rows, int64_t n, int type) {
   int parts = 1;
   while (parts < MAX_CLUSTER && rows * parts * 2 <= 2 * sms() && row_bytes(n, type) / (parts * 2) >= 8192) parts *= 2;
   return parts;
+}
+
+// CTAs a row of the kernel that keeps it; 0 where it does not fit.  Parts of 64 KB or less, three
+// CTAs an SM, where 8 parts allow it, and where rows are few as many parts as fit the SMs.
+int keep_parts(int64_t rows, int64_t n, int type) {
+  const int64_t bytes = row_bytes(n, type);
+  int parts = 1;
+  while (parts < MAX_CLUSTER &&
+         (bytes / parts > 64 * 1024 || (rows * parts * 2 <= 2 * sms() && bytes / (parts * 2) >= 8192)))
+    parts *= 2;
+  return keep_bytes(n, type, parts) <= KEEP_SHARED ? parts : 0;
 }
 
 cudaError_t launch_rows(const LogprobArgs& a, const PolicyHow& how, cudaStream_t stream) {
@@ -637,6 +902,11 @@ cudaError_t launch_rows(const LogprobArgs& a, const PolicyHow& how, cudaStream_t
         if (is_short(a.n, a.type)) {
           const int64_t grid = (a.rows + SHORT_THREADS / 32 - 1) / (SHORT_THREADS / 32);
           return launch_kernel(k_logprobs_short<T, E, G>, dim3(static_cast<unsigned>(grid)), dim3(SHORT_THREADS), 0, stream, a, how);
+        }
+        if constexpr (G) {
+          const int keep = keep_parts(a.rows, a.n, a.type);
+          if (keep)
+            return launch_clusters_most(k_policy_keep<T, E>, a.rows * keep, KEEP_THREADS, keep, keep_bytes(a.n, a.type, keep), KEEP_SHARED, stream, a, how);
         }
         const int parts = cluster_for(a.rows, a.n, a.type);
         return launch_clusters(k_logprobs<T, E, G>, a.rows * parts, THREADS, parts, 0, stream, a, how);
@@ -658,8 +928,9 @@ cudaError_t launch_token_logprobs_backward(const LogprobBackwardArgs& a, cudaStr
         const int64_t grid = (a.rows + SHORT_THREADS / 32 - 1) / (SHORT_THREADS / 32);
         return launch_kernel(k_logprobs_backward_short<T, E>, dim3(static_cast<unsigned>(grid)), dim3(SHORT_THREADS), 0, stream, a);
       }
-      int64_t parts = 1;
-      while (parts < 64 && a.rows * parts < 8 * sms() && row_bytes(a.n, a.type) / (parts * 2) >= 16384) parts *= 2;
+      // Parts of 32 KB: the last CTAs are not long alone.  (1500 x 128003 float32, forward and backward: 354 us, with parts of
+      // 16 KB 383, of 128 KB 360, a row a CTA 378; 8192 x 131072 bfloat16, a third of it left out: 752, 822, 762, 770.)
+      const int64_t parts = std::min(std::max<int64_t>(row_bytes(a.n, a.type) / 32768, 1), (int64_t(1) << 30) / a.rows);
       return launch_kernel(k_logprobs_backward<T, E>, dim3(static_cast<unsigned>(a.rows * parts)), dim3(THREADS), 0, stream, a,
                            static_cast<int>(parts));
     });
@@ -676,10 +947,13 @@ cudaError_t launch_policy_loss(const LogprobArgs& a, const PolicyHow& how, const
 cudaError_t launch_preference_loss(const LogprobArgs& a, const PreferenceHow& how, const PreferenceOut& out, cudaStream_t stream) {
   cudaError_t err = a.rows > 0 ? launch_rows(a, PolicyHow{}, stream) : cudaSuccess;
   if (err != cudaSuccess) return err;
+  // A warp a pair where pairs are many or short (8 pairs of 2 x 64 rows: FILLms; by the CTA FILL; 8 of 2 x
+  // 512: FILL, by a warp FILL).
   const int64_t pairs = a.sequences / 2;
-  const int team = pairs >= 4 * JOIN_CLUSTER ? 32 : JOIN_THREADS;
-  const int cluster = pairs * team > JOIN_THREADS ? JOIN_CLUSTER : 1;
-  return launch_clusters(k_preference_join, cluster, JOIN_THREADS, cluster, 0, stream, a, how, out, team);
+  const bool warps = pairs >= 4 * JOIN_CLUSTER || a.rows <= 192 * pairs;
+  const int cluster = pairs > (warps ? JOIN_WARPS : 1) ? JOIN_CLUSTER : 1;
+  return warps ? launch_clusters(k_preference_join<32>, cluster, JOIN_THREADS, cluster, 0, stream, a, how, out)
+               : launch_clusters(k_preference_join<JOIN_THREADS>, cluster, JOIN_THREADS, cluster, 0, stream, a, how, out);
 }
 
 }  // namespace profk

@@ -35,16 +35,31 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 // x 2^x from becoming inf * 0 where a logit is -inf.
 constexpr float NO_MASS = -300.f;
 
-// What has been seen of a row: its largest logit m, s = sum 2^x and t = sum x 2^x with
-// x = (l - m) c, c = log2(e) / T.  s and t are sums of many terms (a thread of a long
-// row adds millions): each carries what its additions lost in a second float.  A NaN or
-// +inf logit makes s NaN (inf - inf), and it stays so; s = 0 says that nothing but -inf came.
+// The exponents of a row: x = (l - m) c for a largest logit m, c = log2(e) / T.  Where m c is of
+// ordinary size they are taken as one fused product, l c - (m c rounded): off the definition
+// by the same r = m c - (m c rounded) for every l of the row, |r| <= 2^-5, which the row's sums are
+// freed of at the end (centred).  Otherwise, where r could be anything or m c overflow, as the difference first.
+struct Centre {
+  float m, c, by;  // by: -(m c rounded), or -m
+  bool fused;
+  __device__ __forceinline__ Centre(float largest, float c_) : m(largest), c(c_) {
+    if (m == -INFINITY) m = 0.f;  // (any finite number while there is nothing)
+    const float mc = m * c;
+    fused = fabsf(mc) < 1048576.f;
+    by = fused ? -mc : -m;
+  }
+  __device__ __forceinline__ float operator()(float l) const { return fused ? fmaf(l, c, by) : (l + by) * c; }
+  // r: what the fused exponents are too large by.
+  __device__ __forceinline__ float off() const { return fused ? fmaf(m, c, by) : 0.f; }
+};
+
+// What has been seen of a row: its largest logit m, s = sum 2^x and t = sum x 2^x by
+// m's centre.  A NaN or +inf logit makes s NaN (inf - inf), and it stays so; s = 0 says that
+// nothing but -inf came.  The sums of a long row have millions of terms a thread: what an
+// addition loses is carried along in a second float.
 struct Running {
   float m, s, t, s_lost, t_lost;
 };
-
-// m as the point that others are taken from: any finite number while all are -inf.
-__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
 
 // sum + v exactly, as a float and what it lost.
 __device__ __forceinline__ void add_exact(float& sum, float& lost, float v) {
@@ -53,16 +68,26 @@ __device__ __forceinline__ void add_exact(float& sum, float& lost, float v) {
   sum = r;
 }
 
-// The exponent by which sums relative to `from` shrink when taken relative to `to`.
-// (fmaxf gives NO_MASS where both are infinite: what is NaN already stays it, what is zero too.)
-__device__ __forceinline__ float shrink(float from, float to, float c) { return fmaxf((from - to) * c, NO_MASS); }
+// The exponent by which sums by the centre of `from` shrink when taken by that of `to`.
+// (fmaxf gives NO_MASS where it is NaN, at infinite ones: what is NaN already stays it, what is zero too.)
+__device__ __forceinline__ float shrink(float from, float to, float c) {
+  const Centre a(from, c), b(to, c);
+  return fmaxf(from == -INFINITY ? NO_MASS : a.fused && b.fused ? b.by - a.by : (a.m - b.m) * c, NO_MASS);
+}
 
 // Row results that the kernels exchange.
-struct RowSum {
+struct alignas(16) RowSum {
   float m, s, t;
 };
 
 __device__ __forceinline__ RowSum total(const Running& r) { return {r.m, r.s + r.s_lost, r.t + r.t_lost}; }
+
+// Sums by the centre of m as sums by m itself (to which m's own logit gives 1, whatever was rounded).
+__device__ __forceinline__ RowSum centred(const RowSum& y, float c) {
+  const float r = Centre(y.m, c).off(), f = lm_exp2(-r);
+  const float s = f * y.s;
+  return {y.m, s > 0.f && s < 1.f ? 1.f : s, f * (y.t - r * y.s)};
+}
 
 // Joins over the warp: all lanes get the same, in the same order every time.
 template <bool ENTROPY>
@@ -84,12 +109,13 @@ __device__ __forceinline__ RowSum joined(const RowSum& y, const RowSum& z, float
 // A token's log-probability from its logit and the row's sums: -inf where the row holds
 // nothing, NaN where it holds a NaN or +inf.
 __device__ __forceinline__ float row_logprob(const RowSum& r, float logit, float T) {
-  return r.s == 0.f ? -INFINITY : (logit - reference(r.m)) / T - logf(r.s);
+  return r.s == 0.f ? -INFINITY : (logit - r.m) / T - logf(r.s);
 }
 
 // log s - (sum x exp x) / s; 0 for a row that holds nothing.
 __device__ __forceinline__ float row_entropy(const RowSum& r) {
-  return r.s == 0.f ? 0.f : logf(r.s) - r.t * LN2 / r.s;
+  const float H = logf(r.s) - r.t * LN2 / r.s;
+  return r.s == 0.f || H < 0.f ? 0.f : H;  // (below it only by rounding)
 }
 
 // log2(e) / T; NaN where T is no positive number, or so near to zero (or infinity) that

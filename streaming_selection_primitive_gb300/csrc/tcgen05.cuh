@@ -48,6 +48,23 @@ __device__ __forceinline__ bool barrier_wait(uint64_t* b, unsigned parity, volat
   return false;
 }
 
+// ---- clusters ----
+
+// The cluster's first barrier in two halves, without a fence (fence.mbarrier_init orders the
+// barriers' beginnings): behind the second one every CTA of the cluster runs.
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// 16 bytes to the same place of CTA `rank`'s shared memory, counted on its barrier.
+__device__ __forceinline__ void store_remote(void* to, float4 v, uint64_t* counted_on, int rank) {
+  uint32_t a, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(to)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(shared_address(counted_on)), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w), "r"(b)
+               : "memory");
+}
+
 // ---- tile copies ----
 
 __device__ __forceinline__ void copy_tile(void* to, const void* map, int x, int y, uint64_t* done) {
@@ -56,6 +73,15 @@ __device__ __forceinline__ void copy_tile(void* to, const void* map, int x, int 
       "l"(map), "r"(x), "r"(y), "r"(shared_address(done))
       : "memory");
 }
+
+// A run of bytes: both addresses and the length are multiples of 16.
+__device__ __forceinline__ void copy_bytes(void* to, const void* from, unsigned bytes, uint64_t* done) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(shared_address(to)), "l"(from),
+               "r"(bytes), "r"(shared_address(done))
+               : "memory");
+}
+// Orders this thread's accesses to shared memory before the copies it issues.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---- products ----
 

@@ -88,6 +88,18 @@ def test_rows_at_their_limits(pk, cuda_device, dtype, n):
     assert (pk.token_logprobs_backward(logits, tokens, r) == 0).all()
 
 
+@pytest.mark.parametrize("n", [50, 301, 6001])
+@pytest.mark.parametrize("base", [3e2, 3e5, 7e5, 1e6, 1e9, -7e5, -1e9])
+def test_logits_far_from_zero(pk, cuda_device, n, base):
+    # Only differences count; single elements at a row's ends and whole vectors have to agree on what they are taken from.
+    logits, tokens, _ = make(9, n, torch.float32, n + 1, offset=3)
+    logits += base
+    for r in range(9):  # the largest one at the ends, and next to them
+        logits[r, r if r < 5 else n - 10 + r] += 2 * abs(base) * 2.0 ** -23 + 4
+    check(pk, logits, tokens)
+    check(pk, logits, tokens, 0.01 if abs(base) > 1e8 else 0.3)
+
+
 def test_a_rows_own_bad_temperature(pk, cuda_device):
     for n in (64, 6000):
         logits, tokens, _ = make(5, n, torch.float32)
