@@ -40,11 +40,15 @@ class TokenLogprobs(NamedTuple):
 
 
 class PolicyLoss(NamedTuple):
-    """What policy_loss() returns: loss, a float32 scalar tensor; sums (3,) float32, see kl, clipped and
-    entropy; logprobs (rows,) float32; entropies (rows,) float32 or None; stats and slopes (rows: d loss / d
-    logprob), entropy_slopes (or None), for policy_loss_backward; grad_logits (or None); the temperature."""
+    """What policy_loss() returns: loss, kl (the weighted sum of the KL terms, before their factor; 0 without a
+    reference), clipped (the weight of the tokens whose ratio is clipped) and entropy (the weighted sum of the
+    entropies; 0 where they were not asked for), float32 scalar tensors; logprobs (rows,) float32; entropies
+    (rows,) float32 or None; stats and slopes (rows: d loss / d logprob), entropy_slopes (or None), for
+    policy_loss_backward; grad_logits (or None); the temperature."""
     loss: Any
-    sums: Any
+    kl: Any
+    clipped: Any
+    entropy: Any
     logprobs: Any
     entropies: Any
     stats: Any
@@ -52,21 +56,6 @@ class PolicyLoss(NamedTuple):
     entropy_slopes: Any
     grad_logits: Any
     temperature: Any
-
-    @property
-    def kl(self):
-        """The weighted sum of the KL terms, before their factor (0 without a reference)."""
-        return self.sums[0]
-
-    @property
-    def clipped(self):
-        """The weight of the tokens whose ratio is clipped."""
-        return self.sums[1]
-
-    @property
-    def entropy(self):
-        """The weighted sum of the entropies (0 where they were not asked for)."""
-        return self.sums[2]
 
 
 class PreferenceLoss(NamedTuple):
@@ -214,9 +203,9 @@ def _autograd():
                     _, entropies, stats = out
                     constants = (stats,)
                 elif name == "policy_loss":
-                    out = _call(name, x, tokens, *args[:4], temperature, *args[4:], False, None, None)[:7]
-                    _, sums, logprobs, entropies, stats, slopes, entropy_slopes = out
-                    constants = (sums, logprobs, entropies, stats, slopes, entropy_slopes)
+                    out = _call(name, x, tokens, *args[:4], temperature, *args[4:], False, None, None)[:9]
+                    entropies, stats, slopes, entropy_slopes = out[5:]
+                    constants = out[1:]
                 else:
                     out = _call(name, x, tokens, *args, temperature, None)
                     _, margins, logprobs, stats, slopes = out

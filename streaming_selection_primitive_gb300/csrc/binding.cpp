@@ -292,12 +292,15 @@ struct Temperature {
 };
 
 // Several float32 outputs in one piece of memory: a small call's time is spent in making its
-// tensors, and most of that in asking for their memory (a policy loss FILL).  They are
+// tensors, and most of that in asking for their memory (a policy loss 14.2 us, and
+// 10.2 so).  They are
 // tensors of their own to autograd, and the memory lives as long as any of them.
 class Floats {
  public:
-  Floats(const Place& place, int64_t rows, int64_t arrays) : each_((rows + 3) / 4 * 4), all_(place.empty({each_ * arrays}, at::kFloat)) {}
-  // The next `arrays` of the arrays as one tensor (each begins at a multiple of 16 bytes).
+  // Of arrays of so many elements, which begin at multiples of 16 bytes; 1: of single numbers.
+  Floats(const Place& place, int64_t elements, int64_t arrays)
+      : each_(elements == 1 ? 1 : (elements + 3) / 4 * 4), all_(place.empty({each_ * arrays}, at::kFloat)) {}
+  // The next `arrays` of the arrays as one tensor.
   Tensor take(at::IntArrayRef shape, int64_t arrays = 1) {
     Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all_.storage()), all_.key_set(), all_.dtype());
     t.unsafeGetTensorImpl()->set_storage_offset(at_);
@@ -342,7 +345,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int64_t* tokens = tokens_of(arg[1], like, x.rows);
   const Temperature T(arg[2], like, x.rows);
   const Place place(arg[4], like);
-  Floats floats(place, x.rows, arg[3] == Py_True ? 4 : 3);
+  Floats floats(place, std::max<int64_t>(x.rows, 4), arg[3] == Py_True ? 4 : 3);
   const Tensor logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2);
   Tensor entropies;
   if (arg[3] == Py_True) entropies = floats.take({x.rows});
@@ -432,10 +435,10 @@ PyObject* policy_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const bool entropy = arg[10] != Py_None, gradient = arg[11] == Py_True;
   if (entropy) how.entropy = static_cast<float>(number(arg[10]));
   const Place place(arg[13], like);
-  // (What is kept for the record, the loss and its sums, does not hold the rows' memory.)
-  Floats few(place, 4, 2), floats(place, x.rows, 4 + entropy + (how.entropy != 0.f));
-  const Tensor loss = few.take({}), sums = few.take({3}), logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2),
-               slopes = floats.take({x.rows});
+  // (What is kept for the record, the loss and the sums one behind the other, does not hold the rows' memory.)
+  Floats few(place, 1, 4), floats(place, std::max<int64_t>(x.rows, 4), 4 + entropy + (how.entropy != 0.f));
+  const Tensor loss = few.take({}), kl = few.take({}), clipped = few.take({}), entropies_sum = few.take({}),
+               logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2), slopes = floats.take({x.rows});
   Tensor entropies, entropy_slopes, grad;
   int64_t grad_ld = 0;
   if (entropy) entropies = floats.take({x.rows});
@@ -448,9 +451,9 @@ PyObject* policy_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
     refuse(PyExc_ValueError, "out is for gradient=True");
   }
   const int code = profk_policy_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, &how, data(loss),
-                                     data(sums), data(logprobs), data(entropies), data(stats), data(slopes),
+                                     data(kl), data(logprobs), data(entropies), data(stats), data(slopes),
                                      data(entropy_slopes), grad.defined() ? grad.data_ptr() : nullptr, grad_ld, place.stream());
-  return code == PROFK_OK ? tuple_of({loss, sums, logprobs, entropies, stats, slopes, entropy_slopes, grad}) : PyLong_FromLong(code);
+  return code == PROFK_OK ? tuple_of({loss, kl, clipped, entropies_sum, logprobs, entropies, stats, slopes, entropy_slopes, grad}) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
 
@@ -469,7 +472,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
                              static_cast<float>(number(arg[5])), static_cast<float>(number(arg[6])), arg[7] == Py_True};
   const Temperature T(arg[8], like, x.rows);
   const Place place(arg[9], like);
-  Floats few(place, std::max<int64_t>(pairs, 1), 2), floats(place, x.rows, 4);
+  Floats few(place, std::max<int64_t>(pairs, 4), 2), floats(place, std::max<int64_t>(x.rows, 4), 4);
   const Tensor loss = few.take({}), margins = few.take({pairs}), logprobs = floats.take({x.rows}), stats = floats.take({x.rows, 2}, 2),
                slopes = floats.take({x.rows});
   const int code = profk_preference_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all,

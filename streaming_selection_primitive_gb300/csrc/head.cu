@@ -2,7 +2,7 @@
 // on the tensor cores whose result, the logits, is turned into row maxima and sums tile
 // by tile and never leaves the chip.
 //
-// A tile is 128 rows of hidden states by up to 256 tokens of the vocabulary.  A CTA (one an SM)
+// A tile is 128 rows of hidden states by 256 tokens of the vocabulary.  A CTA (one an SM)
 // has a warp that copies pieces of both, 64 deep, into a ring in shared memory, a warp
 // that issues the products into one half of the tensor memory, and eight warps that
 // meanwhile take the finished tile in the other half: a thread has half of a row's
@@ -14,7 +14,6 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "../../include/profk.h"
 #include "lm.h"
@@ -25,7 +24,7 @@ namespace profk {
 namespace {
 
 constexpr int TILE_ROWS = 128;
-constexpr int TILE_TOKENS = 256;  // at most: the width is chosen for each call (plan_for)
+constexpr int TILE_TOKENS = 256;
 constexpr int DEPTH = 64;   // of a piece: 128 bytes a row, the widest swizzle
 constexpr int MAX_STAGES = 6;  // pieces in the ring
 constexpr int TAKERS = 8;   // warps that take tiles: two for each quarter of the lanes
@@ -36,15 +35,18 @@ constexpr int PARTS = 2;    // a row's columns are taken by two threads, 32 by 3
 
 constexpr int ROWS_BYTES = TILE_ROWS * DEPTH * 2;
 constexpr int RING_BYTES = 4 * (ROWS_BYTES + TILE_TOKENS * DEPTH * 2);
-constexpr int SHARED_BYTES = RING_BYTES + 1024;  // (the ring begins at a multiple of 1024 bytes)
+constexpr int SHARED_BYTES = RING_BYTES + ROWS_BYTES + 1024;  // (the last product of few rows looks past the ring, which begins at a multiple of 1024 bytes)
 
 // How the work is cut: run r is row tile r % row_tiles and the vocabulary's tiles
 // (r / row_tiles) * run and on, `run` of them, so that CTAs that work at the same time share
 // their tiles of the matrix in L2.
 struct Plan {
-  int width;  // tokens of a tile: a multiple of 32
+  int rows;   // rows of hidden states that are copied for a tile: a multiple of 8
   int row_tiles, token_tiles, run, runs, pieces, stages;
-  __host__ __device__ int stage_bytes() const { return ROWS_BYTES + width * DEPTH * 2; }
+  // A stage: the rows, then the tokens.  Of fewer rows than a tile has the product takes what comes
+  // behind them for the others (whose results nobody looks at).
+  __host__ __device__ int rows_bytes() const { return rows * DEPTH * 2; }
+  __host__ __device__ int stage_bytes() const { return rows_bytes() + TILE_TOKENS * DEPTH * 2; }
 };
 
 struct Barriers {
@@ -59,12 +61,12 @@ __device__ __forceinline__ void take_columns(RowSum& r, float (&v)[32], float c)
   float m = r.m;
 #pragma unroll
   for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
-  if (m > r.m) {
-    const float d = shrink(r.m, m, c), f = lm_exp2(d);
-    if (ENTROPY) r.t = f * (r.t + d * r.s);
-    r.s *= f;
-    r.m = m;
-  }
+  // (Not only where m has grown: 32 lanes with a row each are never of one mind, and the branch
+  // cost 2048 x 64 x 131072 96 us instead of 88.)
+  const float d = shrink(r.m, m, c), f = lm_exp2(d);
+  if (ENTROPY) r.t = f * (r.t + d * r.s);
+  r.s *= f;
+  r.m = m;
   const Centre at(m, c);
   Pair s[2] = {0, 0}, t[2] = {0, 0};
   const Pair by = pair(at.by, at.by), cc = pair(c, c);
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ Barriers sync;
   uint8_t* ring = raw + (1024 - shared_address(raw) % 1024) % 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int limit = wait_limit(waits), stages = plan.stages, stage_bytes = plan.stage_bytes();
+  const int limit = wait_limit(waits), stages = plan.stages, stage_bytes = plan.stage_bytes(), rows_bytes = plan.rows_bytes();
   if (threadIdx.x == 0) {
     for (int i = 0; i < plan.stages; ++i) {
       barrier_init(&sync.full[i], 1);
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint8_t* to = ring + stage * stage_bytes;
             barrier_arrive_expect(&sync.full[stage], stage_bytes);
             copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[stage]);
-            copy_tile(to + ROWS_BYTES, &weight, piece * DEPTH, tile * plan.width, &sync.full[stage]);
+            copy_tile(to + rows_bytes, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[stage]);
             issued = min(issued + 1, stages);
             if (++stage == stages) {
               stage = 0;
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = barrier_wait(&sync.full[stage], parity, &sync.given_up, limit);
             if (!ok) break;
             after_barrier();
-            const uint64_t x = tile_descriptor(ring + stage * stage_bytes), w = tile_descriptor(ring + stage * stage_bytes + ROWS_BYTES);
+            const uint64_t x = tile_descriptor(ring + stage * stage_bytes), w = tile_descriptor(ring + stage * stage_bytes + rows_bytes);
 #pragma unroll
             for (int k = 0; k < DEPTH / 16; ++k)  // 32 bytes on along the rows: 2 in the descriptor's units
               multiply(to, x + 2 * k, w + 2 * k, product, piece + k > 0);
@@ -214,9 +216,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         after_barrier();
         const uint32_t from = tensor + (uint32_t(quarter * 32) << 16) + half * TILE_TOKENS;
-        const int64_t column0 = int64_t(tile) * plan.width;
+        const int64_t column0 = int64_t(tile) * TILE_TOKENS;
 #pragma unroll 1
-        for (int i = side * 32; i < plan.width; i += 32 * PARTS) {
+        for (int i = side * 32; i < TILE_TOKENS; i += 32 * PARTS) {
           float v[32];
           tensor_load(v, from + i);
           tensor_loaded();
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 constexpr int JOIN_THREADS = 128;
 
-// A row's parts joined, by a warp.
+// A row's parts joined, by a warp.  (Parts of a row one behind the other: with those of a part, which the
+// kernel before would write in one piece, and a row a lane, 5 x 1024 x 32768 took 22.2 us in all, not 18.5.)
 __global__ void __launch_bounds__(JOIN_THREADS) k_head_join(HeadArgs a, const float4* parts, const float* logits, int count) {
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
@@ -316,20 +319,9 @@ bool describe(CUtensorMap* map, const void* p, bool bf16, int64_t rows, int64_t 
 Plan plan_for(const HeadArgs& a) {
   Plan p;
   p.row_tiles = static_cast<int>((a.rows + TILE_ROWS - 1) / TILE_ROWS);
+  p.rows = static_cast<int>(std::min<int64_t>(TILE_ROWS, (a.rows + 7) / 8 * 8));
   p.pieces = static_cast<int>((a.width + DEPTH - 1) / DEPTH);
-  // The width that leaves the SMs least idle: rounds of one tile an SM times the width (a narrow tile
-  // reads the hidden states more often, so it has to gain a sixteenth).
-  p.width = 0;
-  int64_t best = 0;
-  for (int width = TILE_TOKENS; width >= 128; width -= 32) {
-    const int64_t tiles = p.row_tiles * ((a.n + width - 1) / width), cost = (tiles + sms() - 1) / sms() * width;
-    if (!p.width || cost * 16 < best * 15) {
-      p.width = width;
-      best = cost;
-    }
-  }
-  if (getenv("HW")) p.width = atoi(getenv("HW"));
-  p.token_tiles = static_cast<int>((a.n + p.width - 1) / p.width);
+  p.token_tiles = static_cast<int>((a.n + TILE_TOKENS - 1) / TILE_TOKENS);
   p.stages = std::min(MAX_STAGES, RING_BYTES / p.stage_bytes());
   // Runs of up to 4 tiles, while there are 8 runs or more for each SM.
   const int64_t tiles = int64_t(p.row_tiles) * p.token_tiles;
@@ -344,8 +336,8 @@ cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
   const bool bf16 = a.type == PROFK_BF16;
   const Plan plan = plan_for(a);
   CUtensorMap hidden, weight;
-  if (!describe(&hidden, a.hidden, bf16, a.rows, a.width, a.hidden_ld, TILE_ROWS) ||
-      !describe(&weight, a.weight, bf16, a.n, a.width, a.weight_ld, plan.width))
+  if (!describe(&hidden, a.hidden, bf16, a.rows, a.width, a.hidden_ld, plan.rows) ||
+      !describe(&weight, a.weight, bf16, a.n, a.width, a.weight_ld, TILE_TOKENS))
     return cudaErrorInvalidValue;
   const int runs = (plan.token_tiles + plan.run - 1) / plan.run, count = runs * PARTS;
   cudaMemPool_t pool;
@@ -362,7 +354,7 @@ cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
   err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED_BYTES);
   if (err == cudaSuccess)
     err = launch_kernel(kernel, dim3(grid), dim3(THREADS), size_t(SHARED_BYTES), stream, hidden, weight, a, plan,
-                        product_descriptor(bf16, TILE_ROWS, plan.width), parts, runs, logits, head_wait());
+                        product_descriptor(bf16, TILE_ROWS, TILE_TOKENS), parts, runs, logits, head_wait());
   if (err == cudaSuccess)
     err = launch_kernel(k_head_join, dim3(static_cast<unsigned>((a.rows + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32))), dim3(JOIN_THREADS), 0, stream,
                         a, parts, logits, count);

@@ -24,9 +24,10 @@ namespace cg = cooperative_groups;
 namespace profk {
 namespace {
 
-constexpr int THREADS = 256;    // of a CTA that takes a row or a part of one
+constexpr int THREADS = 128;    // of a CTA that takes a row or a part of one
 constexpr int WARPS = THREADS / 32;
 constexpr int SHORT_THREADS = 256;  // of a CTA whose warps take a row each
+constexpr int SHORT_PER_SM = 4;     // such CTAs on an SM
 constexpr int LOADS = 4;        // 16-byte loads of a thread before it looks at what came
 constexpr int KEEP_LOADS = 4;   // the same from shared memory
 constexpr int MAX_CLUSTER = 8;
@@ -138,16 +139,14 @@ __device__ __forceinline__ int part_begin(int vectors, int rank, int parts) {
 template <typename T, bool ENTROPY, bool LONG, int COUNT>
 __device__ __forceinline__ void take(Running& r, const uint4 (&v)[COUNT], float c) {
   const float m = fmaxf(r.m, largest(v, T{}));
-  if (m > r.m) {
-    const float d = shrink(r.m, m, c), f = lm_exp2(d);
-    if (ENTROPY) {
-      r.t = f * (r.t + d * r.s);
-      if (LONG) r.t_lost = f * (r.t_lost + d * r.s_lost);
-    }
-    r.s *= f;
-    if (LONG) r.s_lost *= f;
-    r.m = m;
+  const float d = shrink(r.m, m, c), f = lm_exp2(d);
+  if (ENTROPY) {
+    r.t = f * (r.t + d * r.s);
+    if (LONG) r.t_lost = f * (r.t_lost + d * r.s_lost);
   }
+  r.s *= f;
+  if (LONG) r.s_lost *= f;
+  r.m = m;
   const Centre at(m, c);
   Pair s[2] = {0, 0}, t[2] = {0, 0};
   const auto add = [&](Pair x, int i) {
@@ -376,16 +375,14 @@ __device__ __forceinline__ bool row_live(const LogprobArgs& a, int64_t row) {
   return live;
 }
 
-template <typename T, bool GRADIENT>
-__device__ __forceinline__ Row<GRADIENT> load_row(const LogprobArgs& a, const PolicyHow& how, int64_t row) {
+// All but the token's logit.
+template <bool GRADIENT>
+__device__ __forceinline__ Row<GRADIENT> load_inputs(const LogprobArgs& a, const PolicyHow& how, int64_t row) {
   Row<GRADIENT> r;
   r.token = a.tokens[row];
   r.temperature = a.temperature ? a.temperature[row] : a.all_temperature;
   r.c = inverse_temperature(r.temperature);
   r.live = row_live(a, row);
-  // A token that the vocabulary has not is no number.
-  r.logit = NAN;
-  if (r.live && r.token < a.n) r.logit = lm_float(static_cast<const T*>(a.logits)[row * a.ld + r.token]);
   if (GRADIENT) {
     r.old_lp = how.old_logprobs[row];
     r.advantage = how.advantages[row];
@@ -393,6 +390,11 @@ __device__ __forceinline__ Row<GRADIENT> load_row(const LogprobArgs& a, const Po
     r.weight = how.weights ? how.weights[row] : how.all_weight;
   }
   return r;
+}
+
+template <typename T, bool GRADIENT>
+__device__ __forceinline__ void load_logit(Row<GRADIENT>& r, const T* p, int n) {
+  r.logit = r.live && r.token < n ? lm_float(p[r.token]) : NAN;  // (a token that the vocabulary has not is no number)
 }
 
 __device__ __forceinline__ void store_left_out(const LogprobArgs& a, int64_t row) {
@@ -454,7 +456,7 @@ struct Exchange {
 };
 
 template <typename T, bool ENTROPY, bool GRADIENT>
-__global__ void __launch_bounds__(THREADS, 4) k_logprobs(LogprobArgs a, PolicyHow how) {
+__global__ void __launch_bounds__(THREADS, 8) k_logprobs(LogprobArgs a, PolicyHow how) {
   pdl_wait();
   pdl_trigger();  // (behind it: what follows may read what this reads)
   __shared__ Exchange<WARPS> exchange;
@@ -464,7 +466,8 @@ __global__ void __launch_bounds__(THREADS, 4) k_logprobs(LogprobArgs a, PolicyHo
   const int thread = threadIdx.x, n = static_cast<int>(a.n);
   const T* p = static_cast<const T*>(a.logits) + row * a.ld;
   T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
-  const Row<GRADIENT> r = load_row<T, GRADIENT>(a, how, row);
+  Row<GRADIENT> r = load_inputs<GRADIENT>(a, how, row);
+  load_logit(r, p, n);
   if (!r.live) {  // the same for the whole cluster: none of it waits
     if (rank == 0 && thread == 0) store_left_out(a, row);
     if (GRADIENT) {
@@ -492,35 +495,45 @@ __global__ void __launch_bounds__(THREADS, 4) k_logprobs(LogprobArgs a, PolicyHo
   }
 }
 
-// A row by a warp.
+// A row by a warp, which (without the gradient, where it goes on to another) has the next row's inputs on their way meanwhile.
 template <typename T, bool ENTROPY, bool GRADIENT>
-__global__ void __launch_bounds__(SHORT_THREADS) k_logprobs_short(LogprobArgs a, PolicyHow how) {
+__global__ void __launch_bounds__(SHORT_THREADS, GRADIENT ? 3 : SHORT_PER_SM) k_logprobs_short(LogprobArgs a, PolicyHow how) {
   pdl_wait();
   pdl_trigger();  // (behind it: what follows may read what this reads)
   const int lane = threadIdx.x & 31, n = static_cast<int>(a.n);
-  const int64_t row = int64_t(blockIdx.x) * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
-  if (row >= a.rows) return;
-  const T* p = static_cast<const T*>(a.logits) + row * a.ld;
-  T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
-  const Row<GRADIENT> r = load_row<T, GRADIENT>(a, how, row);
-  if (!r.live) {
-    if (lane == 0) store_left_out(a, row);
-    if (GRADIENT) {
-      const Layout<T> to(out, n);
-      write_zeros<T, 32>(out, to, 0, to.vectors, lane, to.single(lane, true, true));
+  const int64_t step = int64_t(gridDim.x) * (SHORT_THREADS / 32);
+  int64_t row = int64_t(blockIdx.x) * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
+  Row<false> next{};
+  if (!GRADIENT && row < a.rows) next = load_inputs<false>(a, how, row);
+  for (; row < a.rows; row += step) {
+    Row<GRADIENT> r;
+    if constexpr (GRADIENT)
+      r = load_inputs<true>(a, how, row);
+    else
+      r = next;
+    const T* p = static_cast<const T*>(a.logits) + row * a.ld;
+    T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
+    load_logit(r, p, n);
+    if (!GRADIENT && row + step < a.rows) next = load_inputs<false>(a, how, row + step);
+    if (!r.live) {
+      if (lane == 0) store_left_out(a, row);
+      if (GRADIENT) {
+        const Layout<T> to(out, n);
+        write_zeros<T, 32>(out, to, 0, to.vectors, lane, to.single(lane, true, true));
+      }
+      continue;
     }
-    return;
-  }
-  const Layout<T> at(p, n);
-  const int single = at.single(lane, true, true);
-  const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
-  RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, 32>(reinterpret_cast<const uint4*>(p + at.head), 0, at.vectors, lane, alone, r.c)), r.c);
-  y = centred(y, r.c);
-  if (!(r.c > 0.f)) y.s = NAN;
-  const float lp = store_row(a, row, y, r.logit, r.temperature, lane == 0);
-  if (GRADIENT) {
-    const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
-    write_gradient<T, ENTROPY, 32>(p, out, n, lane, place_in(r.token, a.n, 0), k);
+    const Layout<T> at(p, n);
+    const int single = at.single(lane, true, true);
+    const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
+    RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, 32>(reinterpret_cast<const uint4*>(p + at.head), 0, at.vectors, lane, alone, r.c)), r.c);
+    y = centred(y, r.c);
+    if (!(r.c > 0.f)) y.s = NAN;
+    const float lp = store_row(a, row, y, r.logit, r.temperature, lane == 0);
+    if (GRADIENT) {
+      const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
+      write_gradient<T, ENTROPY, 32>(p, out, n, lane, place_in(r.token, a.n, 0), k);
+    }
   }
 }
 
@@ -528,14 +541,12 @@ __global__ void __launch_bounds__(SHORT_THREADS) k_logprobs_short(LogprobArgs a,
 // The policy loss with its gradient, a row by a cluster whose CTAs keep their parts of it in
 // shared memory: the row is read from memory once, and its sums and its gradient are both
 // made from the copy.  Many such CTAs share an SM, so that some copy while others work.
-constexpr int KEEP_THREADS = 256;
-constexpr int KEEP_WARPS = KEEP_THREADS / 32;
 constexpr int KEEP_SHARED = 112 * 1024;  // dynamic shared memory at most
 
-template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(KEEP_THREADS, 4) k_policy_keep(LogprobArgs a, PolicyHow how) {
+template <typename T, bool ENTROPY, int KEEP_THREADS>
+__global__ void __launch_bounds__(KEEP_THREADS, 1024 / KEEP_THREADS) k_policy_keep(LogprobArgs a, PolicyHow how) {
   extern __shared__ __align__(128) uint8_t room[];
-  __shared__ Exchange<KEEP_WARPS> exchange;
+  __shared__ Exchange<KEEP_THREADS / 32> exchange;
   __shared__ uint64_t full;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -566,7 +577,8 @@ __global__ void __launch_bounds__(KEEP_THREADS, 4) k_policy_keep(LogprobArgs a, 
   }
   __syncthreads();
   cluster_begin();
-  const Row<true> r = load_row<T, true>(a, how, row);
+  Row<true> r = load_inputs<true>(a, how, row);
+  load_logit(r, p, n);
   const Span<T> mine(at, begin, end, rank == 0, rank == parts - 1);
   T* copy = reinterpret_cast<T*>(room + 16) - (rank == 0 ? at.head : 0);  // the span's first element
   const int single = at.single(thread, rank == 0, rank == parts - 1);
@@ -589,47 +601,66 @@ __global__ void __launch_bounds__(KEEP_THREADS, 4) k_policy_keep(LogprobArgs a, 
 
 // ---------------------------------------------------------------------------
 // The gradient from a forward pass's row sums: `parts` CTAs a row, or a warp a row.
+struct BackwardRow {
+  int64_t token;
+  float g, h, temperature, entropy;
+  float2 stats;
+};
+
+template <bool ENTROPY>
+__device__ __forceinline__ BackwardRow backward_inputs(const LogprobBackwardArgs& a, int64_t row) {
+  BackwardRow r;
+  r.token = a.tokens[row];
+  r.g = a.grad_logprobs ? a.grad_logprobs[row] : 0.f;
+  r.h = ENTROPY ? a.grad_entropies[row] : 0.f;
+  r.temperature = a.temperature ? a.temperature[row] : a.all_temperature;
+  r.stats = a.stats[row];
+  r.entropy = ENTROPY ? a.entropies[row] : 0.f;
+  return r;
+}
+
 template <typename T, bool ENTROPY, int STEP>
-__device__ __forceinline__ void backward_row(const LogprobBackwardArgs& a, int64_t row, int rank, int parts, int thread) {
+__device__ __forceinline__ void backward_row(const LogprobBackwardArgs& a, int64_t row, const BackwardRow& r, int rank, int parts, int thread) {
   const int n = static_cast<int>(a.n);
   const T* p = static_cast<const T*>(a.logits) + row * a.ld;
   T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
-  const int64_t token = a.tokens[row];
-  float g = a.grad_logprobs ? a.grad_logprobs[row] : 0.f;
-  float h = ENTROPY ? a.grad_entropies[row] : 0.f;
-  if (token < 0 || (g == 0.f && h == 0.f)) {  // left out, whatever the logits hold
+  if (r.token < 0 || (r.g == 0.f && r.h == 0.f)) {  // left out, whatever the logits hold
     const Layout<T> to(out, n);
     write_zeros<T, STEP>(out, to, part_begin(to.vectors, rank, parts), part_begin(to.vectors, rank + 1, parts), thread,
                          to.single(thread, rank == 0, rank == parts - 1));
     return;
   }
-  if (a.scale) {
-    g *= *a.scale;
-    h *= *a.scale;
-  }
-  if (token >= n) g = NAN;
+  const float scale = a.scale ? *a.scale : 1.f;
+  const float g = r.token < n ? r.g * scale : NAN, h = r.h * scale;
   const Layout<T> at(p, n);
-  const float temperature = a.temperature ? a.temperature[row] : a.all_temperature, c = inverse_temperature(temperature);
-  const float2 stats = a.stats[row];
-  const float mean_x = ENTROPY ? (logf(stats.y) - a.entropies[row]) * LOG2E : 0.f;
-  const Slopes k = slopes_of<ENTROPY>(stats.x, stats.y, mean_x, temperature, c, g, h);
+  const float mean_x = ENTROPY ? (logf(r.stats.y) - r.entropy) * LOG2E : 0.f;
+  const Slopes k = slopes_of<ENTROPY>(r.stats.x, r.stats.y, mean_x, r.temperature, inverse_temperature(r.temperature), g, h);
   const Span<T> mine(at, part_begin(at.vectors, rank, parts), part_begin(at.vectors, rank + 1, parts), rank == 0, rank == parts - 1);
-  write_gradient<T, ENTROPY, STEP>(p + mine.first, out + mine.first, mine.count, thread, place_in(token, n, mine.first), k);
+  write_gradient<T, ENTROPY, STEP>(p + mine.first, out + mine.first, mine.count, thread, place_in(r.token, n, mine.first), k);
 }
 
 template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(THREADS, 4) k_logprobs_backward(LogprobBackwardArgs a, int parts) {
+__global__ void __launch_bounds__(THREADS, 8) k_logprobs_backward(LogprobBackwardArgs a, int parts) {
   pdl_trigger();
   pdl_wait();
-  backward_row<T, ENTROPY, THREADS>(a, a.rows - 1 - blockIdx.x / parts, static_cast<int>(blockIdx.x % parts), parts, threadIdx.x);
+  // From the last row on: of what the forward pass has read, that is what L2 still holds.
+  const int64_t row = a.rows - 1 - blockIdx.x / parts;
+  backward_row<T, ENTROPY, THREADS>(a, row, backward_inputs<ENTROPY>(a, row), static_cast<int>(blockIdx.x % parts), parts, threadIdx.x);
 }
 
 template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(SHORT_THREADS) k_logprobs_backward_short(LogprobBackwardArgs a) {
+__global__ void __launch_bounds__(SHORT_THREADS, SHORT_PER_SM) k_logprobs_backward_short(LogprobBackwardArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int64_t row = int64_t(blockIdx.x) * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
-  if (row < a.rows) backward_row<T, ENTROPY, 32>(a, row, 0, 1, threadIdx.x & 31);
+  const int64_t step = int64_t(gridDim.x) * (SHORT_THREADS / 32);
+  int64_t back = int64_t(blockIdx.x) * (SHORT_THREADS / 32) + (threadIdx.x >> 5);  // rows from the last on
+  BackwardRow next{};
+  if (back < a.rows) next = backward_inputs<ENTROPY>(a, a.rows - 1 - back);
+  for (; back < a.rows; back += step) {
+    const BackwardRow r = next;
+    if (back + step < a.rows) next = backward_inputs<ENTROPY>(a, a.rows - 1 - back - step);
+    backward_row<T, ENTROPY, 32>(a, a.rows - 1 - back, r, 0, 1, threadIdx.x & 31);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -873,22 +904,49 @@ int64_t row_bytes(int64_t n, int type) { return n * (type == PROFK_F32 ? 4 : 2);
 // Shared memory of a CTA that keeps a part of a row: its vectors, and room for single elements before and behind.
 int64_t keep_bytes(int64_t n, int type, int parts) { return (row_bytes(n, type) / parts + 16 + 2 * 16 + 127) / 128 * 128; }
 
-bool is_short(int64_t n, int type) { return row_bytes(n, type) <= 8192; }
+// Whether a warp takes a row, and not CTAs: rows up to so many bytes, more where there are rows for all warps of the
+// SMs.  Microseconds by warps and by CTAs, bfloat16:
+//   forward   300 x 2000 2.8, 3.3; 400 x 5001 4.1, 3.9; 2000 x 5001 7.4, 11.8; 1000 x 16384 12.8, 9.5;
+//             4000 x 32768 44.9, 48.4; 2000 x 65536 50.7, 45.1
+//   with the policy's gradient  300 x 2000 7.6, 7.0; 3000 x 2000 10.2, 17.9; 400 x 5001 9.3, 8.4;
+//             2000 x 5001 15.0, 18.0; 1000 x 16384 25.0, 18.5
+//   backward  3000 x 2000 5.3, 7.1; 400 x 5001 4.6, 3.0; 2000 x 5001 10.0, 6.9; 20000 x 5001 62, 63
+int64_t short_bytes(int64_t rows, bool gradient) {
+  if (gradient) return rows >= 4 * sms() ? 16384 : 2048;
+  return rows >= 24 * sms() ? 65536 : rows >= 4 * sms() ? 16384 : 8192;
+}
+constexpr int64_t SHORT_BACKWARD = 8192;
 
-// CTAs a row: as many as fit the SMs at once, of 8 KB or more each.
-int cluster_for(int64_t rows, int64_t n, int type) {
-  int parts = 1;
-  while (parts < MAX_CLUSTER && rows * parts * 2 <= 2 * sms() && row_bytes(n, type) / (parts * 2) >= 8192) parts *= 2;
-  return parts;
+// CTAs of warps that take rows: those that fit the SMs, or (once) one for every 8 rows.
+unsigned short_grid(int64_t rows, bool once) {
+  const int64_t all = (rows + SHORT_THREADS / 32 - 1) / (SHORT_THREADS / 32);
+  return static_cast<unsigned>(once ? all : std::min<int64_t>(all, SHORT_PER_SM * sms()));
 }
 
-// CTAs a row of the kernel that keeps it; 0 where it does not fit.  Parts of 64 KB or less, three
-// CTAs an SM, where 8 parts allow it, and where rows are few as many parts as fit the SMs.
+// CTAs a row, of 8 KB or more each: what takes the fewest rounds of CTAs on the SMs, where a CTA costs
+// as much as 24 KB besides its own (500 x 65536 bfloat16, two CTAs a row: 14.1 us, one 16.6; 1500 x 128003 float32, four:
+// 347 us forward and backward, one 371).
+int cluster_for(int64_t rows, int64_t n, int type) {
+  const int64_t bytes = row_bytes(n, type), slots = 8 * sms();
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int parts = 1; parts <= MAX_CLUSTER && (parts == 1 || bytes / parts >= 8192); parts *= 2) {
+    const int64_t cost = (rows * parts + slots - 1) / slots * (bytes / parts + 24576);
+    if (cost < least) {
+      least = cost;
+      best = parts;
+    }
+  }
+  return best;
+}
+
+// CTAs a row of the kernel that keeps it; 0 where it does not fit.  Parts of 32 KB or less where 8 parts allow
+// it (4096 x 131072 bfloat16: 332 us; of 64 KB 340), and where rows are few as many as fit the SMs.
 int keep_parts(int64_t rows, int64_t n, int type) {
   const int64_t bytes = row_bytes(n, type);
   int parts = 1;
   while (parts < MAX_CLUSTER &&
-         (bytes / parts > 64 * 1024 || (rows * parts * 2 <= 2 * sms() && bytes / (parts * 2) >= 8192)))
+         (bytes / parts > 32768 || (rows * parts * 2 <= 4 * sms() && bytes / (parts * 2) >= 8192)))
     parts *= 2;
   return keep_bytes(n, type, parts) <= KEEP_SHARED ? parts : 0;
 }
@@ -899,14 +957,18 @@ cudaError_t launch_rows(const LogprobArgs& a, const PolicyHow& how, cudaStream_t
       return by_flag(a.grad_logits != nullptr, [&](auto gradient) {
         using T = decltype(type);
         constexpr bool E = decltype(entropy)::value, G = decltype(gradient)::value;
-        if (is_short(a.n, a.type)) {
-          const int64_t grid = (a.rows + SHORT_THREADS / 32 - 1) / (SHORT_THREADS / 32);
-          return launch_kernel(k_logprobs_short<T, E, G>, dim3(static_cast<unsigned>(grid)), dim3(SHORT_THREADS), 0, stream, a, how);
-        }
+        // (With the gradient a warp that went on to another row would hold its registers' worth of others
+        // back: 20000 x 2000 54 us, and 44 with a warp for every row; without it 19.8 and 21.6.)
+        if (row_bytes(a.n, a.type) <= short_bytes(a.rows, G))
+          return launch_kernel(k_logprobs_short<T, E, G>, dim3(short_grid(a.rows, G)), dim3(SHORT_THREADS), 0, stream, a, how);
         if constexpr (G) {
           const int keep = keep_parts(a.rows, a.n, a.type);
           if (keep)
-            return launch_clusters_most(k_policy_keep<T, E>, a.rows * keep, KEEP_THREADS, keep, keep_bytes(a.n, a.type, keep), KEEP_SHARED, stream, a, how);
+            // (4 warps for 32 KB, 8 for more: 1000 x 16384 bfloat16 18.5 us, 19.2 by 8; 2000 x 65536 in one part 90, 98 by 4.)
+            return by_flag(row_bytes(a.n, a.type) / keep <= 32768, [&](auto few) {
+              constexpr int N = decltype(few)::value ? 128 : 256;
+              return launch_clusters_most(k_policy_keep<T, E, N>, a.rows * keep, N, keep, keep_bytes(a.n, a.type, keep), KEEP_SHARED, stream, a, how);
+            });
         }
         const int parts = cluster_for(a.rows, a.n, a.type);
         return launch_clusters(k_logprobs<T, E, G>, a.rows * parts, THREADS, parts, 0, stream, a, how);
@@ -924,10 +986,8 @@ cudaError_t launch_token_logprobs_backward(const LogprobBackwardArgs& a, cudaStr
     return by_flag(a.grad_entropies != nullptr, [&](auto entropy) {
       using T = decltype(type);
       constexpr bool E = decltype(entropy)::value;
-      if (is_short(a.n, a.type)) {
-        const int64_t grid = (a.rows + SHORT_THREADS / 32 - 1) / (SHORT_THREADS / 32);
-        return launch_kernel(k_logprobs_backward_short<T, E>, dim3(static_cast<unsigned>(grid)), dim3(SHORT_THREADS), 0, stream, a);
-      }
+      if (row_bytes(a.n, a.type) <= SHORT_BACKWARD)
+        return launch_kernel(k_logprobs_backward_short<T, E>, dim3(short_grid(a.rows, false)), dim3(SHORT_THREADS), 0, stream, a);
       // Parts of 32 KB: the last CTAs are not long alone.  (1500 x 128003 float32, forward and backward: 354 us, with parts of
       // 16 KB 383, of 128 KB 360, a row a CTA 378; 8192 x 131072 bfloat16, a third of it left out: 752, 822, 762, 770.)
       const int64_t parts = std::min(std::max<int64_t>(row_bytes(a.n, a.type) / 32768, 1), (int64_t(1) << 30) / a.rows);
@@ -947,8 +1007,8 @@ cudaError_t launch_policy_loss(const LogprobArgs& a, const PolicyHow& how, const
 cudaError_t launch_preference_loss(const LogprobArgs& a, const PreferenceHow& how, const PreferenceOut& out, cudaStream_t stream) {
   cudaError_t err = a.rows > 0 ? launch_rows(a, PolicyHow{}, stream) : cudaSuccess;
   if (err != cudaSuccess) return err;
-  // A warp a pair where pairs are many or short (8 pairs of 2 x 64 rows: FILLms; by the CTA FILL; 8 of 2 x
-  // 512: FILL, by a warp FILL).
+  // A warp a pair where pairs are many or short.  (Captured alone: 8 pairs of 2 x 64 rows 6.4 us by warps; 5 of
+  // 2 x 150 11.4 by warps, 8 of 2 x 512 7.5 by CTAs.)
   const int64_t pairs = a.sequences / 2;
   const bool warps = pairs >= 4 * JOIN_CLUSTER || a.rows <= 192 * pairs;
   const int cluster = pairs > (warps ? JOIN_WARPS : 1) ? JOIN_CLUSTER : 1;

@@ -52,8 +52,14 @@ __device__ __forceinline__ bool barrier_wait(uint64_t* b, unsigned parity, volat
 
 // The cluster's first barrier in two halves, without a fence (fence.mbarrier_init orders the
 // barriers' beginnings): behind the second one every CTA of the cluster runs.
-__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begin() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begun() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // 16 bytes to the same place of CTA `rank`'s shared memory, counted on its barrier.
 __device__ __forceinline__ void store_remote(void* to, float4 v, uint64_t* counted_on, int rank) {

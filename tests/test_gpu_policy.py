@@ -42,32 +42,34 @@ def check_policy(pk, rows, n, dtype, *, ld=0, T=1.0, kl=0.1, entropy=0.05, with_
     how = dict(ref_logprobs=refs, weights=w, temperature=T, clip_low=low, clip_high=high, kl=kl, entropy=entropy)
     fused = pk.policy_loss(logits, tokens, old, A, gradient=True, out=out, **how)
     plain = pk.policy_loss(logits, tokens, old, A, **how)
-    for name in ("loss", "sums", "logprobs", "entropies", "slopes", "entropy_slopes"):
-        a, b = getattr(fused, name), getattr(plain, name)
-        assert (a is None and b is None) or torch.equal(a, b), name
     assert plain.grad_logits is None
     x, mean = sizes(l, T)
     at = np.take_along_axis(x, np.clip(t, 0, n - 1)[:, None], 1)[:, 0]
     d = np.where(live, row_error(mean, at, lp), 0.0)  # of the log-probabilities
     dH = np.where(live, row_error(mean, value=H) + 2.0 ** -18 * mean, 0.0)
-    close(as_numpy(plain.logprobs), np.where(live, lp, 0.0), d, "logprobs")
     # A term moves with lp by its slopes: A r and kl (e^q - 1), and each of its few operations by a step.
     ratio, A64 = np.exp(lp - as_numpy(old)), np.abs(as_numpy(A))
     e = np.exp(as_numpy(refs) - lp) if with_ref else np.zeros(rows)
     moves = A64 * ratio + abs(kl) * (e + 1)
     step = d + 2.0 ** -22 * (1 + np.abs(as_numpy(old) - lp))
     term = np.where(live, w64 * (moves * step + abs(entropy or 0) * dH), 0.0).sum()
-    close(as_numpy(plain.loss), want[0], term + 2.0 ** -23 * abs(want[0]), "loss")
-    close(as_numpy(plain.kl), want[1], np.where(live, w64 * (e + 1) * step, 0).sum(), "kl")
-    close(as_numpy(plain.clipped), want[2], 2.0 ** -23 * want[2], "clipped")
-    if entropy is not None:
-        close(as_numpy(plain.entropies), np.where(live, H, 0.0), dH, "entropies")
-        close(as_numpy(plain.entropy), want[3], np.where(live, w64 * dH, 0).sum() + 2.0 ** -23 * want[3], "entropy")
-    else:
-        assert plain.entropies is None and plain.entropy == 0
     # A slope is w (-A r + kl (1 - e^q)): relative to lp's error and its own operations.
     ds = np.where(live, w64 * moves * 2 * step, 0.0)
-    close(as_numpy(plain.slopes), want[4], ds, "slopes")
+    for r in (fused, plain):  # (not by the same kernel: a row's sums may be added up in another order)
+        close(as_numpy(r.logprobs), np.where(live, lp, 0.0), d, "logprobs")
+        close(as_numpy(r.loss), want[0], term + 2.0 ** -23 * abs(want[0]), "loss")
+        close(as_numpy(r.kl), want[1], np.where(live, w64 * (e + 1) * step, 0).sum(), "kl")
+        close(as_numpy(r.clipped), want[2], 2.0 ** -23 * want[2], "clipped")
+        if entropy is not None:
+            close(as_numpy(r.entropies), np.where(live, H, 0.0), dH, "entropies")
+            close(as_numpy(r.entropy), want[3], np.where(live, w64 * dH, 0).sum() + 2.0 ** -23 * want[3], "entropy")
+        else:
+            assert r.entropies is None and r.entropy == 0
+        close(as_numpy(r.slopes), want[4], ds, "slopes")
+        if entropy:
+            close(as_numpy(r.entropy_slopes), want[5], 2.0 ** -23 * np.abs(want[5]), "entropy slopes")
+        else:
+            assert r.entropy_slopes is None
     grad = ref.gradient(l, t, T, want[4], want[5])
     off = gradient_error(l, T, want[4], want[5], grad, dtype)
     p = np.where(np.isfinite(l), np.exp(-x), 0.0)
@@ -114,7 +116,7 @@ def test_left_out_tokens_hold_anything(pk, cuda_device, dtype, n):
     bad = torch.tensor([2, 5, 7], device=cuda_device)
     logits[bad], old[bad], A[bad], refs[bad] = float("nan"), INF, float("nan"), float("nan")
     got = pk.policy_loss(logits, tokens, old, A, weights=w, gradient=True, **how)
-    assert torch.equal(got.loss, want.loss) and torch.equal(got.grad_logits, want.grad_logits) and torch.equal(got.sums, want.sums)
+    assert torch.equal(got.loss, want.loss) and torch.equal(got.grad_logits, want.grad_logits) and all(torch.equal(a, b) for a, b in zip(got[:4], want[:4]))
     assert (got.grad_logits[bad] == 0).all() and (got.logprobs[bad] == 0).all()
     back = pk.policy_loss_backward(logits, tokens, got)
     assert (back[bad] == 0).all() and not back.isnan().any()
@@ -127,7 +129,7 @@ def test_left_out_tokens_hold_anything(pk, cuda_device, dtype, n):
 def test_no_token_at_all(pk, cuda_device):
     logits, tokens, old, A, refs, w, _, _ = policy_inputs(12, 5000, torch.bfloat16)
     r = pk.policy_loss(logits, tokens, old, A, weights=0 * w, ref_logprobs=refs, kl=1.0, entropy=1.0, gradient=True)
-    assert r.loss == 0 and (r.grad_logits == 0).all() and (r.sums == 0).all()
+    assert (r.grad_logits == 0).all() and all(t == 0 for t in r[:4])
     none = torch.empty(0, device=cuda_device)
     r = pk.policy_loss(logits[:0], tokens[:0], none, none, gradient=True)
     assert r.loss == 0 and r.grad_logits.shape == (0, 5000) and r.kl == 0
@@ -311,7 +313,7 @@ def test_equal_calls_give_equal_bits(pk, cuda_device):
         for _ in range(4):
             r = pk.policy_loss(logits, tokens, old, A, ref_logprobs=refs, weights=w, kl=0.1, entropy=0.1, gradient=True)
             q = pk.preference_loss(logits, tokens, offsets, ref_logprobs=refs)
-            now = [r.loss, r.sums, r.grad_logits, r.slopes, q.loss, q.margins, q.slopes]
+            now = [*r[:4], r.grad_logits, r.slopes, q.loss, q.margins, q.slopes]
             first = first or now
             assert all(torch.equal(a, b) for a, b in zip(now, first))
 

@@ -181,7 +181,7 @@ class StandIn:
         lp, H = ref.logprobs(logits.numpy(), tokens.numpy(), temperature)
         got = ref.policy(lp, H, old.numpy(), A.numpy(), None, np.full(len(lp), 1 / len(lp)), np.ones(len(lp), bool), low, high, kl, entropy)
         f = lambda v: torch.from_numpy(np.asarray(v)).float()  # noqa: E731
-        return f(got[0]), f(got[1:4]), f(lp), f(H), torch.zeros(len(lp), 2), f(got[4]), f(got[5]), None
+        return f(got[0]), f(got[1]), f(got[2]), f(got[3]), f(lp), f(H), torch.zeros(len(lp), 2), f(got[4]), f(got[5]), None
 
     def preference_loss(self, logits, tokens, offsets, refs, beta, smoothing, margin, average, temperature, stream):
         lp, _ = ref.logprobs(logits.numpy(), tokens.numpy(), temperature)
