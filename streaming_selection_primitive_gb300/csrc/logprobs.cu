@@ -11,6 +11,7 @@
 // (k_logprobs_short): one pass with a running maximum and sums, one exchange.  For a
 // policy loss with its gradient the same CTAs then go over their part again.
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -38,24 +39,36 @@ constexpr int MAX_CLUSTER = 8;
 template <typename T>
 constexpr int PER_VECTOR = 16 / int(sizeof(T));
 
-// Pair i of the elements in v.
+// Pair i of the elements in v.  BOUNDED: with -inf, and what is below LOWEST, as LOWEST (by one instruction
+// for two elements of 16 bits; small enough to be multiplied with any slope).
 template <typename T>
-__device__ __forceinline__ Pair element_pair(const uint4& v, int i);
+constexpr float LOWEST = -INFINITY;
 template <>
-__device__ __forceinline__ Pair element_pair<float>(const uint4& v, int i) {
-  return i == 0 ? pair(__uint_as_float(v.x), __uint_as_float(v.y)) : pair(__uint_as_float(v.z), __uint_as_float(v.w));
-}
+constexpr float LOWEST<__nv_bfloat16> = -0x1p40f;
+template <>
+constexpr float LOWEST<__half> = -65504.f;
+
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-template <>
-__device__ __forceinline__ Pair element_pair<__nv_bfloat16>(const uint4& v, int i) {
-  const uint32_t w = word(v, i);
-  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+template <typename T, bool BOUNDED>
+__device__ __forceinline__ Pair element_pair(const uint4& v, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return i == 0 ? pair(__uint_as_float(v.x), __uint_as_float(v.y)) : pair(__uint_as_float(v.z), __uint_as_float(v.w));
+  } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    uint32_t w = word(v, i);
+    if (BOUNDED) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(w), "r"(0xd380d380u));
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    uint32_t w = word(v, i);
+    if (BOUNDED) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(w) : "r"(w), "r"(0xfbfffbffu));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pair(f.x, f.y);
+  }
 }
-template <>
-__device__ __forceinline__ Pair element_pair<__half>(const uint4& v, int i) {
-  const uint32_t w = word(v, i);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pair(f.x, f.y);
+
+// Whether LOWEST may stand for -inf: it has no mass by this centre, and a finite exponent.
+template <typename T>
+__device__ __forceinline__ bool lowest_will_do(const Centre& at) {
+  return sizeof(T) == 2 && at.fused && (at.m - LOWEST<T>) * at.c > 200.f && at.c < 0x1p27f;
 }
 
 // The largest of all elements (NaN is passed over).
@@ -149,24 +162,30 @@ __device__ __forceinline__ void take(Running& r, const uint4 (&v)[COUNT], float 
   r.m = m;
   const Centre at(m, c);
   Pair s[2] = {0, 0}, t[2] = {0, 0};
-  const auto add = [&](Pair x, int i) {
+  // Of a -inf, x 2^x is to be 0, not inf * 0: x is bounded, or the logit has been.
+  const auto add = [&](Pair x, int i, auto bounded) {
     float x0, x1;
     split(x, x0, x1);
     const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
     s[i & 1] = add2(s[i & 1], e);
-    if (ENTROPY) t[i & 1] = fma2(pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i & 1]);
+    if (ENTROPY) t[i & 1] = fma2(decltype(bounded)::value ? x : pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), e, t[i & 1]);
   };
   const Pair by = pair(at.by, at.by), cc = pair(c, c);
-  if (at.fused) {
+  if (ENTROPY && lowest_will_do<T>(at)) {
 #pragma unroll
     for (int u = 0; u < COUNT; ++u)
 #pragma unroll
-      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(fma2(element_pair<T>(v[u], i), cc, by), i);
+      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(fma2(element_pair<T, true>(v[u], i), cc, by), i, std::true_type{});
+  } else if (at.fused) {
+#pragma unroll
+    for (int u = 0; u < COUNT; ++u)
+#pragma unroll
+      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(fma2(element_pair<T, false>(v[u], i), cc, by), i, std::false_type{});
   } else {
 #pragma unroll
     for (int u = 0; u < COUNT; ++u)
 #pragma unroll
-      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(mul2(add2(element_pair<T>(v[u], i), by), cc), i);
+      for (int i = 0; i < PER_VECTOR<T> / 2; ++i) add(mul2(add2(element_pair<T, false>(v[u], i), by), cc), i, std::false_type{});
   }
   float a, b;
   if (ENTROPY) {
@@ -258,76 +277,80 @@ __device__ __forceinline__ float slope_at(const Slopes& k, float l) {
   return e * (ENTROPY ? fmaf(k.k1, fmaxf(x, NO_MASS), k.k0) : k.k0);
 }
 
-// 16 bytes that begin `shift` bytes into the first of two vectors.
-__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int shift) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (shift & 8)
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  if (shift & 4)
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  const int bits = (shift & 3) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                    __funnelshift_r(w[3], w[4], bits));
+// 16 bytes from anywhere: words, of which half-words are put together where `odd` says that p does
+// not stand on one (then from the word before p to the one behind).
+__device__ __forceinline__ uint4 load_words(const char* p, bool odd) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(p - (odd ? 2 : 0));
+  uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+  if (odd) {
+    v.x = __funnelshift_r(v.x, v.y, 16);
+    v.y = __funnelshift_r(v.y, v.z, 16);
+    v.z = __funnelshift_r(v.z, v.w, 16);
+    v.w = __funnelshift_r(v.w, w[4], 16);
+  }
+  return v;
 }
 
 // The gradient of `count` elements from `p` (in global or in shared memory) to `out`, by STEP
 // threads; `token` is the token's place among them, out of range where it is none.  Where p and
-// out stand differently to the 16-byte boundaries, 16 bytes of the gradient come from two
-// vectors of p.  (p may be out: an element is read by the thread that writes it.)
+// out stand differently to the 16-byte boundaries, 16 bytes of the gradient come from p's words.  (p may be out: an element is read by the thread that writes it.)
 template <typename T, bool ENTROPY, int STEP, int COUNT = LOADS>
 __device__ __forceinline__ void write_gradient(const T* p, T* out, int count, int thread, int token, const Slopes& k) {
   constexpr int N = PER_VECTOR<T>, SIZE = sizeof(T);
   int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / SIZE, count);
   int vectors = (count - head) / N;
-  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p + head) & 15);
-  if (shift) {  // (nothing outside the elements is read: the first or last vector may be left to single threads)
-    if (vectors > 0 && shift > head * SIZE) {
-      head += N;
+  const bool same = (reinterpret_cast<uintptr_t>(p + head) & 15) == 0, odd = (reinterpret_cast<uintptr_t>(p + head) & 3) != 0;
+  if (odd) {  // (nothing outside the elements is read: the first or last vector may be left to single threads)
+    if (vectors > 0 && head == 0) {
+      head = N;
       --vectors;
     }
-    if (vectors > 0 && head * SIZE - shift + (vectors + 1) * 16 > count * SIZE) --vectors;
+    if (vectors > 0 && head + vectors * N == count) --vectors;
   }
   const int tail = count - head - vectors * N;
   const int single = thread < head ? thread : thread >= 16 && thread < 16 + tail ? head + vectors * N + thread - 16 : -1;
   if (single >= 0) out[single] = lm_cast<T>(slope_at<ENTROPY>(k, lm_float(p[single])) + (single == token ? k.one : 0.f));
-  const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p + head) - shift);
+  const char* from = reinterpret_cast<const char*>(p + head);
   uint4* to = reinterpret_cast<uint4*>(out + head);
   // The token's element is written once more by the thread that has its vector.
   const int place = token - head;
   const bool has_token = place >= 0 && place < vectors * N && (place / N) % STEP == thread;
   const float token_slope = has_token ? slope_at<ENTROPY>(k, lm_float(p[token])) + k.one : 0.f;
   const Pair by = pair(k.at.by, k.at.by), cc = pair(k.at.c, k.at.c), k0 = pair(k.k0, k.k0), k1 = pair(k.k1, k.k1);
+  const bool bounded = lowest_will_do<T>(k.at);
   for (int i = thread; i < vectors; i += COUNT * STEP) {
     uint4 v[COUNT];
-    if (shift) {
+    if (same) {
 #pragma unroll
       for (int u = 0; u < COUNT; ++u)
-        if (i + u * STEP < vectors) v[u] = shifted(from[i + u * STEP], from[i + u * STEP + 1], shift);
+        if (i + u * STEP < vectors) v[u] = reinterpret_cast<const uint4*>(from)[i + u * STEP];
     } else {
 #pragma unroll
       for (int u = 0; u < COUNT; ++u)
-        if (i + u * STEP < vectors) v[u] = from[i + u * STEP];
+        if (i + u * STEP < vectors) v[u] = load_words(from + int64_t(i + u * STEP) * 16, odd);
     }
 #pragma unroll
     for (int u = 0; u < COUNT; ++u) {
       const int j = i + u * STEP;
       if (j >= vectors) break;
       alignas(16) T y[N];
-      const auto put = [&](Pair x, int q) {
+      const auto put = [&](Pair x, int q, auto bounded) {
         float x0, x1, y0, y1;
         split(x, x0, x1);
         const Pair e = pair(lm_exp2(x0), lm_exp2(x1));
-        split(mul2(e, ENTROPY ? fma2(k1, pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS)), k0) : k0), y0, y1);
+        const Pair kept = decltype(bounded)::value ? x : pair(fmaxf(x0, NO_MASS), fmaxf(x1, NO_MASS));
+        split(mul2(e, ENTROPY ? fma2(k1, kept, k0) : k0), y0, y1);
         put_pair(y + 2 * q, y0, y1);
       };
-      if (k.at.fused) {
+      if (ENTROPY && bounded) {
 #pragma unroll
-        for (int q = 0; q < N / 2; ++q) put(fma2(element_pair<T>(v[u], q), cc, by), q);
+        for (int q = 0; q < N / 2; ++q) put(fma2(element_pair<T, true>(v[u], q), cc, by), q, std::true_type{});
+      } else if (k.at.fused) {
+#pragma unroll
+        for (int q = 0; q < N / 2; ++q) put(fma2(element_pair<T, false>(v[u], q), cc, by), q, std::false_type{});
       } else {
 #pragma unroll
-        for (int q = 0; q < N / 2; ++q) put(mul2(add2(element_pair<T>(v[u], q), by), cc), q);
+        for (int q = 0; q < N / 2; ++q) put(mul2(add2(element_pair<T, false>(v[u], q), by), cc), q, std::false_type{});
       }
       to[j] = *reinterpret_cast<const uint4*>(y);
     }
@@ -740,29 +763,45 @@ __device__ __forceinline__ TokenInputs token_inputs(const LogprobArgs& a, const 
 }
 
 __global__ void __launch_bounds__(JOIN_THREADS) k_policy_join(LogprobArgs a, PolicyHow how, PolicyOut out) {
+  constexpr int AHEAD = 4;  // rows whose inputs are on their way at once
   const int64_t step = int64_t(gridDim.x) * JOIN_THREADS;
   int64_t row = int64_t(blockIdx.x) * JOIN_THREADS + threadIdx.x;
-  TokenInputs next{};
-  if (row < a.rows) next = token_inputs(a, how, row);
+  TokenInputs in[AHEAD];
+  const auto load = [&] {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (row + i * step < a.rows) in[i] = token_inputs(a, how, row + i * step);
+  };
+  load();
   pdl_wait();
   pdl_trigger();
   Sum sums[4];  // loss, KL terms, clipped weights, entropies
-  for (; row < a.rows; row += step) {
-    const TokenInputs in = next;
-    if (row + step < a.rows) next = token_inputs(a, how, row + step);
-    const float lp = a.logprobs[row], H = a.entropies ? a.entropies[row] : 0.f;
-    float slope = 0.f, h = 0.f;
-    if (in.live) {
-      const PolicyTerm term = policy_term(lp, in.old_lp, in.advantage, how.ref_logprobs != nullptr, in.ref_lp, how);
-      sums[0].add(in.weight * (how.entropy != 0.f ? fmaf(-how.entropy, H, term.loss) : term.loss));
-      sums[1].add(in.weight * term.kl);
-      sums[2].add(term.clipped ? in.weight : 0.f);
-      sums[3].add(in.weight * H);
-      slope = in.weight * term.slope;
-      h = -how.entropy * in.weight;
+  while (row < a.rows) {
+    float lp[AHEAD], H[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const bool there = row + i * step < a.rows;
+      lp[i] = there ? a.logprobs[row + i * step] : 0.f;
+      H[i] = there && a.entropies ? a.entropies[row + i * step] : 0.f;
     }
-    out.slopes[row] = slope;
-    if (out.entropy_slopes) out.entropy_slopes[row] = h;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (row + i * step >= a.rows) break;
+      float slope = 0.f, h = 0.f;
+      if (in[i].live) {
+        const PolicyTerm term = policy_term(lp[i], in[i].old_lp, in[i].advantage, how.ref_logprobs != nullptr, in[i].ref_lp, how);
+        sums[0].add(in[i].weight * (how.entropy != 0.f ? fmaf(-how.entropy, H[i], term.loss) : term.loss));
+        sums[1].add(in[i].weight * term.kl);
+        sums[2].add(term.clipped ? in[i].weight : 0.f);
+        sums[3].add(in[i].weight * H[i]);
+        slope = in[i].weight * term.slope;
+        h = -how.entropy * in[i].weight;
+      }
+      out.slopes[row + i * step] = slope;
+      if (out.entropy_slopes) out.entropy_slopes[row + i * step] = h;
+    }
+    row += AHEAD * step;
+    load();
   }
   cluster_sum(sums);
   if (blockIdx.x == 0 && threadIdx.x == 0) {

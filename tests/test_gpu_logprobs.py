@@ -279,3 +279,138 @@ def test_messages(pk, cuda_device):
             (lambda: pk.token_logprobs_backward(z[:5], t[:5], r, grad_logprobs=one), ValueError, "stats must have shape")):
         with pytest.raises(error, match=words):
             call()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,n", [(5000, 700), (2500, 6000), (4000, 9000), (700, 5000), (1300, 16400), (40, 70001), (5, 300_000)])
+def test_many_rows_and_parts(pk, cuda_device, dtype, rows, n):
+    # Rows by warps that go on to others, by CTAs, and by clusters of 2 to 8 of them.
+    logits, tokens, g = make(rows, n, dtype, left_out=0.1)
+    r = pk.token_logprobs(logits, tokens, entropy=True)
+    dg = torch.randn(rows, generator=g, device=cuda_device)
+    grad = pk.token_logprobs_backward(logits, tokens, r, grad_logprobs=dg)
+    some = torch.tensor(sorted({0, 1, rows // 2, rows - 2, rows - 1}), device=cuda_device)  # against the definition
+    l, t = as_numpy(logits[some]), tokens[some].cpu().numpy()
+    lp, H = ref.logprobs(l, t)
+    x, mean = sizes(l, 1.0)
+    at = np.take_along_axis(x, np.clip(t, 0, n - 1)[:, None], 1)[:, 0]
+    close(as_numpy(r.logprobs[some]), lp, row_error(mean, at, lp))
+    close(as_numpy(r.entropies[some]), H, row_error(mean, value=H) + 2.0 ** -18 * mean)
+    want = ref.gradient(l, t, 1.0, as_numpy(dg[some]))
+    close(as_numpy(grad[some]), want, gradient_error(l, 1.0, as_numpy(dg[some]), None, want, dtype))
+    # and all of them against the same rows in smaller batches, which go other ways through the kernels
+    for part in torch.arange(rows, device=cuda_device).split(max(1, rows // 7)):
+        q = pk.token_logprobs(logits[part], tokens[part], entropy=True)
+        torch.testing.assert_close(q.logprobs, r.logprobs[part], rtol=2.0 ** -20, atol=2.0 ** -17)
+        torch.testing.assert_close(q.entropies, r.entropies[part], rtol=2.0 ** -20, atol=2.0 ** -16)
+
+
+def test_host_threads(pk, cuda_device):
+    # Four threads, each with inputs and a stream of its own.
+    import threading
+
+    def work(i, out):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            n = (200, 3000, 40000, 9000)[i]
+            logits, tokens, g = make(20 + i, n, torch.bfloat16, seed=i)
+            zero = torch.zeros(20 + i, device=cuda_device)
+            for _ in range(30):
+                r = pk.token_logprobs(logits, tokens, entropy=True)
+                p = pk.policy_loss(logits, tokens, r.logprobs, 1 + zero, gradient=True)
+                d = pk.token_logprobs_backward(logits, tokens, r, grad_logprobs=1 + zero)
+                h = pk.token_logprobs(logits[:, :184], tokens % 64, weight=logits[:8, :184].contiguous().repeat(8, 1)) if n % 8 == 0 else r
+            stream.synchronize()
+            out[i] = [t.cpu() for t in (r.logprobs, r.entropies, p.loss, p.grad_logits, d, h.logprobs)]
+
+    alone, together = {}, {}
+    for i in range(4):
+        work(i, alone)
+    threads = [threading.Thread(target=work, args=(i, together)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(a, b) for i in range(4) for a, b in zip(alone[i], together[i]))
+
+
+@pytest.mark.parametrize("call", ["logprobs", "backward", "policy", "preference", "head"])
+def test_outputs_on_another_stream_leave_freed_blocks_alone(pk, cuda_device, call):
+    # Work queued on the current stream on tensors that have been let go: outputs of a call on another stream must not
+    # be made from their memory.
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        z, t, g = make(512, 640, torch.bfloat16)
+        one = torch.ones(512, device=cuda_device)
+        o = torch.arange(0, 513, 64, device=cuda_device)
+        r = pk.token_logprobs(z, t, entropy=True)
+        few = t % 64
+    calls = {"logprobs": lambda **s: pk.token_logprobs(z, t, entropy=True, **s)[:3],
+             "backward": lambda **s: (pk.token_logprobs_backward(z, t, r, grad_logprobs=one, **s),),
+             "policy": lambda **s: [v for v in pk.policy_loss(z, t, r.logprobs, one, gradient=True, **s)[:10] if v is not None],
+             "preference": lambda **s: pk.preference_loss(z, t, o[:5], **s)[:5],
+             "head": lambda **s: pk.token_logprobs(z, few, weight=z[:64], entropy=True, **s)[:2]}
+    with torch.cuda.stream(side):
+        want = calls[call]()
+    torch.cuda.synchronize()
+    freed = [torch.full((v.untyped_storage().nbytes() // 4,), 7.0, device=cuda_device) for v in want]
+    kept = [torch.zeros_like(f) for f in freed]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for a, b in zip(kept, freed):
+        a.copy_(b)
+    spans = [(f.data_ptr(), f.data_ptr() + f.numel() * 4) for f in freed]
+    del freed, a, b
+    got = calls[call](stream=side)
+    assert not any(lo <= v.data_ptr() < hi for v in got for lo, hi in spans)
+    side.synchronize()
+    assert all(torch.equal(x.cpu(), y.cpu()) for x, y in zip(got, want))
+    torch.cuda.synchronize()
+    assert all((k == 7).all() for k in kept)
+
+
+def test_forward_mode_and_transforms_are_refused(pk, cuda_device):
+    import torch.autograd.forward_ad as fwd
+    z, t, _ = make(10, 16, torch.float32)
+    one = torch.ones(10, device=cuda_device)
+    o = torch.tensor([0, 5, 10], device=cuda_device)
+    r = pk.token_logprobs(z, t)
+    h = z.bfloat16()
+    with fwd.dual_level():
+        dual = lambda v: fwd.make_dual(v, torch.ones_like(v))  # noqa: E731
+        for call in (lambda: pk.token_logprobs(dual(z), t), lambda: pk.token_logprobs(z, t, temperature=dual(one)),
+                     lambda: pk.token_logprobs_backward(z, t, r, grad_logprobs=dual(one)), lambda: pk.policy_loss(dual(z), t, one, one),
+                     lambda: pk.policy_loss(z, t, dual(one), one), lambda: pk.policy_loss(z, t, one, one, weights=dual(one)),
+                     lambda: pk.preference_loss(dual(z), t, o), lambda: pk.preference_loss(z, t, o, ref_logprobs=dual(one)),
+                     lambda: pk.token_logprobs(dual(h), t, weight=h), lambda: pk.token_logprobs(h, t, weight=dual(h))):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+    with pytest.raises(Exception):
+        torch.func.grad(lambda v: pk.token_logprobs(v, t).logprobs.sum())(z)
+    with pytest.raises(Exception):
+        torch.vmap(lambda v: pk.token_logprobs(v, t).logprobs)(z.expand(3, 10, 16))
+
+
+@pytest.mark.parametrize("of", ["logprobs", "policy", "preference"])
+def test_a_second_derivative_raises(pk, cuda_device, of):
+    z, t, _ = make(10, 16, torch.float32)
+    z = z.clone().requires_grad_()
+    one = torch.ones(10, device=cuda_device)
+    y = {"logprobs": lambda: pk.token_logprobs(z, t).logprobs.sum(), "policy": lambda: pk.policy_loss(z, t, -2 * one, one).loss,
+         "preference": lambda: pk.preference_loss(z, t, torch.tensor([0, 5, 10], device=cuda_device)).loss}[of]()
+    grad, = torch.autograd.grad(y, z, create_graph=True)
+    with pytest.raises(NotImplementedError):
+        (y * 0 + grad.square().sum()).backward()
+
+
+def test_inputs_changed_in_between_are_noticed(pk, cuda_device):
+    z, t, _ = make(10, 16, torch.float32)
+    z = z.clone().requires_grad_()
+    for change in ("logits", "tokens"):
+        x = z * 1.0
+        tokens = t.clone()
+        r = pk.token_logprobs(x, tokens)
+        (x.detach() if change == "logits" else tokens).zero_()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            r.logprobs.sum().backward()

@@ -336,3 +336,54 @@ def test_messages(pk, cuda_device):
             (lambda: pk.preference_loss(z, t, torch.zeros(3, dtype=torch.int64, device=cuda_device), beta=INF), pk.ProfkError, "")):
         with pytest.raises(error, match=words):
             call()
+
+
+def test_rows_longer_than_shared_memory(pk, cuda_device):
+    # Beyond 8 x 112 KB a row is read twice.
+    check_policy(pk, 2, 500_001, torch.bfloat16)
+    check_policy(pk, 3, 240_000, torch.float32, with_ref=False, entropy=None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [3, 700])
+def test_rows_kept_whole_and_in_parts(pk, cuda_device, dtype, rows):
+    # Sizes about those at which the number of CTAs a row or of their threads changes.
+    for n in (8191, 8193, 16384, 16400, 33000, 65536) if rows == 3 else (4097, 8190, 8200, 16390):
+        check_policy(pk, rows, n, dtype, left_out=0.1, entropy=None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_logits_and_sharp_temperatures(pk, cuda_device, dtype):
+    for n in (300, 9001, 40000):
+        check_policy(pk, 7, n, dtype, T=0.02, kl=0.0, with_ref=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [300, 9001])
+@pytest.mark.parametrize("T", [1e-3, 1.0, 900.0, 1e5])
+def test_masked_logits_at_all_temperatures(pk, cuda_device, dtype, n, T):
+    # -inf, and the type's lowest value, at temperatures at which a bounded stand-in would or would not have mass.
+    logits, tokens, g = make(8, n, dtype, spread=3.0 * min(1.0, T * 10))
+    logits[:, n // 3: n // 2] = -INF
+    logits[3, n // 2: n // 2 + 9] = torch.finfo(dtype).min
+    logits[4, : n // 3] = logits[4, n // 2:] = torch.finfo(dtype).min
+    tokens.fill_(n - 1)
+    h = torch.full((8,), 1000.0, device=cuda_device)
+    dg = torch.randn(8, generator=g, device=cuda_device)
+    r = pk.token_logprobs(logits, tokens, temperature=T, entropy=True)
+    got = pk.token_logprobs_backward(logits, tokens, r, grad_logprobs=dg, grad_entropies=h)
+    assert not got.isnan().any() and not r.entropies.isnan().any()
+    l, t = as_numpy(logits), tokens.cpu().numpy()
+    lp, H = ref.logprobs(l, t, T)
+    x, mean = sizes(l, T)
+    at = np.take_along_axis(x, t[:, None], 1)[:, 0]
+    close(as_numpy(r.logprobs), lp, row_error(mean, at, lp))
+    close(as_numpy(r.entropies), H, row_error(mean, value=H) + 2.0 ** -18 * mean)
+    want = ref.gradient(l, t, T, as_numpy(dg), as_numpy(h))
+    # An entropy's slope takes the mean of x as log s - H, each with its rounding: 2^-22 of their sizes.
+    extra = 1000.0 / T * np.where(np.isfinite(l), np.exp(-x), 0.0) / np.exp(-x).sum(1, keepdims=True) * (2.0 ** -21 * (np.log(n) + np.abs(H)))[:, None]
+    off = gradient_error(l, T, as_numpy(dg), as_numpy(h), want, dtype) + extra
+    if dtype == torch.float16:  # from 65520 on its rounding is infinite
+        want = np.where(np.abs(want) - off > 65520, np.copysign(INF, want), want)
+    close(as_numpy(got), want, off)
+    assert (got[:, n // 3: n // 2] == 0).all()
