@@ -490,7 +490,8 @@ int profk_token_logprobs(const void* logits, int type, int64_t rows, int64_t n, 
  *   grad_logprobs, grad_entropies  device, rows float, or NULL
  *   scale        device, one float, or NULL: 1
  *   grad_logits  device, row r at r*grad_ld elements, n values of `type`; it may
- *                be the logits themselves (grad_ld = ld) */
+ *                be the logits themselves (grad_ld = ld), but not lie across them
+ *                (PROFK_ERR_INVALID, by the ranges from the first to the last element) */
 int profk_token_logprobs_backward(const void* logits, int type, int64_t rows, int64_t n, int64_t ld,
                                   const int64_t* tokens, const float* temperature, float all_temperature,
                                   const float* stats, const float* entropies, const float* grad_logprobs,
@@ -535,8 +536,9 @@ typedef struct profk_policy {
  *   out_slopes         device, rows floats: d loss / d logprob (for the backward call)
  *   out_entropy_slopes device, rows floats: d loss / d entropy, or NULL
  *   grad_logits        device, or NULL: the gradient of the loss with respect to the logits,
- *                      from the same launch; as in profk_token_logprobs_backward, which gives
- *                      the same from out_slopes.  It may be the logits themselves */
+ *                      from the same launch; profk_token_logprobs_backward gives it from
+ *                      out_slopes too, to rounding.  It may be the logits themselves
+ *                      (grad_ld = ld), but not lie across them */
 int profk_policy_loss(const void* logits, int type, int64_t rows, int64_t n, int64_t ld, const int64_t* tokens,
                       const float* temperature, float all_temperature, const profk_policy* how, float* out_loss,
                       float* out_sums, float* out_logprobs, float* out_entropies, float* out_stats, float* out_slopes,

@@ -17,12 +17,16 @@ from . import _abi, _lm
 from ._lm import _torch
 
 
-def _call(name: str, *args):
-    """A call of the native half; its status raises."""
-    r = getattr(_lm._ext or _lm._native(), name)(*args)
+def _ext():
+    """The native half.  Its calls return their outputs and the temperature, or a status."""
+    return _lm._ext or _lm._native()
+
+
+def _made(kind, r):
+    """The outputs as a named tuple (made without its constructor, a Python function); a status raises."""
     if type(r) is int:
         _abi.check(r)
-    return r
+    return tuple.__new__(kind, r) if kind else r
 
 
 def _handle(stream):
@@ -84,11 +88,11 @@ def token_logprobs(x, tokens, *, weight=None, temperature=1.0, entropy: bool = F
     Where logits requires a gradient, logprobs and entropies carry it (token_logprobs_backward).  From
     hidden states there is no gradient: what requires one raises, unless under torch.no_grad()."""
     if weight is not None:
-        return TokenLogprobs(*_call("head_logprobs", x, weight, tokens, temperature, bool(entropy), _handle(stream)), temperature)
+        return _made(TokenLogprobs, _ext().head_logprobs(x, weight, tokens, temperature, bool(entropy), _handle(stream)))
     if getattr(x, "requires_grad", False) and _torch().is_grad_enabled():
         out = _record(x, stream, "token_logprobs", tokens, temperature, (bool(entropy),), {"temperature": temperature})
         return TokenLogprobs(*out, temperature)
-    return TokenLogprobs(*_call("token_logprobs", x, tokens, temperature, bool(entropy), _handle(stream)), temperature)
+    return _made(TokenLogprobs, _ext().token_logprobs(x, tokens, temperature, bool(entropy), _handle(stream)))
 
 
 def token_logprobs_backward(logits, tokens, r: TokenLogprobs, *, grad_logprobs=None, grad_entropies=None, out=None, stream=None):
@@ -99,8 +103,8 @@ def token_logprobs_backward(logits, tokens, r: TokenLogprobs, *, grad_logprobs=N
     logits themselves.  The result comes without a graph."""
     if r.stats is None:
         raise ValueError("there is no gradient from hidden states: give logits")
-    return _call("token_logprobs_backward", logits, tokens, r.temperature, r.stats, r.entropies, grad_logprobs, grad_entropies, None,
-                 out, _handle(stream))
+    return _made(None, _ext().token_logprobs_backward(logits, tokens, r.temperature, r.stats, r.entropies, grad_logprobs, grad_entropies,
+                                                      None, out, _handle(stream)))
 
 
 def policy_loss(logits, tokens, old_logprobs, advantages, *, ref_logprobs=None, weights=None, temperature=1.0,
@@ -126,16 +130,16 @@ def policy_loss(logits, tokens, old_logprobs, advantages, *, ref_logprobs=None, 
         r = _record(logits, stream, "policy_loss", tokens, temperature,
                     (old_logprobs, advantages, ref_logprobs, weights, clip_low, clip_high, kl, entropy), constants)
         return PolicyLoss(*r, None, temperature)
-    return PolicyLoss(*_call("policy_loss", logits, tokens, old_logprobs, advantages, ref_logprobs, weights, temperature, clip_low,
-                             clip_high, kl, entropy, bool(gradient), out, _handle(stream)), temperature)
+    return _made(PolicyLoss, _ext().policy_loss(logits, tokens, old_logprobs, advantages, ref_logprobs, weights, temperature, clip_low,
+                                                clip_high, kl, entropy, bool(gradient), out, _handle(stream)))
 
 
 def policy_loss_backward(logits, tokens, r: PolicyLoss, *, grad_loss=None, out=None, stream=None):
     """Gradient of policy_loss()'s loss with respect to the logits, in their type.
 
     grad_loss: a float32 tensor of one element on the device; None: 1.  out: as in token_logprobs_backward."""
-    return _call("token_logprobs_backward", logits, tokens, r.temperature, r.stats, r.entropies, r.slopes, r.entropy_slopes, grad_loss,
-                 out, _handle(stream))
+    return _made(None, _ext().token_logprobs_backward(logits, tokens, r.temperature, r.stats, r.entropies, r.slopes, r.entropy_slopes,
+                                                      grad_loss, out, _handle(stream)))
 
 
 def preference_loss(logits, tokens, offsets, *, ref_logprobs=None, beta: float = 0.1, label_smoothing: float = 0.0,
@@ -157,15 +161,16 @@ def preference_loss(logits, tokens, offsets, *, ref_logprobs=None, beta: float =
                     (offsets, ref_logprobs, beta, label_smoothing, margin, bool(average)),
                     {"ref_logprobs": ref_logprobs, "temperature": temperature})
         return PreferenceLoss(*r, temperature)
-    return PreferenceLoss(*_call("preference_loss", logits, tokens, offsets, ref_logprobs, beta, label_smoothing, margin, bool(average),
-                                 temperature, _handle(stream)), temperature)
+    return _made(PreferenceLoss, _ext().preference_loss(logits, tokens, offsets, ref_logprobs, beta, label_smoothing, margin, bool(average),
+                                                        temperature, _handle(stream)))
 
 
 def preference_loss_backward(logits, tokens, r: PreferenceLoss, *, grad_loss=None, out=None, stream=None):
     """Gradient of preference_loss()'s loss with respect to the logits, in their type.
 
     grad_loss: a float32 tensor of one element on the device; None: 1.  out: as in token_logprobs_backward."""
-    return _call("token_logprobs_backward", logits, tokens, r.temperature, r.stats, None, r.slopes, None, grad_loss, out, _handle(stream))
+    return _made(None, _ext().token_logprobs_backward(logits, tokens, r.temperature, r.stats, None, r.slopes, None, grad_loss, out,
+                                                      _handle(stream)))
 
 
 def _record(logits, stream, name, tokens, temperature, args, constants):
@@ -190,8 +195,8 @@ def _autograd():
         def gradient(logits, tokens, stats, entropies, slopes, entropy_slopes, temperature, scale):
             def plain(t):
                 return None if t is None else t.detach().float().contiguous()
-            return _call("token_logprobs_backward", logits.detach(), tokens, temperature, stats, entropies, plain(slopes),
-                         plain(entropy_slopes), plain(scale), None, None)
+            return _made(None, _ext().token_logprobs_backward(logits.detach(), tokens, temperature, stats, entropies, plain(slopes),
+                                                              plain(entropy_slopes), plain(scale), None, None))
 
         class Logprobs(torch.autograd.Function):
             @staticmethod
@@ -199,15 +204,15 @@ def _autograd():
                 x = logits.detach()
                 entropies = entropy_slopes = slopes = None
                 if name == "token_logprobs":
-                    out = _call(name, x, tokens, temperature, *args, None)
+                    out = _made(None, _ext().token_logprobs(x, tokens, temperature, *args, None))[:3]
                     _, entropies, stats = out
                     constants = (stats,)
                 elif name == "policy_loss":
-                    out = _call(name, x, tokens, *args[:4], temperature, *args[4:], False, None, None)[:9]
+                    out = _made(None, _ext().policy_loss(x, tokens, *args[:4], temperature, *args[4:], False, None, None))[:9]
                     entropies, stats, slopes, entropy_slopes = out[5:]
                     constants = out[1:]
                 else:
-                    out = _call(name, x, tokens, *args, temperature, None)
+                    out = _made(None, _ext().preference_loss(x, tokens, *args, temperature, None))[:5]
                     _, margins, logprobs, stats, slopes = out
                     constants = (margins, logprobs, stats, slopes)
                 ctx.mark_non_differentiable(*(t for t in constants if t is not None))

@@ -144,6 +144,16 @@ PyObject* tuple_of(std::initializer_list<Tensor> tensors) {
   return t;
 }
 
+// The same with a Python object behind the tensors.
+PyObject* tuple_of(std::initializer_list<Tensor> tensors, PyObject* last) {
+  PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()) + 1);
+  if (!t) throw python_error();
+  Py_ssize_t i = 0;
+  for (const Tensor& x : tensors) PyTuple_SET_ITEM(t, i++, x.defined() ? THPVariable_Wrap(x) : Py_NewRef(Py_None));
+  PyTuple_SET_ITEM(t, i, Py_NewRef(last));
+  return t;
+}
+
 void expect(Py_ssize_t got, Py_ssize_t want) {
   if (got != want) refuse(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
 }
@@ -292,8 +302,8 @@ struct Temperature {
 };
 
 // Several float32 outputs in one piece of memory: a small call's time is spent in making its
-// tensors, and most of that in asking for their memory (a policy loss 14.2 us, and
-// 10.2 so).  They are
+// tensors, and most of that in asking for their memory (a policy loss 14 us, and
+// 10 so).  They are
 // tensors of their own to autograd, and the memory lives as long as any of them.
 class Floats {
  public:
@@ -351,7 +361,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   if (arg[3] == Py_True) entropies = floats.take({x.rows});
   const int code = profk_token_logprobs(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, data(logprobs),
                                         data(entropies), data(stats), place.stream());
-  return code == PROFK_OK ? tuple_of({logprobs, entropies, stats}) : PyLong_FromLong(code);
+  return code == PROFK_OK ? tuple_of({logprobs, entropies, stats}, arg[2]) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
 
@@ -416,7 +426,7 @@ PyObject* head_logprobs(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int code = profk_head_logprobs(hidden.data_ptr(), weight.data_ptr(), s == at::kHalf ? PROFK_F16 : PROFK_BF16, rows, n,
                                        width, rows > 1 ? hidden_ld : whole_rows, n > 1 ? weight_ld : whole_rows, tokens, T.rows,
                                        T.all, data(logprobs), data(entropies), place.stream());
-  return code == PROFK_OK ? tuple_of({logprobs, entropies, Tensor()}) : PyLong_FromLong(code);
+  return code == PROFK_OK ? tuple_of({logprobs, entropies, Tensor()}, arg[3]) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
 
@@ -453,7 +463,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int code = profk_policy_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, &how, data(loss),
                                      data(kl), data(logprobs), data(entropies), data(stats), data(slopes),
                                      data(entropy_slopes), grad.defined() ? grad.data_ptr() : nullptr, grad_ld, place.stream());
-  return code == PROFK_OK ? tuple_of({loss, kl, clipped, entropies_sum, logprobs, entropies, stats, slopes, entropy_slopes, grad}) : PyLong_FromLong(code);
+  return code == PROFK_OK ? tuple_of({loss, kl, clipped, entropies_sum, logprobs, entropies, stats, slopes, entropy_slopes, grad}, arg[6]) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
 
@@ -478,7 +488,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int code = profk_preference_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all,
                                          static_cast<const int64_t*>(o.data_ptr()), pairs, &how, data(loss), data(margins),
                                          data(logprobs), data(stats), data(slopes), place.stream());
-  return code == PROFK_OK ? tuple_of({loss, margins, logprobs, stats, slopes}) : PyLong_FromLong(code);
+  return code == PROFK_OK ? tuple_of({loss, margins, logprobs, stats, slopes}, arg[8]) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
 

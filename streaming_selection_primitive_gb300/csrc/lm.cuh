@@ -73,7 +73,7 @@ __device__ __forceinline__ float warp_max(float v) {
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_clusters_most(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, size_t smem,
                                         size_t most, cudaStream_t stream, Args... args) {
-  if (most > 48 * 1024) {
+  if (smem > 48 * 1024) {  // (with less any limit will do)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }

@@ -7,9 +7,23 @@
 //   logprob = ln 2 x_token - ln s,   H = ln s - ln 2 t / s,
 //   d(g logprob + h H) / d l_i = [g 1(i = token) - p_i (g + h ln 2 (x_i - t / s))] / T,  p_i = 2^x_i / s.
 //
-// A row is taken by a cluster of CTAs (k_logprobs) or, where it is short, by a warp
-// (k_logprobs_short): one pass with a running maximum and sums, one exchange.  For a
-// policy loss with its gradient the same CTAs then go over their part again.
+// A row is taken by a CTA or a cluster of them (k_logprobs) or, where it is short, by a warp
+// (k_logprobs_short): one pass with a running maximum and sums, one exchange.  A policy
+// loss with its gradient keeps the row in shared memory between its sums and its gradient
+// (k_policy_keep); only rows beyond 8 x 112 KB are read twice.  The sums over rows are a small
+// kernel of their own, and the gradient of the rest is one (k_logprobs_backward): from
+// saved maxima and sums, a row read and written once.
+//
+// What bounds it (device times by captured calls, inputs beyond L2; MB are what has to move):
+//   many rows: memory.  4096 x 131072 bfloat16 forward 163 us (1074 MB, 6.6 TB/s), with policy loss
+//     and gradient 335 (2148 MB, 6.4 TB/s), and 478 when the row was read a second time: L2 kept nothing
+//     of what 608 CTAs had in work.  Forward and backward of 1500 x 128003 float32 347 (2304 MB, 6.6 TB/s).
+//   entropies of 16-bit logits, more so into a gradient that stands otherwise to the 16-byte boundaries:
+//     instructions.  600 x 100001 float16 issues 2.9 of 4 a cycle at 45 % of the memory's rate;
+//     1001 of them 79 us (370 MB, 4.7 TB/s), 264 with single stores.
+//   rows of 10 to 60 KB: a CTA's beginning and end, 4 to 5 us of which eight on an SM hide most.
+//     1000 x 16384 bfloat16 forward 9.4 us (33 MB), 12.5 by CTAs of 256 threads.
+//   few rows: latency.  1 x 32768 2.9 us, of which the launch is 2.5; 16 of them with policy loss and gradient 6.6.
 #include <algorithm>
 #include <type_traits>
 
@@ -402,6 +416,7 @@ __device__ __forceinline__ bool row_live(const LogprobArgs& a, int64_t row) {
 template <bool GRADIENT>
 __device__ __forceinline__ Row<GRADIENT> load_inputs(const LogprobArgs& a, const PolicyHow& how, int64_t row) {
   Row<GRADIENT> r;
+  r.logit = 0.f;
   r.token = a.tokens[row];
   r.temperature = a.temperature ? a.temperature[row] : a.all_temperature;
   r.c = inverse_temperature(r.temperature);
@@ -464,13 +479,15 @@ struct Exchange {
     barrier_arrive_expect(&all, parts * COUNT * sizeof(RowSum));
   }
   // By all threads, once every CTA of the cluster has begun: the row's sums, the same in
-  // every warp; by m itself.
+  // every warp; by m itself.  The logit of the row's token comes from the first warp of all: whoever
+  // writes a gradient over the logits does so after it has been read.
   template <bool ENTROPY>
-  __device__ __forceinline__ RowSum join(RowSum y, float c, int parts, int rank) {
+  __device__ __forceinline__ RowSum join(RowSum y, float& logit, float c, int parts, int rank) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane < parts) store_remote(&sums[rank * COUNT + warp], make_float4(y.m, y.s, y.t, 0.f), &all, lane);
-    if (!__all_sync(FULL_MASK, barrier_wait(&all, 0, &given_up, WAIT_POLLS))) return {0.f, NAN, NAN};
-    y = {-INFINITY, 0.f, 0.f};
+    if (lane < parts) store_remote(&sums[rank * COUNT + warp], make_float4(y.m, y.s, y.t, logit), &all, lane);
+    if (!__all_sync(FULL_MASK, barrier_wait(&all, 0, &given_up, WAIT_POLLS))) return {0.f, NAN, NAN, NAN};
+    logit = sums[0].logit;
+    y = {-INFINITY, 0.f, 0.f, 0.f};
     for (int i = lane; i < parts * COUNT; i += 32) y = joined(y, sums[i], c);
     y = centred(warp_join<ENTROPY>(y, c), c);
     if (!(c > 0.f)) y.s = NAN;
@@ -490,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 8) k_logprobs(LogprobArgs a, PolicyHo
   const T* p = static_cast<const T*>(a.logits) + row * a.ld;
   T* out = static_cast<T*>(a.grad_logits) + row * a.grad_ld;
   Row<GRADIENT> r = load_inputs<GRADIENT>(a, how, row);
-  load_logit(r, p, n);
+  if (rank == 0 && thread < 32) load_logit(r, p, n);
   if (!r.live) {  // the same for the whole cluster: none of it waits
     if (rank == 0 && thread == 0) store_left_out(a, row);
     if (GRADIENT) {
@@ -509,7 +526,7 @@ __global__ void __launch_bounds__(THREADS, 8) k_logprobs(LogprobArgs a, PolicyHo
   const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
   RowSum y = warp_join<ENTROPY>(total(pass<T, ENTROPY, THREADS>(reinterpret_cast<const uint4*>(p + at.head), begin, end, thread, alone, r.c)), r.c);
   cluster_begun();
-  y = exchange.template join<ENTROPY>(y, r.c, parts, rank);
+  y = exchange.template join<ENTROPY>(y, r.logit, r.c, parts, rank);
   const float lp = store_row(a, row, y, r.logit, r.temperature, rank == 0 && thread == 0);
   if (GRADIENT) {
     const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
@@ -601,7 +618,7 @@ __global__ void __launch_bounds__(KEEP_THREADS, 1024 / KEEP_THREADS) k_policy_ke
   __syncthreads();
   cluster_begin();
   Row<true> r = load_inputs<true>(a, how, row);
-  load_logit(r, p, n);
+  if (rank == 0 && thread < 32) load_logit(r, p, n);
   const Span<T> mine(at, begin, end, rank == 0, rank == parts - 1);
   T* copy = reinterpret_cast<T*>(room + 16) - (rank == 0 ? at.head : 0);  // the span's first element
   const int single = at.single(thread, rank == 0, rank == parts - 1);
@@ -612,7 +629,7 @@ __global__ void __launch_bounds__(KEEP_THREADS, 1024 / KEEP_THREADS) k_policy_ke
   RowSum y = warp_join<ENTROPY>(
       total(pass_shared<T, ENTROPY, KEEP_THREADS>(reinterpret_cast<const uint4*>(room + 16), end - begin, thread, alone, r.c)), r.c);
   if (!__all_sync(FULL_MASK, there)) y.s = NAN;
-  y = exchange.template join<ENTROPY>(y, r.c, parts, rank);
+  y = exchange.template join<ENTROPY>(y, r.logit, r.c, parts, rank);
   const float lp = store_row(a, row, y, r.logit, r.temperature, rank == 0 && thread == 0);
   const Slopes k = policy_slopes<ENTROPY>(r, y, lp, how);
   write_gradient<T, ENTROPY, KEEP_THREADS, KEEP_LOADS>(copy, out + mine.first, mine.count, thread, place_in(r.token, a.n, mine.first), k);

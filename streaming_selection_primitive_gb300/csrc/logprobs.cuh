@@ -75,18 +75,18 @@ __device__ __forceinline__ float shrink(float from, float to, float c) {
   return fmaxf(from == -INFINITY ? NO_MASS : a.fused && b.fused ? b.by - a.by : (a.m - b.m) * c, NO_MASS);
 }
 
-// Row results that the kernels exchange.
+// Row results that the kernels exchange (and the logit of the row's token with them, where they do).
 struct alignas(16) RowSum {
-  float m, s, t;
+  float m, s, t, logit;
 };
 
-__device__ __forceinline__ RowSum total(const Running& r) { return {r.m, r.s + r.s_lost, r.t + r.t_lost}; }
+__device__ __forceinline__ RowSum total(const Running& r) { return {r.m, r.s + r.s_lost, r.t + r.t_lost, 0.f}; }
 
 // Sums by the centre of m as sums by m itself (to which m's own logit gives 1, whatever was rounded).
 __device__ __forceinline__ RowSum centred(const RowSum& y, float c) {
   const float r = Centre(y.m, c).off(), f = lm_exp2(-r);
   const float s = f * y.s;
-  return {y.m, s > 0.f && s < 1.f ? 1.f : s, f * (y.t - r * y.s)};
+  return {y.m, s > 0.f && s < 1.f ? 1.f : s, f * (y.t - r * y.s), 0.f};
 }
 
 // Joins over the warp: all lanes get the same, in the same order every time.
@@ -96,14 +96,14 @@ __device__ __forceinline__ RowSum warp_join(RowSum r, float c) {
   const float d = shrink(r.m, m, c), f = lm_exp2(d);
   const float s = warp_sum(r.s * f);
   const float t = ENTROPY ? warp_sum(f * (r.t + d * r.s)) : 0.f;
-  return {m, s, t};
+  return {m, s, t, 0.f};
 }
 
 // Two parts of a row as one.
 __device__ __forceinline__ RowSum joined(const RowSum& y, const RowSum& z, float c) {
   const float m = fmaxf(y.m, z.m), dy = shrink(y.m, m, c), dz = shrink(z.m, m, c);
   const float fy = lm_exp2(dy), fz = lm_exp2(dz);
-  return {m, fy * y.s + fz * z.s, fy * (y.t + dy * y.s) + fz * (z.t + dz * z.s)};
+  return {m, fy * y.s + fz * z.s, fy * (y.t + dy * y.s) + fz * (z.t + dz * z.s), 0.f};
 }
 
 // A token's log-probability from its logit and the row's sums: -inf where the row holds

@@ -1,5 +1,6 @@
-// The tensor cores' instructions as head.cu uses them: asynchronous tile copies, the
-// product with its accumulator in tensor memory, and barriers whose waits are bounded.
+// Instructions of the asynchronous units, as logprobs.cu and head.cu use them: barriers in
+// shared memory whose waits are bounded, copies that count on them, stores to other CTAs of
+// a cluster, and (head.cu) products on the tensor cores with their accumulators in tensor memory.
 #pragma once
 
 #include <cstdint>
@@ -61,7 +62,8 @@ __device__ __forceinline__ void cluster_begun() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 16 bytes to the same place of CTA `rank`'s shared memory, counted on its barrier.
+// 16 bytes to the same place of CTA `rank`'s shared memory, counted on its barrier.  Only in kernels that
+// are launched as clusters, of one CTA too: without the launch's attribute this is an illegal instruction.
 __device__ __forceinline__ void store_remote(void* to, float4 v, uint64_t* counted_on, int rank) {
   uint32_t a, b;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(to)), "r"(rank));

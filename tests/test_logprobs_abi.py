@@ -169,7 +169,7 @@ class StandIn:
     def token_logprobs(self, logits, tokens, temperature, entropy, stream):
         lp, H = ref.logprobs(logits.numpy(), tokens.numpy(), temperature)
         f = lambda v: torch.from_numpy(np.asarray(v)).float()  # noqa: E731
-        return f(lp), f(H) if entropy else None, torch.zeros(len(lp), 2)
+        return f(lp), f(H) if entropy else None, torch.zeros(len(lp), 2), temperature
 
     def token_logprobs_backward(self, logits, tokens, temperature, stats, entropies, g, h, scale, out, stream):
         s = 1.0 if scale is None else scale.item()
@@ -181,13 +181,13 @@ class StandIn:
         lp, H = ref.logprobs(logits.numpy(), tokens.numpy(), temperature)
         got = ref.policy(lp, H, old.numpy(), A.numpy(), None, np.full(len(lp), 1 / len(lp)), np.ones(len(lp), bool), low, high, kl, entropy)
         f = lambda v: torch.from_numpy(np.asarray(v)).float()  # noqa: E731
-        return f(got[0]), f(got[1]), f(got[2]), f(got[3]), f(lp), f(H), torch.zeros(len(lp), 2), f(got[4]), f(got[5]), None
+        return f(got[0]), f(got[1]), f(got[2]), f(got[3]), f(lp), f(H), torch.zeros(len(lp), 2), f(got[4]), f(got[5]), None, temperature
 
     def preference_loss(self, logits, tokens, offsets, refs, beta, smoothing, margin, average, temperature, stream):
         lp, _ = ref.logprobs(logits.numpy(), tokens.numpy(), temperature)
         loss, d, slopes = ref.preference(lp, tokens.numpy(), offsets.numpy(), None, beta, smoothing, margin, average)
         f = lambda v: torch.from_numpy(np.asarray(v)).float()  # noqa: E731
-        return f(loss), f(d), f(lp), torch.zeros(len(lp), 2), f(slopes)
+        return f(loss), f(d), f(lp), torch.zeros(len(lp), 2), f(slopes), temperature
 
 
 @pytest.fixture()
