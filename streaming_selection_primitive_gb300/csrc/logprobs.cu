@@ -485,7 +485,7 @@ struct Exchange {
   __device__ __forceinline__ RowSum join(RowSum y, float& logit, float c, int parts, int rank) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane < parts) store_remote(&sums[rank * COUNT + warp], make_float4(y.m, y.s, y.t, logit), &all, lane);
-    if (!__all_sync(FULL_MASK, barrier_wait(&all, 0, &given_up, WAIT_POLLS))) return {0.f, NAN, NAN, NAN};
+    if (!__all_sync(FULL_MASK, barrier_wait<true>(&all, 0, &given_up, WAIT_POLLS))) return {0.f, NAN, NAN, NAN};
     logit = sums[0].logit;
     y = {-INFINITY, 0.f, 0.f, 0.f};
     for (int i = lane; i < parts * COUNT; i += 32) y = joined(y, sums[i], c);
@@ -625,6 +625,7 @@ __global__ void __launch_bounds__(KEEP_THREADS, 1024 / KEEP_THREADS) k_policy_ke
   const float alone = single >= 0 ? lm_float(p[single]) : -INFINITY;
   if (single >= 0) copy[single - mine.first] = p[single];
   cluster_begun();  // (the barriers are there, in all CTAs)
+  __syncthreads();  // (and so are the single elements)
   const bool there = barrier_wait(&full, 0, &exchange.given_up, WAIT_POLLS);
   RowSum y = warp_join<ENTROPY>(
       total(pass_shared<T, ENTROPY, KEEP_THREADS>(reinterpret_cast<const uint4*>(room + 16), end - begin, thread, alone, r.c)), r.c);

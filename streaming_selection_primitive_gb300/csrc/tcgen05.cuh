@@ -26,23 +26,35 @@ __device__ __forceinline__ void barrier_arrive_expect(uint64_t* b, unsigned byte
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(b)), "r"(bytes) : "memory");
 }
 
+// CLUSTER: what other CTAs of the cluster wrote before their arrivals is seen, too.
+template <bool CLUSTER>
 __device__ __forceinline__ bool barrier_passed(uint64_t* b, unsigned parity) {
   unsigned ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(shared_address(b)), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(shared_address(b)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(shared_address(b)), "r"(parity)
+        : "memory");
   return ok != 0;
 }
 
 // Waits for the phase of that parity; false if it did not come within `limit` polls or
 // another warp of the CTA has given up (*given_up, in shared memory, which this sets too).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool barrier_wait(uint64_t* b, unsigned parity, volatile int* given_up, int limit) {
   for (int poll = 0; poll < limit; ++poll) {
-    if (barrier_passed(b, parity)) return true;
+    if (barrier_passed<CLUSTER>(b, parity)) return true;
     if (*given_up) return false;
   }
   *given_up = 1;
