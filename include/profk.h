@@ -562,7 +562,7 @@ typedef struct profk_preference {
  * the mean of the pairs' terms (0 without a pair).
  *   offsets      device, 2*pairs + 1 int64, not falling, within 0 .. rows.  Rows before
  *                the first and from the last on are left out.  A sequence whose offsets are
- *                not so makes its pair's margin and the loss NaN
+ *                not so makes its pair's margin and the loss NaN (its rows' slopes are not set)
  *   out_loss     device, one float
  *   out_margins  device, pairs floats: d
  *   out_slopes   device, rows floats: d loss / d logprob (for the backward call) */

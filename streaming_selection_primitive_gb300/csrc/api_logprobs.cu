@@ -172,7 +172,7 @@ int profk_preference_loss(const void* logits, int type, int64_t rows, int64_t n,
   if (!aligned(offsets, 8) || !floats(how->ref_logprobs, out_loss, out_margins, out_logprobs, out_slopes) || !aligned(out_stats, 8))
     return PROFK_ERR_UNSUPPORTED;
   LogprobArgs a = row_args(logits, type, rows, n, ld, tokens, temperature, all_temperature, out_logprobs, nullptr, out_stats);
-  a.zeros = out_slopes;
+  a.lacks = out_slopes;  // until the slopes are there
   a.offsets = offsets;
   a.sequences = 2 * pairs;
   const PreferenceHow h{how->ref_logprobs, how->beta, how->label_smoothing, how->margin, how->average != 0};

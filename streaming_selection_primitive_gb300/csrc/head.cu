@@ -40,8 +40,16 @@ constexpr int DEPTH = 64;   // of a piece: 128 bytes a row, the widest swizzle
 constexpr int MAX_STAGES = 6;  // pieces in the ring
 constexpr int TAKERS = 8;   // warps that take tiles: two for each quarter of the lanes
 constexpr int COPIER = TAKERS, MULTIPLIER = TAKERS + 1;  // the other two warps
-constexpr int THREADS = 32 * (TAKERS + 2);
+constexpr int THREADS = 32 * (TAKERS + 4);  // (two warps have nothing to do: registers are handed over by groups of four)
+// Registers a thread where a tile has segments: of 168 at the launch the takers, who hold 128 sums each,
+// get more from the others.  (256 * 232 + 128 * 40 = 384 * 168.)
+constexpr int TAKER_REGISTERS = 232, OTHER_REGISTERS = 40;
 constexpr int TENSOR_COLUMNS = 2 * TILE_TOKENS;  // all there are: two accumulators
+// Pieces whose products the tensor cores add up.  They cut their sums off instead of rounding them, and what
+// that takes away grows with the depth: 3453 deep it put log-probabilities off by 1.6e-6 of themselves, in
+// two segments by 7e-7 (a float32 product: 5e-7).  Segments are added by the takers, which costs 4096 x 4096 x
+// 32768 650 us instead of 604; segments of 1024 would be 3.6e-7, and 2048 x 131072 1285 us instead of 1161.
+constexpr int SEGMENT = 32;
 constexpr int PARTS = 2;    // a row's columns are taken by two threads, 32 by 32 in turn
 
 constexpr int ROWS_BYTES = TILE_ROWS * DEPTH * 2;
@@ -54,6 +62,7 @@ constexpr int SHARED_BYTES = RING_BYTES + ROWS_BYTES + 1024;  // (the last produ
 struct Plan {
   int rows;   // rows of hidden states that are copied for a tile: a multiple of 8
   int row_tiles, token_tiles, run, runs, pieces, stages;
+  int segments;  // of a tile
   // A stage: the rows, then the tokens.  Of fewer rows than a tile has the product takes what comes
   // behind them for the others (whose results nobody looks at).
   __host__ __device__ int rows_bytes() const { return rows * DEPTH * 2; }
@@ -66,6 +75,9 @@ struct Barriers {
   uint32_t tensor;                       // address of the tensor memory
   int given_up;
 };
+
+// The pieces of a tile up to the end of a segment (whose lengths differ by one at most).
+__device__ __forceinline__ int segment_end(const Plan& plan, int segment) { return plan.pieces * (segment + 1) / plan.segments; }
 
 template <bool ENTROPY>
 __device__ __forceinline__ void take_columns(RowSum& r, float (&v)[32], float c) {
@@ -104,7 +116,8 @@ __device__ __forceinline__ void take_columns(RowSum& r, float (&v)[32], float c)
   r.s += a + b;
 }
 
-template <bool ENTROPY>
+// SEGMENTS: a tile has more than one.
+template <bool ENTROPY, bool SEGMENTS>
 __global__ void __launch_bounds__(THREADS, 1)
     k_head(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, HeadArgs a, Plan plan, uint32_t product,
            float4* parts, int count, float* logits, WaitCfg waits) {
@@ -133,84 +146,91 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
   pdl_trigger();  // (behind it: what follows may read what this reads)
 
-  if (warp == COPIER) {
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      unsigned parity = 1;  // (the ring begins empty)
-      for (int run = blockIdx.x; run < plan.runs && !sync.given_up; run += gridDim.x) {
-        const int row0 = run % plan.row_tiles * TILE_ROWS, first = run / plan.row_tiles * plan.run;
-        const int last = min(first + plan.run, plan.token_tiles);
+  if (warp >= TAKERS) {
+    if constexpr (SEGMENTS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGISTERS));
+    if (warp == COPIER) {
+      if (lane == 0) {
+        int stage = 0, issued = 0;
+        unsigned parity = 1;  // (the ring begins empty)
+        for (int run = blockIdx.x; run < plan.runs && !sync.given_up; run += gridDim.x) {
+          const int row0 = run % plan.row_tiles * TILE_ROWS, first = run / plan.row_tiles * plan.run;
+          const int last = min(first + plan.run, plan.token_tiles);
+          bool ok = true;
+          for (int tile = first; tile < last && ok; ++tile)
+            for (int piece = 0; piece < plan.pieces; ++piece) {
+              ok = barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit);
+              if (!ok) break;
+              uint8_t* to = ring + stage * stage_bytes;
+              barrier_arrive_expect(&sync.full[stage], stage_bytes);
+              copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[stage]);
+              copy_tile(to + rows_bytes, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[stage]);
+              issued = min(issued + 1, stages);
+              if (++stage == stages) {
+                stage = 0;
+                parity ^= 1;
+              }
+            }
+        }
+        // The last products' arrivals on the ring.
+        for (int i = 0; i < stages && !sync.given_up; ++i) {
+          if (!barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit)) break;
+          if (++stage == stages) {
+            stage = 0;
+            parity ^= 1;
+          }
+          issued = 0;
+        }
+        if (sync.given_up && issued > 0) {
+          // Nobody may be reading any more, but copies may still be writing: the last turn of each
+          // stage is waited for.  (Whoever has given up has set the flag, which these waits are not to look at.)
+          int nobody = 0;
+          for (int i = 0; i < issued; ++i) {
+            if (stage == 0) parity ^= 1;
+            stage = stage ? stage - 1 : stages - 1;
+            nobody = 0;
+            barrier_wait(&sync.full[stage], parity ^ 1, &nobody, WAIT_POLLS);
+          }
+        }
+      }
+    } else if (warp == MULTIPLIER) {
+      if (lane == 0) {
+        int stage = 0, half = 0;
+        unsigned parity = 0, taken = 1;  // (both accumulators begin free)
         bool ok = true;
-        for (int tile = first; tile < last && ok; ++tile)
-          for (int piece = 0; piece < plan.pieces; ++piece) {
-            ok = barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit);
-            if (!ok) break;
-            uint8_t* to = ring + stage * stage_bytes;
-            barrier_arrive_expect(&sync.full[stage], stage_bytes);
-            copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[stage]);
-            copy_tile(to + rows_bytes, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[stage]);
-            issued = min(issued + 1, stages);
-            if (++stage == stages) {
-              stage = 0;
-              parity ^= 1;
-            }
-          }
-      }
-      // The last products' arrivals on the ring.
-      for (int i = 0; i < stages && !sync.given_up; ++i) {
-        if (!barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit)) break;
-        if (++stage == stages) {
-          stage = 0;
-          parity ^= 1;
-        }
-        issued = 0;
-      }
-      if (sync.given_up && issued > 0) {
-        // Nobody may be reading any more, but copies may still be writing: the last turn of each
-        // stage is waited for.  (Whoever has given up has set the flag, which these waits are not to look at.)
-        int nobody = 0;
-        for (int i = 0; i < issued; ++i) {
-          if (stage == 0) parity ^= 1;
-          stage = stage ? stage - 1 : stages - 1;
-          nobody = 0;
-          barrier_wait(&sync.full[stage], parity ^ 1, &nobody, WAIT_POLLS);
-        }
-      }
-    }
-  } else if (warp == MULTIPLIER) {
-    if (lane == 0) {
-      int stage = 0, half = 0;
-      unsigned parity = 0, taken = 1;  // (both accumulators begin free)
-      bool ok = true;
-      for (int run = blockIdx.x; run < plan.runs && ok; run += gridDim.x) {
-        const int first = run / plan.row_tiles * plan.run, last = min(first + plan.run, plan.token_tiles);
-        for (int tile = first; tile < last && ok; ++tile) {
-          ok = barrier_wait(&sync.taken[half], taken, &sync.given_up, limit);
-          if (!ok) break;
-          after_barrier();
-          const uint32_t to = tensor + half * TILE_TOKENS;
-          for (int piece = 0; piece < plan.pieces; ++piece) {
-            ok = barrier_wait(&sync.full[stage], parity, &sync.given_up, limit);
-            if (!ok) break;
-            after_barrier();
-            const uint64_t x = tile_descriptor(ring + stage * stage_bytes), w = tile_descriptor(ring + stage * stage_bytes + rows_bytes);
+        for (int run = blockIdx.x; run < plan.runs && ok; run += gridDim.x) {
+          const int first = run / plan.row_tiles * plan.run, last = min(first + plan.run, plan.token_tiles);
+          for (int tile = first; tile < last && ok; ++tile) {
+            for (int segment = 0, piece = 0; segment < plan.segments && ok; ++segment) {
+              const int end = SEGMENTS ? segment_end(plan, segment) : plan.pieces;
+              ok = barrier_wait(&sync.taken[half], taken, &sync.given_up, limit);
+              if (!ok) break;
+              after_barrier();
+              const uint32_t to = tensor + half * TILE_TOKENS;
+              for (int first_piece = piece; piece < end; ++piece) {
+                ok = barrier_wait(&sync.full[stage], parity, &sync.given_up, limit);
+                if (!ok) break;
+                after_barrier();
+                const uint64_t x = tile_descriptor(ring + stage * stage_bytes), w = tile_descriptor(ring + stage * stage_bytes + rows_bytes);
 #pragma unroll
-            for (int k = 0; k < DEPTH / 16; ++k)  // 32 bytes on along the rows: 2 in the descriptor's units
-              multiply(to, x + 2 * k, w + 2 * k, product, piece + k > 0);
-            products_arrive(&sync.empty[stage]);
-            if (++stage == stages) {
-              stage = 0;
-              parity ^= 1;
+                for (int k = 0; k < DEPTH / 16; ++k)  // 32 bytes on along the rows: 2 in the descriptor's units
+                  multiply(to, x + 2 * k, w + 2 * k, product, piece - first_piece + k > 0);
+                products_arrive(&sync.empty[stage]);
+                if (++stage == stages) {
+                  stage = 0;
+                  parity ^= 1;
+                }
+              }
+              if (!ok) break;
+              products_arrive(&sync.done[half]);
+              half ^= 1;
+              if (half == 0) taken ^= 1;
             }
           }
-          if (!ok) break;
-          products_arrive(&sync.done[half]);
-          half ^= 1;
-          if (half == 0) taken ^= 1;
         }
       }
     }
   } else {
+    if constexpr (SEGMENTS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TAKER_REGISTERS));
     const int quarter = warp & 3, side = warp >> 2;
     int half = 0;
     unsigned done = 0;
@@ -223,16 +243,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t token = in ? a.tokens[row] : -1;
       RowSum sum{-INFINITY, 0.f, 0.f, 0.f};
       for (int tile = first; tile < last && ok; ++tile) {
-        ok = __all_sync(FULL_MASK, barrier_wait(&sync.done[half], done, &sync.given_up, limit));
-        if (!ok) break;
-        after_barrier();
-        const uint32_t from = tensor + (uint32_t(quarter * 32) << 16) + half * TILE_TOKENS;
         const int64_t column0 = int64_t(tile) * TILE_TOKENS;
-#pragma unroll 1
-        for (int i = side * 32; i < TILE_TOKENS; i += 32 * PARTS) {
-          float v[32];
-          tensor_load(v, from + i);
-          tensor_loaded();
+        const auto take = [&](float(&v)[32], int i) {
           const int64_t column = column0 + i;
           if (column + 32 > a.n) {  // behind the vocabulary
 #pragma unroll
@@ -248,12 +260,49 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (at >= 0 && at < 32 && token < a.n) logits[row] = logit;
           }
           take_columns<ENTROPY>(sum, v, c);
+        };
+        const uint32_t lanes = tensor + (uint32_t(quarter * 32) << 16) + side * 32;
+        const auto wait_done = [&] {
+          ok = __all_sync(FULL_MASK, barrier_wait(&sync.done[half], done, &sync.given_up, limit));
+          after_barrier();
+          return ok;
+        };
+        const auto have_taken = [&] {
+          before_barrier();
+          __syncwarp();
+          if (lane == 0) barrier_arrive(&sync.taken[half]);
+          half ^= 1;
+          if (half == 0) done ^= 1;
+        };
+        constexpr int STEP = 32 * PARTS, MINE = TILE_TOKENS / STEP;  // this side's columns, 32 at a time
+        if constexpr (SEGMENTS) {
+          float v[MINE][32];
+          for (int segment = 0; segment < plan.segments; ++segment) {
+            if (!wait_done()) break;
+#pragma unroll
+            for (int i = 0; i < MINE; ++i) {
+              float w[32];
+              tensor_load(w, lanes + half * TILE_TOKENS + i * STEP);
+              tensor_loaded();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[i][j] = segment == 0 ? w[j] : v[i][j] + w[j];
+            }
+            have_taken();
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) take(v[i], side * 32 + i * STEP);
+        } else {
+          if (!wait_done()) break;
+#pragma unroll 1
+          for (int i = 0; i < MINE; ++i) {
+            float v[32];
+            tensor_load(v, lanes + half * TILE_TOKENS + i * STEP);
+            tensor_loaded();
+            take(v, side * 32 + i * STEP);
+          }
+          have_taken();
         }
-        before_barrier();
-        __syncwarp();
-        if (lane == 0) barrier_arrive(&sync.taken[half]);
-        half ^= 1;
-        if (half == 0) done ^= 1;
       }
       if (!ok) sum.s = NAN;
       if (in) parts[(row * count + index) * PARTS + side] = make_float4(sum.m, sum.s, sum.t, 0.f);
@@ -333,6 +382,7 @@ Plan plan_for(const HeadArgs& a) {
   p.rows = static_cast<int>(std::min<int64_t>(TILE_ROWS, (a.rows + 7) / 8 * 8));
   p.pieces = static_cast<int>((a.width + DEPTH - 1) / DEPTH);
   p.token_tiles = static_cast<int>((a.n + TILE_TOKENS - 1) / TILE_TOKENS);
+  p.segments = (p.pieces + SEGMENT - 1) / SEGMENT;
   p.stages = std::min(MAX_STAGES, RING_BYTES / p.stage_bytes());
   // Runs of up to 4 tiles, while there are 8 runs or more for each SM.
   const int64_t tiles = int64_t(p.row_tiles) * p.token_tiles;
@@ -360,7 +410,8 @@ cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   float4* parts = reinterpret_cast<float4*>(work);
   float* logits = reinterpret_cast<float*>(work + part_bytes);
-  const auto kernel = a.entropies ? k_head<true> : k_head<false>;
+  const bool segments = plan.segments > 1;
+  const auto kernel = a.entropies ? (segments ? k_head<true, true> : k_head<true, false>) : (segments ? k_head<false, true> : k_head<false, false>);
   const unsigned grid = std::min(plan.runs, sms());
   err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED_BYTES);
   if (err == cudaSuccess)

@@ -83,7 +83,7 @@ struct LogprobArgs {
   float* logprobs;
   float* entropies;        // or null
   float2* stats;           // or null: largest logit, sum of exp((l - largest) / T)
-  float* zeros;            // or null: every row gets 0
+  float* lacks;            // or null: what each log-probability lacks as a float (0 of a row left out)
   const float* weights;    // or null; a row of weight 0 is left out
   const int64_t* offsets;  // or null; sequences + 1 of them: rows before the first and from the last on are left out
   int64_t sequences;

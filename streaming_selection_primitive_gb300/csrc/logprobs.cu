@@ -439,16 +439,17 @@ __device__ __forceinline__ void store_left_out(const LogprobArgs& a, int64_t row
   a.logprobs[row] = 0.f;
   if (a.entropies) a.entropies[row] = 0.f;
   if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
-  if (a.zeros) a.zeros[row] = 0.f;
+  if (a.lacks) a.lacks[row] = 0.f;
 }
 
 __device__ __forceinline__ float store_row(const LogprobArgs& a, int64_t row, const RowSum& y, float logit, float temperature, bool write) {
-  const float lp = row_logprob(y, logit, temperature);
+  float lacks;
+  const float lp = row_logprob(y, logit, temperature, lacks);
   if (write) {
     a.logprobs[row] = lp;
     if (a.entropies) a.entropies[row] = row_entropy(y);
     if (a.stats) a.stats[row] = make_float2(y.m, y.s);
-    if (a.zeros) a.zeros[row] = 0.f;
+    if (a.lacks) a.lacks[row] = lacks;
   }
   return lp;
 }
@@ -876,7 +877,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a,
         for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM) {
           const float lp = a.logprobs[row], ref = how.ref_logprobs ? how.ref_logprobs[row] : 0.f;
           if (a.tokens[row] >= 0) {
-            sum[side].add(lp - ref);
+            sum[side].add(lp);
+            sum[side].add(-ref);
+            sum[side].lost += out.slopes[row];  // (what lp lacks: the slopes come in its place)
             ++live[side];
           }
         }

@@ -106,10 +106,37 @@ __device__ __forceinline__ RowSum joined(const RowSum& y, const RowSum& z, float
   return {m, fy * y.s + fz * z.s, fy * (y.t + dy * y.s) + fz * (z.t + dz * z.s), 0.f};
 }
 
-// A token's log-probability from its logit and the row's sums: -inf where the row holds
-// nothing, NaN where it holds a NaN or +inf.
+// ln s as a float and what it lacks, for s >= 1: from s = 2^k f with f in [1, 2), whose logarithm is off by less
+// than that of s (2^-25 of at most 0.7, not of 20).  k times the head of ln 2 (15 bits) is exact.
+__device__ __forceinline__ float log_exactly(float s, float& lacks) {
+  const int bits = __float_as_int(s), k = (bits >> 23) - 127;
+  const float f = __int_as_float((bits & 0x7fffff) | 0x3f800000);
+  constexpr float HEAD = 0.693145751953125f, REST = 1.42860682030941723e-6f;  // ln 2 = HEAD + REST
+  const float a = k * HEAD, b = logf(f), y = a + b, back = y - a;
+  lacks = ((a - (y - back)) + (b - back)) + k * REST;
+  return y;
+}
+
+// A token's log-probability from its logit and the row's sums, and what the float lacks (sums over a
+// sequence take it along): -inf where the row holds nothing, NaN where it holds a NaN or +inf.
+__device__ __forceinline__ float row_logprob(const RowSum& r, float logit, float T, float& lacks) {
+  lacks = 0.f;
+  if (r.s == 0.f) return -INFINITY;
+  if (!(r.s < INFINITY)) return NAN;
+  float of_log;
+  const float a = logit - r.m, x = a / T, L = log_exactly(r.s, of_log);
+  const float y = x - L;
+  if (!(fabsf(y) < INFINITY)) return y;
+  const float back = y - x;
+  const float of_x = fabsf(x) > 0x1p-100f ? fmaf(-x, T, a) / T : 0.f;
+  lacks = ((x - (y - back)) + (-L - back)) + (of_x - of_log);
+  const float z = y + lacks;
+  lacks += y - z;
+  return z;
+}
 __device__ __forceinline__ float row_logprob(const RowSum& r, float logit, float T) {
-  return r.s == 0.f ? -INFINITY : (logit - r.m) / T - logf(r.s);
+  float lacks;
+  return row_logprob(r, logit, T, lacks);
 }
 
 // log s - (sum x exp x) / s; 0 for a row that holds nothing.

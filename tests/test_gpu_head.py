@@ -49,7 +49,8 @@ def check(pk, hidden, weight, tokens, T=1.0, **how):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,width,n", [(1, 1, 1), (1, 8, 3), (3, 17, 40), (5, 64, 255), (17, 65, 256), (2, 100, 257), (129, 72, 513),
                                           (128, 128, 512), (64, 1000, 1000), (300, 333, 1500), (1, 1024, 5001), (16, 512, 40000),
-                                          (7, 2048, 3001), (257, 40, 20011), (1000, 16, 700)])
+                                          (7, 2048, 3001), (257, 40, 20011), (1000, 16, 700), (130, 2049, 700), (64, 4100, 600),
+                                          (3, 9000, 300), (300, 2112, 40000)])
 def test_sizes(pk, cuda_device, dtype, rows, width, n):
     hidden, weight, tokens = inputs(rows, width, n, dtype, left_out=0.2)
     tokens[0], tokens[-1] = 0, n - 1
@@ -118,9 +119,22 @@ def test_no_rows_and_refusals(pk, cuda_device):
         assert torch.equal(pk.token_logprobs(hidden, tokens, weight=weight).logprobs, r.logprobs)
 
 
-def test_a_wait_that_runs_out(pk, cuda_device):
+@pytest.mark.parametrize("width", [1000, 2048, 3000, 6000])
+def test_deep_products_keep_their_precision(pk, cuda_device, width):
+    # The tensor cores cut sums off: each of the 128 steps of a segment of 2048 products loses half a unit of the sum so
+    # far on average (2^-24), and that is half of the whole on average: 128 * 2^-24 / 2 = 2^-18 of a logit; a
+    # log-probability is the difference of two such, of no more than its own size and twice it.  (One segment of 6000
+    # would be 2^-16.4.)
+    hidden, weight, tokens = inputs(500, width, 700, torch.float16)
+    got = as_numpy(pk.token_logprobs(hidden, tokens, weight=weight).logprobs)
+    want, _ = ref.logprobs(as_numpy(hidden) @ as_numpy(weight).T, tokens.cpu().numpy())
+    assert np.linalg.norm(got - want) < 2.0 ** -18 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("width", [200, 2500])
+def test_a_wait_that_runs_out(pk, cuda_device, width):
     # A barrier that waits for one arrival more than comes, with a bound of 4096 polls: the kernel gives up and says so.
-    hidden, weight, tokens = inputs(300, 200, 9000, torch.bfloat16)
+    hidden, weight, tokens = inputs(300, width, 9000, torch.bfloat16)
     tokens[5] = -1
     want = pk.token_logprobs(hidden, tokens, weight=weight)
     pk.set_option(pk.OPT_HEAD_WAIT_TEST, 1)

@@ -387,3 +387,14 @@ def test_masked_logits_at_all_temperatures(pk, cuda_device, dtype, n, T):
         want = np.where(np.abs(want) - off > 65520, np.copysign(INF, want), want)
     close(as_numpy(got), want, off)
     assert (got[:, n // 3: n // 2] == 0).all()
+
+
+def test_margins_of_long_answers(pk, cuda_device):
+    # A float32 log-probability is off by up to 2^-23 of 4 to 8 from its rounding alone; the sums take what it lacks along,
+    # so that a margin over 2 x 2000 tokens is off by their rows' sums (2^-24 each, of either sign) and not by that.
+    logits, tokens, g = make(4000, 700, torch.float16)
+    offsets = torch.tensor([0, 2000, 4000], device=cuda_device)
+    lp, _ = ref.logprobs(as_numpy(logits), tokens.cpu().numpy())
+    r = pk.preference_loss(logits, tokens, offsets, beta=1.0)
+    want = lp[:2000].sum() - lp[2000:].sum()
+    assert abs(r.margins.item() - want) < 2.0 ** -24 * abs(want) + 4000 ** 0.5 * 2.0 ** -23
