@@ -119,3 +119,60 @@ def test_a_step_captured_into_a_graph(pk, cuda_device):
         got = [t.clone() for t in out]
         want = step()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_step_with_autograd_captured_into_a_graph(pk, cuda_device):
+    g = torch.Generator(device=cuda_device).manual_seed(7)
+    hidden = torch.randn((48, 64), generator=g, device=cuda_device)
+    first = torch.randn((5000, 64), generator=g, device=cuda_device) * 0.2
+    tokens = torch.randint(5000, (48,), generator=g, device=cuda_device)
+    old, A = torch.full((48,), -8.6, device=cuda_device), torch.randn(48, generator=g, device=cuda_device)
+    offsets = torch.tensor([0, 12, 24, 36, 48], device=cuda_device)
+
+    def step(weight):
+        logits = hidden @ weight.t()
+        r = pk.policy_loss(logits, tokens, old, A, entropy=0.1)
+        loss = r.loss + pk.preference_loss(logits, tokens, offsets).loss + pk.token_logprobs(logits, tokens).logprobs.mean()
+        weight.grad = None
+        loss.backward()
+        return loss.detach()
+
+    leaf = first.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(leaf)
+    torch.cuda.current_stream().wait_stream(side)
+    leaf.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = step(leaf)
+    for _ in range(2):
+        hidden.copy_(torch.randn((48, 64), generator=g, device=cuda_device))
+        graph.replay()
+        other = first.clone().requires_grad_()
+        want = step(other)
+        assert torch.equal(loss, want) and torch.equal(leaf.grad, other.grad)
+
+
+def test_without_dependent_launches_the_bits_are_the_same(pk, cuda_device):
+    g = torch.Generator(device=cuda_device).manual_seed(8)
+    for rows, n in ((700, 304), (60, 20000), (2, 500_000)):
+        z = torch.randn((rows, n), generator=g, device=cuda_device).bfloat16()
+        t = torch.randint(n, (rows,), generator=g, device=cuda_device)
+        one = torch.ones(rows, device=cuda_device)
+        offsets = torch.tensor([0, rows // 2, rows], device=cuda_device)
+
+        def calls():
+            r = pk.token_logprobs(z, t, entropy=True)
+            p = pk.policy_loss(z, t, r.logprobs - 0.05, one, ref_logprobs=r.logprobs, kl=0.1, entropy=0.1, gradient=True)
+            q = pk.preference_loss(z, t, offsets)
+            h = pk.token_logprobs(z[:, :96], t % 96, weight=z[:2, :96].repeat(48, 1))
+            return [*r[:3], *p[:10], *q[:5], pk.preference_loss_backward(z, t, q), h.logprobs]
+
+        want = calls()
+        pk.set_option(pk.OPT_PDL, 0)
+        got = calls()
+        pk.set_option(pk.OPT_PDL, 1)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
