@@ -25,6 +25,7 @@
 //     1000 x 16384 bfloat16 forward 9.4 us (33 MB), 12.5 by CTAs of 256 threads.
 //   few rows: latency.  1 x 32768 2.9 us, of which the launch is 2.5; 16 of them with policy loss and gradient 6.6.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -983,15 +984,20 @@ unsigned short_grid(int64_t rows, bool once) {
   return static_cast<unsigned>(once ? all : std::min<int64_t>(all, SHORT_PER_SM * sms()));
 }
 
-// CTAs a row, of 8 KB or more each: what takes the fewest rounds of CTAs on the SMs, where a CTA costs
-// as much as 24 KB besides its own (500 x 65536 bfloat16, two CTAs a row: 14.1 us, one 16.6; 1500 x 128003 float32, four:
-// 347 us forward and backward, one 371).
+// CTAs a row, of 8 KB or more each: the number that is quickest by what a CTA was measured to take, 0.35 us of its
+// SM's time for its beginning and end, and its part of the row at the memory's rate, shared with the others that run
+// at once, or (fewer of them) at the 11 KB a microsecond that its own loads in flight allow.  (300 x 128000 bfloat16
+// 17.4 us by two CTAs a row, 25.7 by one and 21.2 by four; 300 x 128003 float32 30.7, 47.5, 36.8;
+// 1500 of them 120, 133, 129; 700 x 50001 27.7 by one, 31.4 by two; 200 x 16384 bfloat16 3.8 by two, 4.2 by one.)
 int cluster_for(int64_t rows, int64_t n, int type) {
-  const int64_t bytes = row_bytes(n, type), slots = 8 * sms();
+  constexpr double EACH = 0.35, RATE = 6700., OWN = 11.;  // microseconds, KB a microsecond
+  const double kb = double(row_bytes(n, type)) / 1024., sm = sms(), slots = 8 * sm;
+  const auto round = [&](double ctas, double part) { return ctas > 0 ? std::max(ctas * part / RATE, part / OWN) : 0.; };
   int best = 1;
-  int64_t least = INT64_MAX;
-  for (int parts = 1; parts <= MAX_CLUSTER && (parts == 1 || bytes / parts >= 8192); parts *= 2) {
-    const int64_t cost = (rows * parts + slots - 1) / slots * (bytes / parts + 24576);
+  double least = INFINITY;
+  for (int parts = 1; parts <= MAX_CLUSTER && (parts == 1 || kb / parts >= 8.); parts *= 2) {
+    const double ctas = double(rows) * parts, full = std::floor(ctas / slots), part = kb / parts;
+    const double cost = EACH * ctas / sm + full * round(slots, part) + round(ctas - full * slots, part);
     if (cost < least) {
       least = cost;
       best = parts;
