@@ -45,11 +45,11 @@ constexpr int THREADS = 32 * (TAKERS + 4);  // (two warps have nothing to do: re
 // get more from the others.  (256 * 232 + 128 * 40 = 384 * 168.)
 constexpr int TAKER_REGISTERS = 232, OTHER_REGISTERS = 40;
 constexpr int TENSOR_COLUMNS = 2 * TILE_TOKENS;  // all there are: two accumulators
-// Pieces whose products the tensor cores add up.  They cut their sums off instead of rounding them, and what
-// that takes away grows with the depth: 3453 deep it put log-probabilities off by 1.6e-6 of themselves, in
-// two segments by 7e-7 (a float32 product: 5e-7).  Segments are added by the takers, which costs 4096 x 4096 x
-// 32768 650 us instead of 604; segments of 1024 would be 3.6e-7, and 2048 x 131072 1285 us instead of 1161.
-constexpr int SEGMENT = 32;
+// Pieces whose products the tensor cores add up at a temperature of 1 or more (segment_pieces).  They cut their sums
+// off instead of rounding them, and what that takes away grows with the depth: 3453 deep it put log-probabilities off
+// by 1.6e-6 of themselves, in two segments by 7e-7 (a float32 product: 5e-7).  The takers add the segments, which costs
+// 4096 x 4096 x 32768 640 us instead of 604; with segments of half as much 2048 x 131072 would take 1285 instead of 1161.
+constexpr int SEGMENT = 32, LEAST_SEGMENT = 8;
 constexpr int PARTS = 2;    // a row's columns are taken by two threads, 32 by 32 in turn
 
 constexpr int ROWS_BYTES = TILE_ROWS * DEPTH * 2;
@@ -376,13 +376,22 @@ bool describe(CUtensorMap* map, const void* p, bool bf16, int64_t rows, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What a logit lacks counts 1 / T times in a log-probability (of rows with temperatures of their own: twice), and
+// twice as much in an entropy: 1502 deep at 0.556, entropies were off by 2.1e-6 of themselves in one segment (a
+// float32 product: 7.5e-7).
+int segment_pieces(const HeadArgs& a) {
+  const float part = (a.temperature ? 0.5f : std::min(a.all_temperature, 1.f)) * (a.entropies ? 0.5f : 1.f);
+  return std::max(static_cast<int>(SEGMENT * part), LEAST_SEGMENT);
+}
+
 Plan plan_for(const HeadArgs& a) {
   Plan p;
   p.row_tiles = static_cast<int>((a.rows + TILE_ROWS - 1) / TILE_ROWS);
   p.rows = static_cast<int>(std::min<int64_t>(TILE_ROWS, (a.rows + 7) / 8 * 8));
   p.pieces = static_cast<int>((a.width + DEPTH - 1) / DEPTH);
   p.token_tiles = static_cast<int>((a.n + TILE_TOKENS - 1) / TILE_TOKENS);
-  p.segments = (p.pieces + SEGMENT - 1) / SEGMENT;
+  const int most = segment_pieces(a);
+  p.segments = (p.pieces + most - 1) / most;
   p.stages = std::min(MAX_STAGES, RING_BYTES / p.stage_bytes());
   // Runs of up to 4 tiles, while there are 8 runs or more for each SM.
   const int64_t tiles = int64_t(p.row_tiles) * p.token_tiles;

@@ -42,7 +42,8 @@ def check(pk, hidden, weight, tokens, T=1.0, **how):
     # d H / d z_i = -p_i (log p_i + H): the sizes of log p_i + H under p are the mean of x and H.
     close(as_numpy(r.entropies), H, np.where(live, off * (2 * mean + 2 * np.abs(H)) + row_error(mean, value=H) + 2.0 ** -18 * mean, 0), "entropies")
     without = pk.token_logprobs(hidden, tokens, weight=weight, temperature=T, **how)
-    assert torch.equal(without.logprobs, r.logprobs) and without.entropies is None and r.stats is None
+    close(as_numpy(without.logprobs), lp, np.where(live, 2 * off + row_error(mean, at, lp), 0), "logprobs alone")
+    assert without.entropies is None and r.stats is None
     return r
 
 
@@ -129,6 +130,20 @@ def test_deep_products_keep_their_precision(pk, cuda_device, width):
     got = as_numpy(pk.token_logprobs(hidden, tokens, weight=weight).logprobs)
     want, _ = ref.logprobs(as_numpy(hidden) @ as_numpy(weight).T, tokens.cpu().numpy())
     assert np.linalg.norm(got - want) < 2.0 ** -18 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("T", [0.3, 0.6, 1.0])
+def test_entropies_at_low_temperatures(pk, cuda_device, T):
+    # As above, with 1 / T of it and segments the shorter for that: the same bound, twice for an entropy's own sum.
+    hidden, weight, tokens = inputs(400, 1502, 900, torch.float16)
+    got = pk.token_logprobs(hidden, tokens, weight=weight, temperature=T, entropy=True)
+    z = as_numpy(hidden) @ as_numpy(weight).T
+    lp, H = ref.logprobs(z, tokens.cpu().numpy(), T)
+    assert np.linalg.norm(as_numpy(got.logprobs) - lp) < 2.0 ** -18 * np.linalg.norm(lp)
+    assert np.linalg.norm(as_numpy(got.entropies) - H) < 2.0 ** -17 * np.linalg.norm(np.maximum(H, 1))
+    per_row = torch.full((400,), T, device=cuda_device)
+    again = pk.token_logprobs(hidden, tokens, weight=weight, temperature=per_row, entropy=True)
+    assert np.linalg.norm(as_numpy(again.entropies) - H) < 2.0 ** -17 * np.linalg.norm(np.maximum(H, 1))
 
 
 @pytest.mark.parametrize("width", [200, 2500])
