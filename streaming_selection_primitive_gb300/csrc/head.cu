@@ -54,7 +54,8 @@ constexpr int PARTS = 2;    // a row's columns are taken by two threads, 32 by 3
 
 constexpr int ROWS_BYTES = TILE_ROWS * DEPTH * 2;
 constexpr int RING_BYTES = 4 * (ROWS_BYTES + TILE_TOKENS * DEPTH * 2);
-constexpr int SHARED_BYTES = RING_BYTES + ROWS_BYTES + 1024;  // (the last product of few rows looks past the ring, which begins at a multiple of 1024 bytes)
+// (The last product of few rows looks past the ring, which begins at a multiple of 1024 bytes.)
+constexpr int SHARED_BYTES = RING_BYTES + ROWS_BYTES + 1024;
 
 // How the work is cut: run r is row tile r % row_tiles and the vocabulary's tiles
 // (r / row_tiles) * run and on, `run` of them, so that CTAs that work at the same time share
@@ -427,8 +428,8 @@ cudaError_t launch_head_logprobs(const HeadArgs& a, cudaStream_t stream) {
     err = launch_kernel(kernel, dim3(grid), dim3(THREADS), size_t(SHARED_BYTES), stream, hidden, weight, a, plan,
                         product_descriptor(bf16, TILE_ROWS, TILE_TOKENS), parts, runs, logits, head_wait());
   if (err == cudaSuccess)
-    err = launch_kernel(k_head_join, dim3(static_cast<unsigned>((a.rows + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32))), dim3(JOIN_THREADS), 0, stream,
-                        a, parts, logits, count);
+    err = launch_kernel(k_head_join, dim3(static_cast<unsigned>((a.rows + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32))), dim3(JOIN_THREADS), 0,
+                        stream, a, parts, logits, count);
   const cudaError_t freed = cudaFreeAsync(work, stream);
   return err != cudaSuccess ? err : freed;
 }

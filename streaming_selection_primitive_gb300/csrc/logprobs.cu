@@ -308,7 +308,8 @@ __device__ __forceinline__ uint4 load_words(const char* p, bool odd) {
 
 // The gradient of `count` elements from `p` (in global or in shared memory) to `out`, by STEP
 // threads; `token` is the token's place among them, out of range where it is none.  Where p and
-// out stand differently to the 16-byte boundaries, 16 bytes of the gradient come from p's words.  (p may be out: an element is read by the thread that writes it.)
+// out stand differently to the 16-byte boundaries, 16 bytes of the gradient come from p's words.
+// (p may be out: an element is read by the thread that writes it.)
 template <typename T, bool ENTROPY, int STEP, int COUNT = LOADS>
 __device__ __forceinline__ void write_gradient(const T* p, T* out, int count, int thread, int token, const Slopes& k) {
   constexpr int N = PER_VECTOR<T>, SIZE = sizeof(T);
