@@ -67,13 +67,17 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Static shared memory of a kernel that is launched by launch_clusters_most with a few KB of dynamic one
+// below 48 KB: no more than this.
+constexpr size_t STATIC_ROOM = 8 * 1024;
+
 // Launches a kernel whose CTAs form clusters of `cluster`, as launch_kernel does, with `smem`
 // bytes of dynamic shared memory, `most` being what any call of it asks for.  (The
 // limit is the kernel's, for all host threads: it is set to the same number whatever the call.)
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_clusters_most(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, size_t smem,
                                         size_t most, cudaStream_t stream, Args... args) {
-  if (smem > 48 * 1024) {  // (with less any limit will do)
+  if (smem + STATIC_ROOM > 48 * 1024) {  // (what a launch has without asking holds static and dynamic memory together)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }

@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(SHORT_THREADS, GRADIENT ? 3 : SHORT_PER_SM) k_
 // shared memory: the row is read from memory once, and its sums and its gradient are both
 // made from the copy.  Many such CTAs share an SM, so that some copy while others work.
 constexpr int KEEP_SHARED = 112 * 1024;  // dynamic shared memory at most
+static_assert(sizeof(Exchange<8>) + sizeof(uint64_t) <= STATIC_ROOM, "static shared memory of k_policy_keep");
 
 template <typename T, bool ENTROPY, int KEEP_THREADS>
 __global__ void __launch_bounds__(KEEP_THREADS, 1024 / KEEP_THREADS) k_policy_keep(LogprobArgs a, PolicyHow how) {
