@@ -68,11 +68,12 @@ __device__ __forceinline__ void add_exact(float& sum, float& lost, float v) {
   sum = r;
 }
 
-// The exponent by which sums by the centre of `from` shrink when taken by that of `to`.
+// The exponent by which sums by the centre of `from` shrink when taken by that of `to`: what each has besides (m c
+// exactly) counts too, where only one of them is fused.
 // (fmaxf gives NO_MASS where it is NaN, at infinite ones: what is NaN already stays it, what is zero too.)
 __device__ __forceinline__ float shrink(float from, float to, float c) {
   const Centre a(from, c), b(to, c);
-  return fmaxf(from == -INFINITY ? NO_MASS : a.fused && b.fused ? b.by - a.by : (a.m - b.m) * c, NO_MASS);
+  return fmaxf(from == -INFINITY ? NO_MASS : a.fused && b.fused ? b.by - a.by : (a.m - b.m) * c + (b.off() - a.off()), NO_MASS);
 }
 
 // Row results that the kernels exchange (and the logit of the row's token with them, where they do).
