@@ -561,8 +561,8 @@ typedef struct profk_preference {
  * a pair's term is -(1 - e) log sigmoid(d) - e log sigmoid(-d); the loss is
  * the mean of the pairs' terms (0 without a pair).
  *   offsets      device, 2*pairs + 1 int64, not falling, within 0 .. rows.  Rows before
- *                the first and from the last on are left out.  A sequence whose offsets are
- *                not so makes its pair's margin and the loss NaN (its rows' slopes are not set)
+ *                the first and from the last on are left out.  Where any offset is not so, the
+ *                loss, all margins and the slopes of all rows that are not left out are NaN
  *   out_loss     device, one float
  *   out_margins  device, pairs floats: d
  *   out_slopes   device, rows floats: d loss / d logprob (for the backward call) */

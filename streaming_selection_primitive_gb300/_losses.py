@@ -153,7 +153,8 @@ def preference_loss(logits, tokens, offsets, *, ref_logprobs=None, beta: float =
     the sum (average: the mean) of lp - ref over what counts of sequence j,
         d = beta (D_2i - D_2i+1) - margin,
     loss is the mean over the pairs of -(1 - e) log sigmoid(d) - e log sigmoid(-d), e the label_smoothing; margins
-    holds the d.  Offsets that fall or leave the rows give NaN.
+    holds the d.  Where an offset falls or leaves the rows, loss, all margins and the gradient of what is not left
+    out are NaN.
 
     Where logits requires a gradient, loss carries it."""
     if getattr(logits, "requires_grad", False) and _torch().is_grad_enabled():

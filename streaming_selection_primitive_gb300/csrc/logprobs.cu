@@ -836,6 +836,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_policy_join(LogprobArgs a, Pol
 // log(1 + exp v)
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
+// Whether no offset falls or leaves the rows, for all threads of the CTA.  (Of offsets that fall, two sequences that are in
+// order by themselves may share rows, and two teams their slopes: every CTA looks at all of them before any row.)
+__device__ __forceinline__ bool offsets_sound(const LogprobArgs& a) {
+  bool sound = a.offsets[0] >= 0 && a.offsets[a.sequences] <= a.rows;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < a.sequences; i += JOIN_THREADS) sound &= a.offsets[i] <= a.offsets[i + 1];
+  return __syncthreads_and(sound);
+}
+
 // A pair by a team of TEAM threads (a warp, or the CTA): its margin, its term of the loss
 // and its rows' slopes.
 template <int TEAM>
@@ -848,44 +857,46 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a,
   bool waited = a.rows == 0;  // (no kernel went before that let this one start)
   if (waited) pdl_wait();
   Sum loss[1];
+  if (pairs > 0 && !offsets_sound(a)) {  // nothing is known of any sequence (and all CTAs leave)
+    if (!waited) pdl_wait();
+    pdl_trigger();
+    const int64_t step = int64_t(gridDim.x) * JOIN_THREADS, index = int64_t(blockIdx.x) * JOIN_THREADS + threadIdx.x;
+    for (int64_t pair = index; pair < pairs; pair += step) out.margins[pair] = NAN;
+    for (int64_t row = index; row < a.rows; row += step)
+      if (row_live(a, row)) out.slopes[row] = NAN;
+    if (index == 0) *out.loss = NAN;
+    return;
+  }
   // (A team of the whole CTA goes round together: the bound is the same for all of it.)
   for (int64_t pair = first; pair < pairs; pair += teams) {
     Sum sum[2];
     int live[2];
     int64_t edge[3];
-    bool good[2];
 #pragma unroll
     for (int i = 0; i < 3; ++i) edge[i] = a.offsets[2 * pair + i];
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      // Offsets that fall or leave the rows: nothing of the sequence is looked at.
-      good[side] = edge[side] >= 0 && edge[side + 1] >= edge[side] && edge[side + 1] <= a.rows;
-      live[side] = 0;
-    }
+    live[0] = live[1] = 0;
     if (!waited) {  // what is about to be read, on its way while the log-probabilities are not there yet
 #pragma unroll
       for (int side = 0; side < 2; ++side)
-        if (good[side])
-          for (int64_t row = edge[side] + thread * 4; row < edge[side + 1]; row += TEAM * 4) {
-            prefetch(a.tokens + row);
-            if (how.ref_logprobs) prefetch(how.ref_logprobs + row);
-          }
+        for (int64_t row = edge[side] + thread * 4; row < edge[side + 1]; row += TEAM * 4) {
+          prefetch(a.tokens + row);
+          if (how.ref_logprobs) prefetch(how.ref_logprobs + row);
+        }
       pdl_wait();
       waited = true;
     }
 #pragma unroll
     for (int side = 0; side < 2; ++side)
-      if (good[side])
 #pragma unroll 4
-        for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM) {
-          const float lp = a.logprobs[row], ref = how.ref_logprobs ? how.ref_logprobs[row] : 0.f;
-          if (a.tokens[row] >= 0) {
-            sum[side].add(lp);
-            sum[side].add(-ref);
-            sum[side].lost += out.slopes[row];  // (what lp lacks: the slopes come in its place)
-            ++live[side];
-          }
+      for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM) {
+        const float lp = a.logprobs[row], ref = how.ref_logprobs ? how.ref_logprobs[row] : 0.f;
+        if (a.tokens[row] >= 0) {
+          sum[side].add(lp);
+          sum[side].add(-ref);
+          sum[side].lost += out.slopes[row];  // (what lp lacks: the slopes come in its place)
+          ++live[side];
         }
+      }
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       sum[side] = warp_sum(sum[side]);
@@ -917,7 +928,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a,
       d.add(Sum{-sum[1].v, -sum[1].lost});
       apart = d.value();
     }
-    const float margin = good[0] && good[1] ? fmaf(how.beta, apart, -how.margin) : NAN;
+    const float margin = fmaf(how.beta, apart, -how.margin);
     const float eps = how.smoothing, rest = 1.f - eps;
     // (A side without weight is left out: it may be infinite.)
     float term = 0.f, slope = 0.f;
@@ -936,10 +947,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_preference_join(LogprobArgs a,
     const float each = slope * (how.beta / static_cast<float>(pairs));
 #pragma unroll
     for (int side = 0; side < 2; ++side)
-      if (good[side])
 #pragma unroll 4
-        for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM)
-          if (a.tokens[row] >= 0) out.slopes[row] = (side ? -each : each) * share[side];
+      for (int64_t row = edge[side] + thread; row < edge[side + 1]; row += TEAM)
+        if (a.tokens[row] >= 0) out.slopes[row] = (side ? -each : each) * share[side];
   }
   if (!waited) pdl_wait();
   pdl_trigger();
