@@ -29,6 +29,7 @@
 #include "../../include/profk.h"
 #include "lm.h"
 #include "logprobs.cuh"
+#include "ring.h"
 #include "tcgen05.cuh"
 
 namespace profk {
@@ -151,52 +152,37 @@ __global__ void __launch_bounds__(THREADS, 1)
     if constexpr (SEGMENTS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGISTERS));
     if (warp == COPIER) {
       if (lane == 0) {
-        int stage = 0, issued = 0;
-        unsigned parity = 1;  // (the ring begins empty)
+        RingPlace at;
+        int issued = 0;  // copies that may still be on their way: the last one to each stage
         for (int run = blockIdx.x; run < plan.runs && !sync.given_up; run += gridDim.x) {
           const int row0 = run % plan.row_tiles * TILE_ROWS, first = run / plan.row_tiles * plan.run;
           const int last = min(first + plan.run, plan.token_tiles);
           bool ok = true;
           for (int tile = first; tile < last && ok; ++tile)
             for (int piece = 0; piece < plan.pieces; ++piece) {
-              ok = barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit);
+              ok = barrier_wait(&sync.empty[at.stage], at.empty(), &sync.given_up, limit);
               if (!ok) break;
-              uint8_t* to = ring + stage * stage_bytes;
-              barrier_arrive_expect(&sync.full[stage], stage_bytes);
-              copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[stage]);
-              copy_tile(to + rows_bytes, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[stage]);
+              uint8_t* to = ring + at.stage * stage_bytes;
+              barrier_arrive_expect(&sync.full[at.stage], stage_bytes);
+              copy_tile(to, &hidden, piece * DEPTH, row0, &sync.full[at.stage]);
+              copy_tile(to + rows_bytes, &weight, piece * DEPTH, tile * TILE_TOKENS, &sync.full[at.stage]);
               issued = min(issued + 1, stages);
-              if (++stage == stages) {
-                stage = 0;
-                parity ^= 1;
-              }
+              at.next(stages);
             }
         }
-        // The last products' arrivals on the ring.
-        for (int i = 0; i < stages && !sync.given_up; ++i) {
-          if (!barrier_wait(&sync.empty[stage], parity, &sync.given_up, limit)) break;
-          if (++stage == stages) {
-            stage = 0;
-            parity ^= 1;
-          }
-          issued = 0;
-        }
-        if (sync.given_up && issued > 0) {
-          // Nobody may be reading any more, but copies may still be writing: the last turn of each
-          // stage is waited for.  (Whoever has given up has set the flag, which these waits are not to look at.)
-          int nobody = 0;
-          for (int i = 0; i < issued; ++i) {
-            if (stage == 0) parity ^= 1;
-            stage = stage ? stage - 1 : stages - 1;
-            nobody = 0;
-            barrier_wait(&sync.full[stage], parity ^ 1, &nobody, WAIT_POLLS);
-          }
-        }
+        // Whoever gives up sets the flag, which the waits for what is still being copied are not to look at.
+        leave_ring(
+            at, issued, stages, [&](RingPlace p) { return barrier_wait(&sync.empty[p.stage], p.empty(), &sync.given_up, limit); },
+            [&](RingPlace p) {
+              int nobody = 0;
+              barrier_wait(&sync.full[p.stage], p.full(), &nobody, WAIT_POLLS);
+            });
       }
     } else if (warp == MULTIPLIER) {
       if (lane == 0) {
-        int stage = 0, half = 0;
-        unsigned parity = 0, taken = 1;  // (both accumulators begin free)
+        RingPlace at;
+        int half = 0;
+        unsigned taken = 1;  // (both accumulators begin free)
         bool ok = true;
         for (int run = blockIdx.x; run < plan.runs && ok; run += gridDim.x) {
           const int first = run / plan.row_tiles * plan.run, last = min(first + plan.run, plan.token_tiles);
@@ -208,18 +194,15 @@ __global__ void __launch_bounds__(THREADS, 1)
               after_barrier();
               const uint32_t to = tensor + half * TILE_TOKENS;
               for (int first_piece = piece; piece < end; ++piece) {
-                ok = barrier_wait(&sync.full[stage], parity, &sync.given_up, limit);
+                ok = barrier_wait(&sync.full[at.stage], at.full(), &sync.given_up, limit);
                 if (!ok) break;
                 after_barrier();
-                const uint64_t x = tile_descriptor(ring + stage * stage_bytes), w = tile_descriptor(ring + stage * stage_bytes + rows_bytes);
+                const uint64_t x = tile_descriptor(ring + at.stage * stage_bytes), w = tile_descriptor(ring + at.stage * stage_bytes + rows_bytes);
 #pragma unroll
                 for (int k = 0; k < DEPTH / 16; ++k)  // 32 bytes on along the rows: 2 in the descriptor's units
                   multiply(to, x + 2 * k, w + 2 * k, product, piece - first_piece + k > 0);
-                products_arrive(&sync.empty[stage]);
-                if (++stage == stages) {
-                  stage = 0;
-                  parity ^= 1;
-                }
+                products_arrive(&sync.empty[at.stage]);
+                at.next(stages);
               }
               if (!ok) break;
               products_arrive(&sync.done[half]);
