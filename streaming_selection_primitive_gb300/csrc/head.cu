@@ -292,9 +292,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (in) parts[(row * count + index) * PARTS + side] = make_float4(sum.m, sum.s, sum.t, 0.f);
     }
   }
-  // The products in flight are done: what came before a taken tile is, and on giving up
-  // the multiplier's own are waited for.
-  if (warp == MULTIPLIER && lane == 0 && sync.given_up) {
+  // The products in flight are waited for, by a barrier that nothing else can make give up: where the takers' waits
+  // run out, that may be behind the multiplier's last look at the flag.  (Otherwise they are done when the takers are.)
+  if (warp == MULTIPLIER && lane == 0) {
     int nobody = 0;
     __shared__ uint64_t last;
     barrier_init(&last, 1);
