@@ -100,7 +100,9 @@ def token_logprobs_backward(logits, tokens, r: TokenLogprobs, *, grad_logprobs=N
 
     grad_logprobs, grad_entropies: (rows,) float32, or None; the second needs a call with entropy=True.  A row
     whose entries are 0 gets 0, whatever its logits hold.  out: where to write, unit column stride; it may be the
-    logits themselves.  The result comes without a graph."""
+    logits themselves.  Autograd takes it as changed in place: what has saved it raises when it is gone back
+    through, and a leaf that requires a gradient is refused while gradients are recorded.  The result comes without a graph
+    (an `out` as it is)."""
     if r.stats is None:
         raise ValueError("there is no gradient from hidden states: give logits")
     return _made(None, _ext().token_logprobs_backward(logits, tokens, r.temperature, r.stats, r.entropies, grad_logprobs, grad_entropies,
@@ -121,7 +123,7 @@ def policy_loss(logits, tokens, old_logprobs, advantages, *, ref_logprobs=None, 
 
     Where logits requires a gradient, loss carries it.  gradient=True gives grad_logits instead, the gradient
     of the loss in the logits' type, from the same launch (a second look at a row that is still on the chip); out: where
-    to write it, unit column stride; it may be the logits themselves."""
+    to write it, as in token_logprobs_backward."""
     if not gradient and getattr(logits, "requires_grad", False) and _torch().is_grad_enabled():
         constants = {"old_logprobs": old_logprobs, "advantages": advantages, "ref_logprobs": ref_logprobs, "weights": weights,
                      "temperature": temperature}

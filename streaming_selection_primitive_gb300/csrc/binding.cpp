@@ -136,6 +136,12 @@ class Place {
   std::optional<c10::cuda::CUDAStreamGuard> side_;
 };
 
+// A caller's tensor that a call writes to: autograd, which goes by the version, is to notice where it has saved it.
+// (A refused call has written nothing.  A tensor of inference mode has no version, and is never saved.)
+void written(const Tensor& t, int code) {
+  if ((code == PROFK_OK || code == PROFK_ERR_CUDA) && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* tuple_of(std::initializer_list<Tensor> tensors) {
   PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
   if (!t) throw python_error();
@@ -209,6 +215,8 @@ PyObject* sample_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int code = profk_sample_tokens(like.data_ptr(), x.type, x.rows, x.n, x.ld, static_cast<float*>(noise.data_ptr()),
                                        noise_ld, mask, mask_ld, &how, static_cast<int64_t*>(tokens.data_ptr()),
                                        static_cast<float*>(logprobs.data_ptr()), place.stream());
+  if (arg[7] != Py_None)
+    for (const Tensor& t : {tokens, logprobs}) written(t, code);
   return code == PROFK_OK ? tuple_of({tokens, logprobs}) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
@@ -270,6 +278,7 @@ PyObject* route_backward(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   }
   const int code = profk_route_backward(like.data_ptr(), x.type, x.rows, x.n, x.ld, k, &how, chosen, counts, grad_gates,
                                         grad_loss, out.data_ptr(), out_ld, place.stream());
+  if (arg[7] != Py_None) written(out, code);
   return code == PROFK_OK ? THPVariable_Wrap(out) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
@@ -342,6 +351,9 @@ struct GradientOut {
       t = on_device(o, "out", x.t->scalar_type(), *x.t);
       ld = rows_of(t, "out", x.rows, x.n);
       if (ld < x.n) refuse(PyExc_ValueError, "the rows of out must not share memory");
+      const at::TensorBase& of = t.is_view() ? t._base() : static_cast<const at::TensorBase&>(t);
+      if (at::GradMode::is_enabled() && of.requires_grad() && of.is_leaf())
+        refuse(PyExc_ValueError, "out is a leaf that requires a gradient: detach it, or call under torch.no_grad()");
     }
   }
 };
@@ -392,6 +404,7 @@ PyObject* token_logprobs_backward(PyObject*, PyObject* const* arg, Py_ssize_t co
   const GradientOut out(arg[8], x, place);
   const int code = profk_token_logprobs_backward(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, stats,
                                                  entropies, g, h, scale, out.t.data_ptr(), out.ld, place.stream());
+  if (arg[8] != Py_None) written(out.t, code);
   return code == PROFK_OK ? THPVariable_Wrap(out.t) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
@@ -463,6 +476,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const int code = profk_policy_loss(like.data_ptr(), x.type, x.rows, x.n, x.ld, tokens, T.rows, T.all, &how, data(loss),
                                      data(kl), data(logprobs), data(entropies), data(stats), data(slopes),
                                      data(entropy_slopes), grad.defined() ? grad.data_ptr() : nullptr, grad_ld, place.stream());
+  if (arg[12] != Py_None) written(grad, code);
   return code == PROFK_OK ? tuple_of({loss, kl, clipped, entropies_sum, logprobs, entropies, stats, slopes, entropy_slopes, grad}, arg[6]) : PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
