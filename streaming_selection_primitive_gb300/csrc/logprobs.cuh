@@ -153,6 +153,14 @@ __device__ __forceinline__ float inverse_temperature(float T) {
   return c > 0.f && c < INFINITY ? c : NAN;
 }
 
+// exp(q) - 1 - q, e = expm1(q): never below 0.  Near 0, where the difference is e's rounding (and of either sign), by its series:
+// the first term left out is 2^-26 of it at the border, where the difference is off by 2^-20 of itself at most.
+__device__ __forceinline__ float exp_beyond_line(float q, float e) {
+  if (fabsf(q) < 0.25f)
+    return q * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 5040, 1.f / 720), 1.f / 120), 1.f / 24), 1.f / 6), 0.5f);
+  return e == INFINITY ? e : e - q;
+}
+
 // One token's part of the clipped policy loss, by its log-probability.
 struct PolicyTerm {
   float loss;     // without the entropy
@@ -172,7 +180,7 @@ __device__ __forceinline__ PolicyTerm policy_term(float lp, float old_lp, float 
   y.kl = 0.f;
   if (with_ref) {
     const float q = ref_lp - lp, e = expm1f(q);
-    y.kl = e == INFINITY ? e : e - q;
+    y.kl = exp_beyond_line(q, e);
     if (how.kl != 0.f) {
       y.loss += how.kl * y.kl;
       y.slope -= how.kl * e;
