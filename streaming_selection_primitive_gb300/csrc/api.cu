@@ -112,10 +112,14 @@ cudaError_t pool_for_current_device(cudaMemPool_t* out) {
   props.location.type = cudaMemLocationTypeDevice;
   props.location.id = dev;
   cudaMemPool_t pool;
+  // (The first call may be one that is captured: making a pool, no work of the stream, would end the capture.)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaThreadExchangeStreamCaptureMode(&mode);
   e = cudaMemPoolCreate(&pool, &props);
-  if (e != cudaSuccess) return e;
   uint64_t keep = ~0ull;
-  cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+  if (e == cudaSuccess) cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
   pools[dev] = pool;
   *out = pool;
   return cudaSuccess;
