@@ -11,13 +11,13 @@ feed-forward network is split into experts, and an output matrix.  Each step
   (``sample_tokens``, under top-k, top-p and the temperature).
 
 With ``--policy-steps`` and ``--preference-steps`` the trained model is trained on
-by its own samples: a token is rewarded where it follows the table.  Policy steps
+by its own samples: a token is rewarded where it follows the table.  Policy steps (the later ones)
 continue sequences, take the advantage of each token over its group's mean
 reward, and the clipped policy loss with a KL term to the model as it was
 (``policy_loss``; the reference's log-probabilities come straight from its hidden
 states, ``token_logprobs`` with a weight).  Preference steps continue each sequence
 twice and prefer the continuation that followed the table more often
-(``preference_loss``).
+(``preference_loss``); where both did equally often neither counts.
 
 It prints the loss, the balance loss and the share of sampled tokens that
 follow the table as one JSON object.
@@ -130,8 +130,18 @@ def policy_steps(model, table, steps: int, generator, *, groups=32, group=8, len
     return [tuple(v.item() for v in step) for step in history]
 
 
+def preferred(inputs, tokens, reward, pairs: int, length: int):
+    """The better continuation of each two first: (inputs, tokens, whether each pair has one).  Of two that score the
+    same neither is preferred: their tokens are left out (-1), so that no gradient comes from them."""
+    score = reward.view(pairs, 2, length).sum(2)
+    order = torch.argsort(-score, dim=1, stable=True)[:, :, None].expand(pairs, 2, length)
+    inputs, tokens = (torch.gather(t.view(pairs, 2, length), 1, order) for t in (inputs, tokens))
+    apart = score[:, 0] != score[:, 1]
+    return inputs.flatten(), torch.where(apart[:, None, None], tokens, -1).flatten(), apart
+
+
 def preference_steps(model, table, steps: int, generator, *, pairs=32, length=16, beta=0.2):
-    """(loss, mean margin) of each step."""
+    """(loss, mean margin of the pairs that are compared) of each step."""
     reference = copy.deepcopy(model)
     optimizer = torch.optim.Adam(model.parameters(), lr=1e-3)
     offsets = torch.arange(0, 2 * pairs * length + 1, length, device=table.device)
@@ -139,17 +149,14 @@ def preference_steps(model, table, steps: int, generator, *, pairs=32, length=16
     for _ in range(steps):
         first = torch.randint(len(table), (pairs,), generator=generator, device=table.device).repeat_interleave(2)
         inputs, tokens, _, reward = answers(model, table, first, length, generator, 1.0)
-        # The better continuation of each two comes first (of equal ones the one that was there first).
-        score = reward.view(pairs, 2, length).sum(2)
-        order = torch.argsort(-score, dim=1, stable=True)[:, :, None].expand(pairs, 2, length)
-        inputs, tokens = (torch.gather(t.view(pairs, 2, length), 1, order).flatten() for t in (inputs, tokens))
+        inputs, tokens, apart = preferred(inputs, tokens, reward, pairs, length)
         ref = reference_logprobs(reference, inputs, tokens, 1.0)
         logits, _ = model(inputs)
         r = pk.preference_loss(logits, tokens, offsets, ref_logprobs=ref, beta=beta)
         optimizer.zero_grad(set_to_none=True)
         r.loss.backward()
         optimizer.step()
-        history.append((r.loss.detach(), r.margins.mean()))
+        history.append((r.loss.detach(), r.margins.sum() / apart.sum().clamp(min=1)))
     return [tuple(v.item() for v in step) for step in history]
 
 
@@ -162,14 +169,14 @@ def run(steps=200, batch=2048, vocab=512, width=64, experts=16, k=2, balance=0.0
     table = torch.randperm(vocab, generator=generator, device=device)
     history = train(model, table, steps, batch, balance, generator)
     trained_on = {}
+    if preference:  # (first: after policy steps nearly all continuations score the same)
+        margins = preference_steps(model, table, preference, generator)
+        trained_on["preference_loss"] = [margins[0][0], margins[-1][0]]
+        trained_on["margin"] = margins[-1][1]
     if policy:
         rewards = policy_steps(model, table, policy, generator)
         trained_on["reward"] = [rewards[0][0], rewards[-1][0]]
         trained_on["kl"] = rewards[-1][2]
-    if preference:
-        margins = preference_steps(model, table, preference, generator)
-        trained_on["preference_loss"] = [margins[0][0], margins[-1][0]]
-        trained_on["margin"] = margins[-1][1]
     tokens, logprobs = generate(model, torch.arange(sequences, device=device) % vocab, length, generator)
     return {
         "steps": steps,
