@@ -100,8 +100,6 @@ __device__ __forceinline__ void copy_bytes(void* to, const void* from, unsigned 
                "r"(bytes), "r"(shared_address(done))
                : "memory");
 }
-// Orders this thread's accesses to shared memory before the copies it issues.
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---- products ----
 
