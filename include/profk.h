@@ -474,8 +474,10 @@ int profk_route_backward(const void* logits, int type, int64_t tokens, int64_t e
  *                pass; 8-byte aligned
  * A logit of -inf has probability 0.  A row of nothing but -inf gives -inf, the
  * entropy 0 and the gradient 0; one with a NaN or +inf gives NaN.  Sums are
- * float32 with their losses carried along, or double, in a fixed order: the same
- * call gives the same bits.  The calls only enqueue work on `stream`, may be
+ * float32, in a fixed order: the same call gives the same bits.  A sum over rows, and a
+ * thread's sum over a row that it reads from memory, carries along what its additions lose; one
+ * over a part of a row in shared memory (at most 112 KB by 256 threads), over a tile of products
+ * or over the threads does not.  The calls only enqueue work on `stream`, may be
  * captured in a graph, and allow rows = 0. */
 int profk_token_logprobs(const void* logits, int type, int64_t rows, int64_t n, int64_t ld, const int64_t* tokens,
                          const float* temperature, float all_temperature, float* out_logprobs, float* out_entropies,

@@ -81,7 +81,8 @@ def token_logprobs(x, tokens, *, weight=None, temperature=1.0, entropy: bool = F
     `weight` (n, width), hidden states (rows, width), both bfloat16 or both float16, of 16-byte aligned rows:
     the logits are then their product x @ weight.T in float32, which is never in memory; width may be odd.
     tokens: (rows,) int64.  A negative token leaves its row out: its logits may hold anything, its
-    outputs are 0 and so is its gradient.  A token from n on gives NaN.
+    outputs are 0 and so is its gradient.  A token from n on gives NaN.  (With `weight` a row that is left out takes
+    as long as another.)
     temperature: a positive number, or a float32 tensor of one per row.
 
     A row of nothing but -inf gives -inf and the entropy 0; one with a NaN or +inf gives NaN.
@@ -121,7 +122,8 @@ def policy_loss(logits, tokens, old_logprobs, advantages, *, ref_logprobs=None, 
     mask / mask.sum() takes the mean over a mask and any other mean is as easy; 0 leaves a token out
     as a negative token does; None: 1 / rows.  entropy: its factor; None: entropies are not taken at all.
 
-    Where logits requires a gradient, loss carries it.  gradient=True gives grad_logits instead, the gradient
+    Where logits requires a gradient, loss carries it (and going back reads the logits again: 4096 x 131072 bfloat16
+    489 us in all, with gradient=True 339).  gradient=True gives grad_logits instead, the gradient
     of the loss in the logits' type, from the same launch (a second look at a row that is still on the chip); out: where
     to write it, as in token_logprobs_backward."""
     if not gradient and getattr(logits, "requires_grad", False) and _torch().is_grad_enabled():

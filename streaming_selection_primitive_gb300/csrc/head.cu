@@ -20,8 +20,11 @@
 // one's copies were announced to the first by a warp, one exchange more a piece) or copy half
 // of it for both (777 x 1000 x 50001 86 us, 300 x 1024 x 20000 30 instead of 23).
 //
+// Rows that are left out are copied and multiplied like others (4096 x 2048 x 131072 takes the same with half of
+// them left out, by themselves the other half would take 657 us): give only the rows that count where many do not.
+//
 // Every wait is bounded; a CTA whose wait ends without its barrier writes NaN for all rows of
-// its remaining work.
+// its remaining work, and leaves when its copies and products are done.
 #include <cuda.h>
 
 #include <algorithm>
@@ -43,7 +46,8 @@ constexpr int TAKERS = 8;   // warps that take tiles: two for each quarter of th
 constexpr int COPIER = TAKERS, MULTIPLIER = TAKERS + 1;  // the other two warps
 constexpr int THREADS = 32 * (TAKERS + 4);  // (two warps have nothing to do: registers are handed over by groups of four)
 // Registers a thread where a tile has segments: of 168 at the launch the takers, who hold 128 sums each,
-// get more from the others.  (256 * 232 + 128 * 40 = 384 * 168.)
+// get more from the others.  (256 * 232 + 128 * 40 = 384 * 168.)  It is not enough for 32 columns just loaded beside the
+// sums and the row's state: 312 bytes a thread are spilled (with entropies 324), with 224 registers 376.
 constexpr int TAKER_REGISTERS = 232, OTHER_REGISTERS = 40;
 constexpr int TENSOR_COLUMNS = 2 * TILE_TOKENS;  // all there are: two accumulators
 // Pieces whose products the tensor cores add up at a temperature of 1 or more (segment_pieces).  They cut their sums

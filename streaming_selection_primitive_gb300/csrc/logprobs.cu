@@ -467,7 +467,9 @@ __device__ __forceinline__ Slopes policy_slopes(const Row<GRADIENT>& r, const Ro
 
 // The exchange of the warps' sums within a cluster: each CTA has room for those of all, written
 // there by stores that count on its barrier.  (No fence over what threads have written
-// before, as a barrier of the cluster would be.)
+// before, as a barrier of the cluster would be.)  A CTA leaves when all stores to it have come; one whose wait
+// ran out could be gone when they do.  The longest part, 512 MB, takes 0.1 s where all SMs read at once, and a wait
+// WAIT_POLLS polls of 3.8 us: 16 s.
 template <int COUNT>  // warps of a CTA
 struct Exchange {
   RowSum sums[MAX_CLUSTER * COUNT];
@@ -710,7 +712,8 @@ __global__ void __launch_bounds__(SHORT_THREADS, SHORT_PER_SM) k_logprobs_backwa
 
 // ---------------------------------------------------------------------------
 // The sums over rows: floats with their losses carried along (double precision takes
-// several times as long here), in a fixed order: the same call gives the same bits.
+// several times as long here), in a fixed order: the same call gives the same bits.  One cluster has them all, which
+// shows where rows are many and short: of 2^20 rows of 64 a policy loss takes 863 us, 222 of them the join.
 //
 // These kernels follow the one that writes the log-probabilities, which lets them start
 // once it has begun itself, that is once all before it is done: what the user gave can be read

@@ -108,7 +108,8 @@ __device__ __forceinline__ RowSum joined(const RowSum& y, const RowSum& z, float
 }
 
 // ln s as a float and what it lacks, for s >= 1: from s = 2^k f with f in [1, 2), whose logarithm is off by less
-// than that of s (2^-25 of at most 0.7, not of 20).  k times the head of ln 2 (15 bits) is exact.
+// than that of s (2^-25 of at most 0.7, not of 20).  ln 2 is split as Cody and Waite do (Software Manual for the
+// Elementary Functions, 1980): k times its head, 15 bits, is exact.
 __device__ __forceinline__ float log_exactly(float s, float& lacks) {
   const int bits = __float_as_int(s), k = (bits >> 23) - 127;
   const float f = __int_as_float((bits & 0x7fffff) | 0x3f800000);
