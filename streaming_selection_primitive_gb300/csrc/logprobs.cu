@@ -20,7 +20,7 @@
 //     of what 608 CTAs had in work.  Forward and backward of 1500 x 128003 float32 347 (2304 MB, 6.6 TB/s).
 //   entropies of 16-bit logits, more so into a gradient that stands otherwise to the 16-byte boundaries:
 //     instructions.  600 x 100001 float16 issues 2.9 of 4 a cycle at 45 % of the memory's rate;
-//     1001 of them 79 us (370 MB, 4.7 TB/s), 264 with single stores.
+//     1001 of them 81 us (370 MB, 4.6 TB/s), 264 with single stores.
 //   rows of 10 to 60 KB: a CTA's beginning and end, 4 to 5 us of which eight on an SM hide most.
 //     1000 x 16384 bfloat16 forward 9.4 us (33 MB), 12.5 by CTAs of 256 threads.
 //   few rows: latency.  1 x 32768 2.9 us, of which the launch is 2.5; 16 of them with policy loss and gradient 6.6.
@@ -55,7 +55,7 @@ template <typename T>
 constexpr int PER_VECTOR = 16 / int(sizeof(T));
 
 // Pair i of the elements in v.  BOUNDED: with -inf, and what is below LOWEST, as LOWEST (by one instruction
-// for two elements of 16 bits; small enough to be multiplied with any slope).
+// for two elements of 16 bits).
 template <typename T>
 constexpr float LOWEST = -INFINITY;
 template <>
@@ -333,7 +333,7 @@ __device__ __forceinline__ void write_gradient(const T* p, T* out, int count, in
   const bool has_token = place >= 0 && place < vectors * N && (place / N) % STEP == thread;
   const float token_slope = has_token ? slope_at<ENTROPY>(k, lm_float(p[token])) + k.one : 0.f;
   const Pair by = pair(k.at.by, k.at.by), cc = pair(k.at.c, k.at.c), k0 = pair(k.k0, k.k0), k1 = pair(k.k1, k.k1);
-  const bool bounded = lowest_will_do<T>(k.at);
+  const bool bounded = ENTROPY && lowest_will_do<T>(k.at) && fabsf(k.k1 * fmaf(LOWEST<T>, k.at.c, k.at.by)) < INFINITY;
   for (int i = thread; i < vectors; i += COUNT * STEP) {
     uint4 v[COUNT];
     if (same) {
@@ -358,7 +358,7 @@ __device__ __forceinline__ void write_gradient(const T* p, T* out, int count, in
         split(mul2(e, ENTROPY ? fma2(k1, kept, k0) : k0), y0, y1);
         put_pair(y + 2 * q, y0, y1);
       };
-      if (ENTROPY && bounded) {
+      if (bounded) {
 #pragma unroll
         for (int q = 0; q < N / 2; ++q) put(fma2(element_pair<T, true>(v[u], q), cc, by), q, std::true_type{});
       } else if (k.at.fused) {

@@ -88,3 +88,28 @@ def test_from_hidden_states(pk, cuda_device, sign):
         close(as_numpy(r.logprobs), lp, row_error(mean, at, lp))
     r = pk.token_logprobs(hidden.half(), tokens, weight=weight.half(), entropy=True)
     close(as_numpy(r.entropies), H, row_error(mean, value=H) + 2.0 ** -18 * mean)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [40, 301, 9001])
+@pytest.mark.parametrize("h", [1e20, 1e27, 1e33])
+def test_masked_logits_under_large_slopes(pk, cuda_device, dtype, n, h):
+    # A masked element has the gradient 0 however large its row's slope by the entropy is.
+    rng = np.random.default_rng(n)
+    logits = torch.from_numpy(rng.normal(size=(6, n))).to(dtype).cuda()
+    logits[:, n // 3: n // 2] = -float("inf")
+    tokens = torch.full((6,), n - 1, device=cuda_device)
+    r = pk.token_logprobs(logits, tokens, entropy=True)
+    dh = torch.full((6,), h, device=cuda_device)
+    got = pk.token_logprobs_backward(logits, tokens, r, grad_logprobs=0 * dh, grad_entropies=dh)
+    assert (got[:, n // 3: n // 2] == 0).all() and not got.isnan().any()
+    if dtype != torch.float16:  # (beyond what it holds)
+        l, t = as_numpy(logits), tokens.cpu().numpy()
+        zero, h64 = np.zeros(6), as_numpy(dh)
+        want = ref.gradient(l, t, 1.0, zero, h64)
+        # (the mean of x as log s - H: 2^-21 of their sizes, as in the test of masked logits at all temperatures)
+        x, _ = sizes(l, 1.0)
+        p = np.where(np.isfinite(l), np.exp(-x), 0.0)
+        p = p / p.sum(1, keepdims=True)
+        off = gradient_error(l, 1.0, zero, h64, want, dtype) + h * p * 2.0 ** -21 * 2 * np.log(n)
+        close(as_numpy(got), want, off)
